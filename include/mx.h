@@ -323,6 +323,138 @@ mx_status_t mx_fakequant_multi(const mx_tensor_t *tensors, int count,
                                mx_dtype_t dtype, mx_scale_mode_t mode,
                                void *stream);
 
+/* ---- MXFP8 through a transformer layer ---------------------------------------
+ * The MXFP8 format above, with its scale rule and E4M3 codes, on the path that
+ * a quantized layer runs: a norm that hands over 8-bit rows, products of 8-bit
+ * matrices (forward and the two of the backward pass), an 8-bit key/value
+ * cache and the attention that reads it (vLLM MXFP8/MXFP4 page: online MXFP8
+ * quantization for serving; MXFP8 = E4M3 with E8M0 scales). Here a scale
+ * covers `block` = 32 elements of a row (the library's MXFP8 layout) or 128
+ * (coarser: a quarter of the scale bytes); scales are uint8 [rows,
+ * ceil(k / block)], the last block of a row may be short, k is a multiple of
+ * 32. Another block is MX_ERR_SHAPE. Pointer, stream, alignment, aliasing and
+ * error conventions are those of the entry points above; rows == 0 (m, n or
+ * tokens == 0) returns MX_OK. Nothing is allocated or kept between calls. */
+
+/* Quantize x [rows, k] once along its rows (codes [rows, k], scales [rows,
+ * ceil(k / block)]) and once along its columns (codes_t [k, R], scales_t
+ * [k, ceil(rows / block)], R = rows rounded up to a multiple of 32; the codes
+ * past `rows` are 0) from one read of x. Either pair may be NULL (both of a
+ * pair; all four is MX_ERR_NULL). The column form is what the products of a
+ * backward pass sum over: dx = dy w takes w by columns, dw = dy^T x takes dy
+ * and x by columns. With block 32 codes and scales equal mx_quantize_mxfp8. */
+mx_status_t mx_quantize_mxfp8_blocks(const void *x, mx_dtype_t x_dtype, int64_t rows, int64_t k,
+                                     int block, uint8_t *codes, uint8_t *scales,
+                                     uint8_t *codes_t, uint8_t *scales_t, void *stream);
+
+/* h = x + residual (fp32; residual may be NULL: h = x), y = weight * h /
+ * sqrt(sum(h^2) / k + eps), quantized along the row to codes [rows, k] and
+ * scales [rows, ceil(k / block)]. h_out (NULL to leave it out; only with a
+ * residual) receives h rounded to the dtype; it may equal x or residual. x,
+ * residual, weight [k] and h_out share one dtype. The sum and y are fp32; h
+ * enters them unrounded. k <= 65536, rows < 2^31. A row holding NaN or an
+ * infinity gives blocks with scale 255. */
+mx_status_t mx_rmsnorm_mxfp8(const void *x, const void *residual, const void *weight,
+                             mx_dtype_t dtype, int64_t rows, int64_t k, float eps, int block,
+                             uint8_t *codes, uint8_t *scales, void *h_out, void *stream);
+
+/* Gradient of the norm, the quantizer passing gradients through unchanged:
+ * with s = 1 / sqrt(sum(h^2) / k + eps) and g = weight * dy,
+ *   dx = s (g - h s^2 sum(g h) / k) + through   (through: the gradient that
+ *        arrives at h past the norm, or NULL)
+ *   dweight[j] = sum over rows of dy h s        (fp32, overwritten)
+ * dy, h, weight, through and dx share one dtype; sums are fp32, in a fixed
+ * order. dx may equal dy, h or through. rows == 0 writes zeros to dweight.
+ * workspace: mx_rmsnorm_backward_workspace_size(rows, k) bytes of device
+ * scratch, 16-byte aligned (one row of k floats per workgroup). */
+size_t mx_rmsnorm_backward_workspace_size(int64_t rows, int64_t k);
+mx_status_t mx_rmsnorm_backward(const void *dy, const void *h, const void *weight,
+                                const void *through, mx_dtype_t dtype, int64_t rows, int64_t k,
+                                float eps, void *dx, float *dweight, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/* C [m, n] = A B^T for MXFP8 matrices A [m, k] and B [n, k] (codes and scales
+ * as above, the same block for both). c_dtype MX_BF16: the matrix cores'
+ * scaled 8-bit products with fp32 accumulators, rounded once (they drop bits
+ * of a product more than about 2^-14 below the largest of its group of eight:
+ * 1.4e-5 of the result's norm on normal data). c_dtype MX_F32: codes widened
+ * exactly to bf16, fp32 products and sums, half the rate. A scale byte 255 or
+ * a NaN code makes the results it enters NaN. k <= 2^20. workspace:
+ * mx_matmul_mxfp8_workspace_size(...) bytes, 16-byte aligned; 0 bytes (NULL
+ * allowed) where K is not split. k == 0 is MX_ERR_SHAPE. */
+size_t mx_matmul_mxfp8_workspace_size(int64_t m, int64_t n, int64_t k, int block,
+                                      mx_dtype_t c_dtype);
+mx_status_t mx_matmul_mxfp8(const uint8_t *a, const uint8_t *a_scales, const uint8_t *b,
+                            const uint8_t *b_scales, int64_t m, int64_t n, int64_t k, int block,
+                            mx_dtype_t c_dtype, void *c, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/* A paged key/value cache: `page` tokens (a power of two, 32 to 256) of one
+ * kv head share one scale byte for keys and one for values. Keys lie [pages,
+ * heads, page, dim], values transposed [pages, heads, dim, page] (both
+ * products then read 16 codes at once along the dimension they sum over),
+ * scales [pages, heads]. dim is 64 or 128. Contents before the first append
+ * do not matter. */
+typedef struct {
+  uint8_t *k_codes;
+  uint8_t *k_scales;
+  uint8_t *v_codes;
+  uint8_t *v_scales;
+  int64_t pages;
+  int heads;
+  int dim;
+  int page;
+} mx_kv_cache_t;
+
+/* A batch of sequences (device arrays, int32): row i of table [batch, width]
+ * lists the pages of sequence i in order; its new tokens are rows cu[i] ..
+ * cu[i+1] - 1 of the token arrays (cu[0] = 0, cu[batch] = tokens); lengths[i]
+ * is its length. A sequence may have no new tokens. Page numbers outside the
+ * cache are not followed (they are clamped to its last page). Pages that are
+ * written must belong to one sequence. */
+typedef struct {
+  const int32_t *table;
+  const int32_t *cu;
+  const int32_t *lengths;
+  int64_t tokens;
+  int batch;
+  int width;
+} mx_kv_batch_t;
+
+/* Append new tokens' keys and values, k and v [tokens, heads, dim] in dtype
+ * (k_stride, v_stride elements from token to token, multiples of 16 bytes;
+ * heads are adjacent, so both may be parts of one projection's rows). lengths[i]
+ * is what sequence i holds before; its new tokens follow. Per page and head the
+ * scale byte is the larger of the kept tokens' and the one the new tokens need
+ * (the MXFP8 rule over all of them in the page); where it grows the kept codes
+ * are rounded once more to it; a page without kept tokens starts anew. A NaN
+ * or infinity makes its page's scale 255 for that head until the page starts
+ * anew. Slots past the new end are left alone. Tokens past width pages are
+ * dropped. */
+mx_status_t mx_kv_append(const void *k, const void *v, mx_dtype_t dtype, int64_t k_stride,
+                         int64_t v_stride, const mx_kv_cache_t *cache, const mx_kv_batch_t *batch,
+                         void *stream);
+
+/* Causal attention of new tokens over the cache: q [tokens, q_heads, dim]
+ * bf16 (q_stride elements from token to token, a multiple of 8), query head h
+ * reads kv head h / (q_heads / heads); q_heads is a multiple of heads, at most
+ * 128 times it. lengths[i] is the length of sequence i with its new tokens
+ * appended: new token j of n sees keys 0 .. lengths[i] - n + j; one that sees
+ * none gives zeros. out [tokens, q_heads, dim] bf16, contiguous:
+ * softmax(scale q.k) v with fp32 scores, maxima and sums; q is used exactly,
+ * the softmax's weights with a relative error of at most 2^-9. scale > 0.
+ * max_length: an upper bound on lengths that the launch is planned for (0:
+ * width * page); a larger length is still right, only slower. workspace:
+ * mx_kv_attention_workspace_size(...) bytes, 16-byte aligned (partial results
+ * where a sequence is split over workgroups), 0 bytes (NULL allowed) where
+ * none is. */
+size_t mx_kv_attention_workspace_size(int64_t tokens, int batch, int q_heads, int heads, int dim,
+                                      int64_t max_length);
+mx_status_t mx_kv_attention(const void *q, int64_t q_stride, int q_heads,
+                            const mx_kv_cache_t *cache, const mx_kv_batch_t *batch,
+                            int64_t max_length, float scale, void *out, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
 /* Error reporting of this interface (no operation of the method, so no
  * passage defines it): the pages describe no error conventions; these two
  * calls only report the mx_status_t values above. */

@@ -14,6 +14,9 @@ Two layers:
     helpers that allocate outputs with torch and raise on a bad status
     (``ValueError`` for argument errors, as the Axolotl MXFP4 PR page does
     for a block size other than 32; ``RuntimeError`` for HIP errors).
+
+The operators of a transformer layer in MXFP8 (norm, products, KV cache and
+attention) are in ``layer`` and re-exported here, in the same two layers.
 """
 from __future__ import annotations
 
@@ -40,7 +43,10 @@ EXPORTS = ("mx_quantize", "mx_dequantize", "mx_fakequant", "mx_block_mse",
            "mx_fakequant_mxfp8", "mx_nvfp4_workspace_size", "mx_quantize_nvfp4",
            "mx_dequantize_nvfp4", "mx_quantize_mbs", "mx_dequantize_mbs", "mx_quantize_multi",
            "mx_fakequant_multi", "mx_fakequant_nvfp4", "mx_fakequant_mbs", "mx_quantize_fused",
-           "mx_block_mse_noalloc", "mx_status_string", "mx_last_error_detail")
+           "mx_block_mse_noalloc", "mx_quantize_mxfp8_blocks", "mx_rmsnorm_mxfp8",
+           "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace_size", "mx_matmul_mxfp8",
+           "mx_matmul_mxfp8_workspace_size", "mx_kv_append", "mx_kv_attention",
+           "mx_kv_attention_workspace_size", "mx_status_string", "mx_last_error_detail")
 
 _lib = None
 
@@ -87,6 +93,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mx_status_string.restype = ctypes.c_char_p
     lib.mx_last_error_detail.argtypes = []
     lib.mx_last_error_detail.restype = ctypes.c_char_p
+    declare(lib)
     _lib = lib
     return lib
 
@@ -578,3 +585,13 @@ def fakequant_multi(xs, mode: str = "ocp", out=None):
         with torch.cuda.device(dev):
             _raise(mx_fakequant_multi(arr, len(xs), _DTYPES[dt], _MODES[mode], _stream(dev)), True)
     return ys
+
+
+# ---- the transformer-layer operators ---------------------------------------------
+
+from .layer import (  # noqa: E402
+    KVCache, MxKVBatch, MxKVCache, declare, kv_append, kv_attention, kv_cache, matmul_mxfp8,
+    mx_kv_append, mx_kv_attention, mx_kv_attention_workspace_size, mx_matmul_mxfp8,
+    mx_matmul_mxfp8_workspace_size, mx_quantize_mxfp8_blocks, mx_rmsnorm_backward,
+    mx_rmsnorm_backward_workspace_size, mx_rmsnorm_mxfp8, quantize_mxfp8_both,
+    quantize_mxfp8_columns, quantize_mxfp8_rows, rmsnorm_backward, rmsnorm_mxfp8)

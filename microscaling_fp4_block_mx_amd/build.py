@@ -11,13 +11,16 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmx.so")
-SOURCES = ["mx_kernels.hip", "mx_api.cpp"]
+SOURCES = ["mx_kernels.hip", "mx_norm.hip", "mx_matmul.hip", "mx_kv.hip", "mx_api.cpp",
+           "mx_layer_api.cpp"]
 ARCH = "gfx950"
 
 
@@ -26,22 +29,31 @@ def hipcc() -> str:
     return os.path.join(rocm, "bin", "hipcc")
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIB + ".tmp"
-    cmd = [
-        hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
-        "-ffp-contract=off", "-fno-gpu-flush-denormals-to-zero",
-        "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-        "-Wall", "-Wno-unused-command-line-argument",
-        "-I", INCLUDE, "-I", CSRC,
-        "-o", tmp,
-    ] + [os.path.join(CSRC, s) for s in SOURCES]
+def _run(cmd, verbose: bool):
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("hipcc failed building libmx.so")
+
+
+def build(verbose: bool = False) -> str:
+    """Compile every source (side by side) and link them."""
+    tmp = LIB + ".tmp"
+    flags = [
+        f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
+        "-ffp-contract=off", "-fno-gpu-flush-denormals-to-zero",
+        "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+        "-Wall", "-Wno-unused-command-line-argument",
+        "-I", INCLUDE, "-I", CSRC,
+    ]
+    with tempfile.TemporaryDirectory() as d:
+        objects = [os.path.join(d, s + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(4) as pool:
+            list(pool.map(lambda so: _run([hipcc(), *flags, "-c", os.path.join(CSRC, so[0]),
+                                           "-o", so[1]], verbose), zip(SOURCES, objects)))
+        _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objects], verbose)
     os.replace(tmp, LIB)
     return LIB
 

@@ -45,14 +45,15 @@ bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
   return pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
 }
 
-mx_status_t finish(hipError_t e) {
-  if (e == hipSuccess) return MX_OK;
+mx_status_t finish(hipError_t e) { return e == hipSuccess ? MX_OK : mxi_record_hip_error(e); }
+
+}  // namespace
+
+mx_status_t mxi_record_hip_error(hipError_t e) {
   strncpy(g_detail, hipGetErrorString(e), sizeof g_detail - 1);
   g_detail[sizeof g_detail - 1] = 0;
   return MX_ERR_HIP;
 }
-
-}  // namespace
 
 extern "C" {
 

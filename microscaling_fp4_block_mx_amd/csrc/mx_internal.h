@@ -6,6 +6,10 @@
 
 #include "mx.h"
 
+// Records a HIP error's text as the calling thread's mx_last_error_detail();
+// returns MX_ERR_HIP.
+mx_status_t mxi_record_hip_error(hipError_t e);
+
 // nitems = rows * k / 8 (one item = 8 elements = 4 code bytes); callers have
 // validated shapes, alignment and aliasing.
 hipError_t mxi_launch_quantize(const void *x, int bf16, int mode, int64_t nitems,

@@ -1,0 +1,398 @@
+// mx_norm.hip - RMS norm with the residual's addition and MXFP8 output, its
+// gradient, and the MXFP8 quantizer with blocks of 32 or 128 along rows and
+// columns.
+//
+// Norm: h = x + r, y_j = w_j h_j / sqrt(sum h^2 / k + eps), then MXFP8 of y
+// in blocks of 32 or 128 along the row. The sum is fp32 and h enters it
+// unrounded; the copy of h that is written is rounded to the input's type.
+// One workgroup holds one row in registers, so x, r are read once and codes,
+// scales, h written once: bound by HBM.
+//
+// Gradient (with s = 1 / sqrt(sum h^2 / k + eps), g = w dy):
+//   dx_j = s (g_j - h_j s^2 sum(g h) / k) [+ through_j]
+//   dw_j = sum over rows of dy_j h_j s
+// Both row sums come from one pass over registers; each workgroup walks a
+// run of rows and keeps its share of dw in registers, written once as a row
+// of partial sums that a second launch adds in a fixed order (no atomics).
+#include "mx_layer.h"
+#include "mx_layer_device.h"
+
+namespace mxl {
+
+// Sum of one or two values over the workgroup; every thread gets the same
+// bits. `part` is this call's own LDS (two calls in flight alternate).
+template <int T>
+__device__ __forceinline__ f32x2 block_sum2(float a, float b, f32x2 *part) {
+  a = sum64(a);
+  b = sum64(b);
+  if constexpr (T == 64) return f32x2{a, b};
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = f32x2{a, b};
+  __syncthreads();
+  f32x2 t = part[0];
+#pragma unroll
+  for (int i = 1; i < T / 64; i++) {
+    t.x += part[i].x;
+    t.y += part[i].y;
+  }
+  return t;
+}
+
+template <bool BF16, int T, int N>
+__global__ __launch_bounds__(T) void k_rmsnorm(const void *x, const void *residual,
+                                               const void *__restrict__ weight, int k, float eps,
+                                               int wide, uint8_t *__restrict__ codes,
+                                               uint8_t *__restrict__ scales, void *h) {
+  __shared__ f32x2 part[T / 64];
+  const int64_t row = blockIdx.x;
+  const int items = k >> 3;
+  const int64_t base = row * items;
+  Raw<BF16> xr[N], rr[N], wr[N];
+#pragma unroll
+  for (int u = 0; u < N; u++) {
+    const int it = threadIdx.x + u * T;
+    if (it < items) {
+      xr[u] = load_raw<BF16>(x, base + it);
+      if (residual) rr[u] = load_raw<BF16>(residual, base + it);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < N; u++) {  // the weight stays in the caches: default policy
+    const int it = threadIdx.x + u * T;
+    if (it < items) {
+      const u32x4 *p = reinterpret_cast<const u32x4 *>(weight) + (BF16 ? 1 : 2) * it;
+      wr[u].v[0] = p[0];
+      if constexpr (!BF16) wr[u].v[1] = p[1];
+    }
+  }
+  float f[N][8], ss = 0.0f;
+#pragma unroll
+  for (int u = 0; u < N; u++) {
+    const int it = threadIdx.x + u * T;
+    if (it < items) {
+      widen<BF16>(xr[u], f[u]);
+      if (residual) {
+        float r[8];
+        widen<BF16>(rr[u], r);
+#pragma unroll
+        for (int j = 0; j < 8; j++) f[u][j] += r[j];
+        if (h) store8<BF16>(h, base + it, f[u]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; j++) ss = __builtin_fmaf(f[u][j], f[u][j], ss);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; j++) f[u][j] = 0.0f;
+    }
+  }
+  ss = block_sum2<T>(ss, 0.0f, part).x;
+  const float s = 1.0f / __builtin_sqrtf(ss / (float)k + eps);
+  const int lanes = wide ? 16 : 4;  // lanes that share a block (wave-uniform)
+  const int64_t nb = (items + lanes - 1) / lanes;
+#pragma unroll
+  for (int u = 0; u < N; u++) {
+    const int it = threadIdx.x + u * T;
+    float y[8];
+    if (it < items) {
+      float w[8];
+      widen<BF16>(wr[u], w);
+#pragma unroll
+      for (int j = 0; j < 8; j++) y[j] = f[u][j] * s * w[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; j++) y[j] = 0.0f;
+    }
+    // lanes past the row's end take part with zeros: they may sit in the
+    // last, short block
+    uint32_t m = amax8(y);
+    m = wide ? max16(m) : max4(m);
+    if (it < items) {
+      const uint32_t sb = scale_byte8(m);
+      reinterpret_cast<u32x2 *>(codes)[base + it] = encode8(y, sb);
+      if ((it & (lanes - 1)) == 0) scales[row * nb + it / lanes] = (uint8_t)sb;
+    }
+  }
+}
+
+template <bool BF16, int T, int N>
+__global__ __launch_bounds__(T) void k_rmsnorm_backward(
+    const void *dy, const void *h, const void *__restrict__ weight, const void *through,
+    int64_t rows, int k, float eps, void *dx, float *__restrict__ partial) {
+  __shared__ f32x2 part[2][T / 64];
+  const int items = k >> 3;
+  float w[N][8], dw[N][8];
+#pragma unroll
+  for (int u = 0; u < N; u++) {
+    const int it = threadIdx.x + u * T;
+#pragma unroll
+    for (int j = 0; j < 8; j++) w[u][j] = dw[u][j] = 0.0f;
+    if (it < items) widen<BF16>(load_raw<BF16>(weight, it), w[u]);
+  }
+  const float inv_k = 1.0f / (float)k;
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, flip ^= 1) {
+    const int64_t base = row * items;
+    Raw<BF16> dr[N], hr[N], tr[N];
+#pragma unroll
+    for (int u = 0; u < N; u++) {
+      const int it = threadIdx.x + u * T;
+      if (it < items) {
+        dr[u] = load_raw<BF16>(dy, base + it);
+        hr[u] = load_raw<BF16>(h, base + it);
+        if (through) tr[u] = load_raw<BF16>(through, base + it);
+      }
+    }
+    float ss = 0.0f, sg = 0.0f, hv[N][8], dv[N][8];
+#pragma unroll
+    for (int u = 0; u < N; u++) {
+      if (threadIdx.x + u * T < items) {
+        widen<BF16>(hr[u], hv[u]);
+        widen<BF16>(dr[u], dv[u]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) hv[u][j] = dv[u][j] = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        ss = __builtin_fmaf(hv[u][j], hv[u][j], ss);
+        sg = __builtin_fmaf(dv[u][j] * w[u][j], hv[u][j], sg);
+      }
+    }
+    // alternate halves of `part`: a wave may still be reading the last row's
+    const f32x2 t = block_sum2<T>(ss, sg, part[flip]);
+    const float s = 1.0f / __builtin_sqrtf(t.x * inv_k + eps);
+    const float c = t.y * inv_k * s * s;
+#pragma unroll
+    for (int u = 0; u < N; u++) {
+      const int it = threadIdx.x + u * T;
+      if (it < items) {
+        float o[8], th[8];
+        if (through) widen<BF16>(tr[u], th);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          const float g = dv[u][j] * w[u][j];
+          o[j] = s * __builtin_fmaf(-hv[u][j], c, g);
+          if (through) o[j] += th[j];
+          dw[u][j] = __builtin_fmaf(dv[u][j], hv[u][j] * s, dw[u][j]);
+        }
+        store8<BF16>(dx, base + it, o);
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < N; u++) {
+    const int it = threadIdx.x + u * T;
+    if (it < items) {
+      f32x4 *p = reinterpret_cast<f32x4 *>(partial + (int64_t)blockIdx.x * k) + 2 * it;
+      p[0] = f32x4{dw[u][0], dw[u][1], dw[u][2], dw[u][3]};
+      p[1] = f32x4{dw[u][4], dw[u][5], dw[u][6], dw[u][7]};
+    }
+  }
+}
+
+// dweight_j = sum over the n partial rows: 16 columns per workgroup, thread
+// (r, c) adds rows r, r + 16, ... of column c, then the 16 sums in order.
+__global__ __launch_bounds__(256) void k_sum_rows(const float *__restrict__ partial, int n, int k,
+                                                  float *__restrict__ out) {
+  __shared__ float part[16][17];
+  const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
+  const int col = blockIdx.x * 16 + c;  // k is a multiple of 32: every column exists
+  float a = 0.0f, b = 0.0f, d = 0.0f, e = 0.0f;
+  int i = r;
+  for (; i + 48 < n; i += 64) {
+    a += partial[(int64_t)i * k + col];
+    b += partial[(int64_t)(i + 16) * k + col];
+    d += partial[(int64_t)(i + 32) * k + col];
+    e += partial[(int64_t)(i + 48) * k + col];
+  }
+  for (; i < n; i += 16) a += partial[(int64_t)i * k + col];
+  part[r][c] = (a + b) + (d + e);
+  __syncthreads();
+  if (r == 0) {
+    float t = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 16; q++) t += part[q][c];
+    out[col] = t;
+  }
+}
+
+// ---- quantizer: blocks along rows and along columns from one read -----------------
+//
+// A workgroup takes a tile of 128 rows x 128 columns. Rows: thread t holds
+// item t % 16 (eight columns) of rows t / 16 + 16 u; a block of 128 is 16
+// lanes, one of 32 is four. Columns: the tile goes through LDS (bf16 pairs
+// or floats) and thread t takes rows 8 (t % 16) .. + 7 of columns, so that
+// again 16 or 4 lanes share a block. Rows past the end count as zeros; the
+// transposed codes of a ragged last 32 rows are written as zeros.
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_quantize8_blocks(
+    const void *__restrict__ x, int64_t rows, int64_t k, int wide, uint8_t *__restrict__ codes,
+    uint8_t *__restrict__ scales, uint8_t *__restrict__ codes_t, uint8_t *__restrict__ scales_t) {
+  // 65 (129) words per row: the transposed reads, 8 rows apart, spread over the banks
+  constexpr int P = BF16 ? 65 : 129;
+  __shared__ uint32_t tile[128 * P];
+  const int64_t r0 = (int64_t)blockIdx.x * 128, c0 = (int64_t)blockIdx.y * 128;
+  const int q = threadIdx.x & 15, r = threadIdx.x >> 4;
+  const int lanes = wide ? 16 : 4;
+  const int64_t col = c0 + 8 * q;
+  const bool in_k = col < k;  // k is a multiple of 32: items are whole
+  const int64_t nb = (k + 8 * lanes - 1) / (8 * lanes);
+  Raw<BF16> raw[8];
+#pragma unroll
+  for (int u = 0; u < 8; u++) {
+    const int64_t row = r0 + r + 16 * u;
+    if (in_k && row < rows) {
+      raw[u] = load_raw<BF16>(x, (row * k + col) >> 3);
+    } else {
+      raw[u].v[0] = u32x4{0, 0, 0, 0};
+      if constexpr (!BF16) raw[u].v[1] = u32x4{0, 0, 0, 0};
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 8; u++) {
+    const int64_t row = r0 + r + 16 * u;
+    if (codes_t) {
+      uint32_t *d = tile + (r + 16 * u) * P + (BF16 ? 4 : 8) * q;
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        d[j] = raw[u].v[0][j];
+        if constexpr (!BF16) d[4 + j] = raw[u].v[1][j];
+      }
+    }
+    if (codes) {
+      float f[8];
+      widen<BF16>(raw[u], f);
+      uint32_t m = amax8(f);
+      m = wide ? max16(m) : max4(m);
+      if (in_k && row < rows) {
+        const uint32_t sb = scale_byte8(m);
+        *reinterpret_cast<u32x2 *>(codes + row * k + col) = encode8(f, sb);
+        if ((q & (lanes - 1)) == 0) scales[row * nb + col / (8 * lanes)] = (uint8_t)sb;
+      }
+    }
+  }
+  if (!codes_t) return;
+  __syncthreads();
+  const int64_t rows_p = (rows + 31) & ~(int64_t)31;
+  const int64_t row = r0 + 8 * q;
+  const int64_t nbt = (rows + 8 * lanes - 1) / (8 * lanes);
+#pragma unroll
+  for (int u = 0; u < (BF16 ? 4 : 8); u++) {
+    // columns c (and c + 1 of the same word for bf16)
+    const int c = BF16 ? 2 * (r + 16 * u) : r + 16 * u;
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) w[j] = tile[(8 * q + j) * P + (BF16 ? c >> 1 : c)];
+#pragma unroll
+    for (int e = 0; e < (BF16 ? 2 : 1); e++) {
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; j++)
+        f[j] = __uint_as_float(!BF16 ? w[j] : e ? (w[j] & 0xFFFF0000u) : (w[j] << 16));
+      uint32_t m = amax8(f);
+      m = wide ? max16(m) : max4(m);
+      const int64_t cc = c0 + c + e;
+      if (cc < k && row < rows_p) {
+        const uint32_t sb = scale_byte8(m);
+        *reinterpret_cast<u32x2 *>(codes_t + cc * rows_p + row) = encode8(f, sb);
+        if ((q & (lanes - 1)) == 0) scales_t[cc * nbt + row / (8 * lanes)] = (uint8_t)sb;
+      }
+    }
+  }
+}
+
+// Threads and items per thread that hold a row of `items` items. Few rows:
+// as many threads as there are items (latency); many rows: up to `per` items
+// for a thread.
+struct Shape {
+  int t, n;
+};
+static Shape row_shape(int64_t items, int per) {
+  for (int t = 64; t <= 1024; t *= 2)
+    if (items <= (int64_t)t * per) {
+      int n = 1;
+      while ((int64_t)t * n < items) n *= 2;
+      return {t, n};
+    }
+  int n = per;
+  while ((int64_t)1024 * n < items) n *= 2;
+  return {1024, n};
+}
+
+template <bool BF16, typename F>
+static hipError_t with_shape(Shape s, F f) {
+#define MXL_N(T)                                                   \
+  switch (s.n) {                                                   \
+    case 1: return f(std::integral_constant<int, T>(), std::integral_constant<int, 1>()); \
+    case 2: return f(std::integral_constant<int, T>(), std::integral_constant<int, 2>()); \
+    case 4: return f(std::integral_constant<int, T>(), std::integral_constant<int, 4>()); \
+    default: return f(std::integral_constant<int, T>(), std::integral_constant<int, 8>()); \
+  }
+  switch (s.t) {
+    case 64: MXL_N(64)
+    case 128: MXL_N(128)
+    case 256: MXL_N(256)
+    case 512: MXL_N(512)
+    default: MXL_N(1024)
+  }
+#undef MXL_N
+}
+
+}  // namespace mxl
+
+using namespace mxl;
+
+hipError_t mxi_launch_rmsnorm(const void *x, const void *residual, const void *weight, int bf16,
+                              int64_t rows, int64_t k, float eps, int block, uint8_t *codes,
+                              uint8_t *scales, void *h, hipStream_t st) {
+  const Shape s = row_shape(k / 8, rows < 512 ? 1 : 4);
+  auto go = [&](auto bf) {
+    return with_shape<decltype(bf)::value>(s, [&](auto t, auto n) {
+      k_rmsnorm<decltype(bf)::value, decltype(t)::value, decltype(n)::value>
+          <<<dim3((uint32_t)rows), dim3(decltype(t)::value), 0, st>>>(
+              x, residual, weight, (int)k, eps, block == 128, codes, scales, h);
+      return hipGetLastError();
+    });
+  };
+  return bf16 ? go(std::true_type()) : go(std::false_type());
+}
+
+int64_t mxi_rmsnorm_partials(int64_t rows, int64_t k) {
+  const Shape s = row_shape(k / 8, 2);
+  const int64_t most = (int64_t)256 * (1024 / s.t);  // workgroups resident at once
+  return rows < most ? rows : most;
+}
+
+hipError_t mxi_launch_rmsnorm_backward(const void *dy, const void *h, const void *weight,
+                                       const void *through, int bf16, int64_t rows, int64_t k,
+                                       float eps, void *dx, float *dweight, float *partial,
+                                       hipStream_t st) {
+  const Shape s = row_shape(k / 8, 2);
+  const int64_t grid = mxi_rmsnorm_partials(rows, k);
+  auto go = [&](auto bf) {
+    return with_shape<decltype(bf)::value>(s, [&](auto t, auto n) {
+      k_rmsnorm_backward<decltype(bf)::value, decltype(t)::value, decltype(n)::value>
+          <<<dim3((uint32_t)grid), dim3(decltype(t)::value), 0, st>>>(
+              dy, h, weight, through, rows, (int)k, eps, dx, partial);
+      return hipGetLastError();
+    });
+  };
+  if (grid > 0) {
+    const hipError_t e = bf16 ? go(std::true_type()) : go(std::false_type());
+    if (e != hipSuccess) return e;
+  }
+  k_sum_rows<<<dim3((uint32_t)(k / 16)), dim3(256), 0, st>>>(partial, (int)grid, (int)k, dweight);
+  return hipGetLastError();
+}
+
+hipError_t mxi_launch_quantize8_blocks(const void *x, int bf16, int64_t rows, int64_t k, int block,
+                                       uint8_t *codes, uint8_t *scales, uint8_t *codes_t,
+                                       uint8_t *scales_t, hipStream_t st) {
+  const dim3 grid((uint32_t)((rows + 127) / 128), (uint32_t)((k + 127) / 128));
+  if (bf16)
+    k_quantize8_blocks<true><<<grid, 256, 0, st>>>(x, rows, k, block == 128, codes, scales, codes_t,
+                                                   scales_t);
+  else
+    k_quantize8_blocks<false><<<grid, 256, 0, st>>>(x, rows, k, block == 128, codes, scales,
+                                                    codes_t, scales_t);
+  return hipGetLastError();
+}
