@@ -3,21 +3,21 @@
 // A [M, K] and B [N, K] are E4M3 codes, row-major, with one E8M0 byte per 32
 // or 128 elements of a row. K is a multiple of 32; M and N are any.
 //
-// bf16 output runs v_mfma_scale_f32_16x16x128_f8f6f4, which multiplies codes
-// and applies the E8M0 bytes itself. Lane layout (checked on the card): lane
-// l holds row l % 16; with g = l / 16 its first 16 bytes are k = 16 g ..
-// 16 g + 15 and its second 16 bytes are k = 64 + 16 g ..; the scale byte that
-// lane l supplies belongs to row l % 16 and elements k = 32 g .. 32 g + 31.
-// Inside each group of eight products the matrix core drops bits more than
+// bf16 output runs the scaled 8-bit matrix products, which multiply codes and
+// apply the E8M0 bytes themselves. Lane layouts (checked on the card): in
+// v_mfma_scale_f32_16x16x128_f8f6f4 lane l holds row l % 16; with g = l / 16
+// its first 16 bytes are k = 16 g .. 16 g + 15 and its second 16 bytes are
+// k = 64 + 16 g ..; the scale byte that lane l supplies belongs to row l % 16
+// and elements k = 32 g .. 32 g + 31. In v_mfma_scale_f32_32x32x64_f8f6f4 the
+// row is l % 32, with g = l / 32 the bytes are k = 16 g .. and 32 + 16 g ..,
+// and the lane's scale byte covers k = 32 g .. 32 g + 31. Inside each group of eight products the matrix core drops bits more than
 // about 2^-14 below the largest product (1.4e-5 of the result's norm on
 // normal data), which is far inside bf16's rounding (1.7e-3) but not inside
 // fp32's. fp32 output therefore widens the codes to bf16, scales applied
-// (both exact), and runs v_mfma_f32_16x16x32_bf16 at half the rate.
+// (both exact), and runs the bf16 products at half the rate.
 //
 // The weight-side operand B is the matrix core's "A" operand, so that a
-// lane's accumulators are consecutive columns n of one row m of C: column
-// n = 4 NT (r / 4) + 4 t + r % 4 of a wave's 16 NT columns is row r of its
-// tile t, which makes the 4 NT accumulators of a lane one contiguous run.
+// lane's accumulators are columns n of one row m of C.
 #include <algorithm>
 
 #include "mx_layer.h"
@@ -63,81 +63,156 @@ __device__ __forceinline__ f32x4 mfma16(const Wide &a, const Wide &b, f32x4 d) {
   return d;
 }
 
-// L consecutive columns of a row of C from column n on; vec: 16-byte stores
-// are aligned and whole.
-template <int L>
-__device__ __forceinline__ void store_run(void *c, int out_bf16, int64_t at, const float (&v)[L],
-                                          int64_t left, bool vec) {
-  if (out_bf16) {
-    uint16_t *p = reinterpret_cast<uint16_t *>(c) + at;
-    if (vec && left >= L && L % 8 == 0) {
-#pragma unroll
-      for (int j = 0; j + 8 <= L; j += 8)
-        *reinterpret_cast<u32x4 *>(p + j) =
-            u32x4{pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]),
-                  pack_bf16(v[j + 4], v[j + 5]), pack_bf16(v[j + 6], v[j + 7])};
-    } else {
-#pragma unroll
-      for (int j = 0; j < L; j++)
-        if (j < left) p[j] = (uint16_t)pack_bf16(v[j], 0.0f);
-    }
-  } else {
-    float *p = reinterpret_cast<float *>(c) + at;
-    if (vec && left >= L) {
-#pragma unroll
-      for (int j = 0; j < L; j += 4)
-        *reinterpret_cast<f32x4 *>(p + j) = f32x4{v[j], v[j + 1], v[j + 2], v[j + 3]};
-    } else {
-#pragma unroll
-      for (int j = 0; j < L; j++)
-        if (j < left) p[j] = v[j];
-    }
-  }
-}
-
 struct MatArgs {
   const uint8_t *a, *sa, *b, *sb;
   int64_t m, n, k;
   int64_t nb;      // scale bytes per row
   int out_bf16;
   int tm, tn;      // tiles along m and n
-  int steps;       // K steps of 128 of one split (a multiple of 4 unless one split)
+  int steps;       // slabs of 128 of one split (a multiple of 4 unless one split)
   void *c;         // output, or partial sums [split][m][n] fp32
   int partial;
 };
 
 // ---- tiled kernel -----------------------------------------------------------------
 //
-// A workgroup of (BM / TM) (BN / TN) waves owns a BM x BN tile; K runs in
-// steps of 128. Codes go from global memory straight into LDS (16 bytes a
-// lane), double-buffered, one barrier per step: a step first reads its
-// operands from LDS into registers, then starts the next step's loads into
-// the other buffer, then multiplies. Rows are 128 bytes; 16-byte chunk c of
-// row r sits at position c ^ f(r), f chosen so that the 16 rows one read
-// instruction touches spread over all banks. The chunks are swapped on the
-// global side (a lane picks which chunk it loads), since a direct load
-// writes LDS linearly. Scale bytes of four steps are packed into one word
-// per row (and per 32-element block: four words) in LDS; the matrix core
-// picks the step's byte.
+// A workgroup of (BM / TM) (BN / TN) waves owns a BM x BN tile. K runs in
+// slabs of 128, one v_mfma_scale_f32_16x16x128_f8f6f4 deep, which go from
+// global memory straight into LDS (16 bytes a lane, a row's 128 bytes one
+// request), double-buffered. A wave multiplies A's tiles one after the other
+// with all of its B tiles, which it holds; it reads A two tiles ahead and, in
+// the slab's last two tiles, the next slab's B and first A, so LDS is not
+// waited for. The one barrier of a slab stands before those: the next slab
+// has landed, and this one has been read, so that the loads of the slab
+// after next may start. A wave issues in order and a load waits at issue
+// while the memory unit is taken, so loads are dealt out between products.
+//
+// The 16-byte chunk c of row r sits at position c ^ f(r), f chosen so that
+// the 16 rows that a quarter of a read instruction touches fall on different
+// banks. The chunks are swapped on the global side (a lane picks which chunk
+// it loads), since a direct load writes LDS linearly. Scale bytes of four
+// slabs are one word per row (and, with blocks of 32, per block of a slab)
+// in LDS; the matrix core picks the slab's byte.
 
-// Swizzle of A rows (16 consecutive rows per read) and B rows (see the column
-// order above: rows 4 NT apart in fours).
-__device__ __forceinline__ int swz_a(int r) { return (r >> 1) & 7; }
-template <int NT>
-__device__ __forceinline__ int swz_b(int r) {
-  return ((r >> 1) & 1) | (((r / (4 * NT)) & 3) << 1);
-}
+__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
 
 constexpr uint32_t kOut = 0x80000000u;  // an offset past every buffer: loads give 0
 
+// 16 bytes a lane from the buffer straight into LDS, lane after lane from
+// `lds` on (wave-uniform). In assembly, since the compiler would otherwise
+// make every later LDS read wait for it; the kernel waits where it must.
+// It has no output register, and its memory clobber keeps the order.
+__device__ __forceinline__ void load_lds16(i32x4 buffer, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               ::"s"(lds), "v"(offset), "s"(buffer) : "memory");
+}
+__device__ __forceinline__ i32x4 buffer_of(const void *base, uint32_t bytes) {
+  const uint64_t p = (uint64_t)base;
+  return i32x4{__builtin_amdgcn_readfirstlane((int)p), __builtin_amdgcn_readfirstlane((int)(p >> 32) & 0xFFFF),
+               __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
+
+template <int BM, int BN, int TM, int TN, bool BLK32, bool EXACT>
+struct Tiled {
+  static constexpr int WAVES = (BM / TM) * (BN / TN), T = WAVES * 64;
+  static constexpr int MT = TM / 16, NT = TN / 16;
+  static constexpr int ROWS = BM + BN, G = BLK32 ? 4 : 1;
+  static constexpr int PER = T / 8;           // rows one load of the workgroup covers
+  static constexpr int LOADS = ROWS / PER;    // direct loads per thread and slab
+  static constexpr int SROWS = (ROWS + T - 1) / T;  // rows of scales per thread
+  static_assert(MT % 4 == 0 && ROWS % PER == 0 && BM % PER == 0 && PER % 16 == 0, "tile and threads");
+
+  // LDS: A's two slabs, then B's, so that one address per chunk and constant
+  // offsets reach everything a lane reads
+  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
+
+  struct Loader {
+    i32x4 ar, br;     // buffers of the tile's rows of A and B
+    uint32_t o;       // offset of this thread's first chunk in either
+    int kc, k;        // first element of the chunk
+    uint32_t lds;     // where this wave's first chunk goes in slab 0
+  };
+  // Load i of slab `slab`'s codes into buffer `buf`. Offsets are checked
+  // against the end of the tile's rows by the buffer, past a row's end the
+  // offset is moved out: both give zeros.
+  static __device__ __forceinline__ void load(const Loader &l, int slab, int buf, int i) {
+    constexpr int AL = BM / PER;
+    const int k0 = slab * 128;
+    const uint32_t o = k0 + l.kc < l.k ? l.o + k0 : kOut;
+    if (i < AL)
+      load_lds16(l.ar, o + (uint32_t)(i * PER) * l.k, l.lds + buf * A_BYTES + i * T * 16);
+    else
+      load_lds16(l.br, o + (uint32_t)((i - AL) * PER) * l.k,
+                 l.lds + 2 * A_BYTES + buf * B_BYTES + (i - AL) * T * 16);
+  }
+
+  struct Places {
+    const uint8_t *a0, *a1, *b0, *b1;  // this lane's two chunks of tile 0 of A and B
+  };
+  static __device__ __forceinline__ i32x8 read_a(const Places &p, int buf, int i) {
+    return join(*reinterpret_cast<const u32x4 *>(p.a0 + buf * A_BYTES + 2048 * i),
+                *reinterpret_cast<const u32x4 *>(p.a1 + buf * A_BYTES + 2048 * i));
+  }
+  static __device__ __forceinline__ i32x8 read_b(const Places &p, int buf, int j) {
+    return join(*reinterpret_cast<const u32x4 *>(p.b0 + buf * B_BYTES + 2048 * j),
+                *reinterpret_cast<const u32x4 *>(p.b1 + buf * B_BYTES + 2048 * j));
+  }
+};
+
+// A wave's MT x NT accumulator tiles to C, 16 rows at a time through `turn`
+// (wave-private LDS). Row r's 16-byte chunks are moved by r so that the
+// writes of one instruction, which share a chunk number, spread over banks.
+template <int MT, int NT, bool OUT16>
+__device__ __forceinline__ void store_tile(const f32x4 (&acc)[MT][NT], uint8_t *turn, void *c,
+                                           int64_t m, int64_t n, int64_t m0, int64_t n0, int lane) {
+  constexpr int E = OUT16 ? 2 : 4, ROW = 16 * NT * E, CH = ROW / 16, V = 16 / E;
+  const int l16 = lane & 15, lg = lane >> 4;
+  const bool whole = n % V == 0;
+#pragma unroll
+  for (int i = 0; i < MT; i++) {
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+      const int col = 16 * j + 4 * lg;  // four columns of row l16
+      uint8_t *p = turn + l16 * ROW + ((col / V + l16) & (CH - 1)) * 16 + col % V * E;
+      const f32x4 v = acc[i][j];
+      if constexpr (OUT16) *reinterpret_cast<u32x2 *>(p) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+      else *reinterpret_cast<f32x4 *>(p) = v;
+    }
+    // one wave: its LDS operations run in order; the fences keep the compiler's
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    if (whole) {
+#pragma unroll
+      for (int u = 0; u < (16 * CH + 63) / 64; u++) {
+        const int at = u * 64 + lane, row = at / CH, ch = at % CH;
+        const int64_t mm = m0 + 16 * i + row, nn = n0 + ch * V;
+        if (row < 16 && mm < m && nn < n)
+          *reinterpret_cast<u32x4 *>(reinterpret_cast<uint8_t *>(c) + (mm * n + nn) * E) =
+              *reinterpret_cast<const u32x4 *>(turn + row * ROW + ((ch + row) & (CH - 1)) * 16);
+      }
+    } else {
+      for (int at = lane; at < 16 * 16 * NT; at += 64) {
+        const int row = at / (16 * NT), col = at % (16 * NT);
+        const uint8_t *p = turn + row * ROW + ((col / V + row) & (CH - 1)) * 16 + col % V * E;
+        const int64_t mm = m0 + 16 * i + row, nn = n0 + col;
+        if (mm < m && nn < n) {
+          if constexpr (OUT16) reinterpret_cast<uint16_t *>(c)[mm * n + nn] = *reinterpret_cast<const uint16_t *>(p);
+          else reinterpret_cast<float *>(c)[mm * n + nn] = *reinterpret_cast<const float *>(p);
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+}
+
 template <int BM, int BN, int TM, int TN, bool BLK32, bool EXACT>
 __global__ __launch_bounds__((BM / TM) * (BN / TN) * 64) void k_matmul8(const MatArgs g) {
-  constexpr int WAVES = (BM / TM) * (BN / TN), T = WAVES * 64;
-  constexpr int MT = TM / 16, NT = TN / 16;
-  constexpr int ROWS = BM + BN, G = BLK32 ? 4 : 1;
-  constexpr int LOADS = ROWS * 8 / T;  // direct loads per thread and step
-  static_assert(ROWS <= T && ROWS * 8 % T == 0 && BM * 8 % T == 0, "tile and threads");
-  __shared__ __attribute__((aligned(16))) uint8_t codes[2][ROWS * 128];
+  using K = Tiled<BM, BN, TM, TN, BLK32, EXACT>;
+  constexpr int MT = K::MT, NT = K::NT, ROWS = K::ROWS, G = K::G;
+  __shared__ __attribute__((aligned(16))) uint8_t slabs[2 * ROWS * 128];
   __shared__ uint32_t scl[2][G][ROWS];
 
   // XCD-aware order: workgroups are dealt round robin to the 8 XCDs; each
@@ -151,177 +226,216 @@ __global__ __launch_bounds__((BM / TM) * (BN / TN) * 64) void k_matmul8(const Ma
   const int64_t m0 = (int64_t)(8 * s0 + in % high) * BM, n0 = (int64_t)(in / high) * BN;
 
   const int first = blockIdx.y * g.steps;
-  const int all = (int)((g.k + 127) >> 7);
-  const int nk = min(g.steps, all - first);
+  const int nk = min(g.steps, (int)((g.k + 127) >> 7) - first);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
 
-  // direct loads: load i covers LDS rows (i T + tid) / 8, chunk position tid % 8
-  const uint8_t *abase = g.a + m0 * g.k, *bbase = g.b + n0 * g.k;
-  const uint32_t abytes = (uint32_t)(min((int64_t)BM, g.m - m0) * g.k);
-  const uint32_t bbytes = (uint32_t)(min((int64_t)BN, g.n - n0) * g.k);
-  const __amdgpu_buffer_rsrc_t ar =
-      __builtin_amdgcn_make_buffer_rsrc((void *)abase, 0, abytes, 0x00020000);
-  const __amdgpu_buffer_rsrc_t br =
-      __builtin_amdgcn_make_buffer_rsrc((void *)bbase, 0, bbytes, 0x00020000);
-  uint32_t off[LOADS];
-  int kc[LOADS];
-#pragma unroll
-  for (int i = 0; i < LOADS; i++) {
-    const int r = (i * T + (int)threadIdx.x) >> 3, p = threadIdx.x & 7;
-    const bool is_a = i * T / 8 < BM;
-    const int rr = is_a ? r : r - BM;
-    kc[i] = (p ^ (is_a ? swz_a(rr) : swz_b<NT>(rr))) * 16;
-    off[i] = (uint32_t)rr * (uint32_t)g.k + kc[i];
+  // direct loads: load i covers rows i PER + tid / 8, chunk position tid % 8;
+  // the swizzle repeats every 16 rows
+  typename K::Loader ld;
+  ld.k = (int)g.k;
+  ld.lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)slabs + wave * 1024;
+  {
+    const int r = threadIdx.x >> 3;
+    ld.kc = ((threadIdx.x & 7) ^ swz(r)) * 16;
+    ld.o = (uint32_t)r * ld.k + ld.kc;
+    ld.ar = buffer_of(g.a + m0 * g.k, (uint32_t)(min((int64_t)BM, g.m - m0) * g.k));
+    ld.br = buffer_of(g.b + n0 * g.k, (uint32_t)(min((int64_t)BN, g.n - n0) * g.k));
   }
-  const int k32 = (int)g.k;
-  auto load = [&](int step, int buf) {
-    const int kb = (first + step) * 128;
-#pragma unroll
-    for (int i = 0; i < LOADS; i++) {
-      // past the row's end: zeros (past the last row the buffer's end does it)
-      const uint32_t o = kb + kc[i] < k32 ? off[i] + kb : kOut;
-      auto *dst = (__attribute__((address_space(3))) void *)(codes[buf] + (i * T + wave * 64) * 16);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(i * T / 8 < BM ? ar : br, dst, 16, o, 0, 0, 0);
-    }
-  };
 
   // scales: thread r holds row r of the tile (A rows, then B rows), clamped
-  // to the matrix; bytes past a row's end repeat its last one
-  const int srow = min((int)threadIdx.x, ROWS - 1);
-  const uint8_t *sp = srow < BM ? g.sa + min(m0 + srow, g.m - 1) * g.nb
-                                : g.sb + min(n0 + srow - BM, g.n - 1) * g.nb;
-  uint32_t sw[G];
+  // to the matrix. Four slabs take 16 bytes of a row with blocks of 32 and 4
+  // with blocks of 128; where they would pass the row's end, the row's last
+  // ones are read and shifted down (the elements past the end are zeros). A
+  // row with fewer has one chunk only; the loads for chunks that do not
+  // exist read something valid and are not used.
+  constexpr int SB = 4 * G, SR = K::SROWS, T = K::T;
+  const bool brief = g.nb < SB;
+  const int slast = brief ? 0 : (int)g.nb - SB;
+  const uint8_t *sp[SR];  // wave-uniform: a wave's rows are all A's or all B's
+  uint32_t so[SR], raw[SR][G];
+#pragma unroll
+  for (int q = 0; q < SR; q++) {
+    const int row = min((int)threadIdx.x + q * T, ROWS - 1);
+    const bool is_a = min(wave * 64 + q * T, ROWS - 1) < BM;
+    static_assert(BM % 64 == 0, "a wave's rows");
+    sp[q] = brief ? g.a : is_a ? g.sa + m0 * g.nb : g.sb + n0 * g.nb;  // codes: at least 32 bytes
+    so[q] = brief ? 0 : (uint32_t)((is_a ? min((int64_t)row, g.m - 1 - m0)
+                                         : min((int64_t)row - BM, g.n - 1 - n0)) * g.nb);
+  }
   auto load_scales = [&](int chunk) {
-    const int64_t at = ((int64_t)first + 4 * chunk) * G;
-    uint8_t b[4 * G];
-    if (at + 4 * G <= g.nb) {
-      __builtin_memcpy(b, sp + at, 4 * G);
-    } else {
+    const int at = (first + 4 * chunk) * G, from = min(at, slast), by = at - from;
 #pragma unroll
-      for (int j = 0; j < 4 * G; j++) b[j] = sp[min(at + j, g.nb - 1)];
+    for (int q = 0; q < SR; q++) {
+      if constexpr (BLK32) {
+        __builtin_memcpy(raw[q], sp[q] + from + so[q], 16);
+        if (by) {  // wave-uniform, only near the row's end; by < 16 where the slab exists
+          unsigned __int128 w;
+          __builtin_memcpy(&w, raw[q], 16);
+          w >>= 8 * min(by, 15);
+          __builtin_memcpy(raw[q], &w, 16);
+        }
+      } else {
+        uint32_t w;
+        __builtin_memcpy(&w, sp[q] + from + so[q], 4);
+        raw[q][0] = w >> (8 * min(by, 3));
+      }
     }
-#pragma unroll
-    for (int q = 0; q < G; q++)
-      sw[q] = (uint32_t)b[q] | (uint32_t)b[G + q] << 8 | (uint32_t)b[2 * G + q] << 16 |
-              (uint32_t)b[3 * G + q] << 24;
   };
   auto put_scales = [&](int buf) {
-    if ((int)threadIdx.x < ROWS) {
 #pragma unroll
-      for (int q = 0; q < G; q++) scl[buf][q][threadIdx.x] = sw[q];
+    for (int q = 0; q < SR; q++) {
+      const int row = threadIdx.x + q * T;
+      if (ROWS % T == 0 || row < ROWS) {
+        if constexpr (BLK32) {  // word s holds slab s's four blocks: turn the 4 x 4 bytes
+          const uint32_t *w = raw[q];
+          const uint32_t p0 = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u),
+                         p1 = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u),
+                         q0 = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u),
+                         q1 = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+          scl[buf][0][row] = __builtin_amdgcn_perm(p1, p0, 0x05040100u);
+          scl[buf][1][row] = __builtin_amdgcn_perm(p1, p0, 0x07060302u);
+          scl[buf][2][row] = __builtin_amdgcn_perm(q1, q0, 0x05040100u);
+          scl[buf][3][row] = __builtin_amdgcn_perm(q1, q0, 0x07060302u);
+        } else {
+          scl[buf][0][row] = raw[q][0];
+        }
+      }
     }
   };
 
   const int wm = wave % (BM / TM) * TM, wn = wave / (BM / TM) * TN;
+  // this lane's operand rows: A row wm + 16 i + l16, B row wn + 16 j + l16;
+  // the swizzle does not depend on i and j
+  const int ra = wm + l16, rb = wn + l16;
+  const int lo = (lg ^ swz(l16)) * 16, hi = lo ^ 64;
+  const uint8_t *pa = slabs + ra * 128, *pb = slabs + 2 * K::A_BYTES + rb * 128;
+  const typename K::Places pl = {pa + lo, pa + hi, pb + lo, pb + hi};
   f32x4 acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; i++)
 #pragma unroll
     for (int j = 0; j < NT; j++) acc[i][j] = f32x4{0, 0, 0, 0};
 
-  load(0, 0);
-  load_scales(0);
+  if (brief) {
+#pragma unroll
+    for (int q = 0; q < SR; q++) {
+#pragma unroll
+      for (int e = 0; e < G; e++) raw[q][e] = 0;
+      const int row = min((int)threadIdx.x + q * T, ROWS - 1);
+      const uint8_t *p = row < BM ? g.sa + min(m0 + row, g.m - 1) * g.nb
+                                  : g.sb + min(n0 + row - BM, g.n - 1) * g.nb;
+      for (int j = 0; j < (int)g.nb; j++) {
+        const uint32_t b = (uint32_t)p[j] << (8 * (j & 3));
+#pragma unroll
+        for (int e = 0; e < G; e++)
+          if (j >> 2 == e) raw[q][e] |= b;
+      }
+    }
+  } else {
+    load_scales(0);
+  }
   put_scales(0);
+
+  // Loads of a slab: the first START of them in the last two tiles of the
+  // slab before the last, the others in the first two of the next.
+  constexpr int LOADS = K::LOADS, START = MT >= 8 ? LOADS / 2 : LOADS;
+#pragma unroll
+  for (int i = 0; i < LOADS; i++) K::load(ld, first, 0, i);
+#pragma unroll
+  for (int i = 0; i < START; i++) K::load(ld, first + 1, 1, i);
+  // the first slab has landed (the second may be in flight)
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(START) : "memory");
   uint32_t as[MT][2], bs[NT][2];
-  auto step = [&](int s, auto jt) {
-    constexpr int J = decltype(jt)::value;
-    const int buf = s & 1;
-    // this step's loads have landed, and every wave is done with the other buffer
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    if constexpr (J == 0) {
-      const int sb = (s >> 2) & 1;
-#pragma unroll
-      for (int i = 0; i < MT; i++) {
-        const int r = wm + 16 * i + l16;
-        if constexpr (EXACT && BLK32) {
-          as[i][0] = scl[sb][lg >> 1][r];
-          as[i][1] = scl[sb][2 + (lg >> 1)][r];
-        } else {
-          as[i][0] = scl[sb][BLK32 ? lg : 0][r];
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < NT; j++) {
-        const int r = BM + wn + 4 * NT * (l16 >> 2) + 4 * j + (l16 & 3);
-        if constexpr (EXACT && BLK32) {
-          bs[j][0] = scl[sb][lg >> 1][r];
-          bs[j][1] = scl[sb][2 + (lg >> 1)][r];
-        } else {
-          bs[j][0] = scl[sb][BLK32 ? lg : 0][r];
-        }
-      }
-    }
-    i32x8 av[MT], bv[NT];
-#pragma unroll
-    for (int j = 0; j < NT; j++) {
-      const int r = wn + 4 * NT * (l16 >> 2) + 4 * j + (l16 & 3);
-      const uint8_t *p = codes[buf] + (BM + r) * 128;
-      const int x = swz_b<NT>(r);
-      bv[j] = join(*reinterpret_cast<const u32x4 *>(p + (lg ^ x) * 16),
-                   *reinterpret_cast<const u32x4 *>(p + ((lg + 4) ^ x) * 16));
-    }
+  auto get_scales = [&](int buf) {
+    // exact: the lane's halves lie in blocks lg / 2 and 2 + lg / 2 of a slab
+    const int g0 = !BLK32 ? 0 : EXACT ? lg >> 1 : lg, g1 = EXACT && BLK32 ? 2 + (lg >> 1) : g0;
 #pragma unroll
     for (int i = 0; i < MT; i++) {
-      const int r = wm + 16 * i + l16;
-      const uint8_t *p = codes[buf] + r * 128;
-      const int x = swz_a(r);
-      av[i] = join(*reinterpret_cast<const u32x4 *>(p + (lg ^ x) * 16),
-                   *reinterpret_cast<const u32x4 *>(p + ((lg + 4) ^ x) * 16));
+      as[i][0] = scl[buf][g0][ra + 16 * i];
+      as[i][1] = EXACT && BLK32 ? scl[buf][g1][ra + 16 * i] : as[i][0];
     }
-    if (s + 1 < nk) load(s + 1, buf ^ 1);
-    if constexpr (J == 0) {
-      if (s + 4 < nk) load_scales((s >> 2) + 1);
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+      bs[j][0] = scl[buf][g0][BM + rb + 16 * j];
+      bs[j][1] = EXACT && BLK32 ? scl[buf][g1][BM + rb + 16 * j] : bs[j][0];
     }
+  };
+  i32x8 a[4], b[NT];
+  get_scales(0);
+#pragma unroll
+  for (int j = 0; j < NT; j++) b[j] = K::read_b(pl, 0, j);
+  a[0] = K::read_a(pl, 0, 0);
+  a[1] = K::read_a(pl, 0, 1);
+
+  auto step = [&](int s, auto jt) {
+    constexpr int J = decltype(jt)::value, CUR = J & 1;
+    Wide bw[EXACT ? NT : 1];
     if constexpr (EXACT) {
-      Wide bw[NT];
 #pragma unroll
       for (int j = 0; j < NT; j++)
-        bw[j] = widen32(bv[j], bs[j][0] >> (8 * J) & 255, bs[j][BLK32 ? 1 : 0] >> (8 * J) & 255);
+        bw[j] = widen32(b[j], bs[j][0] >> (8 * J) & 255, bs[j][1] >> (8 * J) & 255);
+    }
+    if constexpr (J == 0) load_scales((s >> 2) + 1);
 #pragma unroll
-      for (int i = 0; i < MT; i++) {
-        const Wide aw =
-            widen32(av[i], as[i][0] >> (8 * J) & 255, as[i][BLK32 ? 1 : 0] >> (8 * J) & 255);
+    for (int i = 0; i < MT; i++) {
+      if (i == MT - 2) {
+        // the next slab (this wave's loads of it) has landed and this one
+        // has been read; past the barrier that holds for every wave
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        // the next chunk's scales: read two slabs on
+        if constexpr (J == 1) put_scales(((s >> 2) + 1) & 1);
+      }
+      // a slab's loads in up to four parts of at most HALF
+      constexpr int HALF = (START + 1) / 2;
+#pragma unroll
+      for (int q = 0; q < LOADS; q++) {
+        if (i < 2 && q >= START + i * HALF && q < START + (i + 1) * HALF)
+          K::load(ld, first + s + 1, CUR ^ 1, q);
+        if (i >= MT - 2 && q < START && q >= (i - MT + 2) * HALF && q < (i - MT + 3) * HALF)
+          K::load(ld, first + s + 2, CUR, q);
+      }
+      a[(i + 2) & 3] = i < MT - 2 ? K::read_a(pl, CUR, i + 2) : K::read_a(pl, CUR ^ 1, i + 2 - MT);
+      if constexpr (EXACT) {
+        const Wide aw = widen32(a[i & 3], as[i][0] >> (8 * J) & 255, as[i][1] >> (8 * J) & 255);
 #pragma unroll
         for (int j = 0; j < NT; j++) acc[i][j] = mfma16(bw[j], aw, acc[i][j]);
       }
-    } else {
 #pragma unroll
-      for (int i = 0; i < MT; i++)
-#pragma unroll
-        for (int j = 0; j < NT; j++)
-          acc[i][j] = mfma8<J>(bv[j], av[i], acc[i][j], bs[j][0], as[i][0]);
+      for (int j = 0; j < NT; j++) {
+        if constexpr (!EXACT)
+          acc[i][j] = mfma8<J>(b[j], a[i & 3], acc[i][j], bs[j][0], as[i][0]);
+        // the last use of a B tile: its next one takes its place
+        if (i == MT - 1) {
+          __builtin_amdgcn_sched_barrier(0);
+          b[j] = K::read_b(pl, CUR ^ 1, j);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if constexpr (J == 3) put_scales(((s >> 2) + 1) & 1);
+    if constexpr (J == 3) get_scales(((s >> 2) + 1) & 1);
   };
+  // whole chunks of four slabs: past K the codes are zeros
   for (int s = 0; s < nk; s += 4) {
     step(s, std::integral_constant<int, 0>());
-    if (s + 1 < nk) step(s + 1, std::integral_constant<int, 1>());
-    if (s + 2 < nk) step(s + 2, std::integral_constant<int, 2>());
-    if (s + 3 < nk) step(s + 3, std::integral_constant<int, 3>());
+    step(s + 1, std::integral_constant<int, 1>());
+    step(s + 2, std::integral_constant<int, 2>());
+    step(s + 3, std::integral_constant<int, 3>());
   }
+  // nothing may still be landing in LDS, and every wave is done reading it
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
-  void *c = g.c;
-  int out_bf16 = g.out_bf16;
-  if (g.partial) {
-    c = reinterpret_cast<float *>(g.c) + (int64_t)blockIdx.y * g.m * g.n;
-    out_bf16 = 0;
-  }
-  const bool vec = g.n % (out_bf16 ? 8 : 4) == 0;
-  const int64_t n = n0 + wn + 4 * NT * lg;
-#pragma unroll
-  for (int i = 0; i < MT; i++) {
-    const int64_t m = m0 + wm + 16 * i + l16;
-    if (m < g.m && n < g.n) {
-      float v[4 * NT];
-#pragma unroll
-      for (int j = 0; j < NT; j++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) v[4 * j + e] = acc[i][j][e];
-      store_run<4 * NT>(c, out_bf16, m * g.n + n, v, g.n - n, vec);
-    }
-  }
+  // Output: a lane's accumulators are 4-column runs of one row, which would
+  // be written in pieces of 8 or 16 bytes. Each wave turns 16 rows at a time
+  // through its own part of LDS and writes whole rows of its tile.
+  uint8_t *turn = slabs + wave * (16 * TN * 4);
+  static_assert(K::WAVES * 16 * TN * 4 <= 2 * ROWS * 128, "turning space");
+  if (g.out_bf16 && !g.partial)
+    store_tile<MT, NT, true>(acc, turn, g.c, g.m, g.n, m0 + wm, n0 + wn, lane);
+  else
+    store_tile<MT, NT, false>(acc, turn, reinterpret_cast<float *>(g.c) +
+                                             (g.partial ? (int64_t)blockIdx.y * g.m * g.n : 0),
+                              g.m, g.n, m0 + wm, n0 + wn, lane);
 }
 
 // Sum of the splits' partial results in order, rounded to the output type.
@@ -464,7 +578,7 @@ static Plan plan_of(int64_t m, int64_t n, int64_t k, int out_bf16) {
   }
   p.steps = all;
   const int64_t t = tiles(p.bm, p.bn);
-  // split K where the tiles leave most of the card idle, at least eight steps each
+  // split K where the tiles leave most of the card idle, at least eight slabs each
   if (t < 192) {
     int want = (int)std::min<int64_t>((384 + t - 1) / t, all / 8);
     if (want > 1) {
@@ -495,7 +609,7 @@ static hipError_t launch(const Plan &p, MatArgs g, hipStream_t st) {
     }
   }
   if (p.bm == 128) k_matmul8<128, 128, 64, 64, BLK32, EXACT><<<grid, 256, 0, st>>>(g);
-  else k_matmul8<64, 64, 32, 32, BLK32, EXACT><<<grid, 256, 0, st>>>(g);
+  else k_matmul8<64, 64, 64, 16, BLK32, EXACT><<<grid, 256, 0, st>>>(g);
   return hipGetLastError();
 }
 
