@@ -47,22 +47,22 @@ struct AppendArgs {
 };
 
 // Which sequence a unit of work belongs to: sequence i owns units from
-// cu[i] / per + extra i on, which leaves it at least n / per + extra.
+// cu[i] / per + extra i on, which leaves it at least n / per + extra. The
+// wave's lanes look at up to 64 sequences at once (one trip to memory for up
+// to 64 sequences, two up to 4096).
 __device__ __forceinline__ int find_sequence(const int32_t *cu, int batch, int per, int extra,
                                              int unit) {
-  int lo = 0, hi = batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cu[mid] / per + extra * mid <= unit) lo = mid;
-    else hi = mid - 1;
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = batch;
+  while (n > 1) {
+    const int step = (n + 63) >> 6, at = lo + lane * step;
+    const bool below = lane * step < n && cu[at] / per + extra * at <= unit;
+    // the lanes that hold are the first ones; sequence lo always does
+    const int skip = max(__popcll(__ballot(below)) - 1, 0) * step;
+    lo += skip;
+    n = min(step, n - skip);
   }
-  return lo;
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t amax_row8(const void *base, int64_t elem, float (&f)[8]) {
-  widen<BF16>(load_raw<BF16>(reinterpret_cast<const uint8_t *>(base) + elem * (BF16 ? 2 : 4), 0), f);
-  return amax8(f);
+  return __builtin_amdgcn_readfirstlane(lo);
 }
 
 // Four codes moved from scale byte s to s + d (d > 0), or to a NaN block.
@@ -76,15 +76,23 @@ __device__ __forceinline__ uint32_t move4(uint32_t w, int d, bool nan) {
   return (uint32_t)r;
 }
 
-constexpr int kMaxPage = 256, kMaxDim = 128;
+// Items of eight elements that a thread keeps between the two passes (what a
+// page of 64 tokens of 128 dims takes); larger pages read the rest twice.
+constexpr int kKeep = 4;
+
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> load_at(const void *base, int64_t elem) {
+  return load_raw<BF16>(reinterpret_cast<const uint8_t *>(base) + elem * (BF16 ? 2 : 4), 0);
+}
 
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_kv_append(const AppendArgs a) {
   // new values' codes, [dim][token]; rows are 16 bytes longer than a page's
   // so that a row's byte writes and the next row's fall on other banks
-  __shared__ __attribute__((aligned(16))) uint8_t vt[kMaxDim * (kMaxPage + 16)];
+  extern __shared__ __attribute__((aligned(16))) uint8_t vt[];
   __shared__ uint32_t am[2][4];
-  const int unit = blockIdx.x, head = blockIdx.y, P = a.c.page, D = a.c.dim;
+  const int unit = blockIdx.x / a.c.heads, head = blockIdx.x % a.c.heads;
+  const int P = a.c.page, D = a.c.dim;
   const int i = find_sequence(a.b.cu, a.b.batch, P, 2, unit);
   const int c0 = a.b.cu[i], n = a.b.cu[i + 1] - c0, held = a.b.lengths[i];
   const int j = (held >> a.shift) + unit - (c0 / P + 2 * i);  // page of the sequence
@@ -95,16 +103,41 @@ __global__ __launch_bounds__(256) void k_kv_append(const AppendArgs a) {
   const int64_t src0 = (int64_t)c0 + ((int64_t)j << a.shift) - held;  // token of slot 0
   const int64_t most = a.b.tokens - 1;
   const int64_t at = id * a.c.heads + head;
-  const int per = D >> 3, items = (end - kept) * per;  // items of eight elements
-
-  uint32_t mk = 0, mv = 0;
-  for (int it = threadIdx.x; it < items; it += 256) {
-    const int slot = kept + it / per, d = (it % per) * 8;
-    const int64_t tok = min(max(src0 + slot, (int64_t)0), most);
-    float f[8];
-    mk = max(mk, amax_row8<BF16>(a.k, tok * a.k_stride + (int64_t)head * D + d, f));
-    mv = max(mv, amax_row8<BF16>(a.v, tok * a.v_stride + (int64_t)head * D + d, f));
+  const int per = D >> 3, bits = D == 128 ? 4 : 3, items = (end - kept) << bits;
+  uint32_t was_k = 0, was_v = 0;
+  if (kept) {
+    was_k = a.c.k_scales[at];
+    was_v = a.c.v_scales[at];
   }
+  auto slot_of = [&](int it) { return kept + (it >> bits); };
+  auto dim_of = [&](int it) { return (it & (per - 1)) * 8; };
+  auto load = [&](const void *x, int64_t stride, int it) {
+    const int64_t tok = min(max(src0 + slot_of(it), (int64_t)0), most);
+    return load_at<BF16>(x, tok * stride + (int64_t)head * D + dim_of(it));
+  };
+
+  Raw<BF16> kr[kKeep], vr[kKeep];
+#pragma unroll
+  for (int u = 0; u < kKeep; u++) {
+    const int it = threadIdx.x + 256 * u;
+    if (it < items) {
+      kr[u] = load(a.k, a.k_stride, it);
+      vr[u] = load(a.v, a.v_stride, it);
+    }
+  }
+  uint32_t mk = 0, mv = 0;
+  auto take = [&](const Raw<BF16> &k, const Raw<BF16> &v) {
+    float f[8];
+    widen<BF16>(k, f);
+    mk = max(mk, amax8(f));
+    widen<BF16>(v, f);
+    mv = max(mv, amax8(f));
+  };
+#pragma unroll
+  for (int u = 0; u < kKeep; u++)
+    if ((int)threadIdx.x + 256 * u < items) take(kr[u], vr[u]);
+  for (int it = threadIdx.x + 256 * kKeep; it < items; it += 256)
+    take(load(a.k, a.k_stride, it), load(a.v, a.v_stride, it));
   mk = max16(mk);
   mv = max16(mv);
   mk = max(mk, (uint32_t)__shfl_xor((int)mk, 16));
@@ -114,11 +147,6 @@ __global__ __launch_bounds__(256) void k_kv_append(const AppendArgs a) {
   if ((threadIdx.x & 63) == 0) {
     am[0][threadIdx.x >> 6] = mk;
     am[1][threadIdx.x >> 6] = mv;
-  }
-  uint32_t was_k = 0, was_v = 0;
-  if (kept) {
-    was_k = a.c.k_scales[at];
-    was_v = a.c.v_scales[at];
   }
   __syncthreads();
   mk = max(max(am[0][0], am[0][1]), max(am[0][2], am[0][3]));
@@ -144,21 +172,25 @@ __global__ __launch_bounds__(256) void k_kv_append(const AppendArgs a) {
     __syncthreads();  // before the new tokens' bytes of the same words
   }
   const int row = P + 16;
-  for (int it = threadIdx.x; it < items; it += 256) {
-    const int slot = kept + it / per, d = (it % per) * 8;
-    const int64_t tok = min(max(src0 + slot, (int64_t)0), most);
+  auto put = [&](const Raw<BF16> &k, const Raw<BF16> &v, int it) {
+    const int slot = slot_of(it), d = dim_of(it);
     float f[8];
-    amax_row8<BF16>(a.k, tok * a.k_stride + (int64_t)head * D + d, f);
+    widen<BF16>(k, f);
     *reinterpret_cast<u32x2 *>(kc + slot * D + d) = encode8(f, sk);
-    amax_row8<BF16>(a.v, tok * a.v_stride + (int64_t)head * D + d, f);
+    widen<BF16>(v, f);
     const u32x2 w = encode8(f, sv);
 #pragma unroll
     for (int e = 0; e < 8; e++) vt[(d + e) * row + slot] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
-  }
+  };
+#pragma unroll
+  for (int u = 0; u < kKeep; u++)
+    if ((int)threadIdx.x + 256 * u < items) put(kr[u], vr[u], threadIdx.x + 256 * u);
+  for (int it = threadIdx.x + 256 * kKeep; it < items; it += 256)
+    put(load(a.k, a.k_stride, it), load(a.v, a.v_stride, it), it);
   __syncthreads();
-  const int chunks = P >> 4;
-  for (int it = threadIdx.x; it < D * chunks; it += 256) {
-    const int d = it / chunks, s = (it % chunks) * 16;
+  const int cshift = a.shift - 4;
+  for (int it = threadIdx.x; it < D << cshift; it += 256) {
+    const int d = it >> cshift, s = (it & ((1 << cshift) - 1)) * 16;
     const int lo = max(kept, s), hi = min(end, s + 16);
     if (lo >= hi) continue;
     uint8_t *dst = vc + (int64_t)d * P;
@@ -185,7 +217,7 @@ struct AttnArgs {
   int shift;
   int block_tokens;  // tokens of a workgroup's block of rows
   int chunk;         // kv tiles (of 128 tokens) per split
-  int splits;
+  int splits, units;
   float scale2;      // softmax scale times log2(e)
   uint16_t *out;
   float *part;       // [token, q head, split][dim + 2]: sums, then maximum and total
@@ -195,18 +227,20 @@ __device__ __forceinline__ i32x8 join8(u32x4 lo, u32x4 hi) {
   return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
                (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
+// D += A B^T over 128 elements; A's scale is byte JA of sa, B's byte JB of sb.
+template <int JA, int JB>
 __device__ __forceinline__ f32x4 mma(i32x8 a, i32x8 b, f32x4 d, uint32_t sa, uint32_t sb) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, d, 0, 0, 0, (int)sa, 0, (int)sb);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, d, 0, 0, JA, (int)sa, JB, (int)sb);
 }
 
 // A row of q as the second operand: hi and lo, each 32 codes (dim 128), or
 // hi in the first 16 bytes and lo in the second (dim 64, where one product
-// of length 128 takes both against the keys' codes given twice). `byte` is
-// the E8M0 byte of hi; lo's is byte - 4.
+// of length 128 takes both against the keys' codes given twice). Byte i of
+// `bytes` is the E8M0 byte of v[i]; lo's is 4 below hi's.
 template <int D>
 struct Query {
   i32x8 v[D / 64];
-  uint32_t byte[D / 64];
+  uint32_t bytes;
 };
 
 __device__ __forceinline__ void split4(const float (&x)[4], float to, float back, uint32_t &hi,
@@ -259,14 +293,23 @@ __device__ __forceinline__ Query<D> load_query(const uint16_t *row, int lg) {
 #pragma unroll
     for (int j = 0; j < 4; j++) hi[4 + j] = lo[j];
     q.v[0] = hi;
-    q.byte[0] = bad ? 255u : lg < 2 ? byte : byte - 4u;
+    q.bytes = bad ? 255u : lg < 2 ? byte : byte - 4u;
   } else {
     q.v[0] = hi;
     q.v[1] = lo;
-    q.byte[0] = bad ? 255u : byte;
-    q.byte[1] = bad ? 255u : byte - 4u;
+    q.bytes = bad ? 0xFFFFu : byte | (byte - 4u) << 8;
   }
   return q;
+}
+
+// Largest of the four lanes l % 16 + 16 g (a row of scores is spread over them).
+__device__ __forceinline__ float max_groups(float v) {
+  typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
+  const uint32_t x = __float_as_uint(v);
+  const u32x2v a = __builtin_bit_cast(u32x2v, __builtin_amdgcn_permlane16_swap(x, x, false, false));
+  const uint32_t y = __float_as_uint(__builtin_fmaxf(__uint_as_float(a.x), __uint_as_float(a.y)));
+  const u32x2v b = __builtin_bit_cast(u32x2v, __builtin_amdgcn_permlane32_swap(y, y, false, false));
+  return __builtin_fmaxf(__uint_as_float(b.x), __uint_as_float(b.y));
 }
 
 // Running state of 16 rows: maximum (in units of log2), sums, total.
@@ -282,49 +325,65 @@ struct Rows {
   }
 };
 
-// Weights of 128 scores (see the order above): masks tokens past `limit`
-// where `masked`, moves the running maximum, and gives hi and lo operands
-// 256 p = hi + lo / 16.
-template <int D>
-__device__ __forceinline__ void softmax_tile(f32x4 (&s)[8], Rows<D> &r, float c, bool masked,
-                                             int limit, i32x8 &hi, i32x8 &lo) {
+// Weights of RT x 16 rows of 128 scores (see the order above): masks tokens
+// past `limit` where `masked`, moves the running maxima, and gives the parts
+// of 256 p = hi + lo / 16. Branches are taken for all rows at once.
+template <int D, int RT>
+__device__ __forceinline__ void softmax_tile(f32x4 (&s)[RT][8], Rows<D> (&r)[RT], float c,
+                                             bool masked, const int (&limit)[RT], i32x8 (&hi)[RT],
+                                             i32x8 (&lo)[RT]) {
   if (masked) {
+#pragma unroll
+    for (int x = 0; x < RT; x++)
+#pragma unroll
+      for (int t = 0; t < 8; t++) {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          if (64 * (t >> 2) + 4 * (t & 3) + i > limit[x]) s[x][t][i] = -__builtin_inff();
+        __builtin_amdgcn_sched_barrier(0);  // few conditions alive at a time
+      }
+  }
+  float m[RT], to8[RT];
+  bool moved = false;
+#pragma unroll
+  for (int x = 0; x < RT; x++) {
+    float top = s[x][0][0];
 #pragma unroll
     for (int t = 0; t < 8; t++)
 #pragma unroll
+      for (int i = 0; i < 4; i++) top = __builtin_fmaxf(top, s[x][t][i]);
+    m[x] = __builtin_fmaxf(r[x].m, max_groups(top) * c);
+    moved |= m[x] != r[x].m;
+    // nothing seen yet: weights are 0
+    to8[x] = 8.0f - (m[x] == -__builtin_inff() ? 0.0f : m[x]);
+  }
+  if (__any(moved)) {
+#pragma unroll
+    for (int x = 0; x < RT; x++) {
+      const float alpha = __builtin_amdgcn_exp2f(r[x].m + (to8[x] - 8.0f));
+#pragma unroll
+      for (int d = 0; d < D / 16; d++) r[x].o[d] *= alpha;
+      r[x].l *= alpha;
+      r[x].m = m[x];
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < RT; x++)
+#pragma unroll
+    for (int t = 0; t < 8; t++) {
+      float p[4];
+#pragma unroll
       for (int i = 0; i < 4; i++)
-        if (64 * (t >> 2) + 4 * (t & 3) + i > limit) s[t][i] = -__builtin_inff();
-  }
-  float top = s[0][0];
-#pragma unroll
-  for (int t = 0; t < 8; t++)
-#pragma unroll
-    for (int i = 0; i < 4; i++) top = __builtin_fmaxf(top, s[t][i]);
-  top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-  top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-  const float m = __builtin_fmaxf(r.m, top * c);
-  const float ms = m == -__builtin_inff() ? 0.0f : m;  // nothing seen yet: weights are 0
-  if (__any(m != r.m)) {
-    const float alpha = __builtin_amdgcn_exp2f(r.m - ms);
-#pragma unroll
-    for (int d = 0; d < D / 16; d++) r.o[d] *= alpha;
-    r.l *= alpha;
-    r.m = m;
-  }
-  const float to8 = 8.0f - ms;  // 256 p
-#pragma unroll
-  for (int t = 0; t < 8; t++) {
-    float p[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], c, to8));
-    uint32_t a, b;
-    split4(p, 1.0f, 0.0625f, a, b);
-    hi[t] = (int)a;
-    lo[t] = (int)b;
-  }
+        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][i], c, to8[x]));
+      uint32_t a, b;
+      split4(p, 1.0f, 0.0625f, a, b);
+      hi[x][t] = (int)a;
+      lo[x][t] = (int)b;
+    }
 }
 
-constexpr uint32_t kHi = 127 - 8, kLo = 127 - 12;  // bytes of the weights' two parts
+// Scale bytes of the weights' two parts, and 1.
+constexpr uint32_t kParts = (127 - 8) | (127 - 12) << 8 | 127 << 16;
 
 // Zero the codes of tokens past the sequence's end (what a page holds there
 // may decode to NaN): the lane's 16 bytes start at token `from`, `len` valid.
@@ -345,12 +404,14 @@ struct Block {  // a block of query rows and the keys it sees
   int last_page;
 };
 __device__ __forceinline__ bool find_block(const AttnArgs &a, int unit, Block &b) {
-  const int i = find_sequence(a.b.cu, a.b.batch, a.block_tokens, 1, unit);
-  const int c0 = a.b.cu[i], n = a.b.cu[i + 1] - c0;
+  // everything here is the same for the whole workgroup: kept in scalar registers
+  auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+  const int i = uniform(find_sequence(a.b.cu, a.b.batch, a.block_tokens, 1, unit));
+  const int c0 = uniform(a.b.cu[i]), n = uniform(a.b.cu[i + 1]) - c0;
   const int at = (unit - (c0 / a.block_tokens + i)) * a.block_tokens;
   if (at >= n || at < 0 || c0 < 0 || (int64_t)c0 + n > a.b.tokens) return false;
   const int64_t room = (int64_t)a.b.width << a.shift;
-  b.len = (int)min((int64_t)max(a.b.lengths[i], 0), room);
+  b.len = (int)min((int64_t)max(uniform(a.b.lengths[i]), 0), room);
   b.tok0 = c0 + at;
   b.count = min(a.block_tokens, n - at);
   b.seen0 = b.len - n + at + 1;
@@ -359,75 +420,73 @@ __device__ __forceinline__ bool find_block(const AttnArgs &a, int unit, Block &b
   return true;
 }
 
-// The pages of the four runs of 32 tokens of tile `tile`, past the end the last page.
-struct Pages {
-  int id[4];
-};
-__device__ __forceinline__ Pages pages_of(const AttnArgs &a, const Block &b, int tile) {
-  Pages p;
-#pragma unroll
-  for (int j = 0; j < 4; j++)
-    p.id[j] = clamp_page(b.table[min((tile * 128 + 32 * j) >> a.shift, b.last_page)], a.c.pages);
-  return p;
+// The pages of the four runs of 32 tokens of a tile: lane j holds run j % 4's;
+// past the end the last page.
+__device__ __forceinline__ int page_of(const AttnArgs &a, const Block &b, int tile, int lane) {
+  return clamp_page(b.table[min((tile * 128 + 32 * (lane & 3)) >> a.shift, b.last_page)], a.c.pages);
 }
-__device__ __forceinline__ int pick4(const int (&x)[4], int i) {
-  const int a = (i & 1) ? x[1] : x[0], b = (i & 1) ? x[3] : x[2];
-  return (i & 2) ? b : a;
+struct Runs {
+  int a, b, c, d;
+};
+__device__ __forceinline__ Runs runs_of(int mine) {
+  return Runs{__builtin_amdgcn_readlane(mine, 0), __builtin_amdgcn_readlane(mine, 1),
+              __builtin_amdgcn_readlane(mine, 2), __builtin_amdgcn_readlane(mine, 3)};
+}
+__device__ __forceinline__ int of_run(const Runs &r, int j) {  // j may differ from lane to lane
+  const int lo = (j & 1) ? r.b : r.a, hi = (j & 1) ? r.d : r.c;
+  return (j & 2) ? hi : lo;
 }
 
-// Scale bytes of a tile as the matrix core wants them. A page whose values
+// Scale bytes of a tile's pages: lane j % 4 holds run j's key byte, lane 4 +
+// j its value byte. `bytes_of` turns them into the word that the matrix core
+// picks from: bytes 0 and 1 are for the keys that this lane's row holds in
+// tiles 0 .. 3 and 4 .. 7, byte 2 for the values of run lg. A page whose values
 // are NaN must reach only the rows that see it: its keys are made NaN
 // instead (masked scores are dropped, visible ones make the row NaN) and its
 // values, whose codes are signed zeros, get a finite scale.
-struct TileScales {
-  uint32_t k[2], v;
-};
-__device__ __forceinline__ TileScales scales_of(const AttnArgs &a, const Pages &p, int head,
-                                                int l16, int lg) {
-  int ks[4], vs[4];
+__device__ __forceinline__ uint32_t load_bytes(const AttnArgs &a, int page, int head, int lane) {
+  const int64_t at = (int64_t)page * a.c.heads + head;
+  return (lane & 4) ? a.c.v_scales[at] : a.c.k_scales[at];
+}
+__device__ __forceinline__ uint32_t bytes_of(uint32_t mine, int l16, int lg) {
+  uint32_t k[4], v[4];
 #pragma unroll
   for (int j = 0; j < 4; j++) {
-    const int64_t at = (int64_t)p.id[j] * a.c.heads + head;
-    vs[j] = a.c.v_scales[at];
-    ks[j] = vs[j] == 255 ? 255 : a.c.k_scales[at];
-    vs[j] = vs[j] == 255 ? 127 : vs[j];
+    k[j] = (uint32_t)__builtin_amdgcn_readlane((int)mine, j);
+    v[j] = (uint32_t)__builtin_amdgcn_readlane((int)mine, 4 + j);
+    k[j] = v[j] == 255u ? 255u : k[j];
+    v[j] = v[j] == 255u ? 127u : v[j];
   }
-  TileScales s;
-  s.k[0] = (uint32_t)((l16 & 8) ? ks[1] : ks[0]);
-  s.k[1] = (uint32_t)((l16 & 8) ? ks[3] : ks[2]);
-  s.v = (uint32_t)pick4(vs, lg);
-  return s;
+  const uint32_t even = k[0] | k[2] << 8, odd = k[1] | k[3] << 8;
+  const uint32_t v01 = (lg & 1) ? v[1] : v[0], v23 = (lg & 1) ? v[3] : v[2];
+  return ((l16 & 8) ? odd : even) | ((lg & 2) ? v23 : v01) << 16;
 }
 
 template <int D>
-__device__ __forceinline__ void scores(const i32x8 *kv, const Query<D> &q, const TileScales &sc,
+__device__ __forceinline__ void scores(const i32x8 *kv, const Query<D> &q, uint32_t sc,
                                        f32x4 (&s)[8]) {
 #pragma unroll
   for (int t = 0; t < 8; t++) {
-    s[t] = mma(kv[t], q.v[0], f32x4{0, 0, 0, 0}, sc.k[t >> 2], q.byte[0]);
-    if constexpr (D == 128) s[t] = mma(kv[t], q.v[1], s[t], sc.k[t >> 2], q.byte[1]);
+    const f32x4 z = {0, 0, 0, 0};
+    s[t] = t < 4 ? mma<0, 0>(kv[t], q.v[0], z, sc, q.bytes) : mma<1, 0>(kv[t], q.v[0], z, sc, q.bytes);
+    if constexpr (D == 128)
+      s[t] = t < 4 ? mma<0, 1>(kv[t], q.v[1], s[t], sc, q.bytes) : mma<1, 1>(kv[t], q.v[1], s[t], sc, q.bytes);
   }
 }
 
-__device__ __forceinline__ i32x8 ones() {
-  const int w = 0x38383838;
-  return i32x8{w, w, w, w, w, w, w, w};
-}
-
-// One lane's run of outputs of a row: 4 D / 16 consecutive numbers.
-template <int D>
-__device__ __forceinline__ void store_out(uint16_t *p, const float (&v)[D / 4]) {
-#pragma unroll
-  for (int j = 0; j < D / 4; j += 8)
-    *reinterpret_cast<u32x4 *>(p + j) =
-        u32x4{pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]),
-              pack_bf16(v[j + 4], v[j + 5]), pack_bf16(v[j + 6], v[j + 7])};
+// Sum of the 128 weights on top of l: a product with a row of ones (E2M1,
+// which takes half the registers of E4M3).
+__device__ __forceinline__ f32x4 add_weights(i32x8 hi, i32x8 lo, f32x4 l) {
+  const int w = 0x22222222;
+  const i32x8 ones = {w, w, w, w, 0, 0, 0, 0};
+  l = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ones, hi, l, 4, 0, 2, (int)kParts, 0, (int)kParts);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ones, lo, l, 4, 0, 2, (int)kParts, 1, (int)kParts);
 }
 
 // Few rows: a workgroup of four waves takes up to 16 RT rows of one sequence
 // and kv head and one split of its keys; wave w takes tiles w, w + 4, ....
 template <int D, int RT>
-__global__ __launch_bounds__(256) void k_attn_rows(const AttnArgs a) {
+__global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_rows(const AttnArgs a) {
   constexpr int DT = D / 16, W = 4;
   __shared__ float merge_o[W][16][D + 4];
   __shared__ float merge_ml[W][16][2];
@@ -457,62 +516,77 @@ __global__ __launch_bounds__(256) void k_attn_rows(const AttnArgs a) {
   }
   const int64_t PD = (int64_t)a.c.page * D;
   const int mask = a.c.page - 1;
-  Pages pg;
-  if (t0 + wave < t1) pg = pages_of(a, b, t0 + wave);
-  for (int tile = t0 + wave; tile < t1; tile += W) {
-    const TileScales sc = scales_of(a, pg, head, l16, lg);
-    i32x8 kv[8], vv[DT];
-    // keys: row (token) of this lane in tile t; its page by run of 32 tokens
-    const uint8_t *kp[2], *vp[2];
+  // keys: this lane's row (token) of tile t, in the page of run 2 (t / 4) + l16 / 8
+  auto load_keys = [&](int tile, const Runs &id, i32x8 (&kv)[8]) {
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-      kp[h] = a.c.k_codes + ((int64_t)((l16 & 8) ? pg.id[2 * h + 1] : pg.id[2 * h]) * a.c.heads + head) * PD;
-      vp[h] = a.c.v_codes + ((int64_t)((lg & 2) ? pg.id[2 * h + 1] : pg.id[2 * h]) * a.c.heads + head) * PD;
-    }
+      const int tok = tile * 128 + 64 * h + 16 * (l16 >> 2) + (l16 & 3);
+      const uint8_t *p = a.c.k_codes +
+                         ((int64_t)of_run(id, 2 * h + (l16 >> 3)) * a.c.heads + head) * PD +
+                         (tok & mask) * D + 16 * lg;
 #pragma unroll
-    for (int t = 0; t < 8; t++) {
-      const int tok = tile * 128 + 64 * (t >> 2) + 16 * (l16 >> 2) + 4 * (t & 3) + (l16 & 3);
-      const uint8_t *p = kp[t >> 2] + (tok & mask) * D + 16 * lg;
-      const u32x4 x = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
-      if constexpr (D == 128)
-        kv[t] = join8(x, __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + 64)));
-      else
-        kv[t] = join8(x, x);
+      for (int t = 0; t < 4; t++) {
+        const u32x4 x = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + 4 * t * D));
+        if constexpr (D == 128)
+          kv[4 * h + t] = join8(x, __builtin_nontemporal_load(
+                                       reinterpret_cast<const u32x4 *>(p + 4 * t * D + 64)));
+        else
+          kv[4 * h + t] = join8(x, x);
+      }
     }
+  };
+  auto load_values = [&](int tile, const Runs &id, i32x8 (&vv)[DT]) {
+    const int dim = 4 * DT * (l16 >> 2) + (l16 & 3);
+    const uint8_t *p[2];
 #pragma unroll
-    for (int d = 0; d < DT; d++) {
-      const int dim = 4 * DT * (l16 >> 2) + 4 * d + (l16 & 3);
-      const int s0 = (tile * 128 + 16 * lg) & mask, s1 = (tile * 128 + 64 + 16 * lg) & mask;
-      vv[d] = join8(__builtin_nontemporal_load(
-                        reinterpret_cast<const u32x4 *>(vp[0] + (int64_t)dim * a.c.page + s0)),
-                    __builtin_nontemporal_load(
-                        reinterpret_cast<const u32x4 *>(vp[1] + (int64_t)dim * a.c.page + s1)));
+    for (int h = 0; h < 2; h++)
+      p[h] = a.c.v_codes + ((int64_t)of_run(id, 2 * h + (lg >> 1)) * a.c.heads + head) * PD +
+             dim * a.c.page + ((tile * 128 + 64 * h + 16 * lg) & mask);
+#pragma unroll
+    for (int d = 0; d < DT; d++)
+      vv[d] = join8(
+          __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p[0] + 4 * d * a.c.page)),
+          __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p[1] + 4 * d * a.c.page)));
+  };
+  // all of a tile's loads are started at once; two waves share a SIMD, so
+  // that one's loads run beside the other's arithmetic
+  int mine = t0 + wave < t1 ? page_of(a, b, t0 + wave, lane) : 0;
+  for (int tile = t0 + wave; tile < t1; tile += W) {
+    const Runs id = runs_of(mine);
+    const uint32_t bytes = load_bytes(a, mine, head, lane);
+    i32x8 kv[8], vv[DT];
+    load_keys(tile, id, kv);
+    load_values(tile, id, vv);
+    if (tile + W < t1) mine = page_of(a, b, tile + W, lane);
+    const uint32_t sc = bytes_of(bytes, l16, lg);
+    f32x4 s[RT][8];
+    i32x8 hi[RT], lo[RT];
+    int limit[RT];
+#pragma unroll
+    for (int x = 0; x < RT; x++) {
+      scores<D>(kv, q[x], sc, s[x]);
+      limit[x] = seen[x] - 1 - tile * 128 - 16 * lg;
     }
-    if (tile + W < t1) pg = pages_of(a, b, tile + W);
-    const bool tail = tile * 128 + 128 > b.len;
-    const bool masked = tile * 128 + 128 > b.seen0;
-    if (tail) {
+    softmax_tile<D, RT>(s, r, a.scale2, tile * 128 + 128 > b.seen0, limit, hi, lo);
+    if (tile * 128 + 128 > b.len) {
+      // the sequence's last tile: what its pages hold past the end may decode
+      // to NaN and is cleared
 #pragma unroll
       for (int d = 0; d < DT; d++) {
-        const u32x4 lo = {(uint32_t)vv[d][0], (uint32_t)vv[d][1], (uint32_t)vv[d][2], (uint32_t)vv[d][3]};
-        const u32x4 hi = {(uint32_t)vv[d][4], (uint32_t)vv[d][5], (uint32_t)vv[d][6], (uint32_t)vv[d][7]};
+        const u32x4 v0 = {(uint32_t)vv[d][0], (uint32_t)vv[d][1], (uint32_t)vv[d][2], (uint32_t)vv[d][3]};
+        const u32x4 v1 = {(uint32_t)vv[d][4], (uint32_t)vv[d][5], (uint32_t)vv[d][6], (uint32_t)vv[d][7]};
         const int from = b.len - tile * 128 - 16 * lg;
-        vv[d] = join8(keep_tokens(lo, from), keep_tokens(hi, from - 64));
+        vv[d] = join8(keep_tokens(v0, from), keep_tokens(v1, from - 64));
       }
     }
 #pragma unroll
     for (int x = 0; x < RT; x++) {
-      f32x4 s[8];
-      scores<D>(kv, q[x], sc, s);
-      i32x8 hi, lo;
-      softmax_tile<D>(s, r[x], a.scale2, masked, seen[x] - 1 - tile * 128 - 16 * lg, hi, lo);
 #pragma unroll
       for (int d = 0; d < DT; d++) {
-        r[x].o[d] = mma(vv[d], hi, r[x].o[d], sc.v, kHi);
-        r[x].o[d] = mma(vv[d], lo, r[x].o[d], sc.v, kLo);
+        r[x].o[d] = mma<2, 0>(vv[d], hi[x], r[x].o[d], sc, kParts);
+        r[x].o[d] = mma<2, 1>(vv[d], lo[x], r[x].o[d], sc, kParts);
       }
-      r[x].l = mma(ones(), hi, r[x].l, 127, kHi);
-      r[x].l = mma(ones(), lo, r[x].l, 127, kLo);
+      r[x].l = add_weights(hi[x], lo[x], r[x].l);
     }
   }
   // merge the four waves, 16 rows at a time
@@ -567,70 +641,111 @@ __global__ __launch_bounds__(256) void k_attn_rows(const AttnArgs a) {
   }
 }
 
-// Joins the splits of one (token, query head): a wave, two (one) dims a lane.
+// Joins the splits of one (token, query head): thread s takes split s's
+// maximum and total, then D / 4 threads a row add up splits s, s + G, ....
 template <int D>
 __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a) {
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (row >= a.b.tokens * a.q_heads) return;
+  constexpr int C = D / 4, G = 256 / C, P = D + 4;
+  __shared__ float factor[256];
+  __shared__ float red[4];
+  __shared__ f32x4 sums[G][C];
+  const int64_t row = blockIdx.x;
   const int tok = (int)(row / a.q_heads);
   // the token's sequence and how many keys its block saw, as the first kernel had it
-  int lo = 0, hi = a.b.batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.b.cu[mid] <= tok) lo = mid;
-    else hi = mid - 1;
-  }
-  const int c0 = a.b.cu[lo], n = a.b.cu[lo + 1] - c0;
+  const int i = find_sequence(a.b.cu, a.b.batch, 1, 0, tok);
+  const int c0 = a.b.cu[i], n = a.b.cu[i + 1] - c0;
   const int64_t room = (int64_t)a.b.width << a.shift;
-  const int len = (int)min((int64_t)max(a.b.lengths[lo], 0), room);
+  const int len = (int)min((int64_t)max(a.b.lengths[i], 0), room);
   const int at = (tok - c0) / a.block_tokens * a.block_tokens;
   const int end = min(len, len - n + at + min(a.block_tokens, n - at));
   const int tiles = (max(end, 0) + 127) >> 7;
   const int live = max(1, min(a.splits, (tiles + a.chunk - 1) / a.chunk));
-  const float *p = a.part + row * a.splits * (D + 4);
+  const float *p = a.part + row * a.splits * P;
+  const int wave = threadIdx.x >> 6;
+
   float m = -__builtin_inff();
-  for (int s = 0; s < live; s++) m = __builtin_fmaxf(m, p[(int64_t)s * (D + 4) + D]);
+  for (int s = threadIdx.x; s < live; s += 256) m = __builtin_fmaxf(m, p[(int64_t)s * P + D]);
+  for (int d = 1; d < 64; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d));
+  if ((threadIdx.x & 63) == 0) red[wave] = m;
+  __syncthreads();
+  m = __builtin_fmaxf(__builtin_fmaxf(red[0], red[1]), __builtin_fmaxf(red[2], red[3]));
   const float ms = m == -__builtin_inff() ? 0.0f : m;
-  float l = 0.0f, o[D / 64];
+  const int c = threadIdx.x % C, g = threadIdx.x / C;
+  f32x4 o = {0, 0, 0, 0};
+  float l = 0.0f;
+  for (int s0 = 0; s0 < live; s0 += 256) {
+    const int s = s0 + threadIdx.x, many = min(256, live - s0);
+    float f = 0.0f;
+    if (s < live) {
+      f = __builtin_amdgcn_exp2f(p[(int64_t)s * P + D] - ms);
+      l = __builtin_fmaf(f, p[(int64_t)s * P + D + 1], l);
+    }
+    __syncthreads();  // the last round's factors have been used
+    factor[threadIdx.x] = f;
+    __syncthreads();
+#pragma unroll 4
+    for (int q = g; q < many; q += G) {
+      const f32x4 v = *reinterpret_cast<const f32x4 *>(p + (int64_t)(s0 + q) * P + 4 * c);
+      const float w = factor[q];
 #pragma unroll
-  for (int e = 0; e < D / 64; e++) o[e] = 0.0f;
-  for (int s = 0; s < live; s++) {
-    const float *ps = p + (int64_t)s * (D + 4);
-    const float f = __builtin_amdgcn_exp2f(ps[D] - ms);
-    l += f * ps[D + 1];
-#pragma unroll
-    for (int e = 0; e < D / 64; e++) o[e] += f * ps[lane * (D / 64) + e];
+      for (int e = 0; e < 4; e++) o[e] = __builtin_fmaf(w, v[e], o[e]);
+    }
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t *out = a.out + row * D + lane * (D / 64);
-  if constexpr (D == 128) *reinterpret_cast<uint32_t *>(out) = pack_bf16(o[0] * inv, o[1] * inv);
-  else *out = (uint16_t)pack_bf16(o[0] * inv, 0.0f);
+  l = sum64(l);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[wave] = l;
+  sums[g][c] = o;
+  __syncthreads();
+  l = (red[0] + red[1]) + (red[2] + red[3]);
+  if (g == 0) {
+#pragma unroll
+    for (int q = 1; q < G; q++) o += sums[q][c];
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    *reinterpret_cast<u32x2 *>(a.out + row * D + 4 * c) =
+        u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+  }
 }
 
 // Many rows: four waves of 32 rows share tiles of 128 tokens through LDS,
-// loaded directly and double-buffered. Rows are `tokens x group` of one kv
-// head. Chunks of 16 bytes are swapped within their row so that the 16 rows
-// a read touches spread over all banks.
+// loaded directly and double-buffered; two workgroups share a compute unit,
+// so that one's softmax runs beside the other's products. Rows are `tokens x
+// group` of one kv head.
+//
+// Keys lie in LDS as rows of D bytes (tokens), values as rows of 128 bytes
+// (dims). The 16-byte chunk c of row r sits at position c ^ f(r), f chosen so
+// that the 16 rows of a read fall on different banks; the chunks are swapped
+// on the global side. A load of keys covers rows of one run of 32 tokens,
+// whose page is wave-uniform; a lane's chunk of values lies in one of four.
 template <int D>
 __device__ __forceinline__ int swz_k(int r) {
   if constexpr (D == 128) return ((r >> 1) & 1) | (((r >> 4) & 3) << 1);
   return (r >> 4) & 3;
 }
-template <int D>
-__device__ __forceinline__ int swz_v(int r) {
-  return ((r >> 1) & 1) | (((r / (D / 4)) & 3) << 1);
+__device__ __forceinline__ int swz_v(int r) { return (r >> 1) & 7; }
+
+// 16 bytes a lane straight into LDS, lane after lane from `lds` on. In
+// assembly, since the compiler would otherwise make every later LDS read
+// wait for it; the kernel waits where it must. No output register.
+__device__ __forceinline__ void load_lds16(const uint8_t *base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               ::"s"(lds), "v"(offset), "s"(base) : "memory");
+}
+__device__ __forceinline__ void load_lds16(uint64_t address, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               ::"s"(lds), "v"(address) : "memory");
 }
 
 template <int D>
 __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
-  constexpr int DT = D / 16, RT = 2, T = 256;
-  constexpr int KL = 128 * D / 16 / T, VL = KL;  // direct loads per thread and tile
-  __shared__ __attribute__((aligned(16))) uint8_t ks[2][128 * D], vs[2][128 * D];
+  constexpr int DT = D / 16, RT = 2, S = 128 * D, T = 256;
+  constexpr int KL = S / 4096, VL = KL;  // direct loads per thread and tile
+  __shared__ __attribute__((aligned(16))) uint8_t ks[2 * S], vs[2 * S];
+  // kv heads fastest: the eight XCDs, which are dealt workgroups in turn,
+  // keep to few heads each. The last blocks of a sequence see the most keys:
+  // they start first.
+  const int head = blockIdx.x % a.c.heads;
   Block b;
-  // the last blocks of a sequence see the most keys: they start first
-  if (!find_block(a, gridDim.x - 1 - blockIdx.x, b)) return;
-  const int head = blockIdx.y;
+  if (!find_block(a, a.units - 1 - (int)(blockIdx.x / a.c.heads), b)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
   const int end = min(b.len, b.seen0 + b.count - 1);
@@ -649,101 +764,140 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
     r[x].clear();
   }
   const int64_t PD = (int64_t)a.c.page * D;
-  const int mask = a.c.page - 1;
-  auto load = [&](int tile, int buf, const Pages &pg) {
+  const int mask = a.c.page - 1, P = a.c.page;
+
+  // loads: this thread's offsets in a page's keys (rows tid / 8 or tid / 4 of
+  // a run; every other load's rows swizzle by 64 bytes more) and values
+  const int kr = threadIdx.x / (D / 16), kc = (threadIdx.x & (D / 16 - 1)) ^ swz_k<D>(kr);
+  const uint32_t koff = (uint32_t)((kr & 31) * D + kc * 16);
+  const int vr = threadIdx.x >> 3, vc = (threadIdx.x & 7) ^ swz_v(vr);
+  const uint32_t voff = (uint32_t)(vr * P + (vc & 1) * 16);
+  const uint32_t klds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)ks + wave * 1024;
+  const uint32_t vlds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)vs + wave * 1024;
+  auto load = [&](int tile, int buf, const Runs &id) {
 #pragma unroll
     for (int i = 0; i < KL; i++) {
-      constexpr int CH = D / 16;  // chunks per row
-      const int e = i * T + (int)threadIdx.x, row = e / CH, c = (e % CH) ^ swz_k<D>(row);
-      const uint8_t *src = a.c.k_codes +
-                           ((int64_t)pick4(pg.id, row >> 5) * a.c.heads + head) * PD +
-                           ((tile * 128 + row) & mask) * D + 16 * c;
-      __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void *)src,
-          (__attribute__((address_space(3))) void *)(ks[buf] + (i * T + wave * 64) * 16), 16, 0, 0);
+      const int j = D == 128 ? i : 2 * i + (wave >> 1);  // wave-uniform
+      const uint8_t *base = a.c.k_codes + ((int64_t)of_run(id, j) * a.c.heads + head) * PD +
+                            (int64_t)((tile * 128 + 32 * j) & mask) * D;
+      load_lds16(base, D == 128 && (i & 1) ? koff ^ 64u : koff, klds + buf * S + i * 4096);
     }
+    const int j = vc >> 1;
+    uint64_t v = (uint64_t)a.c.v_codes + ((int64_t)of_run(id, j) * a.c.heads + head) * PD +
+                 (uint32_t)(((tile * 128 + 32 * j) & mask) + (int)voff);
 #pragma unroll
-    for (int i = 0; i < VL; i++) {
-      const int e = i * T + (int)threadIdx.x, row = e >> 3, c = (e & 7) ^ swz_v<D>(row);
-      const uint8_t *src = a.c.v_codes + ((int64_t)pick4(pg.id, c >> 1) * a.c.heads + head) * PD +
-                           (int64_t)row * a.c.page + ((tile * 128 + 16 * c) & mask);
-      __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void *)src,
-          (__attribute__((address_space(3))) void *)(vs[buf] + (i * T + wave * 64) * 16), 16, 0, 0);
-    }
+    for (int i = 0; i < VL; i++, v += 32 * P) load_lds16(v, vlds + buf * S + i * 4096);
   };
-  Pages pg, nx;
+  // operand addresses in LDS: keys' row 64 (t / 4) + 16 (l16 / 4) + 4 (t % 4)
+  // + l16 % 4 of tile t, values' row 16 d + l16
+  const int krow = 16 * (l16 >> 2) + (l16 & 3);
+  const uint8_t *kp0 = ks + krow * D + 16 * (lg ^ swz_k<D>(krow));
+  const uint8_t *kp1 = ks + krow * D + 16 * ((lg + 4) ^ swz_k<D>(krow));
+  const uint8_t *vp0 = vs + l16 * 128 + 16 * (lg ^ swz_v(l16));
+  const uint8_t *vp1 = vs + l16 * 128 + 16 * ((lg + 4) ^ swz_v(l16));
+
+  int mine = 0;        // pages of the next tile
+  uint32_t bytes = 0;  // scale bytes of this one
   if (tiles > 0) {
-    pg = pages_of(a, b, 0);
-    load(0, 0, pg);
+    const int now = page_of(a, b, 0, lane);
+    bytes = load_bytes(a, now, head, lane);
+    mine = page_of(a, b, 1, lane);
+    load(0, 0, runs_of(now));
   }
+  int flip = S;
   for (int tile = 0; tile < tiles; tile++) {
-    const int buf = tile & 1;
-    const TileScales sc = scales_of(a, pg, head, l16, lg);
-    if (tile + 1 < tiles) nx = pages_of(a, b, tile + 1);
-    // this tile's loads have landed, and every wave is done with the other buffer
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    if (tile + 1 < tiles) load(tile + 1, buf ^ 1, nx);
+    // this tile's codes, its scale bytes and the next one's pages have
+    // arrived, and every wave is done with the other buffer
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    const uint32_t sc = bytes_of(bytes, l16, lg);
+    const Runs id = runs_of(mine);
+    __builtin_amdgcn_sched_barrier(0);
+    if (tile + 1 < tiles) {
+      bytes = load_bytes(a, mine, head, lane);
+      mine = page_of(a, b, tile + 2, lane);
+      load(tile + 1, (tile + 1) & 1, id);
+    }
+    auto keys = [&](int t) {
+      const int at = (64 * (t >> 2) + 4 * (t & 3)) * D;
+      const u32x4 lo = *reinterpret_cast<const u32x4 *>(kp0 + at);
+      if constexpr (D == 64) return join8(lo, lo);
+      else return join8(lo, *reinterpret_cast<const u32x4 *>(kp1 + at));
+    };
+    auto values = [&](int d) {
+      return join8(*reinterpret_cast<const u32x4 *>(vp0 + 2048 * d),
+                   *reinterpret_cast<const u32x4 *>(vp1 + 2048 * d));
+    };
+    // operands are read two tiles ahead
     f32x4 s[RT][8];
+    i32x8 f[3] = {keys(0), keys(1)};
 #pragma unroll
     for (int t = 0; t < 8; t++) {
-      const int row = 64 * (t >> 2) + 16 * (l16 >> 2) + 4 * (t & 3) + (l16 & 3);
-      const uint8_t *p = ks[buf] + row * D;
-      const u32x4 lo = *reinterpret_cast<const u32x4 *>(p + 16 * (lg ^ swz_k<D>(row)));
-      u32x4 hi = lo;
-      if constexpr (D == 128) hi = *reinterpret_cast<const u32x4 *>(p + 16 * ((lg + 4) ^ swz_k<D>(row)));
-      const i32x8 kv = join8(lo, hi);
+      if (t + 2 < 8) f[(t + 2) % 3] = keys(t + 2);
 #pragma unroll
-      for (int x = 0; x < RT; x++) {
-        s[x][t] = mma(kv, q[x].v[0], f32x4{0, 0, 0, 0}, sc.k[t >> 2], q[x].byte[0]);
-        if constexpr (D == 128) s[x][t] = mma(kv, q[x].v[1], s[x][t], sc.k[t >> 2], q[x].byte[1]);
+      for (int x = 0; x < RT; x++)
+        s[x][t] = t < 4 ? mma<0, 0>(f[t % 3], q[x].v[0], f32x4{0, 0, 0, 0}, sc, q[x].bytes)
+                        : mma<1, 0>(f[t % 3], q[x].v[0], f32x4{0, 0, 0, 0}, sc, q[x].bytes);
+      if constexpr (D == 128) {
+#pragma unroll
+        for (int x = 0; x < RT; x++)
+          s[x][t] = t < 4 ? mma<0, 1>(f[t % 3], q[x].v[1], s[x][t], sc, q[x].bytes)
+                          : mma<1, 1>(f[t % 3], q[x].v[1], s[x][t], sc, q[x].bytes);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    const bool masked = tile * 128 + 128 > b.seen0;
-    i32x8 hi[RT], lo[RT];
+    // all scores are taken here, while a key operand is at hand (the compiler
+    // would move some past the branches below, and keep the operands)
 #pragma unroll
     for (int x = 0; x < RT; x++)
-      softmax_tile<D>(s[x], r[x], a.scale2, masked, seen[x] - 1 - tile * 128 - 16 * lg, hi[x], lo[x]);
-    const bool tail = tile * 128 + 128 > b.len;
+#pragma unroll
+      for (int t = 0; t < 8; t++) asm volatile("" : "+v"(s[x][t]));
+    i32x8 hi[RT], lo[RT];
+    int limit[RT];
+#pragma unroll
+    for (int x = 0; x < RT; x++) limit[x] = seen[x] - 1 - tile * 128 - 16 * lg;
+    softmax_tile<D, RT>(s, r, a.scale2, tile * 128 + 128 > b.seen0, limit, hi, lo);
+    if (tile * 128 + 128 > b.len) {
+      // the sequence's last tile: what its pages hold past the end may decode
+      // to NaN and is cleared (16 bytes: one chunk of a row of values)
+      for (int e = threadIdx.x; e < D * 8; e += T) {
+        const int row = e >> 3, c = e & 7, keep = b.len - tile * 128 - 16 * c;
+        u32x4 *p = reinterpret_cast<u32x4 *>(vs + (tile & 1) * S + row * 128 + 16 * (c ^ swz_v(row)));
+        if (keep < 16) *p = keep_tokens(*p, keep);
+      }
+      __syncthreads();
+    }
+    f[0] = values(0);
+    f[1] = values(1);
 #pragma unroll
     for (int d = 0; d < DT; d++) {
-      const int row = 4 * DT * (l16 >> 2) + 4 * d + (l16 & 3);
-      const uint8_t *p = vs[buf] + row * 128;
-      u32x4 v0 = *reinterpret_cast<const u32x4 *>(p + 16 * (lg ^ swz_v<D>(row)));
-      u32x4 v1 = *reinterpret_cast<const u32x4 *>(p + 16 * ((lg + 4) ^ swz_v<D>(row)));
-      if (tail) {
-        const int from = b.len - tile * 128 - 16 * lg;
-        v0 = keep_tokens(v0, from);
-        v1 = keep_tokens(v1, from - 64);
-      }
-      const i32x8 vv = join8(v0, v1);
+      if (d + 2 < DT) f[(d + 2) % 3] = values(d + 2);
 #pragma unroll
-      for (int x = 0; x < RT; x++) {
-        r[x].o[d] = mma(vv, hi[x], r[x].o[d], sc.v, kHi);
-        r[x].o[d] = mma(vv, lo[x], r[x].o[d], sc.v, kLo);
-      }
+      for (int x = 0; x < RT; x++) r[x].o[d] = mma<2, 0>(f[d % 3], hi[x], r[x].o[d], sc, kParts);
+#pragma unroll
+      for (int x = 0; x < RT; x++) r[x].o[d] = mma<2, 1>(f[d % 3], lo[x], r[x].o[d], sc, kParts);
     }
 #pragma unroll
-    for (int x = 0; x < RT; x++) {
-      r[x].l = mma(ones(), hi[x], r[x].l, 127, kHi);
-      r[x].l = mma(ones(), lo[x], r[x].l, 127, kLo);
-    }
-    pg = nx;
+    for (int x = 0; x < RT; x++) r[x].l = add_weights(hi[x], lo[x], r[x].l);
+    kp0 += flip;  // to the other buffer
+    kp1 += flip;
+    vp0 += flip;
+    vp1 += flip;
+    flip = -flip;
   }
 #pragma unroll
   for (int x = 0; x < RT; x++) {
     const int row = 32 * wave + 16 * x + l16;
     if (row < rows) {
       const float l = r[x].l[0], inv = l == 0.0f ? 0.0f : 1.0f / l;
-      float v[D / 4];
-#pragma unroll
-      for (int d = 0; d < DT; d++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) v[4 * d + e] = r[x].o[d][e] * inv;
       const int64_t tok = b.tok0 + row / a.group;
       const int64_t qh = (int64_t)head * a.group + row % a.group;
-      store_out<D>(a.out + (tok * a.q_heads + qh) * D + 4 * DT * lg, v);
+      uint16_t *p = a.out + (tok * a.q_heads + qh) * D + 4 * lg;
+#pragma unroll
+      for (int d = 0; d < DT; d++) {
+        const f32x4 o = r[x].o[d];
+        *reinterpret_cast<u32x2 *>(p + 16 * d) =
+            u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+      }
     }
   }
 }
@@ -771,10 +925,11 @@ static AttnPlan attn_plan(int64_t tokens, int batch, int q_heads, int heads, int
   p.chunk = tiles > 0 ? tiles : 1;
   p.splits = 1;
   if (p.few) {
-    // enough workgroups to fill the card twice over; at least a tile a wave
+    // enough workgroups to fill the card four times over, and at least two
+    // tiles a wave: below that the sum over splits costs more than it saves
     const int64_t base = std::max<int64_t>(1, (int64_t)batch * heads);
-    const int64_t want = std::max<int64_t>(1, 4096 / base);
-    const int64_t c = std::max<int64_t>(4, (tiles + want - 1) / want);
+    const int64_t want = std::max<int64_t>(1, 2048 / base);
+    const int64_t c = std::max<int64_t>(8, (tiles + want - 1) / want);
     p.chunk = (int)((c + 3) / 4 * 4);
     p.splits = std::max(1, (tiles + p.chunk - 1) / p.chunk);
   }
@@ -789,10 +944,10 @@ hipError_t mxi_launch_kv_append(const void *k, const void *v, int bf16, int64_t 
                                 int64_t v_stride, const mx_kv_cache_t &cache,
                                 const mx_kv_batch_t &batch, hipStream_t st) {
   const AppendArgs a = {k, v, k_stride, v_stride, cache, batch, log2_of(cache.page)};
-  const dim3 grid((uint32_t)(batch.tokens / cache.page + 2 * (int64_t)batch.batch),
-                  (uint32_t)cache.heads);
-  if (bf16) k_kv_append<true><<<grid, 256, 0, st>>>(a);
-  else k_kv_append<false><<<grid, 256, 0, st>>>(a);
+  const dim3 grid((uint32_t)((batch.tokens / cache.page + 2 * (int64_t)batch.batch) * cache.heads));
+  const size_t lds = (size_t)cache.dim * (cache.page + 16);  // at most 34 KiB
+  if (bf16) k_kv_append<true><<<grid, 256, lds, st>>>(a);
+  else k_kv_append<false><<<grid, 256, lds, st>>>(a);
   return hipGetLastError();
 }
 
@@ -809,14 +964,15 @@ hipError_t mxi_launch_kv_attention(const void *q, int64_t q_stride, int q_heads,
   const AttnPlan p = attn_plan(batch.tokens, batch.batch, q_heads, cache.heads, max_length);
   const AttnArgs a = {reinterpret_cast<const uint16_t *>(q), q_stride, q_heads,
                       q_heads / cache.heads, cache, batch, log2_of(cache.page), p.block_tokens,
-                      p.chunk, p.splits, scale * 1.44269504088896340736f,
+                      p.chunk, p.splits, (int)p.units, scale * 1.44269504088896340736f,
                       reinterpret_cast<uint16_t *>(out), reinterpret_cast<float *>(workspace)};
-  const dim3 grid((uint32_t)p.units, (uint32_t)cache.heads, (uint32_t)p.splits);
   if (!p.few) {
+    const dim3 grid((uint32_t)(p.units * cache.heads));
     if (cache.dim == 64) k_attn_tiles<64><<<grid, 256, 0, st>>>(a);
     else k_attn_tiles<128><<<grid, 256, 0, st>>>(a);
     return hipGetLastError();
   }
+  const dim3 grid((uint32_t)p.units, (uint32_t)cache.heads, (uint32_t)p.splits);
   if (cache.dim == 64) {
     if (p.rt == 1) k_attn_rows<64, 1><<<grid, 256, 0, st>>>(a);
     else k_attn_rows<64, 2><<<grid, 256, 0, st>>>(a);
@@ -826,7 +982,7 @@ hipError_t mxi_launch_kv_attention(const void *q, int64_t q_stride, int q_heads,
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  const dim3 jgrid((uint32_t)((batch.tokens * q_heads + 3) / 4));
+  const dim3 jgrid((uint32_t)(batch.tokens * q_heads));
   if (cache.dim == 64) k_attn_join<64><<<jgrid, 256, 0, st>>>(a);
   else k_attn_join<128><<<jgrid, 256, 0, st>>>(a);
   return hipGetLastError();

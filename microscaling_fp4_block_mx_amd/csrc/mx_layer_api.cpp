@@ -62,6 +62,8 @@ mx_status_t check_cache(const mx_kv_cache_t *c, const mx_kv_batch_t *b) {
   // lengths and positions are 32-bit
   if ((int64_t)b->width * c->page > INT32_MAX) return MX_ERR_SHAPE;
   if (b->tokens > 0 && (b->batch < 1 || b->width < 1 || c->pages < 1)) return MX_ERR_SHAPE;
+  // workgroups of one launch: at most two pages more than whole ones per sequence
+  if (b->tokens / c->page + 2 * (int64_t)b->batch > INT32_MAX / c->heads) return MX_ERR_SHAPE;
   return MX_OK;
 }
 mx_status_t check_cache_pointers(const mx_kv_cache_t *c, const mx_kv_batch_t *b) {
@@ -230,7 +232,8 @@ static mx_status_t check_attention(int64_t tokens, int batch, int q_heads, int h
   if (heads < 1 || heads > 65535 || q_heads < heads || q_heads % heads || q_heads / heads > 128)
     return MX_ERR_SHAPE;
   if ((dim != 64 && dim != 128) || max_length < 0 || max_length > INT32_MAX) return MX_ERR_SHAPE;
-  if (tokens > 0 && (batch < 1 || tokens > (int64_t)INT32_MAX * 2 / q_heads)) return MX_ERR_SHAPE;
+  // workgroups of one launch: a row of heads per token, and per sequence
+  if (tokens > 0 && (batch < 1 || (tokens + batch) > INT32_MAX / q_heads)) return MX_ERR_SHAPE;
   return MX_OK;
 }
 

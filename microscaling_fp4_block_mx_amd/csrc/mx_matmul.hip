@@ -79,13 +79,13 @@ struct MatArgs {
 // A workgroup of (BM / TM) (BN / TN) waves owns a BM x BN tile. K runs in
 // slabs of 128, one v_mfma_scale_f32_16x16x128_f8f6f4 deep, which go from
 // global memory straight into LDS (16 bytes a lane, a row's 128 bytes one
-// request), double-buffered. A wave multiplies A's tiles one after the other
-// with all of its B tiles, which it holds; it reads A two tiles ahead and, in
-// the slab's last two tiles, the next slab's B and first A, so LDS is not
-// waited for. The one barrier of a slab stands before those: the next slab
-// has landed, and this one has been read, so that the loads of the slab
-// after next may start. A wave issues in order and a load waits at issue
-// while the memory unit is taken, so loads are dealt out between products.
+// request), through BUFS buffers. A wave multiplies A's tiles one after the
+// other with all of its B tiles, which it holds; it reads A two tiles ahead
+// and, in the slab's last two tiles, the next slab's B and first A, so LDS is
+// not waited for. The one barrier of a slab stands before those: the next
+// slab has landed, and this one has been read, so that its buffer's next
+// loads may start. A wave issues in order and a load waits at issue while
+// the memory unit is taken, so loads are dealt out between products.
 //
 // The 16-byte chunk c of row r sits at position c ^ f(r), f chosen so that
 // the 16 rows that a quarter of a read instruction touches fall on different
@@ -112,7 +112,7 @@ __device__ __forceinline__ i32x4 buffer_of(const void *base, uint32_t bytes) {
                __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
 }
 
-template <int BM, int BN, int TM, int TN, bool BLK32, bool EXACT>
+template <int BM, int BN, int TM, int TN, int BUFS, bool BLK32, bool EXACT>
 struct Tiled {
   static constexpr int WAVES = (BM / TM) * (BN / TN), T = WAVES * 64;
   static constexpr int MT = TM / 16, NT = TN / 16;
@@ -122,9 +122,7 @@ struct Tiled {
   static constexpr int SROWS = (ROWS + T - 1) / T;  // rows of scales per thread
   static_assert(MT % 4 == 0 && ROWS % PER == 0 && BM % PER == 0 && PER % 16 == 0, "tile and threads");
 
-  // LDS: A's two slabs, then B's, so that one address per chunk and constant
-  // offsets reach everything a lane reads
-  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
+  static constexpr int BYTES = ROWS * 128;  // a slab in LDS: A's rows, then B's
 
   struct Loader {
     i32x4 ar, br;     // buffers of the tile's rows of A and B
@@ -139,23 +137,21 @@ struct Tiled {
     constexpr int AL = BM / PER;
     const int k0 = slab * 128;
     const uint32_t o = k0 + l.kc < l.k ? l.o + k0 : kOut;
-    if (i < AL)
-      load_lds16(l.ar, o + (uint32_t)(i * PER) * l.k, l.lds + buf * A_BYTES + i * T * 16);
-    else
-      load_lds16(l.br, o + (uint32_t)((i - AL) * PER) * l.k,
-                 l.lds + 2 * A_BYTES + buf * B_BYTES + (i - AL) * T * 16);
+    const uint32_t to = l.lds + buf * BYTES + i * T * 16;
+    if (i < AL) load_lds16(l.ar, o + (uint32_t)(i * PER) * l.k, to);
+    else load_lds16(l.br, o + (uint32_t)((i - AL) * PER) * l.k, to);
   }
 
   struct Places {
-    const uint8_t *a0, *a1, *b0, *b1;  // this lane's two chunks of tile 0 of A and B
+    const uint8_t *a0, *a1, *b0, *b1;  // this lane's two chunks of tile 0 of A and B in a slab
   };
-  static __device__ __forceinline__ i32x8 read_a(const Places &p, int buf, int i) {
-    return join(*reinterpret_cast<const u32x4 *>(p.a0 + buf * A_BYTES + 2048 * i),
-                *reinterpret_cast<const u32x4 *>(p.a1 + buf * A_BYTES + 2048 * i));
+  static __device__ __forceinline__ i32x8 read_a(const Places &p, int i) {
+    return join(*reinterpret_cast<const u32x4 *>(p.a0 + 2048 * i),
+                *reinterpret_cast<const u32x4 *>(p.a1 + 2048 * i));
   }
-  static __device__ __forceinline__ i32x8 read_b(const Places &p, int buf, int j) {
-    return join(*reinterpret_cast<const u32x4 *>(p.b0 + buf * B_BYTES + 2048 * j),
-                *reinterpret_cast<const u32x4 *>(p.b1 + buf * B_BYTES + 2048 * j));
+  static __device__ __forceinline__ i32x8 read_b(const Places &p, int j) {
+    return join(*reinterpret_cast<const u32x4 *>(p.b0 + 2048 * j),
+                *reinterpret_cast<const u32x4 *>(p.b1 + 2048 * j));
   }
 };
 
@@ -208,11 +204,11 @@ __device__ __forceinline__ void store_tile(const f32x4 (&acc)[MT][NT], uint8_t *
   }
 }
 
-template <int BM, int BN, int TM, int TN, bool BLK32, bool EXACT>
+template <int BM, int BN, int TM, int TN, int BUFS, bool BLK32, bool EXACT>
 __global__ __launch_bounds__((BM / TM) * (BN / TN) * 64) void k_matmul8(const MatArgs g) {
-  using K = Tiled<BM, BN, TM, TN, BLK32, EXACT>;
+  using K = Tiled<BM, BN, TM, TN, BUFS, BLK32, EXACT>;
   constexpr int MT = K::MT, NT = K::NT, ROWS = K::ROWS, G = K::G;
-  __shared__ __attribute__((aligned(16))) uint8_t slabs[2 * ROWS * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t slabs[BUFS * K::BYTES];
   __shared__ uint32_t scl[2][G][ROWS];
 
   // XCD-aware order: workgroups are dealt round robin to the 8 XCDs; each
@@ -309,8 +305,8 @@ __global__ __launch_bounds__((BM / TM) * (BN / TN) * 64) void k_matmul8(const Ma
   // the swizzle does not depend on i and j
   const int ra = wm + l16, rb = wn + l16;
   const int lo = (lg ^ swz(l16)) * 16, hi = lo ^ 64;
-  const uint8_t *pa = slabs + ra * 128, *pb = slabs + 2 * K::A_BYTES + rb * 128;
-  const typename K::Places pl = {pa + lo, pa + hi, pb + lo, pb + hi};
+  const uint8_t *pa = slabs + ra * 128, *pb = slabs + (BM + rb) * 128;
+  typename K::Places pl = {pa + lo, pa + hi, pb + lo, pb + hi};
   f32x4 acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; i++)
@@ -338,14 +334,13 @@ __global__ __launch_bounds__((BM / TM) * (BN / TN) * 64) void k_matmul8(const Ma
   put_scales(0);
 
   // Loads of a slab: the first START of them in the last two tiles of the
-  // slab before the last, the others in the first two of the next.
+  // slab whose buffer they take, the others in the first two of the next.
   constexpr int LOADS = K::LOADS, START = MT >= 8 ? LOADS / 2 : LOADS;
 #pragma unroll
-  for (int i = 0; i < LOADS; i++) K::load(ld, first, 0, i);
-#pragma unroll
-  for (int i = 0; i < START; i++) K::load(ld, first + 1, 1, i);
-  // the first slab has landed (the second may be in flight)
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(START) : "memory");
+  for (int i = 0; i < (BUFS - 1) * LOADS + START; i++)
+    K::load(ld, first + i / LOADS, i / LOADS, i % LOADS);
+  // the first slab has landed (the others may be in flight)
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"((BUFS - 2) * LOADS + START) : "memory");
   uint32_t as[MT][2], bs[NT][2];
   auto get_scales = [&](int buf) {
     // exact: the lane's halves lie in blocks lg / 2 and 2 + lg / 2 of a slab
@@ -364,12 +359,14 @@ __global__ __launch_bounds__((BM / TM) * (BN / TN) * 64) void k_matmul8(const Ma
   i32x8 a[4], b[NT];
   get_scales(0);
 #pragma unroll
-  for (int j = 0; j < NT; j++) b[j] = K::read_b(pl, 0, j);
-  a[0] = K::read_a(pl, 0, 0);
-  a[1] = K::read_a(pl, 0, 1);
+  for (int j = 0; j < NT; j++) b[j] = K::read_b(pl, j);
+  a[0] = K::read_a(pl, 0);
+  a[1] = K::read_a(pl, 1);
 
+  int buf = 0;  // of slab s
   auto step = [&](int s, auto jt) {
-    constexpr int J = decltype(jt)::value, CUR = J & 1;
+    constexpr int J = decltype(jt)::value;
+    const int prev = buf == 0 ? BUFS - 1 : buf - 1;
     Wide bw[EXACT ? NT : 1];
     if constexpr (EXACT) {
 #pragma unroll
@@ -382,20 +379,26 @@ __global__ __launch_bounds__((BM / TM) * (BN / TN) * 64) void k_matmul8(const Ma
       if (i == MT - 2) {
         // the next slab (this wave's loads of it) has landed and this one
         // has been read; past the barrier that holds for every wave
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"((BUFS - 2) * LOADS) : "memory");
         // the next chunk's scales: read two slabs on
         if constexpr (J == 1) put_scales(((s >> 2) + 1) & 1);
+        // from here on, reads are of the next slab
+        const int by = buf + 1 == BUFS ? -(BUFS - 1) * K::BYTES : K::BYTES;
+        pl.a0 += by;
+        pl.a1 += by;
+        pl.b0 += by;
+        pl.b1 += by;
       }
       // a slab's loads in up to four parts of at most HALF
       constexpr int HALF = (START + 1) / 2;
 #pragma unroll
       for (int q = 0; q < LOADS; q++) {
         if (i < 2 && q >= START + i * HALF && q < START + (i + 1) * HALF)
-          K::load(ld, first + s + 1, CUR ^ 1, q);
+          K::load(ld, first + s - 1 + BUFS, prev, q);
         if (i >= MT - 2 && q < START && q >= (i - MT + 2) * HALF && q < (i - MT + 3) * HALF)
-          K::load(ld, first + s + 2, CUR, q);
+          K::load(ld, first + s + BUFS, buf, q);
       }
-      a[(i + 2) & 3] = i < MT - 2 ? K::read_a(pl, CUR, i + 2) : K::read_a(pl, CUR ^ 1, i + 2 - MT);
+      a[(i + 2) & 3] = K::read_a(pl, i < MT - 2 ? i + 2 : i + 2 - MT);
       if constexpr (EXACT) {
         const Wide aw = widen32(a[i & 3], as[i][0] >> (8 * J) & 255, as[i][1] >> (8 * J) & 255);
 #pragma unroll
@@ -408,12 +411,13 @@ __global__ __launch_bounds__((BM / TM) * (BN / TN) * 64) void k_matmul8(const Ma
         // the last use of a B tile: its next one takes its place
         if (i == MT - 1) {
           __builtin_amdgcn_sched_barrier(0);
-          b[j] = K::read_b(pl, CUR ^ 1, j);
+          b[j] = K::read_b(pl, j);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (J == 3) get_scales(((s >> 2) + 1) & 1);
+    buf = buf + 1 == BUFS ? 0 : buf + 1;
   };
   // whole chunks of four slabs: past K the codes are zeros
   for (int s = 0; s < nk; s += 4) {
@@ -429,7 +433,7 @@ __global__ __launch_bounds__((BM / TM) * (BN / TN) * 64) void k_matmul8(const Ma
   // be written in pieces of 8 or 16 bytes. Each wave turns 16 rows at a time
   // through its own part of LDS and writes whole rows of its tile.
   uint8_t *turn = slabs + wave * (16 * TN * 4);
-  static_assert(K::WAVES * 16 * TN * 4 <= 2 * ROWS * 128, "turning space");
+  static_assert(K::WAVES * 16 * TN * 4 <= BUFS * K::BYTES, "turning space");
   if (g.out_bf16 && !g.partial)
     store_tile<MT, NT, true>(acc, turn, g.c, g.m, g.n, m0 + wm, n0 + wn, lane);
   else
@@ -571,7 +575,10 @@ static Plan plan_of(int64_t m, int64_t n, int64_t k, int out_bf16) {
   auto tiles = [&](int bm, int bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
   if (out_bf16 && tiles(256, 256) >= 192) {
     p.bm = p.bn = 256;
-  } else if (tiles(128, 128) >= 192) {
+  } else if (tiles(256, 128) >= 160) {
+    p.bm = 256;
+    p.bn = 128;
+  } else if (tiles(128, 128) >= 160) {
     p.bm = p.bn = 128;
   } else {
     p.bm = p.bn = 64;
@@ -603,13 +610,14 @@ static hipError_t launch(const Plan &p, MatArgs g, hipStream_t st) {
   g.steps = p.steps;
   const dim3 grid((uint32_t)(g.tm * g.tn), (uint32_t)p.splits);
   if constexpr (!EXACT) {
-    if (p.bm == 256) {
-      k_matmul8<256, 256, 128, 64, BLK32, false><<<grid, 512, 0, st>>>(g);
+    if (p.bm == 256 && p.bn == 256) {
+      k_matmul8<256, 256, 128, 64, 2, BLK32, false><<<grid, 512, 0, st>>>(g);
       return hipGetLastError();
     }
   }
-  if (p.bm == 128) k_matmul8<128, 128, 64, 64, BLK32, EXACT><<<grid, 256, 0, st>>>(g);
-  else k_matmul8<64, 64, 64, 16, BLK32, EXACT><<<grid, 256, 0, st>>>(g);
+  if (p.bm == 256) k_matmul8<256, 128, 64, 64, 3, BLK32, EXACT><<<grid, 512, 0, st>>>(g);
+  else if (p.bm == 128) k_matmul8<128, 128, 64, 64, 4, BLK32, EXACT><<<grid, 256, 0, st>>>(g);
+  else k_matmul8<64, 64, 64, 16, 4, BLK32, EXACT><<<grid, 256, 0, st>>>(g);
   return hipGetLastError();
 }
 

@@ -128,19 +128,30 @@ __global__ __launch_bounds__(T) void k_rmsnorm_backward(
     if (it < items) widen<BF16>(load_raw<BF16>(weight, it), w[u]);
   }
   const float inv_k = 1.0f / (float)k;
-  int flip = 0;
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, flip ^= 1) {
-    const int64_t base = row * items;
-    Raw<BF16> dr[N], hr[N], tr[N];
+  // The next row is loaded while this one is summed and written.
+  Raw<BF16> dr[N], hr[N], tr[N];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int u = 0; u < N; u++) {
       const int it = threadIdx.x + u * T;
       if (it < items) {
-        dr[u] = load_raw<BF16>(dy, base + it);
-        hr[u] = load_raw<BF16>(h, base + it);
-        if (through) tr[u] = load_raw<BF16>(through, base + it);
+        dr[u] = load_raw<BF16>(dy, row * items + it);
+        hr[u] = load_raw<BF16>(h, row * items + it);
       }
     }
+  };
+  auto fetch_through = [&](int64_t row) {
+#pragma unroll
+    for (int u = 0; u < N; u++) {
+      const int it = threadIdx.x + u * T;
+      if (it < items) tr[u] = load_raw<BF16>(through, row * items + it);
+    }
+  };
+  fetch(blockIdx.x);
+  if (through) fetch_through(blockIdx.x);
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, flip ^= 1) {
+    const int64_t next = row + gridDim.x;
     float ss = 0.0f, sg = 0.0f, hv[N][8], dv[N][8];
 #pragma unroll
     for (int u = 0; u < N; u++) {
@@ -157,6 +168,7 @@ __global__ __launch_bounds__(T) void k_rmsnorm_backward(
         sg = __builtin_fmaf(dv[u][j] * w[u][j], hv[u][j], sg);
       }
     }
+    if (next < rows) fetch(next);
     // alternate halves of `part`: a wave may still be reading the last row's
     const f32x2 t = block_sum2<T>(ss, sg, part[flip]);
     const float s = 1.0f / __builtin_sqrtf(t.x * inv_k + eps);
@@ -174,9 +186,10 @@ __global__ __launch_bounds__(T) void k_rmsnorm_backward(
           if (through) o[j] += th[j];
           dw[u][j] = __builtin_fmaf(dv[u][j], hv[u][j] * s, dw[u][j]);
         }
-        store8<BF16>(dx, base + it, o);
+        store8<BF16>(dx, row * items + it, o);
       }
     }
+    if (through && next < rows) fetch_through(next);
   }
 #pragma unroll
   for (int u = 0; u < N; u++) {

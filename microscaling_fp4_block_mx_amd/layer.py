@@ -16,7 +16,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import _DTYPES, _need, _raise, _stream, load_library
+from . import _DTYPES, _need, _raise, load_library
 
 BLOCKS = (32, 128)
 
@@ -130,12 +130,21 @@ def _matrix(x, name: str, dtypes=_DTYPES):
         raise ValueError(f"{name} must be a GPU tensor")
     if x.dtype not in dtypes:
         raise ValueError(f"{name} must be one of {list(dtypes)}, got {x.dtype}")
-    if x.dim() == 0 or not x.is_contiguous():
+    shape = x.shape
+    if not shape or not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous, with at least one dimension")
-    k = x.shape[-1]
+    k = shape[-1]
     if k <= 0 or k % 32:
         raise ValueError(f"{name}'s last dimension must be a positive multiple of 32")
-    return x.numel() // k, k
+    return (shape[0] if len(shape) == 2 else x.numel() // k), k
+
+
+def _want(t, name: str, dev, dtype, numel: int):
+    """_need() with its outcome found in fewer steps where all is well (these
+    helpers run once per layer and token, where the host's time counts)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == numel
+            and t.device == dev and t.is_contiguous()):
+        _need(t, name, dev, dtype, numel)
 
 
 def _block(block: int) -> int:
@@ -150,11 +159,12 @@ def _ptr(t):
 
 def _call(device, fn, *args):
     """fn(*args, stream) on the device's current stream, raising on a bad status."""
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, _stream(device))
+    index = device.index
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, _stream(device))
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if status:
         _raise(status)
 
@@ -206,18 +216,18 @@ def rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     or None without a residual). out_h may be x or residual."""
     rows, k = _matrix(x, "x")
     dev = x.device
-    _need(weight, "weight", dev, x.dtype, k)
-    nb, lead = -(-k // _block(block)), tuple(x.shape[:-1])
+    _want(weight, "weight", dev, x.dtype, k)
+    nb, lead = -(-k // _block(block)), x.shape[:-1]
     if residual is not None:
-        _need(residual, "residual", dev, x.dtype, x.numel())
+        _want(residual, "residual", dev, x.dtype, x.numel())
         if out_h is None:
             out_h = torch.empty_like(x)
         else:
-            _need(out_h, "out_h", dev, x.dtype, x.numel())
+            _want(out_h, "out_h", dev, x.dtype, x.numel())
     elif out_h is not None:
         raise ValueError("out_h needs a residual")
     codes = torch.empty(x.shape, dtype=torch.uint8, device=dev)
-    scales = torch.empty(lead + (nb,), dtype=torch.uint8, device=dev)
+    scales = torch.empty((*lead, nb), dtype=torch.uint8, device=dev)
     _call(dev, load_library().mx_rmsnorm_mxfp8, x.data_ptr(), _ptr(residual), weight.data_ptr(),
           _DTYPES[x.dtype], rows, k, eps, block, codes.data_ptr(), scales.data_ptr(), _ptr(out_h))
     return codes, scales, out_h
@@ -230,10 +240,10 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, ep
     reaches h past the norm. dx is the gradient of x and of residual alike."""
     rows, k = _matrix(h, "h")
     dev = h.device
-    _need(dy, "dy", dev, h.dtype, h.numel())
-    _need(weight, "weight", dev, h.dtype, k)
+    _want(dy, "dy", dev, h.dtype, h.numel())
+    _want(weight, "weight", dev, h.dtype, k)
     if through is not None:
-        _need(through, "through", dev, h.dtype, h.numel())
+        _want(through, "through", dev, h.dtype, h.numel())
     lib = load_library()
     dx = torch.empty_like(h)
     dweight = torch.empty(k, dtype=torch.float32, device=dev)
@@ -260,12 +270,12 @@ def matmul_mxfp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sca
     if dtype not in _DTYPES:
         raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
     nb = -(-k // _block(block))
-    _need(a_scales, "a_scales", dev, torch.uint8, m * nb)
-    _need(b_scales, "b_scales", dev, torch.uint8, n * nb)
+    _want(a_scales, "a_scales", dev, torch.uint8, m * nb)
+    _want(b_scales, "b_scales", dev, torch.uint8, n * nb)
     if out is None:
         out = torch.empty(a.shape[:-1] + (n,), dtype=dtype, device=dev)
     else:
-        _need(out, "out", dev, dtype, m * n)
+        _want(out, "out", dev, dtype, m * n)
     lib, cd = load_library(), _DTYPES[dtype]
     size = lib.mx_matmul_mxfp8_workspace_size(m, n, k, block, cd)
     ws = _scratch(size, dev)
@@ -295,22 +305,22 @@ def _cache_of(cache: KVCache):
     if k.dim() != 4:
         raise ValueError("k_codes must be [pages, heads, page, dim]")
     pages, heads, page, dim = k.shape
-    _need(v, "v_codes", dev, torch.uint8)
-    if tuple(v.shape) != (pages, heads, dim, page):
+    _want(v, "v_codes", dev, torch.uint8, k.numel())
+    if v.shape != (pages, heads, dim, page):
         raise ValueError(f"v_codes must be {(pages, heads, dim, page)}, got {tuple(v.shape)}")
-    _need(ks, "k_scales", dev, torch.uint8, pages * heads)
-    _need(vs, "v_scales", dev, torch.uint8, pages * heads)
+    _want(ks, "k_scales", dev, torch.uint8, pages * heads)
+    _want(vs, "v_scales", dev, torch.uint8, pages * heads)
     return dev, MxKVCache(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), pages, heads,
                           dim, page)
 
 
 def _batch_of(dev, table, cu, lengths, tokens):
-    _need(table, "table", dev, torch.int32)
-    if table.dim() != 2:
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be [batch, width]")
     batch, width = table.shape
-    _need(cu, "cu", dev, torch.int32, batch + 1)
-    _need(lengths, "lengths", dev, torch.int32, batch)
+    _want(table, "table", dev, torch.int32, batch * width)
+    _want(cu, "cu", dev, torch.int32, batch + 1)
+    _want(lengths, "lengths", dev, torch.int32, batch)
     return MxKVBatch(table.data_ptr(), cu.data_ptr(), lengths.data_ptr(), tokens, batch, width)
 
 
@@ -349,7 +359,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, cu: torch
     if out is None:
         out = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=dev)
     else:
-        _need(out, "out", dev, torch.bfloat16, tokens * q_heads * dim)
+        _want(out, "out", dev, torch.bfloat16, tokens * q_heads * dim)
     room = b.width * c.page
     max_length = room if max_length <= 0 else min(max_length, room)
     lib = load_library()
