@@ -209,16 +209,13 @@ __global__ __launch_bounds__(256) void k_sum_rows(const float *__restrict__ part
   __shared__ float part[16][17];
   const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
   const int col = blockIdx.x * 16 + c;  // k is a multiple of 32: every column exists
-  float a = 0.0f, b = 0.0f, d = 0.0f, e = 0.0f;
+  float a[8] = {0, 0, 0, 0, 0, 0, 0, 0};  // independent: the loads of a round go together
   int i = r;
-  for (; i + 48 < n; i += 64) {
-    a += partial[(int64_t)i * k + col];
-    b += partial[(int64_t)(i + 16) * k + col];
-    d += partial[(int64_t)(i + 32) * k + col];
-    e += partial[(int64_t)(i + 48) * k + col];
-  }
-  for (; i < n; i += 16) a += partial[(int64_t)i * k + col];
-  part[r][c] = (a + b) + (d + e);
+  for (; i + 7 * 16 < n; i += 8 * 16)
+#pragma unroll
+    for (int q = 0; q < 8; q++) a[q] += partial[(int64_t)(i + 16 * q) * k + col];
+  for (; i < n; i += 16) a[0] += partial[(int64_t)i * k + col];
+  part[r][c] = ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
   __syncthreads();
   if (r == 0) {
     float t = 0.0f;
@@ -370,8 +367,10 @@ hipError_t mxi_launch_rmsnorm(const void *x, const void *residual, const void *w
 }
 
 int64_t mxi_rmsnorm_partials(int64_t rows, int64_t k) {
-  const Shape s = row_shape(k / 8, 2);
-  const int64_t most = (int64_t)256 * (1024 / s.t);  // workgroups resident at once
+  const Shape s = row_shape(k / 8, 1);
+  // 1,024 threads per compute unit; on 8192 x 4096 with a residual, 54 us
+  // (1,536: 57, 2,048: 61; two items a thread and 1,024: 77)
+  const int64_t most = (int64_t)256 * (1024 / s.t);
   return rows < most ? rows : most;
 }
 
@@ -379,7 +378,7 @@ hipError_t mxi_launch_rmsnorm_backward(const void *dy, const void *h, const void
                                        const void *through, int bf16, int64_t rows, int64_t k,
                                        float eps, void *dx, float *dweight, float *partial,
                                        hipStream_t st) {
-  const Shape s = row_shape(k / 8, 2);
+  const Shape s = row_shape(k / 8, 1);
   const int64_t grid = mxi_rmsnorm_partials(rows, k);
   auto go = [&](auto bf) {
     return with_shape<decltype(bf)::value>(s, [&](auto t, auto n) {
