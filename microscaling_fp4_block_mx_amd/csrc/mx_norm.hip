@@ -3,8 +3,11 @@
 // columns.
 //
 // Norm: h = x + r, y_j = w_j h_j / sqrt(sum h^2 / k + eps), then MXFP8 of y
-// in blocks of 32 or 128 along the row. The sum is fp32 and h enters it
-// unrounded; the copy of h that is written is rounded to the input's type.
+// in blocks of 32 or 128 along the row. h enters the sum unrounded (the copy
+// of it that is written is rounded to the input's type); a wave sums in fp32,
+// the waves' sums and the root are in 64 bits, and y keeps what its products
+// round off until the last addition: a block's scale byte changes where its
+// largest value crosses a power of two, so a bit of y can be one of the byte.
 // One workgroup holds one row in registers, so x, r are read once and codes,
 // scales, h written once: bound by HBM.
 //
@@ -37,12 +40,25 @@ __device__ __forceinline__ f32x2 block_sum2(float a, float b, f32x2 *part) {
   return t;
 }
 
+// The same for one value, added up in 64 bits from the waves' sums on.
+template <int T>
+__device__ __forceinline__ double block_sum(float a, float *part) {
+  a = sum64(a);
+  if constexpr (T == 64) return a;
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
+  __syncthreads();
+  double t = part[0];
+#pragma unroll
+  for (int i = 1; i < T / 64; i++) t += part[i];
+  return t;
+}
+
 template <bool BF16, int T, int N>
 __global__ __launch_bounds__(T) void k_rmsnorm(const void *x, const void *residual,
                                                const void *__restrict__ weight, int k, float eps,
                                                int wide, uint8_t *__restrict__ codes,
                                                uint8_t *__restrict__ scales, void *h) {
-  __shared__ f32x2 part[T / 64];
+  __shared__ float part[T / 64];
   const int64_t row = blockIdx.x;
   const int items = k >> 3;
   const int64_t base = row * items;
@@ -84,26 +100,36 @@ __global__ __launch_bounds__(T) void k_rmsnorm(const void *x, const void *residu
       for (int j = 0; j < 8; j++) f[u][j] = 0.0f;
     }
   }
-  ss = block_sum2<T>(ss, 0.0f, part).x;
-  const float s = 1.0f / __builtin_sqrtf(ss / (float)k + eps);
+  const double exact = 1.0 / __builtin_sqrt(block_sum<T>(ss, part) / k + eps);
+  const float s = (float)exact, s_low = (float)(exact - s);
   const int lanes = wide ? 16 : 4;  // lanes that share a block (wave-uniform)
   const int64_t nb = (items + lanes - 1) / lanes;
 #pragma unroll
   for (int u = 0; u < N; u++) {
     const int it = threadIdx.x + u * T;
     float y[8];
+    uint32_t m = 0;
     if (it < items) {
       float w[8];
       widen<BF16>(wr[u], w);
 #pragma unroll
-      for (int j = 0; j < 8; j++) y[j] = f[u][j] * s * w[j];
+      for (int j = 0; j < 8; j++) {
+        const float n = f[u][j] * s;
+        const float low = __builtin_fmaf(f[u][j], s, -n) + f[u][j] * s_low;
+        y[j] = __builtin_fmaf(n, w[j], low * w[j]);
+      }
+      m = amax8(y);
+      if (m >= 0x7F800000u) {  // infinities: their low parts are NaN
+#pragma unroll
+        for (int j = 0; j < 8; j++) y[j] = f[u][j] * s * w[j];
+        m = amax8(y);
+      }
     } else {
 #pragma unroll
       for (int j = 0; j < 8; j++) y[j] = 0.0f;
     }
     // lanes past the row's end take part with zeros: they may sit in the
     // last, short block
-    uint32_t m = amax8(y);
     m = wide ? max16(m) : max4(m);
     if (it < items) {
       const uint32_t sb = scale_byte8(m);
