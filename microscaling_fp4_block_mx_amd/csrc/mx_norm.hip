@@ -143,58 +143,63 @@ template <bool BF16, int T, int N>
 __global__ __launch_bounds__(T) void k_rmsnorm_backward(
     const void *dy, const void *h, const void *__restrict__ weight, const void *through,
     int64_t rows, int k, float eps, void *dx, float *__restrict__ partial) {
+  // One item a thread: the next row is loaded while this one is summed and
+  // written. More take the registers for their own row and widen them, and
+  // read the weight again (from the caches), at each use.
+  constexpr bool AHEAD = N == 1;
   __shared__ f32x2 part[2][T / 64];
   const int items = k >> 3;
-  float w[N][8], dw[N][8];
+  Raw<BF16> dr[N], hr[N], tr[N], wr[N];
+  auto fetch = [&](const void *from, int64_t row, Raw<BF16> (&to)[N]) {
+#pragma unroll
+    for (int u = 0; u < N; u++) {
+      const int it = threadIdx.x + u * T;
+      if (it < items) to[u] = load_raw<BF16>(from, row * items + it);
+    }
+  };
+  float dw[N][8];
 #pragma unroll
   for (int u = 0; u < N; u++) {
-    const int it = threadIdx.x + u * T;
 #pragma unroll
-    for (int j = 0; j < 8; j++) w[u][j] = dw[u][j] = 0.0f;
-    if (it < items) widen<BF16>(load_raw<BF16>(weight, it), w[u]);
+    for (int j = 0; j < 8; j++) dw[u][j] = 0.0f;
+    wr[u] = dr[u] = hr[u] = tr[u] = Raw<BF16>{};
   }
   const float inv_k = 1.0f / (float)k;
-  // The next row is loaded while this one is summed and written.
-  Raw<BF16> dr[N], hr[N], tr[N];
-  auto fetch = [&](int64_t row) {
-#pragma unroll
-    for (int u = 0; u < N; u++) {
-      const int it = threadIdx.x + u * T;
-      if (it < items) {
-        dr[u] = load_raw<BF16>(dy, row * items + it);
-        hr[u] = load_raw<BF16>(h, row * items + it);
-      }
-    }
-  };
-  auto fetch_through = [&](int64_t row) {
-#pragma unroll
-    for (int u = 0; u < N; u++) {
-      const int it = threadIdx.x + u * T;
-      if (it < items) tr[u] = load_raw<BF16>(through, row * items + it);
-    }
-  };
-  fetch(blockIdx.x);
-  if (through) fetch_through(blockIdx.x);
+  if (AHEAD) {
+    fetch(weight, 0, wr);
+    fetch(dy, blockIdx.x, dr);
+    fetch(h, blockIdx.x, hr);
+    if (through) fetch(through, blockIdx.x, tr);
+  }
   int flip = 0;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, flip ^= 1) {
     const int64_t next = row + gridDim.x;
-    float ss = 0.0f, sg = 0.0f, hv[N][8], dv[N][8];
+    if (!AHEAD) {
+      fetch(dy, row, dr);
+      fetch(h, row, hr);
+      fetch(weight, 0, wr);
+      if (through) fetch(through, row, tr);
+    }
+    float ss = 0.0f, sg = 0.0f;
+    Raw<BF16> d[N], g[N];  // of this row; past its end zeros
 #pragma unroll
     for (int u = 0; u < N; u++) {
-      if (threadIdx.x + u * T < items) {
-        widen<BF16>(hr[u], hv[u]);
-        widen<BF16>(dr[u], dv[u]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; j++) hv[u][j] = dv[u][j] = 0.0f;
-      }
+      d[u] = dr[u];
+      g[u] = hr[u];
+      float dv[8], hv[8], w[8];
+      widen<BF16>(d[u], dv);
+      widen<BF16>(g[u], hv);
+      widen<BF16>(wr[u], w);
 #pragma unroll
       for (int j = 0; j < 8; j++) {
-        ss = __builtin_fmaf(hv[u][j], hv[u][j], ss);
-        sg = __builtin_fmaf(dv[u][j] * w[u][j], hv[u][j], sg);
+        ss = __builtin_fmaf(hv[j], hv[j], ss);
+        sg = __builtin_fmaf(dv[j] * w[j], hv[j], sg);
       }
     }
-    if (next < rows) fetch(next);
+    if (AHEAD && next < rows) {
+      fetch(dy, next, dr);
+      fetch(h, next, hr);
+    }
     // alternate halves of `part`: a wave may still be reading the last row's
     const f32x2 t = block_sum2<T>(ss, sg, part[flip]);
     const float s = 1.0f / __builtin_sqrtf(t.x * inv_k + eps);
@@ -203,19 +208,21 @@ __global__ __launch_bounds__(T) void k_rmsnorm_backward(
     for (int u = 0; u < N; u++) {
       const int it = threadIdx.x + u * T;
       if (it < items) {
-        float o[8], th[8];
+        float dv[8], hv[8], w[8], o[8], th[8];
+        widen<BF16>(d[u], dv);
+        widen<BF16>(g[u], hv);
+        widen<BF16>(wr[u], w);
         if (through) widen<BF16>(tr[u], th);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-          const float g = dv[u][j] * w[u][j];
-          o[j] = s * __builtin_fmaf(-hv[u][j], c, g);
+          o[j] = s * __builtin_fmaf(-hv[j], c, dv[j] * w[j]);
           if (through) o[j] += th[j];
-          dw[u][j] = __builtin_fmaf(dv[u][j], hv[u][j] * s, dw[u][j]);
+          dw[u][j] = __builtin_fmaf(dv[j], hv[j] * s, dw[u][j]);
         }
         store8<BF16>(dx, row * items + it, o);
       }
     }
-    if (through && next < rows) fetch_through(next);
+    if (AHEAD && through && next < rows) fetch(through, next, tr);
   }
 #pragma unroll
   for (int u = 0; u < N; u++) {
@@ -343,34 +350,36 @@ struct Shape {
   int t, n;
 };
 static Shape row_shape(int64_t items, int per) {
-  for (int t = 64; t <= 1024; t *= 2)
-    if (items <= (int64_t)t * per) {
-      int n = 1;
-      while ((int64_t)t * n < items) n *= 2;
-      return {t, n};
-    }
+  for (int t = 64; t <= 1024; t *= 2) {
+    if (items <= t && (t == 64 || per == 1)) return {t, 1};
+    if (items <= (int64_t)t * per) return {t, per};
+  }
   int n = per;
   while ((int64_t)1024 * n < items) n *= 2;
   return {1024, n};
 }
 
-template <bool BF16, typename F>
+// FOUR: also the shapes that row_shape(.., 4) gives.
+template <bool FOUR, typename F>
 static hipError_t with_shape(Shape s, F f) {
-#define MXL_N(T)                                                   \
-  switch (s.n) {                                                   \
-    case 1: return f(std::integral_constant<int, T>(), std::integral_constant<int, 1>()); \
-    case 2: return f(std::integral_constant<int, T>(), std::integral_constant<int, 2>()); \
-    case 4: return f(std::integral_constant<int, T>(), std::integral_constant<int, 4>()); \
-    default: return f(std::integral_constant<int, T>(), std::integral_constant<int, 8>()); \
-  }
+  auto at = [&](auto t) {
+    if constexpr (FOUR)
+      if (s.n == 4) return f(t, std::integral_constant<int, 4>());
+    return f(t, std::integral_constant<int, 1>());
+  };
   switch (s.t) {
-    case 64: MXL_N(64)
-    case 128: MXL_N(128)
-    case 256: MXL_N(256)
-    case 512: MXL_N(512)
-    default: MXL_N(1024)
+    case 64: return at(std::integral_constant<int, 64>());
+    case 128: return at(std::integral_constant<int, 128>());
+    case 256: return at(std::integral_constant<int, 256>());
+    case 512: return at(std::integral_constant<int, 512>());
   }
-#undef MXL_N
+  constexpr std::integral_constant<int, 1024> t;
+  switch (s.n) {
+    case 1: return f(t, std::integral_constant<int, 1>());
+    case 2: return f(t, std::integral_constant<int, 2>());
+    case 4: return f(t, std::integral_constant<int, 4>());
+    default: return f(t, std::integral_constant<int, 8>());
+  }
 }
 
 }  // namespace mxl
@@ -382,7 +391,7 @@ hipError_t mxi_launch_rmsnorm(const void *x, const void *residual, const void *w
                               uint8_t *scales, void *h, hipStream_t st) {
   const Shape s = row_shape(k / 8, rows < 512 ? 1 : 4);
   auto go = [&](auto bf) {
-    return with_shape<decltype(bf)::value>(s, [&](auto t, auto n) {
+    return with_shape<true>(s, [&](auto t, auto n) {
       k_rmsnorm<decltype(bf)::value, decltype(t)::value, decltype(n)::value>
           <<<dim3((uint32_t)rows), dim3(decltype(t)::value), 0, st>>>(
               x, residual, weight, (int)k, eps, block == 128, codes, scales, h);
@@ -407,7 +416,7 @@ hipError_t mxi_launch_rmsnorm_backward(const void *dy, const void *h, const void
   const Shape s = row_shape(k / 8, 1);
   const int64_t grid = mxi_rmsnorm_partials(rows, k);
   auto go = [&](auto bf) {
-    return with_shape<decltype(bf)::value>(s, [&](auto t, auto n) {
+    return with_shape<false>(s, [&](auto t, auto n) {
       k_rmsnorm_backward<decltype(bf)::value, decltype(t)::value, decltype(n)::value>
           <<<dim3((uint32_t)grid), dim3(decltype(t)::value), 0, st>>>(
               dy, h, weight, through, rows, (int)k, eps, dx, partial);
