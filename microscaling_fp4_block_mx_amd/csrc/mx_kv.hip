@@ -32,6 +32,8 @@
 
 namespace mxl {
 
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
 __device__ __forceinline__ int clamp_page(int32_t id, int64_t pages) {
   return (int)min((uint32_t)id, (uint32_t)(pages - 1));
 }
@@ -233,6 +235,11 @@ __device__ __forceinline__ f32x4 mma(i32x8 a, i32x8 b, f32x4 d, uint32_t sa, uin
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, d, 0, 0, JA, (int)sa, JB, (int)sb);
 }
 
+// D += A B^T over 32 bf16 elements.
+__device__ __forceinline__ f32x4 mma16(u32x4 a, u32x4 b, f32x4 d) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), d, 0, 0, 0);
+}
+
 // A row of q as the second operand: hi and lo, each 32 codes (dim 128), or
 // hi in the first 16 bytes and lo in the second (dim 64, where one product
 // of length 128 takes both against the keys' codes given twice). Byte i of
@@ -325,13 +332,12 @@ struct Rows {
   }
 };
 
-// Weights of RT x 16 rows of 128 scores (see the order above): masks tokens
-// past `limit` where `masked`, moves the running maxima, and gives the parts
-// of 256 p = hi + lo / 16. Branches are taken for all rows at once.
-template <int D, int RT>
-__device__ __forceinline__ void softmax_tile(f32x4 (&s)[RT][8], Rows<D> (&r)[RT], float c,
-                                             bool masked, const int (&limit)[RT], i32x8 (&hi)[RT],
-                                             i32x8 (&lo)[RT]) {
+// Masks RT x 16 rows of 128 scores past `limit` where `masked` (tile t's
+// accumulator i is token places(t) + i) and moves the running maxima; `less`
+// is what a weight's exponent takes off. Branches are taken for all rows at once.
+template <int D, int RT, typename F>
+__device__ __forceinline__ void running_max(f32x4 (&s)[RT][8], Rows<D> (&r)[RT], float c, bool masked,
+                                            const int (&limit)[RT], F places, float (&less)[RT]) {
   if (masked) {
 #pragma unroll
     for (int x = 0; x < RT; x++)
@@ -339,11 +345,11 @@ __device__ __forceinline__ void softmax_tile(f32x4 (&s)[RT][8], Rows<D> (&r)[RT]
       for (int t = 0; t < 8; t++) {
 #pragma unroll
         for (int i = 0; i < 4; i++)
-          if (64 * (t >> 2) + 4 * (t & 3) + i > limit[x]) s[x][t][i] = -__builtin_inff();
+          if (places(t) + i > limit[x]) s[x][t][i] = -__builtin_inff();
         __builtin_amdgcn_sched_barrier(0);  // few conditions alive at a time
       }
   }
-  float m[RT], to8[RT];
+  float m[RT];
   bool moved = false;
 #pragma unroll
   for (int x = 0; x < RT; x++) {
@@ -355,18 +361,27 @@ __device__ __forceinline__ void softmax_tile(f32x4 (&s)[RT][8], Rows<D> (&r)[RT]
     m[x] = __builtin_fmaxf(r[x].m, max_groups(top) * c);
     moved |= m[x] != r[x].m;
     // nothing seen yet: weights are 0
-    to8[x] = 8.0f - (m[x] == -__builtin_inff() ? 0.0f : m[x]);
+    less[x] = m[x] == -__builtin_inff() ? 0.0f : m[x];
   }
   if (__any(moved)) {
 #pragma unroll
     for (int x = 0; x < RT; x++) {
-      const float alpha = __builtin_amdgcn_exp2f(r[x].m + (to8[x] - 8.0f));
+      const float alpha = __builtin_amdgcn_exp2f(r[x].m - less[x]);
 #pragma unroll
       for (int d = 0; d < D / 16; d++) r[x].o[d] *= alpha;
       r[x].l *= alpha;
       r[x].m = m[x];
     }
   }
+}
+
+// The weights as two E4M3 parts, 256 p = hi + lo / 16.
+template <int D, int RT>
+__device__ __forceinline__ void softmax_tile(f32x4 (&s)[RT][8], Rows<D> (&r)[RT], float c,
+                                             bool masked, const int (&limit)[RT], i32x8 (&hi)[RT],
+                                             i32x8 (&lo)[RT]) {
+  float less[RT];
+  running_max<D, RT>(s, r, c, masked, limit, [](int t) { return 64 * (t >> 2) + 4 * (t & 3); }, less);
 #pragma unroll
   for (int x = 0; x < RT; x++)
 #pragma unroll
@@ -374,7 +389,7 @@ __device__ __forceinline__ void softmax_tile(f32x4 (&s)[RT][8], Rows<D> (&r)[RT]
       float p[4];
 #pragma unroll
       for (int i = 0; i < 4; i++)
-        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][i], c, to8[x]));
+        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][i], c, 8.0f - less[x]));
       uint32_t a, b;
       split4(p, 1.0f, 0.0625f, a, b);
       hi[x][t] = (int)a;
@@ -421,16 +436,17 @@ __device__ __forceinline__ bool find_block(const AttnArgs &a, int unit, Block &b
 }
 
 // The pages of the four runs of 32 tokens of a tile: lane j holds run j % 4's;
-// past the end the last page.
+// past the end the last page. Page numbers are clamped where they are used:
+// at the load, the clamp would have the wave wait for what it just asked for.
 __device__ __forceinline__ int page_of(const AttnArgs &a, const Block &b, int tile, int lane) {
-  return clamp_page(b.table[min((tile * 128 + 32 * (lane & 3)) >> a.shift, b.last_page)], a.c.pages);
+  return b.table[min((tile * 128 + 32 * (lane & 3)) >> a.shift, b.last_page)];
 }
 struct Runs {
   int a, b, c, d;
 };
-__device__ __forceinline__ Runs runs_of(int mine) {
-  return Runs{__builtin_amdgcn_readlane(mine, 0), __builtin_amdgcn_readlane(mine, 1),
-              __builtin_amdgcn_readlane(mine, 2), __builtin_amdgcn_readlane(mine, 3)};
+__device__ __forceinline__ Runs runs_of(const AttnArgs &a, int mine) {
+  auto page = [&](int j) { return clamp_page(__builtin_amdgcn_readlane(mine, j), a.c.pages); };
+  return Runs{page(0), page(1), page(2), page(3)};
 }
 __device__ __forceinline__ int of_run(const Runs &r, int j) {  // j may differ from lane to lane
   const int lo = (j & 1) ? r.b : r.a, hi = (j & 1) ? r.d : r.c;
@@ -445,7 +461,7 @@ __device__ __forceinline__ int of_run(const Runs &r, int j) {  // j may differ f
 // instead (masked scores are dropped, visible ones make the row NaN) and its
 // values, whose codes are signed zeros, get a finite scale.
 __device__ __forceinline__ uint32_t load_bytes(const AttnArgs &a, int page, int head, int lane) {
-  const int64_t at = (int64_t)page * a.c.heads + head;
+  const int64_t at = (int64_t)clamp_page(page, a.c.pages) * a.c.heads + head;
   return (lane & 4) ? a.c.v_scales[at] : a.c.k_scales[at];
 }
 __device__ __forceinline__ uint32_t bytes_of(uint32_t mine, int l16, int lg) {
@@ -460,6 +476,20 @@ __device__ __forceinline__ uint32_t bytes_of(uint32_t mine, int l16, int lg) {
   const uint32_t even = k[0] | k[2] << 8, odd = k[1] | k[3] << 8;
   const uint32_t v01 = (lg & 1) ? v[1] : v[0], v23 = (lg & 1) ? v[3] : v[2];
   return ((l16 & 8) ? odd : even) | ((lg & 2) ? v23 : v01) << 16;
+}
+
+// The same of one tile for the many-rows kernel: the keys' bytes of the four
+// runs in one word, and run j's value byte.
+__device__ __forceinline__ void page_bytes(uint32_t mine, int j, uint32_t &keys, uint32_t &value) {
+  keys = 0;
+  value = 0;
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    const uint32_t k = (uint32_t)__builtin_amdgcn_readlane((int)mine, e);
+    const uint32_t v = (uint32_t)__builtin_amdgcn_readlane((int)mine, 4 + e);
+    keys |= (v == 255u ? 255u : k) << (8 * e);
+    value = j == e ? (v == 255u ? 127u : v) : value;
+  }
 }
 
 template <int D>
@@ -552,7 +582,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_rows(const AttnAr
   // that one's loads run beside the other's arithmetic
   int mine = t0 + wave < t1 ? page_of(a, b, t0 + wave, lane) : 0;
   for (int tile = t0 + wave; tile < t1; tile += W) {
-    const Runs id = runs_of(mine);
+    const Runs id = runs_of(a, mine);
     const uint32_t bytes = load_bytes(a, mine, head, lane);
     i32x8 kv[8], vv[DT];
     load_keys(tile, id, kv);
@@ -718,10 +748,9 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a) {
 // whose page is wave-uniform; a lane's chunk of values lies in one of four.
 template <int D>
 __device__ __forceinline__ int swz_k(int r) {
-  if constexpr (D == 128) return ((r >> 1) & 1) | (((r >> 4) & 3) << 1);
-  return (r >> 4) & 3;
+  if constexpr (D == 128) return ((r >> 1) & 1) | (((r >> 3) & 3) << 1);
+  return (r >> 3) & 3;
 }
-__device__ __forceinline__ int swz_v(int r) { return (r >> 1) & 7; }
 
 // 16 bytes a lane straight into LDS, lane after lane from `lds` on. In
 // assembly, since the compiler would otherwise make every later LDS read
@@ -730,14 +759,31 @@ __device__ __forceinline__ void load_lds16(const uint8_t *base, uint32_t offset,
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                ::"s"(lds), "v"(offset), "s"(base) : "memory");
 }
-__device__ __forceinline__ void load_lds16(uint64_t address, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-               ::"s"(lds), "v"(address) : "memory");
+
+// 16 codes widened with scale 2^(byte-127). Values past bfloat16's range (no
+// quantizer makes them: they need a byte above 246) become its largest, so
+// that a weight of 0 still drops them.
+__device__ __forceinline__ void widen16(u32x4 c, uint32_t byte, u32x4 (&w)[2]) {
+  const float f = __uint_as_float(byte << 23);
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    w[j >> 1][2 * (j & 1)] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)c[j], f, false));
+    w[j >> 1][2 * (j & 1) + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)c[j], f, true));
+  }
+  if (__any(byte > 246u)) {
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      uint32_t x = w[j >> 2][j & 3];
+      if ((x & 0x7FFFu) == 0x7F80u) x -= 1u;
+      if ((x & 0x7FFF0000u) == 0x7F800000u) x -= 0x10000u;
+      w[j >> 2][j & 3] = x;
+    }
+  }
 }
 
 template <int D>
 __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
-  constexpr int DT = D / 16, RT = 2, S = 128 * D, T = 256;
+  constexpr int DT = D / 16, RT = 2, S = 128 * D;
   constexpr int KL = S / 4096, VL = KL;  // direct loads per thread and tile
   __shared__ __attribute__((aligned(16))) uint8_t ks[2 * S], vs[2 * S];
   // kv heads fastest: the eight XCDs, which are dealt workgroups in turn,
@@ -770,31 +816,32 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
   // a run; every other load's rows swizzle by 64 bytes more) and values
   const int kr = threadIdx.x / (D / 16), kc = (threadIdx.x & (D / 16 - 1)) ^ swz_k<D>(kr);
   const uint32_t koff = (uint32_t)((kr & 31) * D + kc * 16);
-  const int vr = threadIdx.x >> 3, vc = (threadIdx.x & 7) ^ swz_v(vr);
-  const uint32_t voff = (uint32_t)(vr * P + (vc & 1) * 16);
+  const int vr = threadIdx.x >> 3, vc = threadIdx.x & 7;  // row and 16 tokens of values
   const uint32_t klds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)ks + wave * 1024;
-  const uint32_t vlds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)vs + wave * 1024;
+  u32x4 raw[VL];
   auto load = [&](int tile, int buf, const Runs &id) {
+    int64_t page[4];  // wave-uniform: where each run's page begins, in keys and values alike
+#pragma unroll
+    for (int j = 0; j < 4; j++) page[j] = ((int64_t)of_run(id, j) * a.c.heads + head) * PD;
 #pragma unroll
     for (int i = 0; i < KL; i++) {
       const int j = D == 128 ? i : 2 * i + (wave >> 1);  // wave-uniform
-      const uint8_t *base = a.c.k_codes + ((int64_t)of_run(id, j) * a.c.heads + head) * PD +
-                            (int64_t)((tile * 128 + 32 * j) & mask) * D;
-      load_lds16(base, D == 128 && (i & 1) ? koff ^ 64u : koff, klds + buf * S + i * 4096);
+      const int64_t at = D == 128 ? page[i] : (wave >> 1) ? page[2 * i + 1] : page[2 * i];
+      load_lds16(a.c.k_codes + at + (int64_t)((tile * 128 + 32 * j) & mask) * D, koff, klds + buf * S + i * 4096);
     }
-    const int j = vc >> 1;
-    uint64_t v = (uint64_t)a.c.v_codes + ((int64_t)of_run(id, j) * a.c.heads + head) * PD +
-                 (uint32_t)(((tile * 128 + 32 * j) & mask) + (int)voff);
+    const int64_t lo = (vc & 2) ? page[1] : page[0], hi = (vc & 2) ? page[3] : page[2];
+    const uint8_t *v = a.c.v_codes + ((vc & 4) ? hi : lo) + (((tile * 128 + 16 * vc) & mask) + vr * P);
 #pragma unroll
-    for (int i = 0; i < VL; i++, v += 32 * P) load_lds16(v, vlds + buf * S + i * 4096);
+    for (int i = 0; i < VL; i++) raw[i] = *reinterpret_cast<const u32x4 *>(v + 32 * i * P);
   };
-  // operand addresses in LDS: keys' row 64 (t / 4) + 16 (l16 / 4) + 4 (t % 4)
-  // + l16 % 4 of tile t, values' row 16 d + l16
-  const int krow = 16 * (l16 >> 2) + (l16 & 3);
+  // operand addresses in LDS: keys' row 32 (t / 2) + 8 (l16 / 4) + 4 (t % 2) +
+  // l16 % 4 of tile t; values' row 16 d + l16, tokens 32 j + 8 lg ..
+  const int krow = 8 * (l16 >> 2) + (l16 & 3);
   const uint8_t *kp0 = ks + krow * D + 16 * (lg ^ swz_k<D>(krow));
   const uint8_t *kp1 = ks + krow * D + 16 * ((lg + 4) ^ swz_k<D>(krow));
-  const uint8_t *vp0 = vs + l16 * 128 + 16 * (lg ^ swz_v(l16));
-  const uint8_t *vp1 = vs + l16 * 128 + 16 * ((lg + 4) ^ swz_v(l16));
+  const uint8_t *vp[4];
+#pragma unroll
+  for (int j = 0; j < 4; j++) vp[j] = vs + l16 * 256 + 16 * ((4 * j + lg) ^ (j >> 1) ^ l16);
 
   int mine = 0;        // pages of the next tile
   uint32_t bytes = 0;  // scale bytes of this one
@@ -802,15 +849,32 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
     const int now = page_of(a, b, 0, lane);
     bytes = load_bytes(a, now, head, lane);
     mine = page_of(a, b, 1, lane);
-    load(0, 0, runs_of(now));
+    load(0, 0, runs_of(a, now));
   }
   int flip = S;
   for (int tile = 0; tile < tiles; tile++) {
     // this tile's codes, its scale bytes and the next one's pages have
     // arrived, and every wave is done with the other buffer
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    const uint32_t sc = bytes_of(bytes, l16, lg);
-    const Runs id = runs_of(mine);
+    uint32_t sc, mv;
+    page_bytes(bytes, vc >> 1, sc, mv);
+    if (tile * 128 + 128 > b.len) {
+      // the sequence's last tile: what its pages hold past the end may decode
+      // to NaN and is cleared
+      asm volatile("");  // a branch, not arithmetic in every tile
+#pragma unroll
+      for (int i = 0; i < VL; i++) raw[i] = keep_tokens(raw[i], b.len - tile * 128 - 16 * vc);
+    }
+#pragma unroll
+    for (int i = 0; i < VL; i++) {
+      u32x4 w[2];
+      widen16(raw[i], mv, w);
+      const int row = vr + 32 * i;
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+        *reinterpret_cast<u32x4 *>(vs + row * 256 + 16 * ((2 * vc + h) ^ (vc >> 2) ^ (row & 15))) = w[h];
+    }
+    const Runs id = runs_of(a, mine);
     __builtin_amdgcn_sched_barrier(0);
     if (tile + 1 < tiles) {
       bytes = load_bytes(a, mine, head, lane);
@@ -818,70 +882,79 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
       load(tile + 1, (tile + 1) & 1, id);
     }
     auto keys = [&](int t) {
-      const int at = (64 * (t >> 2) + 4 * (t & 3)) * D;
+      const int at = (32 * (t >> 1) + 4 * (t & 1)) * D;
       const u32x4 lo = *reinterpret_cast<const u32x4 *>(kp0 + at);
       if constexpr (D == 64) return join8(lo, lo);
       else return join8(lo, *reinterpret_cast<const u32x4 *>(kp1 + at));
     };
-    auto values = [&](int d) {
-      return join8(*reinterpret_cast<const u32x4 *>(vp0 + 2048 * d),
-                   *reinterpret_cast<const u32x4 *>(vp1 + 2048 * d));
-    };
     // operands are read two tiles ahead
     f32x4 s[RT][8];
     i32x8 f[3] = {keys(0), keys(1)};
+    auto score = [&](auto run) {  // the two tiles of a run of 32 tokens
+      constexpr int J = decltype(run)::value;
 #pragma unroll
-    for (int t = 0; t < 8; t++) {
-      if (t + 2 < 8) f[(t + 2) % 3] = keys(t + 2);
+      for (int t = 2 * J; t < 2 * J + 2; t++) {
+        if (t + 2 < 8) f[(t + 2) % 3] = keys(t + 2);
 #pragma unroll
-      for (int x = 0; x < RT; x++)
-        s[x][t] = t < 4 ? mma<0, 0>(f[t % 3], q[x].v[0], f32x4{0, 0, 0, 0}, sc, q[x].bytes)
-                        : mma<1, 0>(f[t % 3], q[x].v[0], f32x4{0, 0, 0, 0}, sc, q[x].bytes);
-      if constexpr (D == 128) {
+        for (int x = 0; x < RT; x++) s[x][t] = mma<J, 0>(f[t % 3], q[x].v[0], f32x4{0, 0, 0, 0}, sc, q[x].bytes);
+        if constexpr (D == 128) {
 #pragma unroll
-        for (int x = 0; x < RT; x++)
-          s[x][t] = t < 4 ? mma<0, 1>(f[t % 3], q[x].v[1], s[x][t], sc, q[x].bytes)
-                          : mma<1, 1>(f[t % 3], q[x].v[1], s[x][t], sc, q[x].bytes);
+          for (int x = 0; x < RT; x++) s[x][t] = mma<J, 1>(f[t % 3], q[x].v[1], s[x][t], sc, q[x].bytes);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    };
+    score(std::integral_constant<int, 0>());
+    score(std::integral_constant<int, 1>());
+    score(std::integral_constant<int, 2>());
+    score(std::integral_constant<int, 3>());
     // all scores are taken here, while a key operand is at hand (the compiler
     // would move some past the branches below, and keep the operands)
 #pragma unroll
     for (int x = 0; x < RT; x++)
 #pragma unroll
       for (int t = 0; t < 8; t++) asm volatile("" : "+v"(s[x][t]));
-    i32x8 hi[RT], lo[RT];
     int limit[RT];
+    float less[RT];
 #pragma unroll
-    for (int x = 0; x < RT; x++) limit[x] = seen[x] - 1 - tile * 128 - 16 * lg;
-    softmax_tile<D, RT>(s, r, a.scale2, tile * 128 + 128 > b.seen0, limit, hi, lo);
-    if (tile * 128 + 128 > b.len) {
-      // the sequence's last tile: what its pages hold past the end may decode
-      // to NaN and is cleared (16 bytes: one chunk of a row of values)
-      for (int e = threadIdx.x; e < D * 8; e += T) {
-        const int row = e >> 3, c = e & 7, keep = b.len - tile * 128 - 16 * c;
-        u32x4 *p = reinterpret_cast<u32x4 *>(vs + (tile & 1) * S + row * 128 + 16 * (c ^ swz_v(row)));
-        if (keep < 16) *p = keep_tokens(*p, keep);
+    for (int x = 0; x < RT; x++) limit[x] = seen[x] - 1 - tile * 128 - 8 * lg;
+    running_max<D, RT>(s, r, a.scale2, tile * 128 + 128 > b.seen0, limit,
+                       [](int t) { return 32 * (t >> 1) + 4 * (t & 1); }, less);
+    u32x4 p[RT][4];  // weights of tokens 32 j + 8 lg ..
+#pragma unroll
+    for (int x = 0; x < RT; x++)
+#pragma unroll
+      for (int t = 0; t < 8; t++) {
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][i], a.scale2, -less[x]));
+        p[x][t >> 1][2 * (t & 1)] = pack_bf16(e[0], e[1]);
+        p[x][t >> 1][2 * (t & 1) + 1] = pack_bf16(e[2], e[3]);
       }
-      __syncthreads();
-    }
-    f[0] = values(0);
-    f[1] = values(1);
+    // the widened values of every wave are in LDS
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    u32x4 g[2][4];
+    auto values = [&](int d) {
+#pragma unroll
+      for (int j = 0; j < 4; j++) g[d & 1][j] = *reinterpret_cast<const u32x4 *>(vp[j] + 4096 * d);
+    };
+    values(0);
 #pragma unroll
     for (int d = 0; d < DT; d++) {
-      if (d + 2 < DT) f[(d + 2) % 3] = values(d + 2);
+      if (d + 1 < DT) values(d + 1);
 #pragma unroll
-      for (int x = 0; x < RT; x++) r[x].o[d] = mma<2, 0>(f[d % 3], hi[x], r[x].o[d], sc, kParts);
+      for (int j = 0; j < 4; j++)
 #pragma unroll
-      for (int x = 0; x < RT; x++) r[x].o[d] = mma<2, 1>(f[d % 3], lo[x], r[x].o[d], sc, kParts);
+        for (int x = 0; x < RT; x++) r[x].o[d] = mma16(g[d & 1][j], p[x][j], r[x].o[d]);
     }
+    const uint32_t one = 0x3F803F80u;
 #pragma unroll
-    for (int x = 0; x < RT; x++) r[x].l = add_weights(hi[x], lo[x], r[x].l);
+    for (int j = 0; j < 4; j++)
+#pragma unroll
+      for (int x = 0; x < RT; x++) r[x].l = mma16(u32x4{one, one, one, one}, p[x][j], r[x].l);
     kp0 += flip;  // to the other buffer
     kp1 += flip;
-    vp0 += flip;
-    vp1 += flip;
     flip = -flip;
   }
 #pragma unroll
