@@ -438,8 +438,11 @@ __device__ __forceinline__ bool find_block(const AttnArgs &a, int unit, Block &b
 // The pages of the four runs of 32 tokens of a tile: lane j holds run j % 4's;
 // past the end the last page. Page numbers are clamped where they are used:
 // at the load, the clamp would have the wave wait for what it just asked for.
+__device__ __forceinline__ const int32_t *page_at(const AttnArgs &a, const Block &b, int tile, int lane) {
+  return b.table + min((tile * 128 + 32 * (lane & 3)) >> a.shift, b.last_page);
+}
 __device__ __forceinline__ int page_of(const AttnArgs &a, const Block &b, int tile, int lane) {
-  return b.table[min((tile * 128 + 32 * (lane & 3)) >> a.shift, b.last_page)];
+  return *page_at(a, b, tile, lane);
 }
 struct Runs {
   int a, b, c, d;
@@ -460,9 +463,9 @@ __device__ __forceinline__ int of_run(const Runs &r, int j) {  // j may differ f
 // are NaN must reach only the rows that see it: its keys are made NaN
 // instead (masked scores are dropped, visible ones make the row NaN) and its
 // values, whose codes are signed zeros, get a finite scale.
-__device__ __forceinline__ uint32_t load_bytes(const AttnArgs &a, int page, int head, int lane) {
+__device__ __forceinline__ const uint8_t *byte_at(const AttnArgs &a, int page, int head, int lane) {
   const int64_t at = (int64_t)clamp_page(page, a.c.pages) * a.c.heads + head;
-  return (lane & 4) ? a.c.v_scales[at] : a.c.k_scales[at];
+  return ((lane & 4) ? a.c.v_scales : a.c.k_scales) + at;
 }
 __device__ __forceinline__ uint32_t bytes_of(uint32_t mine, int l16, int lg) {
   uint32_t k[4], v[4];
@@ -492,15 +495,14 @@ __device__ __forceinline__ void page_bytes(uint32_t mine, int j, uint32_t &keys,
   }
 }
 
-template <int D>
-__device__ __forceinline__ void scores(const i32x8 *kv, const Query<D> &q, uint32_t sc,
+// Scores of half a tile (64 tokens), whose keys' bytes are byte H of sc.
+template <int D, int H>
+__device__ __forceinline__ void scores(const i32x8 (&kv)[4], const Query<D> &q, uint32_t sc,
                                        f32x4 (&s)[8]) {
 #pragma unroll
-  for (int t = 0; t < 8; t++) {
-    const f32x4 z = {0, 0, 0, 0};
-    s[t] = t < 4 ? mma<0, 0>(kv[t], q.v[0], z, sc, q.bytes) : mma<1, 0>(kv[t], q.v[0], z, sc, q.bytes);
-    if constexpr (D == 128)
-      s[t] = t < 4 ? mma<0, 1>(kv[t], q.v[1], s[t], sc, q.bytes) : mma<1, 1>(kv[t], q.v[1], s[t], sc, q.bytes);
+  for (int t = 0; t < 4; t++) {
+    s[4 * H + t] = mma<H, 0>(kv[t], q.v[0], f32x4{0, 0, 0, 0}, sc, q.bytes);
+    if constexpr (D == 128) s[4 * H + t] = mma<H, 1>(kv[t], q.v[1], s[4 * H + t], sc, q.bytes);
   }
 }
 
@@ -513,13 +515,53 @@ __device__ __forceinline__ f32x4 add_weights(i32x8 hi, i32x8 lo, f32x4 l) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ones, lo, l, 4, 0, 2, (int)kParts, 1, (int)kParts);
 }
 
+// 16 bytes a lane straight into LDS, lane after lane from `lds` on. In
+// assembly, since the compiler would otherwise make every later LDS read
+// wait for it; the kernel waits where it must. No output register.
+__device__ __forceinline__ void load_lds16(const uint8_t *base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               ::"s"(lds), "v"(offset), "s"(base) : "memory");
+}
+__device__ __forceinline__ void load_lds16(uint64_t address, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt"
+               ::"s"(lds), "v"(address) : "memory");
+}
+// A word, or a byte widened to one, a lane.
+__device__ __forceinline__ void load_lds4(const int32_t *p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p) : "memory");
+}
+__device__ __forceinline__ void load_lds1(const uint8_t *p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, off" ::"s"(lds), "v"(p) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)p;
+}
+
 // Few rows: a workgroup of four waves takes up to 16 RT rows of one sequence
 // and kv head and one split of its keys; wave w takes tiles w, w + 4, ....
+//
+// A tile comes in four parts (the keys of 64 tokens twice, then the values of
+// half the dims twice), whole rows straight into LDS. A wave has room of its
+// own for two parts: as soon as one has been read the one after the next is
+// asked for in its place, so that some part is always on its way and no wave
+// waits for another. Page numbers and scale bytes come the same way: a load
+// into a register would have the compiler wait for everything asked for
+// since. Keys lie as rows of D bytes (tokens), values as rows of
+// 128 bytes (dims); the 16-byte chunk c of row r sits at position c ^ f(r), f
+// chosen so that the 16 rows of a read fall on different banks, the chunks
+// being swapped on the global side.
+template <int D>
+__device__ __forceinline__ int swz_rows(int r) {
+  if constexpr (D == 128) return ((r >> 1) & 1) | (((r >> 4) & 3) << 1);
+  return (r >> 4) & 3;
+}
 template <int D, int RT>
-__global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_rows(const AttnArgs a) {
-  constexpr int DT = D / 16, W = 4;
-  __shared__ float merge_o[W][16][D + 4];
+__global__ __launch_bounds__(256, 2) void k_attn_rows(const AttnArgs a) {
+  constexpr int DT = D / 16, W = 4, S = 128 * D, L = S / 2048;  // bytes of a tile's keys, loads of a part
+  __shared__ __attribute__((aligned(16))) uint8_t codes[W][S];
+  __shared__ uint32_t pages[W][64], bytes[W][64];
   __shared__ float merge_ml[W][16][2];
+  static_assert(S >= 16 * (D + 4) * 4, "the waves' sums go where the codes were");
   Block b;
   if (!find_block(a, blockIdx.x, b)) return;
   const int head = blockIdx.y, split = blockIdx.z;
@@ -531,6 +573,46 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_rows(const AttnAr
   const int t0 = split * a.chunk, t1 = split + 1 == a.splits ? tiles : min(tiles, t0 + a.chunk);
   if (split > 0 && t0 >= tiles) return;  // the sum takes only splits that exist
   const int rows = b.count * a.group;
+
+  const int64_t PD = (int64_t)a.c.page * D;
+  const int mask = a.c.page - 1, P = a.c.page;
+  // loads: 64 / (D / 16) rows of keys each, all of one run of 32 tokens, and 8
+  // rows of values, whose chunk lies in one of four runs
+  constexpr int KR = 1024 / D;  // rows of a load
+  uint8_t *own = codes[wave];
+  const uint32_t lds = lds_address(own);
+  const int kr = lane / (D / 16), kc = lane & (D / 16 - 1);
+  auto load_keys = [&](int tile, const Runs &id, int part) {
+#pragma unroll
+    for (int i = part * L; i < part * L + L; i++) {
+      const int j = i * KR >> 5;  // run
+      const uint8_t *base = a.c.k_codes + ((int64_t)of_run(id, j) * a.c.heads + head) * PD +
+                            (int64_t)((tile * 128 + i * KR) & mask) * D;
+      load_lds16((uint64_t)base + (uint32_t)(kr * D + (kc ^ swz_rows<D>(i * KR + kr)) * 16), lds + i * 1024);
+    }
+  };
+  const int vr = lane >> 3;
+  auto load_values = [&](int tile, const Runs &id, int part) {
+#pragma unroll
+    for (int h = 0; h < 2; h++) {  // rows 16 n + 8 h ..: one swizzle
+      const int vc = (lane & 7) ^ (((vr + 8 * h) >> 1) & 7);
+      uint64_t v = (uint64_t)a.c.v_codes + ((int64_t)of_run(id, vc >> 1) * a.c.heads + head) * PD +
+                   (uint32_t)(((tile * 128 + 16 * vc) & mask) + (vr + 8 * h + part * (D / 2)) * P);
+#pragma unroll
+      for (int i = 0; i < L / 2; i++, v += 16 * P) load_lds16(v, lds + part * (S / 2) + (2 * i + h) * 1024);
+    }
+  };
+  // a part has landed: only the L loads of the next one are younger
+  auto landed = [] { asm volatile("s_waitcnt vmcnt(%0)" ::"i"(L) : "memory"); };
+  // what was read is in registers: the part's place may be written
+  auto taken = [] { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
+  // operand addresses: keys' row 64 (t / 4) + 16 (l16 / 4) + 4 (t % 4) + l16 % 4
+  // of tile t, values' row 16 d + l16
+  const int krow = 16 * (l16 >> 2) + (l16 & 3);
+  const uint8_t *kp0 = own + krow * D + 16 * (lg ^ swz_rows<D>(krow));
+  const uint8_t *kp1 = own + krow * D + 16 * ((lg + 4) ^ swz_rows<D>(krow));
+  const uint8_t *vp0 = own + l16 * 128 + 16 * (lg ^ ((l16 >> 1) & 7));
+  const uint8_t *vp1 = own + l16 * 128 + 16 * ((lg + 4) ^ ((l16 >> 1) & 7));
 
   Query<D> q[RT];
   Rows<D> r[RT];
@@ -544,81 +626,95 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_rows(const AttnAr
                              ((int64_t)head * a.group + row % a.group) * D, lg);
     r[x].clear();
   }
-  const int64_t PD = (int64_t)a.c.page * D;
-  const int mask = a.c.page - 1;
-  // keys: this lane's row (token) of tile t, in the page of run 2 (t / 4) + l16 / 8
-  auto load_keys = [&](int tile, const Runs &id, i32x8 (&kv)[8]) {
+  // ask for what comes before a tile's codes: its scale bytes, and the pages of
+  // the wave's tile after it
+  auto prepare = [&](int tile, int now) {
+    load_lds1(byte_at(a, now, head, lane), lds_address(bytes[wave]));
+    load_lds4(page_at(a, b, tile + W, lane), lds_address(pages[wave]));
+  };
+  Runs id = {0, 0, 0, 0};
+  if (t0 + wave < t1) {
+    const int now = page_of(a, b, t0 + wave, lane);
+    id = runs_of(a, now);
+    prepare(t0 + wave, now);
+    load_keys(t0 + wave, id, 0);
+    load_keys(t0 + wave, id, 1);
+  }
+  for (int tile = t0 + wave; tile < t1; tile += W) {
+    const int next = tile + W;
+    f32x4 s[RT][8];
+    uint32_t sc = 0;
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-      const int tok = tile * 128 + 64 * h + 16 * (l16 >> 2) + (l16 & 3);
-      const uint8_t *p = a.c.k_codes +
-                         ((int64_t)of_run(id, 2 * h + (l16 >> 3)) * a.c.heads + head) * PD +
-                         (tok & mask) * D + 16 * lg;
+      landed();
+      if (h == 0) sc = bytes_of(bytes[wave][lane], l16, lg);
+      i32x8 kv[4];
 #pragma unroll
       for (int t = 0; t < 4; t++) {
-        const u32x4 x = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + 4 * t * D));
-        if constexpr (D == 128)
-          kv[4 * h + t] = join8(x, __builtin_nontemporal_load(
-                                       reinterpret_cast<const u32x4 *>(p + 4 * t * D + 64)));
-        else
-          kv[4 * h + t] = join8(x, x);
+        const int at = (64 * h + 4 * t) * D;
+        const u32x4 lo = *reinterpret_cast<const u32x4 *>(kp0 + at);
+        if constexpr (D == 64) kv[t] = join8(lo, lo);
+        else kv[t] = join8(lo, *reinterpret_cast<const u32x4 *>(kp1 + at));
+      }
+      taken();
+      load_values(tile, id, h);
+#pragma unroll
+      for (int x = 0; x < RT; x++) {
+        if (h == 0) scores<D, 0>(kv, q[x], sc, s[x]);
+        else scores<D, 1>(kv, q[x], sc, s[x]);
       }
     }
-  };
-  auto load_values = [&](int tile, const Runs &id, i32x8 (&vv)[DT]) {
-    const int dim = 4 * DT * (l16 >> 2) + (l16 & 3);
-    const uint8_t *p[2];
-#pragma unroll
-    for (int h = 0; h < 2; h++)
-      p[h] = a.c.v_codes + ((int64_t)of_run(id, 2 * h + (lg >> 1)) * a.c.heads + head) * PD +
-             dim * a.c.page + ((tile * 128 + 64 * h + 16 * lg) & mask);
-#pragma unroll
-    for (int d = 0; d < DT; d++)
-      vv[d] = join8(
-          __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p[0] + 4 * d * a.c.page)),
-          __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p[1] + 4 * d * a.c.page)));
-  };
-  // all of a tile's loads are started at once; two waves share a SIMD, so
-  // that one's loads run beside the other's arithmetic
-  int mine = t0 + wave < t1 ? page_of(a, b, t0 + wave, lane) : 0;
-  for (int tile = t0 + wave; tile < t1; tile += W) {
-    const Runs id = runs_of(a, mine);
-    const uint32_t bytes = load_bytes(a, mine, head, lane);
-    i32x8 kv[8], vv[DT];
-    load_keys(tile, id, kv);
-    load_values(tile, id, vv);
-    if (tile + W < t1) mine = page_of(a, b, tile + W, lane);
-    const uint32_t sc = bytes_of(bytes, l16, lg);
-    f32x4 s[RT][8];
     i32x8 hi[RT], lo[RT];
     int limit[RT];
 #pragma unroll
-    for (int x = 0; x < RT; x++) {
-      scores<D>(kv, q[x], sc, s[x]);
-      limit[x] = seen[x] - 1 - tile * 128 - 16 * lg;
-    }
+    for (int x = 0; x < RT; x++) limit[x] = seen[x] - 1 - tile * 128 - 16 * lg;
     softmax_tile<D, RT>(s, r, a.scale2, tile * 128 + 128 > b.seen0, limit, hi, lo);
-    if (tile * 128 + 128 > b.len) {
-      // the sequence's last tile: what its pages hold past the end may decode
-      // to NaN and is cleared
 #pragma unroll
-      for (int d = 0; d < DT; d++) {
-        const u32x4 v0 = {(uint32_t)vv[d][0], (uint32_t)vv[d][1], (uint32_t)vv[d][2], (uint32_t)vv[d][3]};
-        const u32x4 v1 = {(uint32_t)vv[d][4], (uint32_t)vv[d][5], (uint32_t)vv[d][6], (uint32_t)vv[d][7]};
-        const int from = b.len - tile * 128 - 16 * lg;
-        vv[d] = join8(keep_tokens(v0, from), keep_tokens(v1, from - 64));
+    for (int h = 0; h < 2; h++) {
+      if (h == 0 || next < t1) landed();
+      else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      i32x8 vv[DT / 2];
+#pragma unroll
+      for (int d = 0; d < DT / 2; d++)
+        vv[d] = join8(*reinterpret_cast<const u32x4 *>(vp0 + h * (S / 2) + 2048 * d),
+                      *reinterpret_cast<const u32x4 *>(vp1 + h * (S / 2) + 2048 * d));
+      taken();
+      if (next < t1) {
+        if (h == 0) {
+          const int now = (int)pages[wave][lane];
+          id = runs_of(a, now);
+          prepare(next, now);
+        }
+        load_keys(next, id, h);
       }
+      if (tile * 128 + 128 > b.len) {
+        // the sequence's last tile: what its pages hold past the end may decode
+        // to NaN and is cleared
+#pragma unroll
+        for (int d = 0; d < DT / 2; d++) {
+          const u32x4 v0 = {(uint32_t)vv[d][0], (uint32_t)vv[d][1], (uint32_t)vv[d][2], (uint32_t)vv[d][3]};
+          const u32x4 v1 = {(uint32_t)vv[d][4], (uint32_t)vv[d][5], (uint32_t)vv[d][6], (uint32_t)vv[d][7]};
+          const int from = b.len - tile * 128 - 16 * lg;
+          vv[d] = join8(keep_tokens(v0, from), keep_tokens(v1, from - 64));
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < RT; x++)
+#pragma unroll
+        for (int d = 0; d < DT / 2; d++) {
+          f32x4 &o = r[x].o[h * (DT / 2) + d];
+          o = mma<2, 0>(vv[d], hi[x], o, sc, kParts);
+          o = mma<2, 1>(vv[d], lo[x], o, sc, kParts);
+        }
     }
 #pragma unroll
-    for (int x = 0; x < RT; x++) {
-#pragma unroll
-      for (int d = 0; d < DT; d++) {
-        r[x].o[d] = mma<2, 0>(vv[d], hi[x], r[x].o[d], sc, kParts);
-        r[x].o[d] = mma<2, 1>(vv[d], lo[x], r[x].o[d], sc, kParts);
-      }
-      r[x].l = add_weights(hi[x], lo[x], r[x].l);
-    }
+    for (int x = 0; x < RT; x++) r[x].l = add_weights(hi[x], lo[x], r[x].l);
   }
+  // no load may land on the sums below
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  auto merge_o = [&](int w, int row, int d) -> float & {
+    return reinterpret_cast<float *>(codes[w])[row * (D + 4) + d];
+  };
   // merge the four waves, 16 rows at a time
 #pragma unroll
   for (int x = 0; x < RT; x++) {
@@ -626,7 +722,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_rows(const AttnAr
 #pragma unroll
     for (int d = 0; d < DT; d++)
 #pragma unroll
-      for (int e = 0; e < 4; e++) merge_o[wave][l16][4 * DT * lg + 4 * d + e] = r[x].o[d][e];
+      for (int e = 0; e < 4; e++) merge_o(wave, l16, 16 * d + 4 * lg + e) = r[x].o[d][e];
     if (lg == 0) {
       merge_ml[wave][l16][0] = r[x].m;
       merge_ml[wave][l16][1] = r[x].l[0];
@@ -646,7 +742,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_rows(const AttnAr
       const float f = __builtin_amdgcn_exp2f(merge_ml[w][row][0] - ms);
       l += f * merge_ml[w][row][1];
 #pragma unroll
-      for (int e = 0; e < D / 16; e++) o[e] += f * merge_o[w][row][d0 + e];
+      for (int e = 0; e < D / 16; e++) o[e] += f * merge_o(w, row, d0 + e);
     }
     const int rr = 16 * x + row;
     if (rr < rows) {
@@ -752,14 +848,6 @@ __device__ __forceinline__ int swz_k(int r) {
   return (r >> 3) & 3;
 }
 
-// 16 bytes a lane straight into LDS, lane after lane from `lds` on. In
-// assembly, since the compiler would otherwise make every later LDS read
-// wait for it; the kernel waits where it must. No output register.
-__device__ __forceinline__ void load_lds16(const uint8_t *base, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               ::"s"(lds), "v"(offset), "s"(base) : "memory");
-}
-
 // 16 codes widened with scale 2^(byte-127). Values past bfloat16's range (no
 // quantizer makes them: they need a byte above 246) become its largest, so
 // that a weight of 0 still drops them.
@@ -847,7 +935,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
   uint32_t bytes = 0;  // scale bytes of this one
   if (tiles > 0) {
     const int now = page_of(a, b, 0, lane);
-    bytes = load_bytes(a, now, head, lane);
+    bytes = *byte_at(a, now, head, lane);
     mine = page_of(a, b, 1, lane);
     load(0, 0, runs_of(a, now));
   }
@@ -877,7 +965,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
     const Runs id = runs_of(a, mine);
     __builtin_amdgcn_sched_barrier(0);
     if (tile + 1 < tiles) {
-      bytes = load_bytes(a, mine, head, lane);
+      bytes = *byte_at(a, mine, head, lane);
       mine = page_of(a, b, tile + 2, lane);
       load(tile + 1, (tile + 1) & 1, id);
     }
