@@ -442,7 +442,9 @@ mx_status_t mx_kv_append(const void *k, const void *v, mx_dtype_t dtype, int64_t
  * appended: new token j of n sees keys 0 .. lengths[i] - n + j; one that sees
  * none gives zeros. out [tokens, q_heads, dim] bf16, contiguous:
  * softmax(scale q.k) v with fp32 scores, maxima and sums; q is used exactly,
- * the softmax's weights with a relative error of at most 2^-9. scale > 0.
+ * the softmax's weights with a relative error of at most 2^-8, and their sum is
+ * that of the weights as used. Cached values past bfloat16's range (a byte
+ * above 246, which no quantizer here makes) may count as its largest. scale > 0.
  * max_length: an upper bound on lengths that the launch is planned for (0:
  * width * page); a larger length is still right, only slower. workspace:
  * mx_kv_attention_workspace_size(...) bytes, 16-byte aligned (partial results

@@ -8,23 +8,28 @@
 // the new tokens need; where it grows, the kept codes are re-rounded to it.
 // One workgroup per (sequence's page, head).
 //
-// Attention, o = sum_j softmax_j(scale q.k_j) v_j, runs on the 8-bit matrix
-// cores without widening the cache. v_mfma_scale_f32_16x16x128_f8f6f4 takes
-// the cache's codes and bytes as they are; the other operand (q, then the
-// softmax's weights p) is split into two E4M3 numbers, x = hi + lo, whose
-// products land in the same accumulator: q's eight significant bits are held
-// exactly, p is off by at most 2^-9 of itself (bf16: 2^-8; measured, the
-// output's error is 1.07 of bf16 rounding's own). Scores are taken
-// transposed (tokens are the accumulator's rows), so that the weights come
-// out in the very lanes and order in which the second product wants them:
-// with g = lane / 16, tile t (of 16 rows) and accumulator i hold token
-// 64 (t / 4) + 16 g + 4 (t % 4) + i of a run of 128, and the second product's
-// lane holds tokens 16 g .. + 15 and 64 + 16 g .. + 15. The weights' sum is a
-// ninth product with a row of ones. Maxima, sums and accumulators are fp32.
+// Attention, o = sum_j softmax_j(scale q.k_j) v_j, takes the cache's keys to
+// the 8-bit matrix cores as they are: v_mfma_scale_f32_16x16x128_f8f6f4
+// multiplies codes and bytes. q is split into two E4M3 numbers, x = hi + lo,
+// whose products land in the same accumulator: its eight significant bits are
+// held exactly. Scores are taken transposed (tokens are the accumulator's
+// rows), so that the weights p come out in the very lanes and order in which
+// the second product wants them. Maxima, sums and accumulators are fp32; the
+// weights' sum is a product with a row of ones, of the weights as rounded.
 //
-// Two kernels: few rows (single tokens) read the cache straight into
-// registers, one wave per 128 tokens at a time, the sequence split over
-// workgroups; many rows (prompts) share tiles of 128 tokens through LDS.
+// Two kernels. Few rows (single tokens) are bound by reading the cache: one
+// wave per 128 tokens at a time, the sequence split over workgroups, and the
+// second product is an 8-bit one too, the weights split as q is (off by at
+// most 2^-9 of themselves). With g = lane / 16, tile t (of 16 rows) and
+// accumulator i hold token 64 (t / 4) + 16 g + 4 (t % 4) + i of 128, and the
+// second product's lane holds tokens 16 g .. + 15 and 64 + 16 g .. + 15.
+//
+// Many rows (prompts) share tiles of 128 tokens through LDS and are bound by
+// instruction issue: per 32 rows and 128 tokens, 2,200 cycles of products
+// beside 2,400 of vector arithmetic, half of it the exponentials. There the
+// workgroup widens the values to bfloat16 once (exact), and the weights are
+// rounded to it (2^-8 of themselves): one conversion where the split takes
+// three and a subtraction. Token 32 (t / 2) + 8 g + 4 (t % 2) + i.
 #include <algorithm>
 
 #include "mx_layer.h"
@@ -546,17 +551,24 @@ __device__ __forceinline__ uint32_t lds_address(const void *p) {
 // asked for in its place, so that some part is always on its way and no wave
 // waits for another. Page numbers and scale bytes come the same way: a load
 // into a register would have the compiler wait for everything asked for
-// since. Keys lie as rows of D bytes (tokens), values as rows of
-// 128 bytes (dims); the 16-byte chunk c of row r sits at position c ^ f(r), f
-// chosen so that the 16 rows of a read fall on different banks, the chunks
-// being swapped on the global side.
+// since. Keys lie as rows of D bytes (tokens), values as rows of 128 bytes
+// (dims); the 16-byte chunk c of row r sits at position c ^ f(r), f chosen so
+// that the 16 rows of a read fall on different banks, the chunks being swapped
+// on the global side.
+//
+// Bound by the cache's bytes: 16 sequences of up to 65,000 tokens, 8 kv heads
+// of 128 dims, 1.19 GB in 220 us (5.4 TB/s; a plain reading of as much reaches
+// 7.0). Loads into registers, a tile at a time, took 250: half of a line per
+// request, and nothing on its way while a wave computes.
 template <int D>
 __device__ __forceinline__ int swz_rows(int r) {
   if constexpr (D == 128) return ((r >> 1) & 1) | (((r >> 4) & 3) << 1);
   return (r >> 4) & 3;
 }
+// (32 rows of 128 dims: one wave a SIMD, two would spill: 93 and 113 us for 16
+// sequences of 4 tokens in 16,000, 8 query heads to a kv head)
 template <int D, int RT>
-__global__ __launch_bounds__(256, 2) void k_attn_rows(const AttnArgs a) {
+__global__ __launch_bounds__(256, D == 128 && RT == 2 ? 1 : 2) void k_attn_rows(const AttnArgs a) {
   constexpr int DT = D / 16, W = 4, S = 128 * D, L = S / 2048;  // bytes of a tile's keys, loads of a part
   __shared__ __attribute__((aligned(16))) uint8_t codes[W][S];
   __shared__ uint32_t pages[W][64], bytes[W][64];
@@ -832,16 +844,23 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a) {
   }
 }
 
-// Many rows: four waves of 32 rows share tiles of 128 tokens through LDS,
-// loaded directly and double-buffered; two workgroups share a compute unit,
-// so that one's softmax runs beside the other's products. Rows are `tokens x
-// group` of one kv head.
+// Many rows: four waves of 32 rows share tiles of 128 tokens through LDS; two
+// workgroups share a compute unit, so that one's softmax runs beside the
+// other's products. Rows are `tokens x group` of one kv head. Keys are loaded
+// directly, double-buffered; values go through registers, where they are
+// widened, a tile ahead of use, into one buffer (a second barrier a tile).
 //
-// Keys lie in LDS as rows of D bytes (tokens), values as rows of 128 bytes
+// Keys lie in LDS as rows of D bytes (tokens), values as rows of 256 bytes
 // (dims). The 16-byte chunk c of row r sits at position c ^ f(r), f chosen so
-// that the 16 rows of a read fall on different banks; the chunks are swapped
-// on the global side. A load of keys covers rows of one run of 32 tokens,
-// whose page is wave-uniform; a lane's chunk of values lies in one of four.
+// that the 16 rows of a read fall on different banks (the keys' chunks are
+// swapped on the global side); for values c ^ (c / 8) ^ r, so that the eight
+// even chunks that a row's lanes write do too. A load of keys covers rows of
+// one run of 32 tokens, whose page is wave-uniform; a lane's chunk of values
+// lies in one of four.
+//
+// 2 x 2048 tokens of 8,192, 32 query heads on 8 of 128 dims: 437 to 480 us
+// (0.9 PFLOP/s), heads of 64: 326 us. With the split weights and 8-bit values
+// 510 and 381.
 template <int D>
 __device__ __forceinline__ int swz_k(int r) {
   if constexpr (D == 128) return ((r >> 1) & 1) | (((r >> 3) & 3) << 1);
@@ -1086,8 +1105,10 @@ static AttnPlan attn_plan(int64_t tokens, int batch, int q_heads, int heads, int
   p.chunk = tiles > 0 ? tiles : 1;
   p.splits = 1;
   if (p.few) {
-    // enough workgroups to fill the card four times over, and at least two
-    // tiles a wave: below that the sum over splits costs more than it saves
+    // enough workgroups to fill the card four times over, since sequences
+    // shorter than the longest leave splits empty (16 ragged ones of up to
+    // 65,000: 220 us; twice over 238, eight times 224), and at least two tiles
+    // a wave: below that the sum over splits costs more than it saves
     const int64_t base = std::max<int64_t>(1, (int64_t)batch * heads);
     const int64_t want = std::max<int64_t>(1, 2048 / base);
     const int64_t c = std::max<int64_t>(8, (tiles + want - 1) / want);
