@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import NamedTuple
 
 import torch
@@ -123,6 +124,21 @@ def declare(lib) -> None:
 
 
 # ---- tensor helpers --------------------------------------------------------
+#
+# They run once per layer and token, where the host's time counts: small
+# allocations go by the call that is fastest here, and the two structures are
+# packed as bytes.
+
+_pack_cache = struct.Struct("@PPPPqiii4x").pack
+_pack_batch = struct.Struct("@PPPqii").pack
+
+
+def _bytes(like, rows: int, cols: int, two: bool):
+    """uint8 [rows, cols] on like's device, or in like's leading shape."""
+    if two:
+        return torch.empty(rows, cols, dtype=torch.uint8, device=like.device)
+    return torch.empty((*like.shape[:-1], cols), dtype=torch.uint8, device=like.device)
+
 
 def _matrix(x, name: str, dtypes=_DTYPES):
     """A contiguous GPU tensor [..., k], k a multiple of 32: (rows, k)."""
@@ -140,8 +156,7 @@ def _matrix(x, name: str, dtypes=_DTYPES):
 
 
 def _want(t, name: str, dev, dtype, numel: int):
-    """_need() with its outcome found in fewer steps where all is well (these
-    helpers run once per layer and token, where the host's time counts)."""
+    """_need() with its outcome found in fewer steps where all is well."""
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == numel
             and t.device == dev and t.is_contiguous()):
         _need(t, name, dev, dtype, numel)
@@ -175,15 +190,13 @@ def _scratch(size: int, device):
 
 def _quantize_blocks(x, block, rows_too: bool, columns: bool):
     rows, k = _matrix(x, "x")
-    nb, dev = -(-k // _block(block)), x.device
-
-    def u8(*shape):
-        return torch.empty(shape, dtype=torch.uint8, device=dev)
-
-    lead = tuple(x.shape[:-1])
-    codes, scales = (u8(*lead, k), u8(*lead, nb)) if rows_too else (None, None)
-    codes_t, scales_t = ((u8(k, -(-rows // 32) * 32), u8(k, -(-rows // block)))
-                         if columns else (None, None))
+    nb, dev, two = -(-k // _block(block)), x.device, x.dim() == 2
+    codes = scales = codes_t = scales_t = None
+    if rows_too:
+        codes, scales = torch.empty_like(x, dtype=torch.uint8), _bytes(x, rows, nb, two)
+    if columns:
+        codes_t = torch.empty(k, -(-rows // 32) * 32, dtype=torch.uint8, device=dev)
+        scales_t = torch.empty(k, -(-rows // block), dtype=torch.uint8, device=dev)
     _call(dev, load_library().mx_quantize_mxfp8_blocks, x.data_ptr(), _DTYPES[x.dtype], rows, k,
           block, _ptr(codes), _ptr(scales), _ptr(codes_t), _ptr(scales_t))
     return codes, scales, codes_t, scales_t
@@ -217,7 +230,7 @@ def rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     rows, k = _matrix(x, "x")
     dev = x.device
     _want(weight, "weight", dev, x.dtype, k)
-    nb, lead = -(-k // _block(block)), x.shape[:-1]
+    nb = -(-k // _block(block))
     if residual is not None:
         _want(residual, "residual", dev, x.dtype, x.numel())
         if out_h is None:
@@ -226,8 +239,7 @@ def rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
             _want(out_h, "out_h", dev, x.dtype, x.numel())
     elif out_h is not None:
         raise ValueError("out_h needs a residual")
-    codes = torch.empty(x.shape, dtype=torch.uint8, device=dev)
-    scales = torch.empty((*lead, nb), dtype=torch.uint8, device=dev)
+    codes, scales = torch.empty_like(x, dtype=torch.uint8), _bytes(x, rows, nb, x.dim() == 2)
     _call(dev, load_library().mx_rmsnorm_mxfp8, x.data_ptr(), _ptr(residual), weight.data_ptr(),
           _DTYPES[x.dtype], rows, k, eps, block, codes.data_ptr(), scales.data_ptr(), _ptr(out_h))
     return codes, scales, out_h
@@ -273,7 +285,8 @@ def matmul_mxfp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sca
     _want(a_scales, "a_scales", dev, torch.uint8, m * nb)
     _want(b_scales, "b_scales", dev, torch.uint8, n * nb)
     if out is None:
-        out = torch.empty(a.shape[:-1] + (n,), dtype=dtype, device=dev)
+        out = (torch.empty(m, n, dtype=dtype, device=dev) if a.dim() == 2
+               else torch.empty(a.shape[:-1] + (n,), dtype=dtype, device=dev))
     else:
         _want(out, "out", dev, dtype, m * n)
     lib, cd = load_library(), _DTYPES[dtype]
@@ -293,12 +306,14 @@ def _heads_of(t, name: str, dev, dtypes):
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, dim]")
     tokens, heads, dim = t.shape
-    if (dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim):
+    step, head, one = t.stride()
+    if (dim > 1 and one != 1) or (heads > 1 and head != dim):
         raise ValueError(f"{name}'s heads must lie next to each other")
-    return tokens, heads, dim, t.stride(0) if tokens > 1 else heads * dim
+    return tokens, heads, dim, step if tokens > 1 else heads * dim
 
 
 def _cache_of(cache: KVCache):
+    """(device, heads, dim, page, mx_kv_cache_t)"""
     k, ks, v, vs = cache
     dev = getattr(k, "device", None)
     _need(k, "k_codes", dev, torch.uint8)
@@ -310,18 +325,20 @@ def _cache_of(cache: KVCache):
         raise ValueError(f"v_codes must be {(pages, heads, dim, page)}, got {tuple(v.shape)}")
     _want(ks, "k_scales", dev, torch.uint8, pages * heads)
     _want(vs, "v_scales", dev, torch.uint8, pages * heads)
-    return dev, MxKVCache(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), pages, heads,
-                          dim, page)
+    return dev, heads, dim, page, _pack_cache(k.data_ptr(), ks.data_ptr(), v.data_ptr(),
+                                              vs.data_ptr(), pages, heads, dim, page)
 
 
 def _batch_of(dev, table, cu, lengths, tokens):
+    """(batch, width, mx_kv_batch_t)"""
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be [batch, width]")
     batch, width = table.shape
     _want(table, "table", dev, torch.int32, batch * width)
     _want(cu, "cu", dev, torch.int32, batch + 1)
     _want(lengths, "lengths", dev, torch.int32, batch)
-    return MxKVBatch(table.data_ptr(), cu.data_ptr(), lengths.data_ptr(), tokens, batch, width)
+    return batch, width, _pack_batch(table.data_ptr(), cu.data_ptr(), lengths.data_ptr(), tokens,
+                                     batch, width)
 
 
 def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor,
@@ -330,16 +347,16 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Ten
     projection's rows are fine) to the cache, in place. table int32 [batch,
     width]: each sequence's pages; cu int32 [batch + 1]: where its new tokens
     start; lengths int32 [batch]: what it held before."""
-    dev, c = _cache_of(cache)
+    dev, held_heads, held_dim, _, c = _cache_of(cache)
     tokens, heads, dim, stride = _heads_of(k, "k", dev, _DTYPES)
-    if _heads_of(v, "v", dev, (k.dtype,))[:3] != (tokens, heads, dim):
+    v_tokens, v_heads, v_dim, v_stride = _heads_of(v, "v", dev, (k.dtype,))
+    if v_tokens != tokens or v_heads != heads or v_dim != dim:
         raise ValueError("k and v must have one shape")
-    if (heads, dim) != (c.heads, c.dim):
-        raise ValueError(f"the cache holds {c.heads} heads of {c.dim}, got {heads} of {dim}")
-    b = _batch_of(dev, table, cu, lengths, tokens)
-    v_stride = v.stride(0) if tokens > 1 else heads * dim
+    if heads != held_heads or dim != held_dim:
+        raise ValueError(f"the cache holds {held_heads} heads of {held_dim}, got {heads} of {dim}")
+    b = _batch_of(dev, table, cu, lengths, tokens)[2]
     _call(dev, load_library().mx_kv_append, k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], stride,
-          v_stride, ctypes.byref(c), ctypes.byref(b))
+          v_stride, c, b)
 
 
 def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, cu: torch.Tensor,
@@ -349,23 +366,22 @@ def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, cu: torch
     [tokens, q_heads, dim]; lengths int32 [batch] count each sequence's new
     tokens too. scale defaults to 1 / sqrt(dim); max_length bounds the lengths
     (0: what the table has room for) and only steers the launch."""
-    dev, c = _cache_of(cache)
+    dev, heads, held_dim, page, c = _cache_of(cache)
     tokens, q_heads, dim, stride = _heads_of(q, "q", dev, (torch.bfloat16,))
-    if dim != c.dim:
-        raise ValueError(f"the cache holds heads of {c.dim}, got {dim}")
-    if q_heads < c.heads or q_heads % c.heads:
-        raise ValueError(f"q_heads must be a multiple of the cache's {c.heads}, got {q_heads}")
-    b = _batch_of(dev, table, cu, lengths, tokens)
+    if dim != held_dim:
+        raise ValueError(f"the cache holds heads of {held_dim}, got {dim}")
+    if q_heads < heads or q_heads % heads:
+        raise ValueError(f"q_heads must be a multiple of the cache's {heads}, got {q_heads}")
+    batch, width, b = _batch_of(dev, table, cu, lengths, tokens)
     if out is None:
-        out = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=dev)
+        out = torch.empty(tokens, q_heads, dim, dtype=torch.bfloat16, device=dev)
     else:
         _want(out, "out", dev, torch.bfloat16, tokens * q_heads * dim)
-    room = b.width * c.page
+    room = width * page
     max_length = room if max_length <= 0 else min(max_length, room)
     lib = load_library()
-    size = lib.mx_kv_attention_workspace_size(tokens, b.batch, q_heads, c.heads, dim, max_length)
+    size = lib.mx_kv_attention_workspace_size(tokens, batch, q_heads, heads, dim, max_length)
     ws = _scratch(size, dev)
-    _call(dev, lib.mx_kv_attention, q.data_ptr(), stride, q_heads, ctypes.byref(c),
-          ctypes.byref(b), max_length, 1.0 / math.sqrt(dim) if scale is None else scale,
-          out.data_ptr(), _ptr(ws), size)
+    _call(dev, lib.mx_kv_attention, q.data_ptr(), stride, q_heads, c, b, max_length,
+          1.0 / math.sqrt(dim) if scale is None else scale, out.data_ptr(), _ptr(ws), size)
     return out
