@@ -521,8 +521,8 @@ __global__ __launch_bounds__(512) void k_matmul8_rows(const MatArgs g) {
 #pragma unroll
       for (int c = 0; c < CT; c++)
         bv[u][c] =
-            join(h0 ? __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(bp[c] + k0)) : zero,
-                 h1 ? __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(bp[c] + k1)) : zero);
+            join(h0 ? *reinterpret_cast<const u32x4 *>(bp[c] + k0) : zero,
+                 h1 ? *reinterpret_cast<const u32x4 *>(bp[c] + k1) : zero);
       av[u] = join(h0 ? *reinterpret_cast<const u32x4 *>(ap + k0) : zero,
                    h1 ? *reinterpret_cast<const u32x4 *>(ap + k1) : zero);
 #pragma unroll
