@@ -87,6 +87,11 @@ __device__ __forceinline__ uint32_t move4(uint32_t w, int d, bool nan) {
 // page of 64 tokens of 128 dims takes); larger pages read the rest twice.
 constexpr int kKeep = 4;
 
+// One workgroup per page and head. Prompts are bound by HBM: 6 sequences of up
+// to 8,000 tokens, 8 heads of 128, 201 MB in 41 us (4.9 TB/s); with the values'
+// bytes written to LDS one at a time 44.6, with the tokens read twice 72. A
+// token per sequence is a chain of loads that wait for each other (cu, table
+// and lengths, scale, codes): 64 sequences 5.6 us.
 template <bool BF16>
 __device__ __forceinline__ Raw<BF16> load_at(const void *base, int64_t elem) {
   return load_raw<BF16>(reinterpret_cast<const uint8_t *>(base) + elem * (BF16 ? 2 : 4), 0);
@@ -94,8 +99,8 @@ __device__ __forceinline__ Raw<BF16> load_at(const void *base, int64_t elem) {
 
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_kv_append(const AppendArgs a) {
-  // new values' codes, [dim][token]; rows are 16 bytes longer than a page's
-  // so that a row's byte writes and the next row's fall on other banks
+  // new values' codes, [dim][token]; rows are one word longer than a page's,
+  // so that the rows that an instruction writes to fall on different banks
   extern __shared__ __attribute__((aligned(16))) uint8_t vt[];
   __shared__ uint32_t am[2][4];
   const int unit = blockIdx.x / a.c.heads, head = blockIdx.x % a.c.heads;
@@ -110,14 +115,22 @@ __global__ __launch_bounds__(256) void k_kv_append(const AppendArgs a) {
   const int64_t src0 = (int64_t)c0 + ((int64_t)j << a.shift) - held;  // token of slot 0
   const int64_t most = a.b.tokens - 1;
   const int64_t at = id * a.c.heads + head;
-  const int per = D >> 3, bits = D == 128 ? 4 : 3, items = (end - kept) << bits;
+  // An item is eight dims of a token. Lanes l, l + 16, l + 32, l + 48 of a wave
+  // hold four tokens that share a word of a values' row.
+  const int wide = D == 128, first = kept & ~3;
   uint32_t was_k = 0, was_v = 0;
   if (kept) {
     was_k = a.c.k_scales[at];
     was_v = a.c.v_scales[at];
   }
-  auto slot_of = [&](int it) { return kept + (it >> bits); };
-  auto dim_of = [&](int it) { return (it & (per - 1)) * 8; };
+  auto word_of = [&](int it) {  // first of the four slots
+    return first + (wide ? it >> 6 << 2 : (it >> 6 << 3) + ((it & 8) >> 1));
+  };
+  auto slot_of = [&](int it) { return word_of(it) + ((it >> 4) & 3); };
+  auto dim_of = [&](int it) { return (it & (wide ? 15 : 7)) * 8; };
+  // whether any lane of the wave has a slot in use: the wave's lanes go together
+  auto any = [&](int it) { return first + (wide ? it >> 6 << 2 : it >> 6 << 3) < end; };
+  auto mine = [&](int it) { return slot_of(it) >= kept && slot_of(it) < end; };
   auto load = [&](const void *x, int64_t stride, int it) {
     const int64_t tok = min(max(src0 + slot_of(it), (int64_t)0), most);
     return load_at<BF16>(x, tok * stride + (int64_t)head * D + dim_of(it));
@@ -127,7 +140,8 @@ __global__ __launch_bounds__(256) void k_kv_append(const AppendArgs a) {
 #pragma unroll
   for (int u = 0; u < kKeep; u++) {
     const int it = threadIdx.x + 256 * u;
-    if (it < items) {
+    kr[u] = vr[u] = Raw<BF16>{};
+    if (mine(it)) {
       kr[u] = load(a.k, a.k_stride, it);
       vr[u] = load(a.v, a.v_stride, it);
     }
@@ -141,10 +155,9 @@ __global__ __launch_bounds__(256) void k_kv_append(const AppendArgs a) {
     mv = max(mv, amax8(f));
   };
 #pragma unroll
-  for (int u = 0; u < kKeep; u++)
-    if ((int)threadIdx.x + 256 * u < items) take(kr[u], vr[u]);
-  for (int it = threadIdx.x + 256 * kKeep; it < items; it += 256)
-    take(load(a.k, a.k_stride, it), load(a.v, a.v_stride, it));
+  for (int u = 0; u < kKeep; u++) take(kr[u], vr[u]);  // zeros where there is none
+  for (int it = threadIdx.x + 256 * kKeep; any(it); it += 256)
+    if (mine(it)) take(load(a.k, a.k_stride, it), load(a.v, a.v_stride, it));
   mk = max16(mk);
   mv = max16(mv);
   mk = max(mk, (uint32_t)__shfl_xor((int)mk, 16));
@@ -178,21 +191,29 @@ __global__ __launch_bounds__(256) void k_kv_append(const AppendArgs a) {
     }
     __syncthreads();  // before the new tokens' bytes of the same words
   }
-  const int row = P + 16;
+  const int row = P + 4;
   auto put = [&](const Raw<BF16> &k, const Raw<BF16> &v, int it) {
-    const int slot = slot_of(it), d = dim_of(it);
     float f[8];
-    widen<BF16>(k, f);
-    *reinterpret_cast<u32x2 *>(kc + slot * D + d) = encode8(f, sk);
+    if (mine(it)) {
+      widen<BF16>(k, f);
+      *reinterpret_cast<u32x2 *>(kc + slot_of(it) * D + dim_of(it)) = encode8(f, sk);
+    }
     widen<BF16>(v, f);
     const u32x2 w = encode8(f, sv);
-#pragma unroll
-    for (int e = 0; e < 8; e++) vt[(d + e) * row + slot] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
+    // four lanes' tokens t = 2 b + a, eight dims each, become two dims of four
+    // tokens: halves of the dims change places over b, then quarters over a
+    const auto x = __builtin_amdgcn_permlane32_swap(w[0], w[1], false, false);
+    const uint32_t lo = __builtin_amdgcn_perm(x[1], x[0], 0x05040100u);  // dims 0, 1 of tokens a, a + 2
+    const uint32_t hi = __builtin_amdgcn_perm(x[1], x[0], 0x07060302u);  // dims 2, 3
+    const auto y = __builtin_amdgcn_permlane16_swap(lo, hi, false, false);
+    uint32_t *to = reinterpret_cast<uint32_t *>(vt + (dim_of(it) + 2 * ((it >> 4) & 3)) * row + word_of(it));
+    to[0] = __builtin_amdgcn_perm(y[1], y[0], 0x06020400u);
+    to[row >> 2] = __builtin_amdgcn_perm(y[1], y[0], 0x07030501u);
   };
 #pragma unroll
   for (int u = 0; u < kKeep; u++)
-    if ((int)threadIdx.x + 256 * u < items) put(kr[u], vr[u], threadIdx.x + 256 * u);
-  for (int it = threadIdx.x + 256 * kKeep; it < items; it += 256)
+    if (any(threadIdx.x + 256 * u)) put(kr[u], vr[u], threadIdx.x + 256 * u);
+  for (int it = threadIdx.x + 256 * kKeep; any(it); it += 256)
     put(load(a.k, a.k_stride, it), load(a.v, a.v_stride, it), it);
   __syncthreads();
   const int cshift = a.shift - 4;
@@ -202,7 +223,8 @@ __global__ __launch_bounds__(256) void k_kv_append(const AppendArgs a) {
     if (lo >= hi) continue;
     uint8_t *dst = vc + (int64_t)d * P;
     if (lo == s && hi == s + 16) {
-      *reinterpret_cast<u32x4 *>(dst + s) = *reinterpret_cast<const u32x4 *>(vt + d * row + s);
+      const uint32_t *from = reinterpret_cast<const uint32_t *>(vt + d * row + s);
+      *reinterpret_cast<u32x4 *>(dst + s) = u32x4{from[0], from[1], from[2], from[3]};
     } else {
       for (int q = lo; q < hi; q++) dst[q] = vt[d * row + q];
     }
@@ -1127,7 +1149,7 @@ hipError_t mxi_launch_kv_append(const void *k, const void *v, int bf16, int64_t 
                                 const mx_kv_batch_t &batch, hipStream_t st) {
   const AppendArgs a = {k, v, k_stride, v_stride, cache, batch, log2_of(cache.page)};
   const dim3 grid((uint32_t)((batch.tokens / cache.page + 2 * (int64_t)batch.batch) * cache.heads));
-  const size_t lds = (size_t)cache.dim * (cache.page + 16);  // at most 34 KiB
+  const size_t lds = (size_t)cache.dim * (cache.page + 4);
   if (bf16) k_kv_append<true><<<grid, 256, lds, st>>>(a);
   else k_kv_append<false><<<grid, 256, lds, st>>>(a);
   return hipGetLastError();
