@@ -91,18 +91,18 @@ constexpr int kKeep = 4;
 // to 8,000 tokens, 8 heads of 128, 201 MB in 41 us (4.9 TB/s); with the values'
 // bytes written to LDS one at a time 44.6, with the tokens read twice 72. A
 // token per sequence is a chain of loads that wait for each other (cu, table
-// and lengths, scale, codes): 64 sequences 5.6 us.
+// and lengths, scale, codes): 64 sequences 5 us, 256 8.5.
 template <bool BF16>
 __device__ __forceinline__ Raw<BF16> load_at(const void *base, int64_t elem) {
   return load_raw<BF16>(reinterpret_cast<const uint8_t *>(base) + elem * (BF16 ? 2 : 4), 0);
 }
 
-template <bool BF16>
-__global__ __launch_bounds__(256) void k_kv_append(const AppendArgs a) {
+template <bool BF16, int T>
+__global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
   // new values' codes, [dim][token]; rows are one word longer than a page's,
   // so that the rows that an instruction writes to fall on different banks
   extern __shared__ __attribute__((aligned(16))) uint8_t vt[];
-  __shared__ uint32_t am[2][4];
+  __shared__ uint32_t am[2][T / 64];
   const int unit = blockIdx.x / a.c.heads, head = blockIdx.x % a.c.heads;
   const int P = a.c.page, D = a.c.dim;
   const int i = find_sequence(a.b.cu, a.b.batch, P, 2, unit);
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(256) void k_kv_append(const AppendArgs a) {
   Raw<BF16> kr[kKeep], vr[kKeep];
 #pragma unroll
   for (int u = 0; u < kKeep; u++) {
-    const int it = threadIdx.x + 256 * u;
+    const int it = threadIdx.x + T * u;
     kr[u] = vr[u] = Raw<BF16>{};
     if (mine(it)) {
       kr[u] = load(a.k, a.k_stride, it);
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(256) void k_kv_append(const AppendArgs a) {
   };
 #pragma unroll
   for (int u = 0; u < kKeep; u++) take(kr[u], vr[u]);  // zeros where there is none
-  for (int it = threadIdx.x + 256 * kKeep; any(it); it += 256)
+  for (int it = threadIdx.x + T * kKeep; any(it); it += T)
     if (mine(it)) take(load(a.k, a.k_stride, it), load(a.v, a.v_stride, it));
   mk = max16(mk);
   mv = max16(mv);
@@ -169,26 +169,41 @@ __global__ __launch_bounds__(256) void k_kv_append(const AppendArgs a) {
     am[1][threadIdx.x >> 6] = mv;
   }
   __syncthreads();
-  mk = max(max(am[0][0], am[0][1]), max(am[0][2], am[0][3]));
-  mv = max(max(am[1][0], am[1][1]), max(am[1][2], am[1][3]));
+#pragma unroll
+  for (int w = 0; w < T / 64; w++) {
+    mk = max(mk, am[0][w]);
+    mv = max(mv, am[1][w]);
+  }
   const uint32_t sk = max(scale_byte8(mk), was_k), sv = max(scale_byte8(mv), was_v);
   uint8_t *kc = a.c.k_codes + at * P * D, *vc = a.c.v_codes + at * P * D;
-  if (kept && sk > was_k) {
-    uint32_t *w = reinterpret_cast<uint32_t *>(kc);
-    for (int it = threadIdx.x; it < kept * D / 4; it += 256)
-      w[it] = move4(w[it], (int)(sk - was_k), sk == 255u);
-  }
-  if (kept && sv > was_v) {
-    // whole words of four tokens; a word that also holds slots past `kept`
-    // keeps those bytes
-    const int words = (kept + 3) >> 2;
-    for (int it = threadIdx.x; it < D * words; it += 256) {
-      const int d = it / words, s = (it % words) * 4;
-      uint32_t *w = reinterpret_cast<uint32_t *>(vc + (int64_t)d * P + s);
-      const uint32_t old = *w, moved = move4(old, (int)(sv - was_v), sv == 255u);
-      const uint32_t mask = kept - s >= 4 ? 0xFFFFFFFFu : (1u << (8 * (kept - s))) - 1;
-      *w = (moved & mask) | (old & ~mask);
+  // kept codes move to the new bytes 16 at a time, four such pieces asked for
+  // together; what a piece holds past the kept tokens stays
+  auto move = [&](int pieces, auto place, auto keeps, int d, bool nan) {
+    for (int c = threadIdx.x; c < pieces; c += 4 * T) {
+      u32x4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; u++) v[u] = *reinterpret_cast<const u32x4 *>(place(min(c + u * T, pieces - 1)));
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        if (c + u * T >= pieces) break;
+        const int keep = keeps(c + u * T);
+        u32x4 w;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const int n = min(max(keep - 4 * e, 0), 4);
+          const uint32_t mask = n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1;
+          w[e] = (move4(v[u][e], d, nan) & mask) | (v[u][e] & ~mask);
+        }
+        *reinterpret_cast<u32x4 *>(place(c + u * T)) = w;
+      }
     }
+  };
+  if (kept && sk > was_k)
+    move(kept * D / 16, [&](int c) { return kc + 16 * c; }, [](int) { return 16; }, (int)(sk - was_k), sk == 255u);
+  if (kept && sv > was_v) {
+    const int n = (kept + 15) >> 4;
+    move(D * n, [&](int c) { return vc + c / n * P + c % n * 16; },
+         [&](int c) { return kept - c % n * 16; }, (int)(sv - was_v), sv == 255u);
     __syncthreads();  // before the new tokens' bytes of the same words
   }
   const int row = P + 4;
@@ -212,15 +227,14 @@ __global__ __launch_bounds__(256) void k_kv_append(const AppendArgs a) {
   };
 #pragma unroll
   for (int u = 0; u < kKeep; u++)
-    if (any(threadIdx.x + 256 * u)) put(kr[u], vr[u], threadIdx.x + 256 * u);
-  for (int it = threadIdx.x + 256 * kKeep; any(it); it += 256)
+    if (any(threadIdx.x + T * u)) put(kr[u], vr[u], threadIdx.x + T * u);
+  for (int it = threadIdx.x + T * kKeep; any(it); it += T)
     put(load(a.k, a.k_stride, it), load(a.v, a.v_stride, it), it);
   __syncthreads();
-  const int cshift = a.shift - 4;
-  for (int it = threadIdx.x; it < D << cshift; it += 256) {
-    const int d = it >> cshift, s = (it & ((1 << cshift) - 1)) * 16;
+  const int piece0 = kept >> 4, chunks = ((end + 15) >> 4) - piece0;  // of a row, with new tokens in them
+  for (int it = threadIdx.x; it < D * chunks; it += T) {
+    const int d = it / chunks, s = (piece0 + it % chunks) * 16;
     const int lo = max(kept, s), hi = min(end, s + 16);
-    if (lo >= hi) continue;
     uint8_t *dst = vc + (int64_t)d * P;
     if (lo == s && hi == s + 16) {
       const uint32_t *from = reinterpret_cast<const uint32_t *>(vt + d * row + s);
@@ -1150,8 +1164,12 @@ hipError_t mxi_launch_kv_append(const void *k, const void *v, int bf16, int64_t 
   const AppendArgs a = {k, v, k_stride, v_stride, cache, batch, log2_of(cache.page)};
   const dim3 grid((uint32_t)((batch.tokens / cache.page + 2 * (int64_t)batch.batch) * cache.heads));
   const size_t lds = (size_t)cache.dim * (cache.page + 4);
-  if (bf16) k_kv_append<true><<<grid, 256, lds, st>>>(a);
-  else k_kv_append<false><<<grid, 256, lds, st>>>(a);
+  // a few new tokens per sequence: one wave a page, so that all pages are at
+  // work at once (256 sequences of one token: 8.5 us; four
+  // waves, and kept codes moved a word at a time: 19)
+  const bool few = batch.tokens <= 4 * (int64_t)batch.batch;
+  if (bf16) few ? k_kv_append<true, 64><<<grid, 64, lds, st>>>(a) : k_kv_append<true, 256><<<grid, 256, lds, st>>>(a);
+  else few ? k_kv_append<false, 64><<<grid, 64, lds, st>>>(a) : k_kv_append<false, 256><<<grid, 256, lds, st>>>(a);
   return hipGetLastError();
 }
 
