@@ -561,18 +561,18 @@ __device__ __forceinline__ f32x4 add_weights(i32x8 hi, i32x8 lo, f32x4 l) {
 // wait for it; the kernel waits where it must. No output register.
 __device__ __forceinline__ void load_lds16(const uint8_t *base, uint32_t offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               ::"s"(lds), "v"(offset), "s"(base) : "memory");
+               ::"s"(lds), "v"(offset), "s"(base) : "memory", "m0");
 }
 __device__ __forceinline__ void load_lds16(uint64_t address, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt"
-               ::"s"(lds), "v"(address) : "memory");
+               ::"s"(lds), "v"(address) : "memory", "m0");
 }
 // A word, or a byte widened to one, a lane.
 __device__ __forceinline__ void load_lds4(const int32_t *p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p) : "memory", "m0");
 }
 __device__ __forceinline__ void load_lds1(const uint8_t *p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, off" ::"s"(lds), "v"(p) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, off" ::"s"(lds), "v"(p) : "memory", "m0");
 }
 __device__ __forceinline__ uint32_t lds_address(const void *p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)p;

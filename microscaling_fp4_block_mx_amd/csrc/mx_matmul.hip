@@ -103,7 +103,7 @@ constexpr uint32_t kOut = 0x80000000u;  // an offset past every buffer: loads gi
 // It has no output register, and its memory clobber keeps the order.
 __device__ __forceinline__ void load_lds16(i32x4 buffer, uint32_t offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               ::"s"(lds), "v"(offset), "s"(buffer) : "memory");
+               ::"s"(lds), "v"(offset), "s"(buffer) : "memory", "m0");
 }
 __device__ __forceinline__ i32x4 buffer_of(const void *base, uint32_t bytes) {
   const uint64_t p = (uint64_t)base;
