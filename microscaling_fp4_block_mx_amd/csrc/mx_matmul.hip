@@ -552,7 +552,7 @@ __global__ __launch_bounds__(256) void k_sum_splits(const float *__restrict__ p,
 // ---- few rows -----------------------------------------------------------------------
 //
 // 16 rows of A (single tokens, small batches), or a few times 16: bound by
-// reading B, 1 x 8192 x 4096 in 9.7 us (3.5 TB/s; launch and one trip to
+// reading B, 1 x 8192 x 4096 in 8.7 us (3.9 TB/s; launch and one trip to
 // memory are half of it). A workgroup owns 16 CT columns (rows of B) and its
 // waves split K into contiguous ranges; a wave loads B's codes straight into
 // the matrix core's layout (each row's 128 bytes of a slab are one cache
