@@ -279,8 +279,8 @@ __global__ __launch_bounds__(kQuantThreads) void k_quantize8_blocks(
   // 65 (129) words per row: the transposed reads, 8 rows apart, spread over the banks
   constexpr int P = BF16 ? 65 : 129, RS = kQuantThreads / 16, U = 128 / RS;
   __shared__ uint32_t tile[128 * P];
-  const uint32_t across = (uint32_t)((k + 127) / 128);
-  const int64_t r0 = (int64_t)(blockIdx.x / across) * 128, c0 = (int64_t)(blockIdx.x % across) * 128;
+  const int64_t r0 = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * 128, c0 = (int64_t)blockIdx.x * 128;
+  if (r0 >= rows) return;
   const int q = threadIdx.x & 15, r = threadIdx.x >> 4;
   const int lanes = wide ? 16 : 4;
   const int64_t col = c0 + 8 * q;
@@ -441,7 +441,9 @@ hipError_t mxi_launch_rmsnorm_backward(const void *dy, const void *h, const void
 hipError_t mxi_launch_quantize8_blocks(const void *x, int bf16, int64_t rows, int64_t k, int block,
                                        uint8_t *codes, uint8_t *scales, uint8_t *codes_t,
                                        uint8_t *scales_t, hipStream_t st) {
-  const dim3 grid((uint32_t)(((rows + 127) / 128) * ((k + 127) / 128)));
+  // tiles down over two dimensions of the grid, of which one is short
+  const int64_t down = (rows + 127) / 128, y = down < 32768 ? down : 32768;
+  const dim3 grid((uint32_t)((k + 127) / 128), (uint32_t)y, (uint32_t)((down + y - 1) / y));
   if (bf16)
     k_quantize8_blocks<true><<<grid, kQuantThreads, 0, st>>>(x, rows, k, block == 128, codes, scales, codes_t,
                                                    scales_t);
