@@ -55,11 +55,12 @@ __device__ __forceinline__ double block_sum(float a, float *part) {
 
 template <bool BF16, int T, int N>
 __global__ __launch_bounds__(T) void k_rmsnorm(const void *x, const void *residual,
-                                               const void *__restrict__ weight, int k, float eps,
+                                               const void *__restrict__ weight, int64_t rows, int k, float eps,
                                                int wide, uint8_t *__restrict__ codes,
                                                uint8_t *__restrict__ scales, void *h) {
   __shared__ float part[T / 64];
-  const int64_t row = blockIdx.x;
+  const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (row >= rows) return;
   const int items = k >> 3;
   const int64_t base = row * items;
   Raw<BF16> xr[N], rr[N], wr[N];
@@ -397,11 +398,14 @@ hipError_t mxi_launch_rmsnorm(const void *x, const void *residual, const void *w
                               int64_t rows, int64_t k, float eps, int block, uint8_t *codes,
                               uint8_t *scales, void *h, hipStream_t st) {
   const Shape s = row_shape(k / 8, rows < 512 ? 1 : 4);
+  // a grid's dimension holds fewer than 2^32 threads
+  const int64_t across = rows < (1 << 21) ? rows : 1 << 21;
+  const dim3 grid((uint32_t)across, (uint32_t)((rows + across - 1) / across));
   auto go = [&](auto bf) {
     return with_shape<true>(s, [&](auto t, auto n) {
       k_rmsnorm<decltype(bf)::value, decltype(t)::value, decltype(n)::value>
-          <<<dim3((uint32_t)rows), dim3(decltype(t)::value), 0, st>>>(
-              x, residual, weight, (int)k, eps, block == 128, codes, scales, h);
+          <<<grid, dim3(decltype(t)::value), 0, st>>>(
+              x, residual, weight, rows, (int)k, eps, block == 128, codes, scales, h);
       return hipGetLastError();
     });
   };
