@@ -815,8 +815,48 @@ __global__ __launch_bounds__(256, D == 128 && RT == 2 ? 1 : 2) void k_attn_rows(
   }
 }
 
-// Joins the splits of one (token, query head): thread s takes split s's
-// maximum and total, then D / 4 threads a row add up splits s, s + G, ....
+// How many splits of a token's block the first kernel wrote, as it had it.
+__device__ __forceinline__ int splits_of(const AttnArgs &a, int tok) {
+  const int i = find_sequence(a.b.cu, a.b.batch, 1, 0, tok);
+  const int c0 = a.b.cu[i], n = a.b.cu[i + 1] - c0;
+  const int64_t room = (int64_t)a.b.width << a.shift;
+  const int len = (int)min((int64_t)max(a.b.lengths[i], 0), room);
+  const int at = (tok - c0) / a.block_tokens * a.block_tokens;
+  const int end = min(len, len - n + at + min(a.block_tokens, n - at));
+  const int tiles = (max(end, 0) + 127) >> 7;
+  return max(1, min(a.splits, (tiles + a.chunk - 1) / a.chunk));
+}
+
+// Joins a few splits of many rows: D / 4 threads a (token, query head), which
+// all go through the splits' maxima and then through their sums.
+template <int D>
+__global__ __launch_bounds__(256) void k_attn_join_few(const AttnArgs a) {
+  constexpr int C = D / 4, R = 256 / C, P = D + 4;
+  const int tok = blockIdx.x, c = threadIdx.x % C, qh = blockIdx.y * R + threadIdx.x / C;
+  const int live = splits_of(a, tok);
+  if (qh >= a.q_heads) return;
+  const int64_t row = (int64_t)tok * a.q_heads + qh;
+  const float *p = a.part + row * a.splits * P;
+  float m = -__builtin_inff();
+  for (int s = 0; s < live; s++) m = __builtin_fmaxf(m, p[s * P + D]);
+  const float ms = m == -__builtin_inff() ? 0.0f : m;
+  f32x4 o = {0, 0, 0, 0};
+  float l = 0.0f;
+  for (int s = 0; s < live; s++) {
+    const float f = __builtin_amdgcn_exp2f(p[s * P + D] - ms);
+    const f32x4 v = *reinterpret_cast<const f32x4 *>(p + s * P + 4 * c);
+    l = __builtin_fmaf(f, p[s * P + D + 1], l);
+#pragma unroll
+    for (int e = 0; e < 4; e++) o[e] = __builtin_fmaf(f, v[e], o[e]);
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  *reinterpret_cast<u32x2 *>(a.out + row * D + 4 * c) =
+      u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+}
+
+// Joins many splits, or those of few rows, of one (token, query head): thread
+// s takes split s's maximum and total, then D / 4 threads a row add up splits
+// s, s + G, ....
 template <int D>
 __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a) {
   constexpr int C = D / 4, G = 256 / C, P = D + 4;
@@ -825,15 +865,7 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a) {
   __shared__ f32x4 sums[G][C];
   const int64_t row = blockIdx.x;
   const int tok = (int)(row / a.q_heads);
-  // the token's sequence and how many keys its block saw, as the first kernel had it
-  const int i = find_sequence(a.b.cu, a.b.batch, 1, 0, tok);
-  const int c0 = a.b.cu[i], n = a.b.cu[i + 1] - c0;
-  const int64_t room = (int64_t)a.b.width << a.shift;
-  const int len = (int)min((int64_t)max(a.b.lengths[i], 0), room);
-  const int at = (tok - c0) / a.block_tokens * a.block_tokens;
-  const int end = min(len, len - n + at + min(a.block_tokens, n - at));
-  const int tiles = (max(end, 0) + 127) >> 7;
-  const int live = max(1, min(a.splits, (tiles + a.chunk - 1) / a.chunk));
+  const int live = splits_of(a, tok);
   const float *p = a.part + row * a.splits * P;
   const int wave = threadIdx.x >> 6;
 
@@ -939,6 +971,11 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
   const int l16 = lane & 15, lg = lane >> 4;
   const int end = min(b.len, b.seen0 + b.count - 1);
   const int tiles = (max(end, 0) + 127) >> 7;
+  // this split's tiles, from an even one on (the buffers take turns); the last
+  // split takes whatever the caller's bound on the lengths left out
+  const int split = blockIdx.y, t0 = split * a.chunk;
+  const int t1 = split + 1 == a.splits ? tiles : min(tiles, t0 + a.chunk);
+  if (split > 0 && t0 >= tiles) return;  // the sum takes only splits that exist
   const int rows = b.count * a.group;
   Query<D> q[RT];
   Rows<D> r[RT];
@@ -988,14 +1025,14 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
 
   int mine = 0;        // pages of the next tile
   uint32_t bytes = 0;  // scale bytes of this one
-  if (tiles > 0) {
-    const int now = page_of(a, b, 0, lane);
+  if (t0 < t1) {
+    const int now = page_of(a, b, t0, lane);
     bytes = *byte_at(a, now, head, lane);
-    mine = page_of(a, b, 1, lane);
-    load(0, 0, runs_of(a, now));
+    mine = page_of(a, b, t0 + 1, lane);
+    load(t0, 0, runs_of(a, now));
   }
   int flip = S;
-  for (int tile = 0; tile < tiles; tile++) {
+  for (int tile = t0; tile < t1; tile++) {
     // this tile's codes, its scale bytes and the next one's pages have
     // arrived, and every wave is done with the other buffer
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -1019,7 +1056,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
     }
     const Runs id = runs_of(a, mine);
     __builtin_amdgcn_sched_barrier(0);
-    if (tile + 1 < tiles) {
+    if (tile + 1 < t1) {
       bytes = *byte_at(a, mine, head, lane);
       mine = page_of(a, b, tile + 2, lane);
       load(tile + 1, (tile + 1) & 1, id);
@@ -1107,12 +1144,22 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
       const float l = r[x].l[0], inv = l == 0.0f ? 0.0f : 1.0f / l;
       const int64_t tok = b.tok0 + row / a.group;
       const int64_t qh = (int64_t)head * a.group + row % a.group;
-      uint16_t *p = a.out + (tok * a.q_heads + qh) * D + 4 * lg;
+      if (a.splits > 1) {
+        float *p = a.part + ((tok * a.q_heads + qh) * a.splits + split) * (D + 4);
 #pragma unroll
-      for (int d = 0; d < DT; d++) {
-        const f32x4 o = r[x].o[d];
-        *reinterpret_cast<u32x2 *>(p + 16 * d) =
-            u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+        for (int d = 0; d < DT; d++) *reinterpret_cast<f32x4 *>(p + 16 * d + 4 * lg) = r[x].o[d];
+        if (lg == 0) {
+          p[D] = r[x].m;
+          p[D + 1] = l;
+        }
+      } else {
+        uint16_t *p = a.out + (tok * a.q_heads + qh) * D + 4 * lg;
+#pragma unroll
+        for (int d = 0; d < DT; d++) {
+          const f32x4 o = r[x].o[d];
+          *reinterpret_cast<u32x2 *>(p + 16 * d) =
+              u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+        }
       }
     }
   }
@@ -1150,6 +1197,18 @@ static AttnPlan attn_plan(int64_t tokens, int batch, int q_heads, int heads, int
     const int64_t c = std::max<int64_t>(8, (tiles + want - 1) / want);
     p.chunk = (int)((c + 3) / 4 * 4);
     p.splits = std::max(1, (tiles + p.chunk - 1) / p.chunk);
+  } else {
+    // two workgroups a compute unit where blocks of rows leave half of that
+    // empty (1 x 512 tokens of 4,096, 32 query heads on 8: 85 us in one piece,
+    // 54 so; 1 x 256 of 8,192: 163 and 56), and at least eight tiles each: with
+    // four 1 x 1,024 of 1,024 take 37, in one piece 29
+    const int64_t base = (tokens + p.block_tokens - 1) / p.block_tokens * heads;
+    const int64_t want = 512 / base;
+    if (want > 1) {
+      const int64_t c = std::max<int64_t>(8, (tiles + want - 1) / want);
+      p.chunk = (int)((c + 1) & ~1);
+      p.splits = std::max(1, (tiles + p.chunk - 1) / p.chunk);
+    }
   }
   return p;
 }
@@ -1188,14 +1247,12 @@ hipError_t mxi_launch_kv_attention(const void *q, int64_t q_stride, int q_heads,
                       q_heads / cache.heads, cache, batch, log2_of(cache.page), p.block_tokens,
                       p.chunk, p.splits, (int)p.units, scale * 1.44269504088896340736f,
                       reinterpret_cast<uint16_t *>(out), reinterpret_cast<float *>(workspace)};
-  if (!p.few) {
-    const dim3 grid((uint32_t)(p.units * cache.heads));
-    if (cache.dim == 64) k_attn_tiles<64><<<grid, 256, 0, st>>>(a);
-    else k_attn_tiles<128><<<grid, 256, 0, st>>>(a);
-    return hipGetLastError();
-  }
   const dim3 grid((uint32_t)p.units, (uint32_t)cache.heads, (uint32_t)p.splits);
-  if (cache.dim == 64) {
+  if (!p.few) {
+    const dim3 tgrid((uint32_t)(p.units * cache.heads), (uint32_t)p.splits);
+    if (cache.dim == 64) k_attn_tiles<64><<<tgrid, 256, 0, st>>>(a);
+    else k_attn_tiles<128><<<tgrid, 256, 0, st>>>(a);
+  } else if (cache.dim == 64) {
     if (p.rt == 1) k_attn_rows<64, 1><<<grid, 256, 0, st>>>(a);
     else k_attn_rows<64, 2><<<grid, 256, 0, st>>>(a);
   } else {
@@ -1204,6 +1261,15 @@ hipError_t mxi_launch_kv_attention(const void *q, int64_t q_stride, int q_heads,
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
+  // 16,384 rows of 4 splits: 14 us less than with a workgroup a row; 512 rows of
+  // 16: 7 us more
+  if (p.splits <= 16 && batch.tokens * q_heads >= 4096) {
+    const int rows = 1024 / cache.dim;  // of a workgroup
+    const dim3 jgrid((uint32_t)batch.tokens, (uint32_t)((q_heads + rows - 1) / rows));
+    if (cache.dim == 64) k_attn_join_few<64><<<jgrid, 256, 0, st>>>(a);
+    else k_attn_join_few<128><<<jgrid, 256, 0, st>>>(a);
+    return hipGetLastError();
+  }
   const dim3 jgrid((uint32_t)(batch.tokens * q_heads));
   if (cache.dim == 64) k_attn_join<64><<<jgrid, 256, 0, st>>>(a);
   else k_attn_join<128><<<jgrid, 256, 0, st>>>(a);
