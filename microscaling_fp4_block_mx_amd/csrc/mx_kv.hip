@@ -1202,7 +1202,7 @@ static AttnPlan attn_plan(int64_t tokens, int batch, int q_heads, int heads, int
     // empty (1 x 512 tokens of 4,096, 32 query heads on 8: 85 us in one piece,
     // 54 so; 1 x 256 of 8,192: 163 and 56), and at least eight tiles each: with
     // four 1 x 1,024 of 1,024 take 37, in one piece 29
-    const int64_t base = (tokens + p.block_tokens - 1) / p.block_tokens * heads;
+    const int64_t base = std::max<int64_t>(1, (tokens + p.block_tokens - 1) / p.block_tokens * heads);
     const int64_t want = 512 / base;
     if (want > 1) {
       const int64_t c = std::max<int64_t>(8, (tiles + want - 1) / want);
