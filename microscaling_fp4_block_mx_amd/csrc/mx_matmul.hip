@@ -92,6 +92,11 @@ struct MatArgs {
 // it loads), since a direct load writes LDS linearly. Scale bytes of four
 // slabs are one word per row (and, with blocks of 32, per block of a slab)
 // in LDS; the matrix core picks the slab's byte.
+//
+// 8192 x 8192 x 4096, bf16 out: 200 to 205 us with blocks of 128 (2.7 PFLOP/s),
+// 211 to 215 with blocks of 32, the matrix cores busy 62 % of the cycles and
+// the card at 2.0 of its 2.4 GHz; 4096 x 4096 x 4096 53 us. fp32 out 427 us
+// (1.3 PFLOP/s): twice the products and the widening.
 
 __device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
 
