@@ -1180,6 +1180,8 @@ static AttnPlan attn_plan(int64_t tokens, int batch, int q_heads, int heads, int
   AttnPlan p;
   const int group = q_heads / heads;
   const int64_t mean = (tokens + batch - 1) / batch * group;  // rows of a sequence
+  // 16 sequences of 16,000 tokens: 16 rows each 64 us (the other kernel, of
+  // 128 rows: 105), 32 rows 94 (109)
   p.few = mean <= 32 && group <= 32;
   p.rt = p.few ? (mean <= 16 && group <= 16 ? 1 : 2) : 2;
   p.block_tokens = (p.few ? 16 * p.rt : 128) / group;
