@@ -14,22 +14,24 @@
 // whose products land in the same accumulator: its eight significant bits are
 // held exactly. Scores are taken transposed (tokens are the accumulator's
 // rows), so that the weights p come out in the very lanes and order in which
-// the second product wants them. Maxima, sums and accumulators are fp32; the
+// the second product wants them. Maxima, sums and accumulators are fp32.
+//
+// The second product is a bfloat16 one: values are widened to it (exact, their
+// bytes applied), weights rounded to it, which moves each by at most 2^-9 of
+// itself however far below the largest it lies. (Two E4M3 parts, as q has,
+// end 2^-22 below the largest weight: a tail of many such keys is lost.) The
 // weights' sum is a product with a row of ones, of the weights as rounded.
 //
 // Two kernels. Few rows (single tokens) are bound by reading the cache: one
-// wave per 128 tokens at a time, the sequence split over workgroups, and the
-// second product is an 8-bit one too, the weights split as q is (off by at
-// most 2^-9 of themselves). With g = lane / 16, tile t (of 16 rows) and
-// accumulator i hold token 64 (t / 4) + 16 g + 4 (t % 4) + i of 128, and the
-// second product's lane holds tokens 16 g .. + 15 and 64 + 16 g .. + 15.
+// wave per 128 tokens at a time, the sequence split over workgroups. With
+// g = lane / 16, tile t (of 16 rows) and accumulator i hold token 64 (t / 4) +
+// 16 g + 4 (t % 4) + i of 128, and the second product's lane holds tokens
+// 16 g .. + 15 and 64 + 16 g .. + 15.
 //
 // Many rows (prompts) share tiles of 128 tokens through LDS and are bound by
 // instruction issue: per 32 rows and 128 tokens, 2,200 cycles of products
 // beside 2,400 of vector arithmetic, half of it the exponentials. There the
-// workgroup widens the values to bfloat16 once (exact), and the weights are
-// rounded to it (2^-8 of themselves): one conversion where the split takes
-// three and a subtraction. Token 32 (t / 2) + 8 g + 4 (t % 2) + i.
+// workgroup widens the values once. Token 32 (t / 2) + 8 g + 4 (t % 2) + i.
 #include <algorithm>
 
 #include "mx_layer.h"
@@ -416,30 +418,52 @@ __device__ __forceinline__ void running_max(f32x4 (&s)[RT][8], Rows<D> (&r)[RT],
   }
 }
 
-// The weights as two E4M3 parts, 256 p = hi + lo / 16.
-template <int D, int RT>
-__device__ __forceinline__ void softmax_tile(f32x4 (&s)[RT][8], Rows<D> (&r)[RT], float c,
-                                             bool masked, const int (&limit)[RT], i32x8 (&hi)[RT],
-                                             i32x8 (&lo)[RT]) {
-  float less[RT];
-  running_max<D, RT>(s, r, c, masked, limit, [](int t) { return 64 * (t >> 2) + 4 * (t & 3); }, less);
+// Weights of RT x 16 rows and 128 tokens, rounded to bfloat16: tiles 2 j and
+// 2 j + 1 are the eight tokens of a lane in the second product's step j.
+template <int RT>
+__device__ __forceinline__ void weights(const f32x4 (&s)[RT][8], float c, const float (&less)[RT],
+                                        u32x4 (&p)[RT][4]) {
 #pragma unroll
   for (int x = 0; x < RT; x++)
 #pragma unroll
     for (int t = 0; t < 8; t++) {
-      float p[4];
+      float e[4];
 #pragma unroll
       for (int i = 0; i < 4; i++)
-        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][i], c, 8.0f - less[x]));
-      uint32_t a, b;
-      split4(p, 1.0f, 0.0625f, a, b);
-      hi[x][t] = (int)a;
-      lo[x][t] = (int)b;
+        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][i], c, -less[x]));
+      p[x][t >> 1][2 * (t & 1)] = pack_bf16(e[0], e[1]);
+      p[x][t >> 1][2 * (t & 1) + 1] = pack_bf16(e[2], e[3]);
     }
 }
 
-// Scale bytes of the weights' two parts, and 1.
-constexpr uint32_t kParts = (127 - 8) | (127 - 12) << 8 | 127 << 16;
+// Sum of the 128 weights on top of l: a product with a row of ones.
+__device__ __forceinline__ f32x4 add_weights(const u32x4 (&p)[4], f32x4 l) {
+  const uint32_t one = 0x3F803F80u;
+#pragma unroll
+  for (int j = 0; j < 4; j++) l = mma16(u32x4{one, one, one, one}, p[j], l);
+  return l;
+}
+
+// 16 codes widened with scale 2^(byte-127). `far`: a lane's byte may be above
+// 246; its values past bfloat16's range (no quantizer makes them) become the
+// largest, so that a weight of 0 still drops them.
+__device__ __forceinline__ void widen16(u32x4 c, uint32_t byte, bool far, u32x4 (&w)[2]) {
+  const float f = __uint_as_float(byte << 23);
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    w[j >> 1][2 * (j & 1)] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)c[j], f, false));
+    w[j >> 1][2 * (j & 1) + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)c[j], f, true));
+  }
+  if (far) {
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      uint32_t x = w[j >> 2][j & 3];
+      if ((x & 0x7FFFu) == 0x7F80u) x -= 1u;
+      if ((x & 0x7FFF0000u) == 0x7F800000u) x -= 0x10000u;
+      w[j >> 2][j & 3] = x;
+    }
+  }
+}
 
 // Zero the codes of tokens past the sequence's end (what a page holds there
 // may decode to NaN): the lane's 16 bytes start at token `from`, `len` valid.
@@ -498,9 +522,10 @@ __device__ __forceinline__ int of_run(const Runs &r, int j) {  // j may differ f
 }
 
 // Scale bytes of a tile's pages: lane j % 4 holds run j's key byte, lane 4 +
-// j its value byte. `bytes_of` turns them into the word that the matrix core
-// picks from: bytes 0 and 1 are for the keys that this lane's row holds in
-// tiles 0 .. 3 and 4 .. 7, byte 2 for the values of run lg. A page whose values
+// j its value byte. `bytes_of` turns them into one word: bytes 0 and 1 are for
+// the keys that this lane's row holds in tiles 0 .. 3 and 4 .. 7 (the matrix
+// core picks them), bytes 2 and 3 for the values of its two runs of tokens,
+// lg / 2 and 2 + lg / 2. A page whose values
 // are NaN must reach only the rows that see it: its keys are made NaN
 // instead (masked scores are dropped, visible ones make the row NaN) and its
 // values, whose codes are signed zeros, get a finite scale.
@@ -518,8 +543,8 @@ __device__ __forceinline__ uint32_t bytes_of(uint32_t mine, int l16, int lg) {
     v[j] = v[j] == 255u ? 127u : v[j];
   }
   const uint32_t even = k[0] | k[2] << 8, odd = k[1] | k[3] << 8;
-  const uint32_t v01 = (lg & 1) ? v[1] : v[0], v23 = (lg & 1) ? v[3] : v[2];
-  return ((l16 & 8) ? odd : even) | ((lg & 2) ? v23 : v01) << 16;
+  const uint32_t v02 = v[0] | v[2] << 8, v13 = v[1] | v[3] << 8;
+  return ((l16 & 8) ? odd : even) | ((lg & 2) ? v13 : v02) << 16;
 }
 
 // The same of one tile for the many-rows kernel: the keys' bytes of the four
@@ -545,15 +570,6 @@ __device__ __forceinline__ void scores(const i32x8 (&kv)[4], const Query<D> &q, 
     s[4 * H + t] = mma<H, 0>(kv[t], q.v[0], f32x4{0, 0, 0, 0}, sc, q.bytes);
     if constexpr (D == 128) s[4 * H + t] = mma<H, 1>(kv[t], q.v[1], s[4 * H + t], sc, q.bytes);
   }
-}
-
-// Sum of the 128 weights on top of l: a product with a row of ones (E2M1,
-// which takes half the registers of E4M3).
-__device__ __forceinline__ f32x4 add_weights(i32x8 hi, i32x8 lo, f32x4 l) {
-  const int w = 0x22222222;
-  const i32x8 ones = {w, w, w, w, 0, 0, 0, 0};
-  l = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ones, hi, l, 4, 0, 2, (int)kParts, 0, (int)kParts);
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ones, lo, l, 4, 0, 2, (int)kParts, 1, (int)kParts);
 }
 
 // 16 bytes a lane straight into LDS, lane after lane from `lds` on. In
@@ -712,11 +728,16 @@ __global__ __launch_bounds__(256, D == 128 && RT == 2 ? 1 : 2) void k_attn_rows(
         else scores<D, 1>(kv, q[x], sc, s[x]);
       }
     }
-    i32x8 hi[RT], lo[RT];
     int limit[RT];
+    float less[RT];
 #pragma unroll
     for (int x = 0; x < RT; x++) limit[x] = seen[x] - 1 - tile * 128 - 16 * lg;
-    softmax_tile<D, RT>(s, r, a.scale2, tile * 128 + 128 > b.seen0, limit, hi, lo);
+    running_max<D, RT>(s, r, a.scale2, tile * 128 + 128 > b.seen0, limit,
+                       [](int t) { return 64 * (t >> 2) + 4 * (t & 3); }, less);
+    u32x4 p[RT][4];
+    weights<RT>(s, a.scale2, less, p);
+    const uint32_t vb0 = sc >> 16 & 255u, vb1 = sc >> 24;
+    const bool far = __any(max(vb0, vb1) > 246u);
 #pragma unroll
     for (int h = 0; h < 2; h++) {
       if (h == 0 || next < t1) landed();
@@ -747,16 +768,26 @@ __global__ __launch_bounds__(256, D == 128 && RT == 2 ? 1 : 2) void k_attn_rows(
         }
       }
 #pragma unroll
-      for (int x = 0; x < RT; x++)
+      for (int d = 0; d < DT / 2; d++) {
+        u32x4 w[4];
 #pragma unroll
-        for (int d = 0; d < DT / 2; d++) {
-          f32x4 &o = r[x].o[h * (DT / 2) + d];
-          o = mma<2, 0>(vv[d], hi[x], o, sc, kParts);
-          o = mma<2, 1>(vv[d], lo[x], o, sc, kParts);
+        for (int q = 0; q < 2; q++) {
+          u32x4 wide[2];
+          widen16(u32x4{(uint32_t)vv[d][4 * q], (uint32_t)vv[d][4 * q + 1], (uint32_t)vv[d][4 * q + 2],
+                        (uint32_t)vv[d][4 * q + 3]}, q ? vb1 : vb0, far, wide);
+          w[2 * q] = wide[0];
+          w[2 * q + 1] = wide[1];
         }
+#pragma unroll
+        for (int x = 0; x < RT; x++) {
+          f32x4 &o = r[x].o[h * (DT / 2) + d];
+#pragma unroll
+          for (int j = 0; j < 4; j++) o = mma16(w[j], p[x][j], o);
+        }
+      }
     }
 #pragma unroll
-    for (int x = 0; x < RT; x++) r[x].l = add_weights(hi[x], lo[x], r[x].l);
+    for (int x = 0; x < RT; x++) r[x].l = add_weights(p[x], r[x].l);
   }
   // no load may land on the sums below
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
@@ -935,27 +966,6 @@ __device__ __forceinline__ int swz_k(int r) {
   return (r >> 3) & 3;
 }
 
-// 16 codes widened with scale 2^(byte-127). Values past bfloat16's range (no
-// quantizer makes them: they need a byte above 246) become its largest, so
-// that a weight of 0 still drops them.
-__device__ __forceinline__ void widen16(u32x4 c, uint32_t byte, u32x4 (&w)[2]) {
-  const float f = __uint_as_float(byte << 23);
-#pragma unroll
-  for (int j = 0; j < 4; j++) {
-    w[j >> 1][2 * (j & 1)] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)c[j], f, false));
-    w[j >> 1][2 * (j & 1) + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)c[j], f, true));
-  }
-  if (__any(byte > 246u)) {
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-      uint32_t x = w[j >> 2][j & 3];
-      if ((x & 0x7FFFu) == 0x7F80u) x -= 1u;
-      if ((x & 0x7FFF0000u) == 0x7F800000u) x -= 0x10000u;
-      w[j >> 2][j & 3] = x;
-    }
-  }
-}
-
 template <int D>
 __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
   constexpr int DT = D / 16, RT = 2, S = 128 * D;
@@ -1048,7 +1058,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < VL; i++) {
       u32x4 w[2];
-      widen16(raw[i], mv, w);
+      widen16(raw[i], mv, __any(mv > 246u), w);
       const int row = vr + 32 * i;
 #pragma unroll
       for (int h = 0; h < 2; h++)
@@ -1100,18 +1110,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
     for (int x = 0; x < RT; x++) limit[x] = seen[x] - 1 - tile * 128 - 8 * lg;
     running_max<D, RT>(s, r, a.scale2, tile * 128 + 128 > b.seen0, limit,
                        [](int t) { return 32 * (t >> 1) + 4 * (t & 1); }, less);
-    u32x4 p[RT][4];  // weights of tokens 32 j + 8 lg ..
-#pragma unroll
-    for (int x = 0; x < RT; x++)
-#pragma unroll
-      for (int t = 0; t < 8; t++) {
-        float e[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-          e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][i], a.scale2, -less[x]));
-        p[x][t >> 1][2 * (t & 1)] = pack_bf16(e[0], e[1]);
-        p[x][t >> 1][2 * (t & 1) + 1] = pack_bf16(e[2], e[3]);
-      }
+    u32x4 p[RT][4];  // of tokens 32 j + 8 lg ..
+    weights<RT>(s, a.scale2, less, p);
     // the widened values of every wave are in LDS
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     u32x4 g[2][4];
@@ -1128,11 +1128,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
 #pragma unroll
         for (int x = 0; x < RT; x++) r[x].o[d] = mma16(g[d & 1][j], p[x][j], r[x].o[d]);
     }
-    const uint32_t one = 0x3F803F80u;
 #pragma unroll
-    for (int j = 0; j < 4; j++)
-#pragma unroll
-      for (int x = 0; x < RT; x++) r[x].l = mma16(u32x4{one, one, one, one}, p[x][j], r[x].l);
+    for (int x = 0; x < RT; x++) r[x].l = add_weights(p[x], r[x].l);
     kp0 += flip;  // to the other buffer
     kp1 += flip;
     flip = -flip;

@@ -1,0 +1,63 @@
+"""Attention's accuracy where one bound on everything would hide it: weights
+many powers of two below the largest."""
+import math
+
+import pytest
+import torch
+
+import layer_reference as ref
+import microscaling_fp4_block_mx_amd as mx
+from test_layer_kv_gpu import World, i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    mx.load_library()
+    yield
+    torch.cuda.synchronize()
+
+
+def world_of(k, v, page=64):
+    """A cache that holds these keys and values [tokens, heads, dim] as one sequence."""
+    tokens, heads, dim = k.shape
+    w = World([tokens], heads, dim, page, 1)
+    cu, held = i32([0, tokens]), i32([0])
+    ref.append(w.cpu, k, v, w.table, cu, held)
+    mx.kv_append(w.gpu, k.cuda(), v.cuda(), w.table.cuda(), cu.cuda(), held.cuda())
+    w.same()
+    return w
+
+
+@pytest.mark.parametrize("new", [1, 100])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("below", [0, 6, 10, 13, 15, 17, 20, 22, 24, 28])
+def test_a_long_flat_tail(new, dim, below):
+    """One key takes (nearly) all, 999 keys share what is left evenly, each with a
+    weight of 2^-below of the first one's; they alone carry dims 2 and up.
+    All scores and values are exact, so a weight is off by its rounding (2^-8 of
+    itself as the header states it), its sum by the same, sums of 1,000 terms in
+    32 bits by 2^-14, the result by 2^-9: 2^-6 in all."""
+    tokens = 1000
+    k = torch.zeros(tokens, 1, dim)
+    k[0, 0, 0] = 16.0
+    v = torch.zeros(tokens, 1, dim)
+    v[1:, 0, 2:] = 1.0
+    v[0, 0, 1] = 1.0
+    w = world_of(k.bfloat16(), v.bfloat16())
+    q = torch.zeros(new, 2, dim, dtype=torch.bfloat16)
+    q[:, :, 0] = 1.0
+    scale = max(below, 1e-3) / 16 * math.log(2.0)
+    scale = float(torch.tensor(scale, dtype=torch.float32))
+    out = mx.kv_attention(q.cuda(), w.gpu, w.table.cuda(), i32([0, new]).cuda(),
+                          i32([tokens]).cuda(), scale).cpu().double()
+    weight = math.exp(-16 * scale)
+    tail = torch.arange(tokens - new, tokens).double()  # keys behind the first that a row sees
+    want = (tail * weight / (1 + tail * weight))[:, None, None]
+    assert bool(((out[:, :, 2:] - want).abs() <= 2.0 ** -6 * want).all()), \
+        float(((out[:, :, 2:] - want).abs() / want).max())
+    one = (1 / (1 + tail * weight))[:, None]
+    assert bool(((out[:, :, 1] - one).abs() <= 2.0 ** -6 * one).all())
