@@ -377,9 +377,18 @@ struct Rows {
 
 // Masks RT x 16 rows of 128 scores past `limit` where `masked` (tile t's
 // accumulator i is token places(t) + i) and moves the running maxima; `less`
-// is what a weight's exponent takes off. Branches are taken for all rows at once.
-template <int D, int RT, typename F>
-__device__ __forceinline__ void running_max(f32x4 (&s)[RT][8], Rows<D> (&r)[RT], float c, bool masked,
+// is what a weight's exponent, s c - less, takes off. Branches are taken for
+// all rows at once.
+//
+// FUSED: the exponent is one operation, which leaves the largest score's off 0
+// by what rounding took from the maximum: up to half a unit in its last place.
+// From 2^24 on that would be whole powers of two (all weights 0, or infinite),
+// so there the scores are multiplied by c as the maximum was, and c becomes 1.
+// Else every exponent is a product and a difference (few rows, whose arithmetic
+// waits for the cache anyway: the branch made 16 sequences of 16,000 tokens, 64
+// dims, 37 -> 41 us).
+template <int D, int RT, bool FUSED, typename F>
+__device__ __forceinline__ void running_max(f32x4 (&s)[RT][8], Rows<D> (&r)[RT], float &c, bool masked,
                                             const int (&limit)[RT], F places, float (&less)[RT]) {
   if (masked) {
 #pragma unroll
@@ -393,7 +402,7 @@ __device__ __forceinline__ void running_max(f32x4 (&s)[RT][8], Rows<D> (&r)[RT],
       }
   }
   float m[RT];
-  bool moved = false;
+  bool moved = false, large = false;
 #pragma unroll
   for (int x = 0; x < RT; x++) {
     float top = s[x][0][0];
@@ -405,6 +414,14 @@ __device__ __forceinline__ void running_max(f32x4 (&s)[RT][8], Rows<D> (&r)[RT],
     moved |= m[x] != r[x].m;
     // nothing seen yet: weights are 0
     less[x] = m[x] == -__builtin_inff() ? 0.0f : m[x];
+    large |= FUSED && __builtin_fabsf(less[x]) >= 0x1p24f;
+  }
+  if (FUSED && __any(large)) {
+#pragma unroll
+    for (int x = 0; x < RT; x++)
+#pragma unroll
+      for (int t = 0; t < 8; t++) s[x][t] *= c;
+    c = 1.0f;
   }
   if (__any(moved)) {
 #pragma unroll
@@ -420,7 +437,7 @@ __device__ __forceinline__ void running_max(f32x4 (&s)[RT][8], Rows<D> (&r)[RT],
 
 // Weights of RT x 16 rows and 128 tokens, rounded to bfloat16: tiles 2 j and
 // 2 j + 1 are the eight tokens of a lane in the second product's step j.
-template <int RT>
+template <int RT, bool FUSED>
 __device__ __forceinline__ void weights(const f32x4 (&s)[RT][8], float c, const float (&less)[RT],
                                         u32x4 (&p)[RT][4]) {
 #pragma unroll
@@ -430,7 +447,7 @@ __device__ __forceinline__ void weights(const f32x4 (&s)[RT][8], float c, const 
       float e[4];
 #pragma unroll
       for (int i = 0; i < 4; i++)
-        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][i], c, -less[x]));
+        e[i] = __builtin_amdgcn_exp2f(FUSED ? __builtin_fmaf(s[x][t][i], c, -less[x]) : s[x][t][i] * c - less[x]);
       p[x][t >> 1][2 * (t & 1)] = pack_bf16(e[0], e[1]);
       p[x][t >> 1][2 * (t & 1) + 1] = pack_bf16(e[2], e[3]);
     }
@@ -729,13 +746,13 @@ __global__ __launch_bounds__(256, D == 128 && RT == 2 ? 1 : 2) void k_attn_rows(
       }
     }
     int limit[RT];
-    float less[RT];
+    float less[RT], c = a.scale2;
 #pragma unroll
     for (int x = 0; x < RT; x++) limit[x] = seen[x] - 1 - tile * 128 - 16 * lg;
-    running_max<D, RT>(s, r, a.scale2, tile * 128 + 128 > b.seen0, limit,
+    running_max<D, RT, false>(s, r, c, tile * 128 + 128 > b.seen0, limit,
                        [](int t) { return 64 * (t >> 2) + 4 * (t & 3); }, less);
     u32x4 p[RT][4];
-    weights<RT>(s, a.scale2, less, p);
+    weights<RT, false>(s, c, less, p);
     const uint32_t vb0 = sc >> 16 & 255u, vb1 = sc >> 24;
     const bool far = __any(max(vb0, vb1) > 246u);
 #pragma unroll
@@ -1105,13 +1122,13 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
 #pragma unroll
       for (int t = 0; t < 8; t++) asm volatile("" : "+v"(s[x][t]));
     int limit[RT];
-    float less[RT];
+    float less[RT], c = a.scale2;
 #pragma unroll
     for (int x = 0; x < RT; x++) limit[x] = seen[x] - 1 - tile * 128 - 8 * lg;
-    running_max<D, RT>(s, r, a.scale2, tile * 128 + 128 > b.seen0, limit,
+    running_max<D, RT, true>(s, r, c, tile * 128 + 128 > b.seen0, limit,
                        [](int t) { return 32 * (t >> 1) + 4 * (t & 1); }, less);
     u32x4 p[RT][4];  // of tokens 32 j + 8 lg ..
-    weights<RT>(s, a.scale2, less, p);
+    weights<RT, true>(s, c, less, p);
     // the widened values of every wave are in LDS
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     u32x4 g[2][4];

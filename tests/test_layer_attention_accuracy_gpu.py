@@ -1,5 +1,5 @@
 """Attention's accuracy where one bound on everything would hide it: weights
-many powers of two below the largest."""
+many powers of two below the largest, scores too large for a weight's exponent."""
 import math
 
 import pytest
@@ -61,3 +61,25 @@ def test_a_long_flat_tail(new, dim, below):
         float(((out[:, :, 2:] - want).abs() / want).max())
     one = (1 / (1 + tail * weight))[:, None]
     assert bool(((out[:, :, 1] - one).abs() <= 2.0 ** -6 * one).all())
+
+
+@pytest.mark.parametrize("new", [1, 100])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 12, 2.0 ** 18, 2.0 ** 24, 2.0 ** 40])
+def test_scores_of_any_size(new, dim, size):
+    """The first key's score is far above every other one's, so the result is its
+    value, however large the scores are (up to 2^92 here): half a step of bf16.
+    The other scores are negative, the first one positive and above 20 dim."""
+    g = torch.Generator().manual_seed(dim)
+    tokens = 300
+    k = -torch.rand(tokens, 2, dim, generator=g).clamp(min=0.25)
+    k[0] = 8.0
+    v = torch.randn(tokens, 2, dim, generator=g)
+    w = world_of((k * size).bfloat16(), v.bfloat16())
+    q = (torch.rand(new, 4, dim, generator=g).clamp(min=0.3) * 8 * size).bfloat16()
+    out = mx.kv_attention(q.cuda(), w.gpu, w.table.cuda(), i32([0, new]).cuda(),
+                          i32([tokens]).cuda(), 1.0).cpu().double()
+    page = w.table[0, 0]
+    first = w.cpu[2][page, :, :, 0].view(ref.F8).double() * ref.pow2(w.cpu[3][page].double())[:, None]
+    want = first.repeat_interleave(2, 0).expand_as(out)
+    assert bool(((out - want).abs() <= 2.0 ** -8 * want.abs()).all())
