@@ -167,8 +167,10 @@ static mx_status_t check_product(int64_t m, int64_t n, int64_t k, int block, int
   if (m < 0 || m > INT32_MAX || n < 0 || n > INT32_MAX || k <= 0 || k % 32 != 0 ||
       k > kMaxProductK)
     return MX_ERR_SHAPE;
-  // the output's elements, and the tiles of 64 x 64 of one launch
-  if (m > 0 && n > 0 && (n > INT64_MAX / 8 / m || ((m + 63) / 64) * ((n + 63) / 64) > INT32_MAX))
+  // the output's elements, and one launch's tiles of 128 x 128, 256 threads
+  // each, whose threads (and those of tiles of 256 x 256) are fewer than 2^32
+  if (m > 0 && n > 0 &&
+      (n > INT64_MAX / 8 / m || ((m + 127) / 128) * ((n + 127) / 128) > (1 << 24) - 2))
     return MX_ERR_SHAPE;
   return MX_OK;
 }

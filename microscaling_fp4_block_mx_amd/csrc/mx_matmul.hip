@@ -567,7 +567,8 @@ template <int CT, bool BLK32, bool EXACT>
 __global__ __launch_bounds__(512) void k_matmul8_rows(const MatArgs g) {
   constexpr int U = 4, WAVES = 8;
   __shared__ float part[WAVES][16][16 * CT + 1];
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * CT);
+  const int64_t n0 = ((int64_t)blockIdx.z * gridDim.x + blockIdx.x) * (16 * CT);
+  if (n0 >= g.n) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
   const int all = (int)((g.k + 127) >> 7), per = (all + WAVES - 1) / WAVES;
@@ -723,7 +724,9 @@ static Plan plan_of(int64_t m, int64_t n, int64_t k, int out_bf16) {
 template <bool BLK32, bool EXACT>
 static hipError_t launch(const Plan &p, MatArgs g, hipStream_t st) {
   if (p.columns) {
-    const dim3 grid((uint32_t)((g.n + 16 * p.columns - 1) / (16 * p.columns)), (uint32_t)((g.m + 15) / 16));
+    // a grid's dimension holds fewer than 2^32 threads
+    const int64_t columns = (g.n + 16 * p.columns - 1) / (16 * p.columns), x = std::min<int64_t>(columns, 1 << 22);
+    const dim3 grid((uint32_t)x, (uint32_t)((g.m + 15) / 16), (uint32_t)((columns + x - 1) / x));
     if (p.columns == 1) k_matmul8_rows<1, BLK32, EXACT><<<grid, 512, 0, st>>>(g);
     else k_matmul8_rows<2, BLK32, EXACT><<<grid, 512, 0, st>>>(g);
     return hipGetLastError();
