@@ -52,7 +52,8 @@ struct AppendArgs {
   int64_t k_stride, v_stride;  // elements between tokens
   mx_kv_cache_t c;
   mx_kv_batch_t b;
-  int shift;  // log2(page)
+  int shift;        // log2(page)
+  uint32_t blocks;  // units times heads
 };
 
 // Which sequence a unit of work belongs to: sequence i owns units from
@@ -105,11 +106,13 @@ __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
   // so that the rows that an instruction writes to fall on different banks
   extern __shared__ __attribute__((aligned(16))) uint8_t vt[];
   __shared__ uint32_t am[2][T / 64];
-  const int unit = blockIdx.x / a.c.heads, head = blockIdx.x % a.c.heads;
+  const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x;
+  if (block >= a.blocks) return;
+  const int unit = block / a.c.heads, head = block % a.c.heads;
   const int P = a.c.page, D = a.c.dim;
   const int i = find_sequence(a.b.cu, a.b.batch, P, 2, unit);
   const int c0 = a.b.cu[i], n = a.b.cu[i + 1] - c0, held = a.b.lengths[i];
-  const int j = (held >> a.shift) + unit - (c0 / P + 2 * i);  // page of the sequence
+  const int j = (held >> a.shift) + (unit - (c0 / P + 2 * i));  // page of the sequence
   if (n <= 0 || held < 0 || j >= a.b.width || ((int64_t)j << a.shift) >= (int64_t)held + n) return;
   const int kept = max(0, held - (j << a.shift));            // slots that stay
   const int end = min((int64_t)P, (int64_t)held + n - ((int64_t)j << a.shift));  // slots in use after
@@ -643,9 +646,12 @@ __global__ __launch_bounds__(256, D == 128 && RT == 2 ? 1 : 2) void k_attn_rows(
   __shared__ uint32_t pages[W][64], bytes[W][64];
   __shared__ float merge_ml[W][16][2];
   static_assert(S >= 16 * (D + 4) * 4, "the waves' sums go where the codes were");
+  // a grid's third dimension counts splits, or, where there are none, what the
+  // first one has no room for
+  const int unit = a.splits > 1 ? blockIdx.x : blockIdx.z * gridDim.x + blockIdx.x;
   Block b;
-  if (!find_block(a, blockIdx.x, b)) return;
-  const int head = blockIdx.y, split = blockIdx.z;
+  if (unit >= a.units || !find_block(a, unit, b)) return;
+  const int head = blockIdx.y, split = a.splits > 1 ? blockIdx.z : 0;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
   const int end = min(b.len, b.seen0 + b.count - 1);  // keys any row sees
@@ -991,9 +997,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
   // kv heads fastest: the eight XCDs, which are dealt workgroups in turn,
   // keep to few heads each. The last blocks of a sequence see the most keys:
   // they start first.
-  const int head = blockIdx.x % a.c.heads;
+  const uint32_t block = blockIdx.z * gridDim.x + blockIdx.x;
+  const int head = block % a.c.heads, from_last = block / a.c.heads;
   Block b;
-  if (!find_block(a, a.units - 1 - (int)(blockIdx.x / a.c.heads), b)) return;
+  if (from_last >= a.units || !find_block(a, a.units - 1 - from_last, b)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
   const int end = min(b.len, b.seen0 + b.count - 1);
@@ -1185,6 +1192,16 @@ static int log2_of(int x) {
   return s;
 }
 
+// Workgroups along one dimension of a grid, whose threads are fewer than 2^32,
+// and along another for the rest.
+struct Spread {
+  uint32_t first, second;
+};
+static Spread spread(int64_t blocks) {
+  const int64_t first = std::min<int64_t>(blocks, 1 << 22);
+  return {(uint32_t)first, (uint32_t)((blocks + first - 1) / first)};
+}
+
 struct AttnPlan {
   bool few;
   int rt, block_tokens, chunk, splits;
@@ -1236,8 +1253,10 @@ using namespace mxl;
 hipError_t mxi_launch_kv_append(const void *k, const void *v, int bf16, int64_t k_stride,
                                 int64_t v_stride, const mx_kv_cache_t &cache,
                                 const mx_kv_batch_t &batch, hipStream_t st) {
-  const AppendArgs a = {k, v, k_stride, v_stride, cache, batch, log2_of(cache.page)};
-  const dim3 grid((uint32_t)((batch.tokens / cache.page + 2 * (int64_t)batch.batch) * cache.heads));
+  const int64_t blocks = (batch.tokens / cache.page + 2 * (int64_t)batch.batch) * cache.heads;
+  const AppendArgs a = {k, v, k_stride, v_stride, cache, batch, log2_of(cache.page), (uint32_t)blocks};
+  const Spread xy = spread(blocks);
+  const dim3 grid(xy.first, xy.second);
   const size_t lds = (size_t)cache.dim * (cache.page + 4);
   // a few new tokens per sequence: one wave a page, so that all pages are at
   // work at once (256 sequences of one token: 8.5 us; four
@@ -1263,9 +1282,11 @@ hipError_t mxi_launch_kv_attention(const void *q, int64_t q_stride, int q_heads,
                       q_heads / cache.heads, cache, batch, log2_of(cache.page), p.block_tokens,
                       p.chunk, p.splits, (int)p.units, scale * 1.44269504088896340736f,
                       reinterpret_cast<uint16_t *>(out), reinterpret_cast<float *>(workspace)};
-  const dim3 grid((uint32_t)p.units, (uint32_t)cache.heads, (uint32_t)p.splits);
+  // (few rows are split for at most 1,024 sequences)
+  const Spread xz = spread(p.few ? p.units : p.units * cache.heads);
+  const dim3 grid(xz.first, (uint32_t)cache.heads, p.splits > 1 ? (uint32_t)p.splits : xz.second);
   if (!p.few) {
-    const dim3 tgrid((uint32_t)(p.units * cache.heads), (uint32_t)p.splits);
+    const dim3 tgrid(xz.first, (uint32_t)p.splits, xz.second);
     if (cache.dim == 64) k_attn_tiles<64><<<tgrid, 256, 0, st>>>(a);
     else k_attn_tiles<128><<<tgrid, 256, 0, st>>>(a);
   } else if (cache.dim == 64) {

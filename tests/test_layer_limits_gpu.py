@@ -44,3 +44,52 @@ def test_tiles_past_the_limit_are_refused():
     # the checks behind the shape's: two rows are fine, operands that overlap are not
     assert mx.mx_matmul_mxfp8(A, B, C, D, 2, 2 ** 31 - 256, 32, 32, mx.MX_BF16, A, None, 0,
                               None) == mx.MX_ERR_ALIAS
+
+
+def test_append_to_three_of_very_many_sequences():
+    """2^24 sequences, all but three of them idle."""
+    batch, heads, dim, page = 1 << 24, 8, 64, 32
+    at = [5, batch // 2, batch - 1]
+    cache, few = mx.kv_cache(4, heads, dim, page), mx.kv_cache(4, heads, dim, page)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    k, v = (torch.randn(3, heads, dim, generator=g, device="cuda").bfloat16() for _ in "kv")
+    new = torch.zeros(batch, dtype=torch.int32, device="cuda")
+    new[at] = 1
+    cu = torch.nn.functional.pad(new.cumsum(0, dtype=torch.int32), (1, 0))
+    table = torch.full((batch, 1), 3, dtype=torch.int32, device="cuda")
+    table[at] = torch.tensor([[2], [0], [1]], dtype=torch.int32, device="cuda")
+    held = torch.zeros(batch, dtype=torch.int32, device="cuda")
+    mx.kv_append(cache, k, v, table, cu, held)
+    mx.kv_append(few, k, v, table[at], torch.arange(4, dtype=torch.int32, device="cuda"), held[:3])
+    for a, b in zip(cache, few):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("heads,group", [(1, 1), (16, 33)])
+def test_attention_over_very_many_sequences(heads, group):
+    """2^24 sequences of one token that share two pages (the few-rows kernel),
+    and 2^20 with 16 kv heads, all but four of them idle, whose queries are
+    more than that kernel takes to a kv head: what a call of four gives."""
+    batch, dim, page, kinds = (1 << 24) // heads, 64, 32, 4
+    cache = mx.kv_cache(2, heads, dim, page)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    k, v = (torch.randn(64, heads, dim, generator=g, device="cuda").bfloat16() for _ in "kv")
+    mx.kv_append(cache, k, v, torch.tensor([[1, 0]], **i32), torch.tensor([0, 64], **i32),
+                 torch.zeros(1, **i32))
+    q = torch.randn(kinds, heads * group, dim, generator=g, device="cuda").bfloat16()
+    lengths = torch.tensor([64, 1, 33, 50], **i32)
+    table = torch.tensor([[1, 0]], **i32).repeat(kinds, 1)
+    cu = torch.arange(kinds + 1, **i32)
+    want = mx.kv_attention(q, cache, table, cu, lengths)
+    assert bool(torch.isfinite(want).all())
+    times = batch // kinds
+    if group == 1:
+        got = mx.kv_attention(q.repeat(times, 1, 1), cache, table.repeat(times, 1),
+                              torch.arange(batch + 1, **i32), lengths.repeat(times))
+        assert bool((got.view(times, *want.shape) == want).all())
+    else:
+        many = torch.full((batch + 1,), kinds, **i32)
+        many[:kinds + 1] = cu
+        got = mx.kv_attention(q, cache, table.repeat(times, 1), many, lengths.repeat(times))
+        assert torch.equal(got, want)
