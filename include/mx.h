@@ -411,8 +411,9 @@ typedef struct {
  * lists the pages of sequence i in order; its new tokens are rows cu[i] ..
  * cu[i+1] - 1 of the token arrays (cu[0] = 0, cu[batch] = tokens); lengths[i]
  * is its length. A sequence may have no new tokens. Page numbers outside the
- * cache are not followed (they are clamped to its last page). Pages that are
- * written must belong to one sequence. */
+ * cache are not followed: tokens appended there are dropped, attention reads
+ * the cache's last page instead. Pages that are written must belong to one
+ * sequence. */
 typedef struct {
   const int32_t *table;
   const int32_t *cu;

@@ -116,7 +116,8 @@ __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
   if (n <= 0 || held < 0 || j >= a.b.width || ((int64_t)j << a.shift) >= (int64_t)held + n) return;
   const int kept = max(0, held - (j << a.shift));            // slots that stay
   const int end = min((int64_t)P, (int64_t)held + n - ((int64_t)j << a.shift));  // slots in use after
-  const int64_t id = clamp_page(a.b.table[(int64_t)i * a.b.width + j], a.c.pages);
+  const int64_t id = a.b.table[(int64_t)i * a.b.width + j];
+  if (id < 0 || id >= a.c.pages) return;  // no page: its tokens are dropped
   const int64_t src0 = (int64_t)c0 + ((int64_t)j << a.shift) - held;  // token of slot 0
   const int64_t most = a.b.tokens - 1;
   const int64_t at = id * a.c.heads + head;

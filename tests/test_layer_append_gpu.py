@@ -1,0 +1,45 @@
+"""Append where its inputs are not of the ordinary kind, bit for bit against
+the reference."""
+import pytest
+import torch
+
+import layer_reference as ref
+import microscaling_fp4_block_mx_amd as mx
+from test_layer_kv_gpu import World, i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    mx.load_library()
+    yield
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [3, 2, 1], [90, 70, 50]])
+def test_pages_outside_the_cache_are_not_written(new):
+    """An entry that names no page (-1, or past the last one) drops its tokens;
+    every page of the cache keeps what it held."""
+    page = 32
+    w = World([128] * 3, 2, 64, page, 21)
+    held = [60, 31, 10]
+    w.append(held, [0] * 3)
+    pool = w.cpu[0].shape[0]
+    for bad in (-1, pool, 2 ** 31 - 1, -2 ** 31):
+        table = w.table.clone()
+        for i in range(3):
+            table[i, held[i] // page] = bad  # where the sequence's new tokens begin
+        cu = [0]
+        for n in new:
+            cu.append(cu[-1] + n)
+        k, v = w.numbers(cu[-1], 2), w.numbers(cu[-1], 2)
+        # the reference has one page more, which takes what names no page
+        more = [torch.cat([t, torch.zeros_like(t[:1])]) for t in w.cpu]
+        ref.append(more, k, v, torch.where(table == bad, pool, table), i32(cu), i32(held))
+        for mine, t in zip(w.cpu, more):
+            mine.copy_(t[:pool])
+        mx.kv_append(w.gpu, k.cuda(), v.cuda(), table.cuda(), i32(cu).cuda(), i32(held).cuda())
+        w.same()
