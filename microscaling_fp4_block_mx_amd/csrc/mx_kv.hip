@@ -68,7 +68,7 @@ __device__ __forceinline__ int find_sequence(const int32_t *cu, int batch, int p
     const int step = (n + 63) >> 6, at = lo + lane * step;
     const bool below = lane * step < n && cu[at] / per + extra * at <= unit;
     // the lanes that hold are the first ones; sequence lo always does
-    const int skip = max(__popcll(__ballot(below)) - 1, 0) * step;
+    const int skip = max((int)__popcll(__ballot(below)) - 1, 0) * step;
     lo += skip;
     n = min(step, n - skip);
   }
@@ -113,7 +113,9 @@ __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
   const int i = find_sequence(a.b.cu, a.b.batch, P, 2, unit);
   const int c0 = a.b.cu[i], n = a.b.cu[i + 1] - c0, held = a.b.lengths[i];
   const int j = (held >> a.shift) + (unit - (c0 / P + 2 * i));  // page of the sequence
-  if (n <= 0 || held < 0 || j >= a.b.width || ((int64_t)j << a.shift) >= (int64_t)held + n) return;
+  // (a unit before the first sequence's has pages before the sequence's first)
+  if (n <= 0 || held < 0 || j < held >> a.shift || j >= a.b.width || ((int64_t)j << a.shift) >= (int64_t)held + n)
+    return;
   const int kept = max(0, held - (j << a.shift));            // slots that stay
   const int end = min((int64_t)P, (int64_t)held + n - ((int64_t)j << a.shift));  // slots in use after
   const int64_t id = a.b.table[(int64_t)i * a.b.width + j];
