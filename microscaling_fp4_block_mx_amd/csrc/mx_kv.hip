@@ -214,15 +214,18 @@ __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
          [&](int c) { return kept - c % n * 16; }, (int)(sv - was_v), sv == 255u);
     __syncthreads();  // before the new tokens' bytes of the same words
   }
+  // a kept byte may be any: above 246 every finite number is below 448 scales
+  auto limit = [](uint32_t b) { return b > 246u ? 0x1.fffffep127f : limit8(b); };
+  const float most_k = limit(sk), most_v = limit(sv);
   const int row = P + 4;
   auto put = [&](const Raw<BF16> &k, const Raw<BF16> &v, int it) {
     float f[8];
     if (mine(it)) {
       widen<BF16>(k, f);
-      *reinterpret_cast<u32x2 *>(kc + slot_of(it) * D + dim_of(it)) = encode8(f, sk);
+      *reinterpret_cast<u32x2 *>(kc + slot_of(it) * D + dim_of(it)) = encode8(f, sk, most_k);
     }
     widen<BF16>(v, f);
-    const u32x2 w = encode8(f, sv);
+    const u32x2 w = encode8(f, sv, most_v);
     // four lanes' tokens t = 2 b + a, eight dims each, become two dims of four
     // tokens: halves of the dims change places over b, then quarters over a
     const auto x = __builtin_amdgcn_permlane32_swap(w[0], w[1], false, false);

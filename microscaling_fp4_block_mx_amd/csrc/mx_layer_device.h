@@ -109,17 +109,21 @@ __device__ __forceinline__ uint32_t amax8(const float (&f)[8]) {
   for (int j = 0; j < 8; j++) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
   return m;
 }
+// 448 at scale byte s, where 32 bits hold it (s <= 246, as of finite numbers).
+__device__ __forceinline__ float limit8(uint32_t s) {
+  return __uint_as_float(((s + 8u) << 23) | 0x600000u);
+}
 // Eight codes at scale byte s: nearest, ties to even, saturating at 448
-// (clamped first: the convert turns larger values into NaN); in a block with
-// s = 255 the sign bits alone.
-__device__ __forceinline__ u32x2 encode8(const float (&f)[8], uint32_t s) {
+// (clamped to `lim` first: the convert turns larger values into NaN); in a
+// block with s = 255 the sign bits alone.
+__device__ __forceinline__ u32x2 encode8(const float (&f)[8], uint32_t s, float lim) {
   if (__builtin_expect(s == 255u, 0)) {
     uint32_t b[2] = {0, 0};
 #pragma unroll
     for (int j = 0; j < 8; j++) b[j >> 2] |= (__float_as_uint(f[j]) >> 31) << (8 * (j & 3) + 7);
     return u32x2{b[0], b[1]};
   }
-  const float sc = __uint_as_float(s << 23), lim = __uint_as_float(((s + 8u) << 23) | 0x600000u);
+  const float sc = __uint_as_float(s << 23);
   float c[8];
 #pragma unroll
   for (int j = 0; j < 8; j++) c[j] = __builtin_amdgcn_fmed3f(f[j], -lim, lim);
@@ -129,6 +133,9 @@ __device__ __forceinline__ u32x2 encode8(const float (&f)[8], uint32_t s) {
   b = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(b, c[4], c[5], sc, false);
   b = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(b, c[6], c[7], sc, true);
   return u32x2{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
+}
+__device__ __forceinline__ u32x2 encode8(const float (&f)[8], uint32_t s) {
+  return encode8(f, s, limit8(s));
 }
 
 }  // namespace mxl

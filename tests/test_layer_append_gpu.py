@@ -43,3 +43,18 @@ def test_pages_outside_the_cache_are_not_written(new):
             mine.copy_(t[:pool])
         mx.kv_append(w.gpu, k.cuda(), v.cuda(), table.cuda(), i32(cu).cuda(), i32(held).cuda())
         w.same()
+
+
+@pytest.mark.parametrize("new", [1, 20])
+@pytest.mark.parametrize("byte", [246, 247, 250, 254])
+def test_kept_pages_with_the_largest_scales(byte, new):
+    """New tokens enter a page whose byte is one that no quantizer here makes
+    (a cache filled by other means) at that byte, like any others."""
+    w = World([64], 1, 64, 32, 23)
+    w.append([5], [0], torch.float32)
+    for t, g in zip(w.cpu, w.gpu):
+        if t.dim() == 2:
+            t.fill_(byte)
+            g.fill_(byte)
+    w.append([new], [5], torch.float32, by=2.0 ** 124)
+    w.same()
