@@ -453,7 +453,8 @@ mx_status_t mx_kv_append(const void *k, const void *v, mx_dtype_t dtype, int64_t
  * width * page); a larger length is still right, only slower. workspace:
  * mx_kv_attention_workspace_size(...) bytes, 16-byte aligned (partial results
  * where a sequence is split over workgroups), 0 bytes (NULL allowed) where
- * none is. */
+ * none is. The size for a max_length is enough for a call with it, or with a
+ * smaller one, over a table of any width; that for 0 for every call. */
 size_t mx_kv_attention_workspace_size(int64_t tokens, int batch, int q_heads, int heads, int dim,
                                       int64_t max_length);
 mx_status_t mx_kv_attention(const void *q, int64_t q_stride, int q_heads,

@@ -1211,6 +1211,7 @@ static Spread spread(int64_t blocks) {
 struct AttnPlan {
   bool few;
   int rt, block_tokens, chunk, splits;
+  int most_splits;  // of any sequence up to max_length
   int64_t units;
 };
 static AttnPlan attn_plan(int64_t tokens, int batch, int q_heads, int heads, int64_t max_length) {
@@ -1225,7 +1226,11 @@ static AttnPlan attn_plan(int64_t tokens, int batch, int q_heads, int heads, int
   p.units = tokens / p.block_tokens + batch;
   const int tiles = (int)((max_length + 127) / 128);
   p.chunk = tiles > 0 ? tiles : 1;
-  p.splits = 1;
+  p.splits = p.most_splits = 1;
+  // No split has fewer than eight tiles, and there are at most `want`: a bound
+  // that grows with the length, where the number of splits itself does not
+  // (chunks are rounded up).
+  auto bound = [&](int64_t want) { return (int)std::max<int64_t>(1, std::min<int64_t>(want, (tiles + 7) / 8)); };
   if (p.few) {
     // enough workgroups to fill the card four times over, since sequences
     // shorter than the longest leave splits empty (16 ragged ones of up to
@@ -1236,6 +1241,7 @@ static AttnPlan attn_plan(int64_t tokens, int batch, int q_heads, int heads, int
     const int64_t c = std::max<int64_t>(8, (tiles + want - 1) / want);
     p.chunk = (int)((c + 3) / 4 * 4);
     p.splits = std::max(1, (tiles + p.chunk - 1) / p.chunk);
+    p.most_splits = bound(want);
   } else {
     // two workgroups a compute unit where blocks of rows leave half of that
     // empty (1 x 512 tokens of 4,096, 32 query heads on 8: 85 us in one piece,
@@ -1247,6 +1253,7 @@ static AttnPlan attn_plan(int64_t tokens, int batch, int q_heads, int heads, int
       const int64_t c = std::max<int64_t>(8, (tiles + want - 1) / want);
       p.chunk = (int)((c + 1) & ~1);
       p.splits = std::max(1, (tiles + p.chunk - 1) / p.chunk);
+      p.most_splits = bound(want);
     }
   }
   return p;
@@ -1276,7 +1283,7 @@ hipError_t mxi_launch_kv_append(const void *k, const void *v, int bf16, int64_t 
 size_t mxi_kv_attention_workspace(int64_t tokens, int batch, int q_heads, int heads, int dim,
                                   int64_t max_length) {
   const AttnPlan p = attn_plan(tokens, batch, q_heads, heads, max_length);
-  return p.splits > 1 ? (size_t)tokens * q_heads * p.splits * (dim + 4) * sizeof(float) : 0;
+  return p.most_splits > 1 ? (size_t)tokens * q_heads * p.most_splits * (dim + 4) * sizeof(float) : 0;
 }
 
 hipError_t mxi_launch_kv_attention(const void *q, int64_t q_stride, int q_heads,

@@ -36,6 +36,7 @@ hipError_t mxi_launch_matmul8(const uint8_t *a, const uint8_t *a_scales, const u
 hipError_t mxi_launch_kv_append(const void *k, const void *v, int bf16, int64_t k_stride,
                                 int64_t v_stride, const mx_kv_cache_t &cache,
                                 const mx_kv_batch_t &batch, hipStream_t st);
+// Enough for a launch with this max_length or any smaller one.
 size_t mxi_kv_attention_workspace(int64_t tokens, int batch, int q_heads, int heads, int dim,
                                   int64_t max_length);
 hipError_t mxi_launch_kv_attention(const void *q, int64_t q_stride, int q_heads,

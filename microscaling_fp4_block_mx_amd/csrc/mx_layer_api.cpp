@@ -243,7 +243,9 @@ size_t mx_kv_attention_workspace_size(int64_t tokens, int batch, int q_heads, in
                                       int64_t max_length) {
   if (check_attention(tokens, batch, q_heads, heads, dim, max_length) != MX_OK || tokens == 0)
     return 0;
-  return mxi_kv_attention_workspace(tokens, batch, q_heads, heads, dim, max_length);
+  // the call plans for the table's room where that is less: the size grows with the length
+  return mxi_kv_attention_workspace(tokens, batch, q_heads, heads, dim,
+                                    max_length == 0 ? INT32_MAX : max_length);
 }
 
 mx_status_t mx_kv_attention(const void *q, int64_t q_stride, int q_heads,
