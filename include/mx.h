@@ -351,9 +351,11 @@ mx_status_t mx_quantize_mxfp8_blocks(const void *x, mx_dtype_t x_dtype, int64_t 
  * sqrt(sum(h^2) / k + eps), quantized along the row to codes [rows, k] and
  * scales [rows, ceil(k / block)]. h_out (NULL to leave it out; only with a
  * residual) receives h rounded to the dtype; it may equal x or residual. x,
- * residual, weight [k] and h_out share one dtype. The sum and y are fp32; h
- * enters them unrounded. k <= 65536, rows < 2^31. A row holding NaN or an
- * infinity gives blocks with scale 255. */
+ * residual, weight [k] and h_out share one dtype. The sum and y are fp32 (64
+ * bits where the squares leave their range, so that a finite h may be of any
+ * size); h enters them unrounded. k <= 65536, rows < 2^31. A row holding NaN,
+ * or zeros alone with eps = 0, gives blocks with scale 255; one holding an
+ * infinity gives 255 to the blocks with it and zeros elsewhere. */
 mx_status_t mx_rmsnorm_mxfp8(const void *x, const void *residual, const void *weight,
                              mx_dtype_t dtype, int64_t rows, int64_t k, float eps, int block,
                              uint8_t *codes, uint8_t *scales, void *h_out, void *stream);

@@ -53,6 +53,26 @@ __device__ __forceinline__ double block_sum(float a, float *part) {
   return t;
 }
 
+// The same of a value that is in 64 bits from the start.
+template <int T>
+__device__ __forceinline__ double block_sum64(double a, double *part) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) a += __shfl_xor(a, d);
+  if constexpr (T == 64) return a;
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
+  __syncthreads();
+  double t = part[0];
+#pragma unroll
+  for (int i = 1; i < T / 64; i++) t += part[i];
+  return t;
+}
+
+// Whether a sum of squares in 32 bits is none to go by: squares overflowed, or
+// are so small that bits of them were lost (`floor`: what is added to the sum).
+__device__ __forceinline__ bool out_of_range(float sum, float floor) {
+  return !(sum < 0x1p127f) || sum + floor < 0x1p-80f;
+}
+
 // T threads of N items (eight elements) hold a row. 8191 x 8192 bf16 with a
 // residual, blocks of 32: 75 us, 6.3 TB/s of 7 bytes an element; 5 x 4096,
 // where one trip to memory and one sum are all there is: 3.4 us.
@@ -62,6 +82,7 @@ __global__ __launch_bounds__(T) void k_rmsnorm(const void *x, const void *residu
                                                int wide, uint8_t *__restrict__ codes,
                                                uint8_t *__restrict__ scales, void *h) {
   __shared__ float part[T / 64];
+  __shared__ double part64[T / 64];
   const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
   if (row >= rows) return;
   const int items = k >> 3;
@@ -104,7 +125,27 @@ __global__ __launch_bounds__(T) void k_rmsnorm(const void *x, const void *residu
       for (int j = 0; j < 8; j++) f[u][j] = 0.0f;
     }
   }
-  const double exact = 1.0 / __builtin_sqrt(block_sum<T>(ss, part) / k + eps);
+  double sum = block_sum<T>(ss, part);
+  int up = 0;  // the row is held times 2^up
+  if (__builtin_expect(out_of_range((float)sum, eps * k), 0)) {
+    // the same for the whole workgroup: the sum again in 64 bits, whose root
+    // decides the power of two that brings the row near 1
+    double wide = 0.0;
+#pragma unroll
+    for (int u = 0; u < N; u++)
+#pragma unroll
+      for (int j = 0; j < 8; j++) wide += (double)f[u][j] * f[u][j];
+    sum = block_sum64<T>(wide, part64);
+    const double mean = sum / k + eps;
+    if (mean > 0.0 && mean < __builtin_inf()) {  // neither zeros, NaN nor infinities
+      up = -(__builtin_amdgcn_frexp_exp(mean) / 2);
+#pragma unroll
+      for (int u = 0; u < N; u++)
+#pragma unroll
+        for (int j = 0; j < 8; j++) f[u][j] = __builtin_ldexpf(f[u][j], up);
+    }
+  }
+  const double exact = __builtin_ldexp(1.0 / __builtin_sqrt(sum / k + eps), -up);
   const float s = (float)exact, s_low = (float)(exact - s);
   const int lanes = wide ? 16 : 4;  // lanes that share a block (wave-uniform)
   const int64_t nb = (items + lanes - 1) / lanes;

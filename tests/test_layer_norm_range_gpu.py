@@ -1,0 +1,63 @@
+"""The norm on rows whose squares leave the range of 32 bits:
+large ones, and with eps = 0 small ones."""
+import math
+
+import pytest
+import torch
+
+import layer_reference as ref
+import microscaling_fp4_block_mx_amd as mx
+from test_layer_norm_gpu import DT, Y_ERR, check_codes
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    mx.load_library()
+    yield
+    torch.cuda.synchronize()
+
+
+SIZES = [1e18, 3e19, 1e25, 1e37]
+SMALL = [1e-18, 1e-20, 1e-25, 1e-36]
+
+
+def rows_of(k, sizes, seed):
+    """Normal rows of these sizes, an ordinary one between any two."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(2 * len(sizes), k, generator=g)
+    for i, s in enumerate(sizes):
+        x[2 * i] *= s
+    return x
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("k", [32, 160, 4096, 16384 + 32])
+@pytest.mark.parametrize("eps", [1e-6, 0.0])
+def test_norm_of_large_and_small_rows(k, eps, dtype):
+    x = rows_of(k, SIZES + (SMALL if eps == 0.0 else []), k).to(DT[dtype])
+    w = (torch.randn(k, generator=torch.Generator().manual_seed(1)) * 0.3 + 1).to(DT[dtype])
+    r = (x * 0.25).contiguous()
+    for res in (None, r):
+        for reps in (1, 200):  # one item a thread, and four
+            a = x.repeat(reps, 1).cuda()
+            b = None if res is None else res.repeat(reps, 1).cuda()
+            c, s, _ = mx.rmsnorm_mxfp8(a, w.cuda(), eps, b, 32)
+            n = x.shape[0]
+            for at in (0, n * (reps - 1)):
+                _, y = ref.norm(x, w, eps, res)
+                check_codes(c[at:at + n].cpu(), s[at:at + n].cpu(), y, 32, (k, eps, dtype))
+
+
+def test_non_finite_rows_stay_as_they_were():
+    x = torch.ones(5, 64)
+    x[0, 3], x[1, 3], x[2], x[3, 5] = math.inf, math.nan, 3e38, 3e38
+    c, s, _ = mx.rmsnorm_mxfp8(x.cuda(), torch.ones(64, device="cuda"), 1e-6, block=32)
+    s = s.cpu().tolist()
+    assert s[0] == [255, 0] and s[1] == [255, 255] and 255 not in s[2] + s[3] + s[4]
+    # a row of zeros without eps: 0 / 0
+    c, s, _ = mx.rmsnorm_mxfp8(torch.zeros(1, 64, device="cuda"), torch.ones(64, device="cuda"), 0.0, block=32)
+    assert s.cpu().tolist() == [[255, 255]]
