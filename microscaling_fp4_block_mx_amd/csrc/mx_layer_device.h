@@ -54,6 +54,13 @@ template <bool BF16>
 struct Raw {
   u32x4 v[BF16 ? 1 : 2];
 };
+// To the compiler another value from here on: what it made of the old one is
+// not kept in registers for later.
+template <bool BF16>
+__device__ __forceinline__ void renew(Raw<BF16> &r) {
+  asm("" : "+v"(r.v[0]));
+  if constexpr (!BF16) asm("" : "+v"(r.v[1]));
+}
 template <bool BF16>
 __device__ __forceinline__ Raw<BF16> load_raw(const void *base, int64_t item) {
   Raw<BF16> r;
@@ -93,6 +100,13 @@ __device__ __forceinline__ void store8(void *base, int64_t item, const float (&f
     p[0] = f32x4{f[0], f[1], f[2], f[3]};
     p[1] = f32x4{f[4], f[5], f[6], f[7]};
   }
+}
+
+// One element.
+template <bool BF16>
+__device__ __forceinline__ float load_one(const void *base, int64_t i) {
+  if constexpr (BF16) return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(base)[i] << 16);
+  else return reinterpret_cast<const float *>(base)[i];
 }
 
 // ---- E4M3 -------------------------------------------------------------------------

@@ -56,21 +56,22 @@ __device__ __forceinline__ double block_sum(float a, float *part) {
 // The same of a value that is in 64 bits from the start.
 template <int T>
 __device__ __forceinline__ double block_sum64(double a, double *part) {
-#pragma unroll
+#pragma unroll 1
   for (int d = 1; d < 64; d <<= 1) a += __shfl_xor(a, d);
   if constexpr (T == 64) return a;
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
   __syncthreads();
   double t = part[0];
-#pragma unroll
+#pragma unroll 1  // few registers: rare, and beside rows held in all the others
   for (int i = 1; i < T / 64; i++) t += part[i];
   return t;
 }
 
 // Whether a sum of squares in 32 bits is none to go by: squares overflowed, or
-// are so small that bits of them were lost (`floor`: what is added to the sum).
+// are so small that bits of them, or of their products with a gradient, may
+// have been lost (`floor`: what is added to the sum).
 __device__ __forceinline__ bool out_of_range(float sum, float floor) {
-  return !(sum < 0x1p127f) || sum + floor < 0x1p-80f;
+  return !(sum < 0x1p127f) || sum + floor < 0x1p-40f;
 }
 
 // T threads of N items (eight elements) hold a row. 8191 x 8192 bf16 with a
@@ -186,8 +187,8 @@ __global__ __launch_bounds__(T) void k_rmsnorm(const void *x, const void *residu
 
 // Bound by HBM: 8192 x 4096 bf16 with a second gradient, 46 to 48 us (5.7 TB/s
 // of 8 bytes an element) and 4 for the sum of 512 partial rows; 8192 x 8192
-// 93 us. Rows of more than 32,768 elements do not fit the registers: 2048 x
-// 32768 347 us.
+// 93 us. Rows of more than 16,384 elements do not fit the registers whole: 2048
+// x 32768 209 us (2.6 TB/s), fp32 491; fp32 4096 x 12288, which does, 158.
 template <bool BF16, int T, int N>
 __global__ __launch_bounds__(T) void k_rmsnorm_backward(
     const void *dy, const void *h, const void *__restrict__ weight, const void *through,
@@ -197,6 +198,7 @@ __global__ __launch_bounds__(T) void k_rmsnorm_backward(
   // read the weight again (from the caches), at each use.
   constexpr bool AHEAD = N == 1;
   __shared__ f32x2 part[2][T / 64];
+  __shared__ double part64[2][T / 64];
   const int items = k >> 3;
   Raw<BF16> dr[N], hr[N], tr[N], wr[N];
   auto fetch = [&](const void *from, int64_t row, Raw<BF16> (&to)[N]) {
@@ -251,13 +253,39 @@ __global__ __launch_bounds__(T) void k_rmsnorm_backward(
     }
     // alternate halves of `part`: a wave may still be reading the last row's
     const f32x2 t = block_sum2<T>(ss, sg, part[flip]);
-    const float s = 1.0f / __builtin_sqrtf(t.x * inv_k + eps);
-    const float c = t.y * inv_k * s * s;
+    float s = 1.0f / __builtin_sqrtf(t.x * inv_k + eps);
+    float c = t.y * inv_k * s * s;
+    const bool lost = __builtin_fabsf(t.y) < 0x1p-80f && t.y != 0.0f;
+    if (__builtin_expect(out_of_range(t.x, eps * k) || !(__builtin_fabsf(t.y) < 0x1p127f) || lost, 0)) {
+      // the same for the whole workgroup: the sums again in 64 bits, element by
+      // element from memory, which costs other rows no registers. s and c
+      // themselves are in range wherever the results are: s h is about 1.
+      double sh = 0.0, sgh = 0.0;
+      int start = threadIdx.x, count = k;
+      float more = eps;
+      // unknown to the compiler, which would make addresses and quotients ahead
+      // of all rows and hold them
+      asm volatile("" : "+v"(start), "+s"(count), "+s"(more));
+#pragma unroll 1
+      for (int e = start; e < count; e += T) {
+        const double hv = load_one<BF16>(h, row * k + e);
+        sh += hv * hv;
+        sgh += (double)load_one<BF16>(dy, row * k + e) * load_one<BF16>(weight, e) * hv;
+      }
+      const double mean = block_sum64<T>(sh, part64[0]) / count + more;
+      s = (float)(1.0 / __builtin_sqrt(mean));
+      c = (float)(block_sum64<T>(sgh, part64[1]) / count / mean);
+    }
 #pragma unroll
     for (int u = 0; u < N; u++) {
       const int it = threadIdx.x + u * T;
       if (it < items) {
         float dv[8], hv[8], w[8], o[8], th[8];
+        if (!AHEAD && (BF16 || N < 4)) {  // widened again: what the sums widened is not held for this
+          renew<BF16>(d[u]);
+          renew<BF16>(g[u]);
+          renew<BF16>(wr[u]);
+        }
         widen<BF16>(d[u], dv);
         widen<BF16>(g[u], hv);
         widen<BF16>(wr[u], w);

@@ -1,4 +1,4 @@
-"""The norm on rows whose squares leave the range of 32 bits:
+"""The norm and its gradient on rows whose squares leave the range of 32 bits:
 large ones, and with eps = 0 small ones."""
 import math
 
@@ -61,3 +61,30 @@ def test_non_finite_rows_stay_as_they_were():
     # a row of zeros without eps: 0 / 0
     c, s, _ = mx.rmsnorm_mxfp8(torch.zeros(1, 64, device="cuda"), torch.ones(64, device="cuda"), 0.0, block=32)
     assert s.cpu().tolist() == [[255, 255]]
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("k", [32, 160, 4096, 16384 + 32])
+@pytest.mark.parametrize("eps", [1e-6, 0.0])
+def test_gradient_of_large_and_small_rows(k, eps, dtype):
+    h = rows_of(k, SIZES[:3] + (SMALL if eps == 0.0 else []), k).to(DT[dtype])
+    g = torch.Generator().manual_seed(2)
+    # gradients as large as the row, so that dx is of ordinary size (and its
+    # products are not): a gradient that meets a norm's large input is scaled back
+    size = h.float().abs().amax(1, keepdim=True)
+    dy = (torch.randn(h.shape, generator=g) * size.clamp(max=1e15)).to(DT[dtype])
+    t = torch.randn(h.shape, generator=g).to(DT[dtype])
+    w = (torch.randn(k, generator=g) * 0.3 + 1).to(DT[dtype])
+    for through in (None, t):
+        dx, dw = mx.rmsnorm_backward(dy.cuda(), h.cuda(), w.cuda(), eps,
+                                     None if through is None else through.cuda())
+        wx, ww = ref.norm_backward(dy, h, w, eps, through)
+        s = 1.0 / torch.sqrt(h.double().square().mean(1, keepdim=True) + eps)
+        gw = (w.double() * dy.double()).abs()
+        mag = s * (gw + h.double().abs() * s * s * (gw * h.double().abs()).mean(1, keepdim=True))
+        if through is not None:
+            mag = mag + through.double().abs()
+        tol = Y_ERR * mag + (2.0 ** -8 * wx.abs() if dtype == "bf16" else 0.0) + 2.0 ** -126
+        assert bool(((dx.cpu().double() - wx).abs() <= tol).all())
+        sw = (dy.double() * h.double() * s).abs().sum(0)
+        assert bool(((dw.cpu().double() - ww).abs() <= Y_ERR * sw + 2.0 ** -126).all())
+
+
