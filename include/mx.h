@@ -366,8 +366,9 @@ mx_status_t mx_rmsnorm_mxfp8(const void *x, const void *residual, const void *we
  *        arrives at h past the norm, or NULL)
  *   dweight[j] = sum over rows of dy h s        (fp32, overwritten)
  * dy, h, weight, through and dx share one dtype; sums are fp32 (64 bits for a
- * row whose squares leave their range), in a fixed order. dx may equal dy, h or through. rows == 0 writes zeros to dweight.
- * workspace: mx_rmsnorm_backward_workspace_size(rows, k) bytes of device
+ * row whose squares leave their range), in a fixed order. dx may equal dy, h
+ * or through. rows == 0 writes zeros to dweight. workspace:
+ * mx_rmsnorm_backward_workspace_size(rows, k) bytes of device
  * scratch, 16-byte aligned (one row of k floats per workgroup). */
 size_t mx_rmsnorm_backward_workspace_size(int64_t rows, int64_t k);
 mx_status_t mx_rmsnorm_backward(const void *dy, const void *h, const void *weight,

@@ -155,11 +155,14 @@ def _matrix(x, name: str, dtypes=_DTYPES):
     return (shape[0] if len(shape) == 2 else x.numel() // k), k
 
 
-def _want(t, name: str, dev, dtype, numel: int):
-    """_need() with its outcome found in fewer steps where all is well."""
+def _want(t, name: str, dev, dtype, numel: int, last: int = 0):
+    """_need() with its outcome found in fewer steps where all is well. `last`:
+    what the last dimension must be (0: any) of more than one."""
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == numel
             and t.device == dev and t.is_contiguous()):
         _need(t, name, dev, dtype, numel)
+    if last and t.dim() > 1 and t.size(-1) != last:
+        raise ValueError(f"{name} must be [..., {last}], got {tuple(t.shape)}")
 
 
 def _block(block: int) -> int:
@@ -229,14 +232,14 @@ def rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     or None without a residual). out_h may be x or residual."""
     rows, k = _matrix(x, "x")
     dev = x.device
-    _want(weight, "weight", dev, x.dtype, k)
+    _want(weight, "weight", dev, x.dtype, k, k)
     nb = -(-k // _block(block))
     if residual is not None:
-        _want(residual, "residual", dev, x.dtype, x.numel())
+        _want(residual, "residual", dev, x.dtype, x.numel(), k)
         if out_h is None:
             out_h = torch.empty_like(x)
         else:
-            _want(out_h, "out_h", dev, x.dtype, x.numel())
+            _want(out_h, "out_h", dev, x.dtype, x.numel(), k)
     elif out_h is not None:
         raise ValueError("out_h needs a residual")
     codes, scales = torch.empty_like(x, dtype=torch.uint8), _bytes(x, rows, nb, x.dim() == 2)
@@ -252,10 +255,10 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, ep
     reaches h past the norm. dx is the gradient of x and of residual alike."""
     rows, k = _matrix(h, "h")
     dev = h.device
-    _want(dy, "dy", dev, h.dtype, h.numel())
-    _want(weight, "weight", dev, h.dtype, k)
+    _want(dy, "dy", dev, h.dtype, h.numel(), k)
+    _want(weight, "weight", dev, h.dtype, k, k)
     if through is not None:
-        _want(through, "through", dev, h.dtype, h.numel())
+        _want(through, "through", dev, h.dtype, h.numel(), k)
     lib = load_library()
     dx = torch.empty_like(h)
     dweight = torch.empty(k, dtype=torch.float32, device=dev)
@@ -282,13 +285,13 @@ def matmul_mxfp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sca
     if dtype not in _DTYPES:
         raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
     nb = -(-k // _block(block))
-    _want(a_scales, "a_scales", dev, torch.uint8, m * nb)
-    _want(b_scales, "b_scales", dev, torch.uint8, n * nb)
+    _want(a_scales, "a_scales", dev, torch.uint8, m * nb, nb)
+    _want(b_scales, "b_scales", dev, torch.uint8, n * nb, nb)
     if out is None:
         out = (torch.empty(m, n, dtype=dtype, device=dev) if a.dim() == 2
                else torch.empty(a.shape[:-1] + (n,), dtype=dtype, device=dev))
     else:
-        _want(out, "out", dev, dtype, m * n)
+        _want(out, "out", dev, dtype, m * n, n)
     lib, cd = load_library(), _DTYPES[dtype]
     size = lib.mx_matmul_mxfp8_workspace_size(m, n, k, block, cd)
     ws = _scratch(size, dev)
@@ -323,8 +326,8 @@ def _cache_of(cache: KVCache):
     _want(v, "v_codes", dev, torch.uint8, k.numel())
     if v.shape != (pages, heads, dim, page):
         raise ValueError(f"v_codes must be {(pages, heads, dim, page)}, got {tuple(v.shape)}")
-    _want(ks, "k_scales", dev, torch.uint8, pages * heads)
-    _want(vs, "v_scales", dev, torch.uint8, pages * heads)
+    _want(ks, "k_scales", dev, torch.uint8, pages * heads, heads)
+    _want(vs, "v_scales", dev, torch.uint8, pages * heads, heads)
     return dev, heads, dim, page, _pack_cache(k.data_ptr(), ks.data_ptr(), v.data_ptr(),
                                               vs.data_ptr(), pages, heads, dim, page)
 
@@ -376,7 +379,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, cu: torch
     if out is None:
         out = torch.empty(tokens, q_heads, dim, dtype=torch.bfloat16, device=dev)
     else:
-        _want(out, "out", dev, torch.bfloat16, tokens * q_heads * dim)
+        _want(out, "out", dev, torch.bfloat16, tokens * q_heads * dim, dim)
     room = width * page
     max_length = room if max_length <= 0 else min(max_length, room)
     lib = load_library()
