@@ -413,12 +413,12 @@ typedef struct {
 /* A batch of sequences (device arrays, int32): row i of table [batch, width]
  * lists the pages of sequence i in order; its new tokens are rows cu[i] ..
  * cu[i+1] - 1 of the token arrays (cu[0] = 0, cu[batch] = tokens); lengths[i]
- * is its length. A sequence may have no new tokens. (Tokens before cu[0], were
- * it not 0, belong to no sequence: nothing is appended for them, and their
- * rows of attention's output are undefined.) Page numbers outside the
- * cache are not followed: tokens appended there are dropped, attention reads
- * the cache's last page instead. Pages that are written must belong to one
- * sequence. */
+ * is its length. A sequence may have no new tokens. width * page is at most
+ * 2^31 - 2048. (Tokens before cu[0], were it not 0, belong to no sequence:
+ * nothing is appended for them, and their rows of attention's output are
+ * undefined.) Page numbers outside the cache are not followed: tokens appended
+ * there are dropped, attention reads the cache's last page instead. Pages that
+ * are written must belong to one sequence. */
 typedef struct {
   const int32_t *table;
   const int32_t *cu;

@@ -50,6 +50,7 @@ hipStream_t stream_of(void *s) { return static_cast<hipStream_t>(s); }
 
 constexpr int64_t kMaxColumns = 65535LL * 128;  // tiles of 128 in one grid dimension
 constexpr int64_t kMaxProductK = 1 << 20;       // 32-bit offsets inside a tile of rows
+constexpr int64_t kMaxLength = INT32_MAX - 2047;
 
 mx_status_t check_cache(const mx_kv_cache_t *c, const mx_kv_batch_t *b) {
   if (!c || !b) return MX_ERR_NULL;
@@ -59,8 +60,8 @@ mx_status_t check_cache(const mx_kv_cache_t *c, const mx_kv_batch_t *b) {
   if (b->tokens < 0 || b->tokens > INT32_MAX / 2 || b->batch < 0 || b->batch > (1 << 24) ||
       b->width < 0)
     return MX_ERR_SHAPE;
-  // lengths and positions are 32-bit
-  if ((int64_t)b->width * c->page > INT32_MAX) return MX_ERR_SHAPE;
+  // lengths and positions are 32-bit, those of the tiles that are asked for ahead too
+  if ((int64_t)b->width * c->page > kMaxLength) return MX_ERR_SHAPE;
   if (b->tokens > 0 && (b->batch < 1 || b->width < 1 || c->pages < 1)) return MX_ERR_SHAPE;
   // workgroups of one launch: at most two pages more than whole ones per sequence
   if (b->tokens / c->page + 2 * (int64_t)b->batch > INT32_MAX / c->heads) return MX_ERR_SHAPE;
