@@ -1,5 +1,7 @@
-"""Append where its inputs are not of the ordinary kind, bit for bit against
-the reference."""
+"""Append of single tokens (the kernel with one wave a page), and append where
+its inputs are not of the ordinary kind, bit for bit against the reference."""
+import math
+
 import pytest
 import torch
 
@@ -17,6 +19,42 @@ def _gpu():
     mx.load_library()
     yield
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("page", [32, 64, 128, 256])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_few_tokens_at_a_time(dim, page, dtype):
+    """One to four tokens a sequence, over page boundaries, magnitudes that
+    grow and shrink, a NaN and an infinity on the way, an idle sequence."""
+    starts = [page - 7, 3, 2 * page - 2, page // 2 + 1]
+    steps = [[1, 0, 1, 1], [4, 0, 2, 3], [3, 1, 4, 4], [1, 1, 1, 1], [4, 4, 4, 4], [2, 3, 1, 0],
+             [4, 4, 4, 4], [1, 2, 3, 4]]
+    totals = [s + sum(st[i] for st in steps) for i, s in enumerate(starts)]
+    w = World(totals, 2, dim, page, dim + page)
+    w.append(starts, [0] * 4, dtype)
+    held = list(starts)
+    for t, new in enumerate(steps):
+        def edit(k, v):
+            if t == 4:
+                k[1, 0, 5] = math.nan   # sequence 0, head 0
+                v[-1, 1, dim - 1] = math.inf  # the last sequence, head 1
+            if t == 2:
+                v[0] = 0
+        w.append(new, held, dtype, by=2.0 ** ((t * 5) % 13 - 6), edit=edit)
+        held = [h + n for h, n in zip(held, new)]
+        w.same()
+
+
+@pytest.mark.parametrize("page", [64, 256])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_single_tokens_fill_a_page(dim, page):
+    """A token at a time through a whole page, the scale growing and the kept
+    codes moving at most steps."""
+    w = World([page + 3], 3, dim, page, 7)
+    for t in range(page + 3):
+        w.append([1], [t], by=2.0 ** (t % 9 - 4 + t // 40))
+    w.same()
 
 
 @pytest.mark.parametrize("new", [[1, 1, 1], [3, 2, 1], [90, 70, 50]])
