@@ -381,7 +381,8 @@ mx_status_t mx_rmsnorm_backward(const void *dy, const void *h, const void *weigh
  * scaled 8-bit products with fp32 accumulators, rounded once (they drop bits
  * of a product more than about 2^-14 below the largest of its group of eight:
  * 1.4e-5 of the result's norm on normal data). c_dtype MX_F32: codes widened
- * exactly to bf16, fp32 products and sums, half the rate. A scale byte 255 or
+ * exactly to bf16 (beside scale bytes 0 to 2, subnormal codes lose what lies
+ * under 2^-133), fp32 products and sums, half the rate. A scale byte 255 or
  * a NaN code makes the results it enters NaN. k <= 2^20, m and n < 2^31, and C
  * has fewer than 2^24 - 1 tiles of 128 x 128 (else MX_ERR_SHAPE). workspace:
  * mx_matmul_mxfp8_workspace_size(...) bytes, 16-byte aligned; 0 bytes (NULL

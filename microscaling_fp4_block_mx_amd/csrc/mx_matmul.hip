@@ -12,8 +12,11 @@
 // matrix core drops bits more than about 2^-14 below the largest product
 // (1.4e-5 of the result's norm on normal data), which is far inside bf16's
 // rounding (1.7e-3) but not inside fp32's. fp32 output therefore widens the
-// codes to bf16, scales applied (both exact), and runs the bf16 products at
-// half the rate.
+// codes to bf16, scales applied, and runs the bf16 products at half the rate.
+// That is exact for bytes 3 to 246; below, subnormal codes lose what lies under
+// 2^-133; where a wave meets one above (no quantizer here makes it), whose
+// values would be infinite, it does its tiles anew with the scales applied to
+// each block's sum.
 //
 // The weight-side operand B is the matrix core's "A" operand, so that a
 // lane's accumulators are columns n of one row m of C.
@@ -72,6 +75,57 @@ struct MatArgs {
   void *c;         // output, or partial sums [split][m][n] fp32
   int partial;
 };
+
+// Bytes of w above 246, as their top bits.
+__device__ __forceinline__ uint32_t far_bytes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x09090909u) & w & 0x80808080u;
+}
+
+// MT x NT tiles of 16 rows of A (from row m0) and of B (from n0), elements k0
+// to k1, for any scale bytes: 32 elements at a time, unscaled, straight from
+// memory, the sums scaled before they are added. Rare, so of little code and
+// few registers.
+template <bool BLK32, int MT, int NT>
+__device__ __forceinline__ void far_tiles(const MatArgs &g, int64_t m0, int64_t n0, int64_t k0, int64_t k1,
+                                          int lane, f32x4 (&acc)[MT][NT]) {
+  const int l16 = lane & 15, lg = lane >> 4;
+  auto codes = [&](const uint8_t *base, int64_t row, int64_t k) {
+    const u32x2 w = *reinterpret_cast<const u32x2 *>(base + row * g.k + k + 8 * lg);
+    return widen8((int)w[0], (int)w[1], 1.0f);
+  };
+#pragma unroll
+  for (int i = 0; i < MT; i++)
+#pragma unroll
+    for (int j = 0; j < NT; j++) acc[i][j] = f32x4{0, 0, 0, 0};
+#pragma unroll 1
+  for (int64_t k = k0; k < k1; k += 32) {
+    const int64_t at = k / (BLK32 ? 32 : 128);
+    bf16x8 a[MT];
+    int sa[MT];
+#pragma unroll
+    for (int i = 0; i < MT; i++) {
+      const int64_t row = min(m0 + 16 * i + l16, g.m - 1);
+      a[i] = codes(g.a, row, k);
+      sa[i] = g.sa[row * g.nb + at];
+    }
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+      const bf16x8 b = codes(g.b, min(n0 + 16 * j + l16, g.n - 1), k);
+      int sb[4];
+#pragma unroll
+      for (int e = 0; e < 4; e++) sb[e] = g.sb[min(n0 + 16 * j + 4 * lg + e, g.n - 1) * g.nb + at];
+#pragma unroll
+      for (int i = 0; i < MT; i++) {
+        const f32x4 t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a[i], f32x4{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const bool nan = sa[i] == 255 || sb[e] == 255;
+          acc[i][j][e] += nan ? __builtin_nanf("") : __builtin_ldexpf(t[e], sa[i] + sb[e] - 254);
+        }
+      }
+    }
+  }
+}
 
 // ---- tiled kernel -----------------------------------------------------------------
 //
@@ -422,7 +476,7 @@ __global__ __launch_bounds__((SIDE / TM) * (SIDE / TN) * 64, SIDE == 128 && BUFS
     K::load(ld, first + i / LOADS, i / LOADS, i % LOADS);
   // the first slab has landed (the others may be in flight)
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"((BUFS - 2) * LOADS + START) : "memory");
-  uint32_t as[MT][2], bs[NT][2];
+  uint32_t as[MT][2], bs[NT][2], far = 0;  // far: bytes past what widening takes
   auto get_scales = [&](int buf) {
     // exact: the lane's halves lie in blocks lg / 2 and 2 + lg / 2 of a slab
     const int g0 = !BLK32 ? 0 : EXACT ? lg >> 1 : lg, g1 = EXACT && BLK32 ? 2 + (lg >> 1) : g0;
@@ -435,6 +489,15 @@ __global__ __launch_bounds__((SIDE / TM) * (SIDE / TN) * 64, SIDE == 128 && BUFS
     for (int j = 0; j < NT; j++) {
       bs[j][0] = scl[buf][g0][BM + rb + 16 * j];
       bs[j][1] = EXACT && BLK32 ? scl[buf][g1][BM + rb + 16 * j] : bs[j][0];
+    }
+    if constexpr (EXACT) {
+#pragma unroll
+      for (int h = 0; h < (BLK32 ? 2 : 1); h++) {
+#pragma unroll
+        for (int i = 0; i < MT; i++) far |= far_bytes(as[i][h]);
+#pragma unroll
+        for (int j = 0; j < NT; j++) far |= far_bytes(bs[j][h]);
+      }
     }
   };
   i32x8 a[4], b[NT];
@@ -507,6 +570,11 @@ __global__ __launch_bounds__((SIDE / TM) * (SIDE / TN) * 64, SIDE == 128 && BUFS
   if (s + 2 < nk) step(s + 2, std::integral_constant<int, 2>());
   // nothing may still be landing in LDS, and every wave is done reading it
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  if constexpr (EXACT) {
+    if (__builtin_expect(__any(far != 0), 0))
+      far_tiles<BLK32, MT, NT>(g, m0 + wm, n0 + wn, (int64_t)first * 128, min(g.k, (int64_t)(first + nk) * 128),
+                               lane, acc);
+  }
 
   // Output: a lane's accumulators are 4-column runs of one row, which would
   // be written in pieces of 8 or 16 bytes, so they are turned in LDS: by each
@@ -584,9 +652,10 @@ __global__ __launch_bounds__(512) void k_matmul8_rows(const MatArgs g) {
   const uint8_t *ap = g.a + m * g.k, *sap = g.sa + m * g.nb;
   const int64_t nb1 = g.nb - 1;
   const u32x4 zero = {0, 0, 0, 0};
-  f32x4 acc[CT];
+  f32x4 acc[1][CT];
+  uint32_t largest = 0;  // scale byte
 #pragma unroll
-  for (int c = 0; c < CT; c++) acc[c] = f32x4{0, 0, 0, 0};
+  for (int c = 0; c < CT; c++) acc[0][c] = f32x4{0, 0, 0, 0};
   for (int s = first; s < last; s += U) {
     i32x8 bv[U][CT], av[U];
     uint32_t bs[U][CT][2], as[U][2];
@@ -616,19 +685,26 @@ __global__ __launch_bounds__(512) void k_matmul8_rows(const MatArgs g) {
     for (int u = 0; u < U; u++) {
       if constexpr (EXACT) {
         const Wide aw = widen32(av[u], as[u][0], as[u][BLK32 ? 1 : 0]);
+        largest = max(largest, max(as[u][0], as[u][BLK32 ? 1 : 0]));
 #pragma unroll
-        for (int c = 0; c < CT; c++)
-          acc[c] = mfma16(widen32(bv[u][c], bs[u][c][0], bs[u][c][BLK32 ? 1 : 0]), aw, acc[c]);
+        for (int c = 0; c < CT; c++) {
+          acc[0][c] = mfma16(widen32(bv[u][c], bs[u][c][0], bs[u][c][BLK32 ? 1 : 0]), aw, acc[0][c]);
+          largest = max(largest, max(bs[u][c][0], bs[u][c][BLK32 ? 1 : 0]));
+        }
       } else {
 #pragma unroll
-        for (int c = 0; c < CT; c++) acc[c] = mfma8<0>(bv[u][c], av[u], acc[c], bs[u][c][0], as[u][0]);
+        for (int c = 0; c < CT; c++) acc[0][c] = mfma8<0>(bv[u][c], av[u], acc[0][c], bs[u][c][0], as[u][0]);
       }
     }
+  }
+  if constexpr (EXACT) {
+    if (__builtin_expect(__any(largest > 246u), 0))
+      far_tiles<BLK32, 1, CT>(g, m0, n0, (int64_t)first * 128, min(g.k, (int64_t)last * 128), lane, acc);
   }
 #pragma unroll
   for (int c = 0; c < CT; c++)
 #pragma unroll
-    for (int e = 0; e < 4; e++) part[wave][l16][16 * c + 4 * lg + e] = acc[c][e];
+    for (int e = 0; e < 4; e++) part[wave][l16][16 * c + 4 * lg + e] = acc[0][c][e];
   __syncthreads();
   for (int i = threadIdx.x; i < 256 * CT; i += WAVES * 64) {
     const int r = i / (16 * CT), c = i % (16 * CT);
