@@ -449,9 +449,12 @@ mx_status_t mx_kv_append(const void *k, const void *v, mx_dtype_t dtype, int64_t
  * 128 times it. lengths[i] is the length of sequence i with its new tokens
  * appended: new token j of n sees keys 0 .. lengths[i] - n + j; one that sees
  * none gives zeros. out [tokens, q_heads, dim] bf16, contiguous:
- * softmax(scale q.k) v with fp32 scores, maxima and sums; q is used exactly,
- * the softmax's weights with a relative error of at most 2^-8, and their sum is
- * that of the weights as used. Cached values past bfloat16's range (a byte
+ * softmax(scale q.k) v with fp32 scores, maxima and sums. Scores are scaled
+ * 8-bit products as those of a bf16 mx_matmul_mxfp8 (the bits that they drop
+ * come to less than 2^-10 of sum |q k|); q enters them exactly where an element
+ * is above 2^-13 of its row's largest, else off by at most 2^-21 of the
+ * largest. The softmax's weights have a relative error of at most 2^-8, and
+ * their sum is that of the weights as used. Cached values past bfloat16's range (a byte
  * above 246, which no quantizer here makes) may count as its largest. scale > 0.
  * max_length: an upper bound on lengths that the launch is planned for (0:
  * width * page); a larger length is still right, only slower. workspace:

@@ -1,5 +1,6 @@
 """Attention's accuracy where one bound on everything would hide it: weights
-many powers of two below the largest, scores too large for a weight's exponent."""
+many powers of two below the largest, scores too large for a weight's exponent,
+small elements of q beside large ones, a channel that dominates a score."""
 import math
 
 import pytest
@@ -83,3 +84,55 @@ def test_scores_of_any_size(new, dim, size):
     first = w.cpu[2][page, :, :, 0].view(ref.F8).double() * ref.pow2(w.cpu[3][page].double())[:, None]
     want = first.repeat_interleave(2, 0).expand_as(out)
     assert bool(((out - want).abs() <= 2.0 ** -8 * want.abs()).all())
+
+
+@pytest.mark.parametrize("new", [1, 60])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("below", [8, 12, 14, 17, 20])
+def test_small_elements_of_q(new, dim, below):
+    """q's first element is 1 and meets keys of 0; the others, about 2^-below,
+    decide. q is exact down to 2^-13 of its row's largest element, below that
+    off by at most 2^-21 of the largest: scores by that times sum |k|, and by
+    2^-10 of sum |q k| (the product), weights by twice as much."""
+    g = torch.Generator().manual_seed(below)
+    tokens = 200
+    k = torch.randn(tokens, 2, dim, generator=g) * 2.0 ** below
+    k[:, :, 0] = 0
+    v = torch.randn(tokens, 2, dim, generator=g)
+    w = world_of(k.bfloat16(), v.bfloat16(), 32)
+    q = torch.randn(new, 4, dim, generator=g) * 2.0 ** -below
+    q[:, :, 0] = 1.0
+    q = q.bfloat16()
+    scale = 1 / math.sqrt(dim)
+    out = mx.kv_attention(q.cuda(), w.gpu, w.table.cuda(), i32([0, new]).cuda(),
+                          i32([tokens]).cuda(), scale).cpu().double()
+    want, mag, reach = ref.attention(q, w.cpu, w.table, i32([0, new]), i32([tokens]), scale)
+    held = w.cpu[0].view(ref.F8).double() * ref.pow2(w.cpu[1].double())[..., None, None]
+    held = held[w.table[0].long()].transpose(1, 2).reshape(-1, 2, dim)[:tokens]
+    off = 2.0 ** -21 * scale * float(held.abs().sum(2).max())
+    eps = 2.0 ** -7 + 2 * 2.0 ** -10 * reach + 2 * off
+    tol = 2.0 ** -8 * want.abs() + eps[..., None] * mag
+    assert bool(((out - want).abs() <= tol).all()), float(((out - want).abs() / mag).max())
+
+
+@pytest.mark.parametrize("new", [1, 60])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_channel_that_dominates_its_group(new, dim):
+    """One channel's product is 2^9 times the others of its group of eight: the
+    matrix core drops bits more than about 2^-14 below it (2^-10 of sum |q k|
+    at most). The keys share that channel's value, so it decides nothing."""
+    g = torch.Generator().manual_seed(4)
+    tokens = 150
+    k = torch.randn(tokens, 2, dim, generator=g)
+    k[:, :, 3] = 32.0
+    v = torch.randn(tokens, 2, dim, generator=g)
+    w = world_of(k.bfloat16(), v.bfloat16(), 32)
+    q = torch.randn(new, 4, dim, generator=g)
+    q[:, :, 3] = 16.0
+    q = q.bfloat16()
+    out = mx.kv_attention(q.cuda(), w.gpu, w.table.cuda(), i32([0, new]).cuda(),
+                          i32([tokens]).cuda()).cpu().double()
+    want, mag, reach = ref.attention(q, w.cpu, w.table, i32([0, new]), i32([tokens]), 1 / math.sqrt(dim))
+    eps = 2.0 ** -7 + 2 * 2.0 ** -10 * reach
+    tol = 2.0 ** -8 * want.abs() + eps[..., None] * mag
+    assert bool(((out - want).abs() <= tol).all())
