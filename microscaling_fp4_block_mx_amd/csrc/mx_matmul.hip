@@ -149,7 +149,7 @@ __device__ __forceinline__ void far_tiles(const MatArgs &g, int64_t m0, int64_t 
 //
 // 8192 x 8192 x 4096, bf16 out: 200 to 205 us with blocks of 128 (2.7 PFLOP/s),
 // 211 to 215 with blocks of 32, the matrix cores busy 62 % of the cycles and
-// the card at 2.0 of its 2.4 GHz; 4096 x 4096 x 4096 53 us. fp32 out 427 us
+// the card at 2.0 of its 2.4 GHz; 4096 x 4096 x 4096 52 to 57 us. fp32 out 427 us
 // (1.3 PFLOP/s): twice the products and the widening.
 
 __device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
@@ -741,23 +741,24 @@ static Plan plan_of(int64_t m, int64_t n, int64_t k, int out_bf16) {
   const int all = (int)((k + 127) >> 7);
   Plan p = {0, 0, 0, 1, all, 0};
   // Up to 16 rows: one reading of B decides. 32 columns a workgroup where
-  // that still gives every compute unit one (16 x 8192 x 4096: 12.7, with 16
-  // columns 14.2), else 16 (16 x 4096 x 4096: 8.2, with 32 11.1).
+  // that still gives every compute unit one (16 x 8192 x 4096: 11.0, with 16
+  // columns 13.2), else 16 (16 x 4096 x 4096: 7.9, with 32 10.4).
   if (m <= 16) {
     p.columns = n >= 32 * 256 ? 2 : 1;
     return p;
   }
   // Up to 64 rows: the same in groups of 16, as long as every compute unit
-  // gets at most one workgroup (32 x 512 x 4096: 7.7, tiles of 64 9.9; 64 x
-  // 1024 x 8192: 13.5 and 20; but 48 x 4096 x 4096: 19.5 and 12).
+  // gets at most one workgroup (32 x 512 x 4096: 7.2, tiles of 64 9.8; 64 x
+  // 1024 x 8192: 12.9 and 21; but 48 x 4096 x 4096: 18.4 and 12).
   if (m <= 64 && ((m + 15) / 16) * ((n + 15) / 16) <= 256) {
     p.columns = 1;
     return p;
   }
   // Tiles of 256 use the matrix cores best where they fill the card in whole
-  // rounds (4096 x 4096 x 4096: 58, tiles of 128 67), not where the last round
-  // is nearly empty (4099 rows, K 1536: 46 and 40). If up to 16 rows open
-  // that round, they go to the few-rows kernel. Tiles of 256 leave no
+  // rounds (4096 x 4096 x 4096: 52 to 57, tiles of 128 63), not where the last
+  // round is nearly empty (4099 x 4096 x 1536: 40 and 35). If up to 16 rows open
+  // that round, they go to the few-rows kernel (4099 rows: 28, 4112: 28; 4112 x
+  // 4096 x 4096: 59, tiles of 256 alone 88, of 128 80). Tiles of 256 leave no
   // registers to widen codes in, which fp32 outputs do.
   const int64_t t256 = tiles_of(m, n, 256), t128 = tiles_of(m, n, 128), t64 = tiles_of(m, n, 64);
   if (out_bf16) {
@@ -775,9 +776,9 @@ static Plan plan_of(int64_t m, int64_t n, int64_t k, int out_bf16) {
     }
   }
   // Tiles of 128: two workgroups a compute unit with two buffers each (2048 x
-  // 4096 x 4096: 35, one with four 42), one with four where there is only one
-  // for each (1024 x 4096 x 4096: 22 and 26). Fewer tiles than 144 leave too
-  // many idle: then tiles of 64 (512 x 4096 x 4096: 17, tiles of 128 20).
+  // 4096 x 4096: 33, one with four 40), one with four where there is only one
+  // for each (1024 x 4096 x 4096: 21 and 25). Fewer tiles than 144 leave too
+  // many idle: then tiles of 64 (512 x 4096 x 4096: 16, tiles of 128 19.5).
   if (t128 >= 144) {
     p.side = 128;
     p.bufs = t128 > 256 ? 2 : 4;
@@ -786,9 +787,9 @@ static Plan plan_of(int64_t m, int64_t n, int64_t k, int out_bf16) {
   p.side = 64;
   p.bufs = 4;
   // Split K where tiles of 64 leave half of the card idle, at least 16 slabs
-  // each, since the sum costs 3 to 4 us (256 x 1024 x 8192: 13, unsplit 21;
-  // 128 x 2048 x 2048 unsplit: 6.6, split 8; up to 64 rows, 64 x 8192 x 4096:
-  // 13 both).
+  // each, since the sum costs 3 to 4 us (256 x 1024 x 8192: 13.5, unsplit 21;
+  // 128 x 2048 x 2048 unsplit: 6.5, split 8.5; up to 64 rows, 64 x 8192 x 4096:
+  // 12.5, split 13.5).
   const int want = m <= 64 ? 1 : (int)std::min<int64_t>(256 / t64, all / 16);
   if (want > 1) {
     p.steps = ((all + want - 1) / want + 3) & ~3;
