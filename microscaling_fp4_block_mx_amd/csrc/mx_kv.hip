@@ -637,16 +637,19 @@ __device__ __forceinline__ uint32_t lds_address(const void *p) {
 // on the global side.
 //
 // Bound by the cache's bytes: 16 sequences of up to 65,000 tokens, 8 kv heads
-// of 128 dims, 1.19 GB in 220 us (5.4 TB/s; a plain reading of as much reaches
-// 7.0). Loads into registers, a tile at a time, took 250: half of a line per
+// of 128 dims, 1.19 GB in 211 to 220 us (5.4 to 5.6 TB/s; a plain reading of as
+// much reaches 7.0). Loads into registers, a tile at a time, took 250: half of a line per
 // request, and nothing on its way while a wave computes.
 template <int D>
 __device__ __forceinline__ int swz_rows(int r) {
   if constexpr (D == 128) return ((r >> 1) & 1) | (((r >> 4) & 3) << 1);
   return (r >> 4) & 3;
 }
-// (32 rows of 128 dims: one wave a SIMD, two would spill: 93 and 113 us for 16
-// sequences of 4 tokens in 16,000, 8 query heads to a kv head)
+// (32 rows of 128 dims: one wave a SIMD, two would spill: 92 and 113 us for 16
+// sequences of 4 tokens in 16,000, 8 query heads to a kv head. Weights in two
+// bfloat16 parts would take the error against 64 bits from 0.0019 of the
+// result's norm to its rounding's 0.0017, and the same call to 100 us, 4
+// sequences of 700 tokens from 9.0 to 9.6.)
 template <int D, int RT>
 __global__ __launch_bounds__(256, D == 128 && RT == 2 ? 1 : 2) void k_attn_rows(const AttnArgs a) {
   constexpr int DT = D / 16, W = 4, S = 128 * D, L = S / 2048;  // bytes of a tile's keys, loads of a part
@@ -988,9 +991,10 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a) {
 // one run of 32 tokens, whose page is wave-uniform; a lane's chunk of values
 // lies in one of four.
 //
-// 2 x 2048 tokens of 8,192, 32 query heads on 8 of 128 dims: 437 to 480 us
-// (0.9 PFLOP/s), heads of 64: 326 us. With the split weights and 8-bit values
-// 510 and 381.
+// 2 x up to 2,048 tokens of 8,192, 32 query heads on 8 of 128 dims: 404 to 419
+// us (1.0 PFLOP/s) in a long run, heads of 64 296 to 302; a few calls after a
+// pause 466 to 514. (Weights in two E4M3 parts and 8-bit values took 510 and 381
+// where this, measured beside it, took 480 and 326.)
 template <int D>
 __device__ __forceinline__ int swz_k(int r) {
   if constexpr (D == 128) return ((r >> 1) & 1) | (((r >> 3) & 3) << 1);
