@@ -17,7 +17,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import _DTYPES, _need, _raise, load_library
+from . import _DTYPES, _need, _raise, _stream, load_library
 
 BLOCKS = (32, 128)
 
@@ -175,14 +175,20 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# torch's own quick ways to the current device and stream (1.4 us a call less than
+# the public ones); a torch without them has the public ones
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
+
+
 def _call(device, fn, *args):
     """fn(*args, stream) on the device's current stream, raising on a bad status."""
     index = device.index
-    if torch._C._cuda_getDevice() == index:
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if _device() == index:
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+            status = fn(*args, _raw_stream(index))
     if status:
         _raise(status)
 
