@@ -469,6 +469,72 @@ mx_status_t mx_kv_attention(const void *q, int64_t q_stride, int q_heads,
                             int64_t max_length, float scale, void *out, void *workspace,
                             size_t workspace_bytes, void *stream);
 
+/* ---- Positions --------------------------------------------------------------
+ * Norms of queries and keys per head and the position rotation, which a layer
+ * has between its first product and the cache. */
+
+/* A rotation of the first `rot` dims of a head (a multiple of 16, at most the
+ * head's dims): pair i turns by an angle whose cosine and sine are elements i
+ * and rot / 2 + i of row positions[token] of table [length, rot] (fp32, device,
+ * 16-byte aligned). Pairs are dims (i, i + rot / 2), or with `paired` (2 i,
+ * 2 i + 1): y_a = x_a cos - x_b sin, y_b = x_b cos + x_a sin. Dims from rot on
+ * pass. A position outside the table makes the rotated dims NaN. */
+typedef struct {
+  const float *table;
+  const int32_t *positions; /* [tokens], device */
+  int64_t length;
+  int rot;
+  int paired;
+} mx_rotary_t;
+
+/* Heads that go through the norm and the rotation: x and y [tokens, heads, dim]
+ * (x_stride, y_stride elements from token to token, multiples of 16 bytes; a
+ * token's heads are adjacent, so x may be a part of a projection's rows), weight
+ * [dim], or NULL for no norm. */
+typedef struct {
+  const void *x;
+  int64_t x_stride;
+  const void *weight;
+  void *y;
+  int64_t y_stride;
+  int heads;
+} mx_heads_t;
+
+/* y = R(weight x / sqrt(sum(x^2) / dim + eps)) for every head of q and, unless
+ * it is NULL, of k, R being the rotation (rotary NULL: none). x, weight and y
+ * share one dtype; the norm and the rotation are formed in 64 bits and rounded
+ * once, so that a finite head may be of any size. dim is 64, 128 or 256. y may
+ * equal x, with its stride (in place); other overlaps of an output are
+ * MX_ERR_ALIAS. A head of zeros alone with eps = 0 gives NaN. */
+mx_status_t mx_norm_rotate(const mx_heads_t *q, const mx_heads_t *k, mx_dtype_t dtype,
+                           int64_t tokens, int dim, float eps, const mx_rotary_t *rotary,
+                           void *stream);
+
+/* Gradients of the same: with n = R^T dy, s = 1 / sqrt(sum(x^2) / dim + eps) and
+ * g = weight n,
+ *   dx = s (g - x s^2 sum(g x) / dim)      dweight = sum over tokens and heads of n x s
+ * Without a weight dx = n; x and dweight are not used then. dy, x, weight and dx
+ * share one dtype; dweight is fp32 [dim], overwritten; its sums are fp32, in a
+ * fixed order. dx may equal dy or x, with its stride. tokens == 0 writes zeros
+ * to the dweights. workspace: mx_norm_rotate_backward_workspace_size(tokens,
+ * dim) bytes, 16-byte aligned; NULL and 0 are enough without any weight. */
+typedef struct {
+  const void *dy;
+  int64_t dy_stride;
+  const void *x;
+  int64_t x_stride;
+  const void *weight;
+  void *dx;
+  int64_t dx_stride;
+  float *dweight;
+  int heads;
+} mx_heads_grad_t;
+size_t mx_norm_rotate_backward_workspace_size(int64_t tokens, int dim);
+mx_status_t mx_norm_rotate_backward(const mx_heads_grad_t *q, const mx_heads_grad_t *k,
+                                    mx_dtype_t dtype, int64_t tokens, int dim, float eps,
+                                    const mx_rotary_t *rotary, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
 /* Error reporting of this interface (no operation of the method, so no
  * passage defines it): the pages describe no error conventions; these two
  * calls only report the mx_status_t values above. */

@@ -16,7 +16,8 @@ Two layers:
     for a block size other than 32; ``RuntimeError`` for HIP errors).
 
 The operators of a transformer layer in MXFP8 (norm, products, KV cache and
-attention) are in ``layer`` and re-exported here, in the same two layers.
+attention) are in ``layer``, those of positions and drafted tokens in
+``draft``; both are re-exported here, in the same two layers.
 """
 from __future__ import annotations
 
@@ -46,7 +47,8 @@ EXPORTS = ("mx_quantize", "mx_dequantize", "mx_fakequant", "mx_block_mse",
            "mx_block_mse_noalloc", "mx_quantize_mxfp8_blocks", "mx_rmsnorm_mxfp8",
            "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace_size", "mx_matmul_mxfp8",
            "mx_matmul_mxfp8_workspace_size", "mx_kv_append", "mx_kv_attention",
-           "mx_kv_attention_workspace_size", "mx_status_string", "mx_last_error_detail")
+           "mx_kv_attention_workspace_size", "mx_norm_rotate", "mx_norm_rotate_backward",
+           "mx_norm_rotate_backward_workspace_size", "mx_status_string", "mx_last_error_detail")
 
 _lib = None
 
@@ -94,6 +96,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mx_last_error_detail.argtypes = []
     lib.mx_last_error_detail.restype = ctypes.c_char_p
     declare(lib)
+    declare_draft(lib)
     _lib = lib
     return lib
 
@@ -595,3 +598,8 @@ from .layer import (  # noqa: E402
     mx_matmul_mxfp8_workspace_size, mx_quantize_mxfp8_blocks, mx_rmsnorm_backward,
     mx_rmsnorm_backward_workspace_size, mx_rmsnorm_mxfp8, quantize_mxfp8_both,
     quantize_mxfp8_columns, quantize_mxfp8_rows, rmsnorm_backward, rmsnorm_mxfp8)
+
+from .draft import (  # noqa: E402
+    MxHeads, MxHeadsGrad, MxRotary, Rotary, declare as declare_draft, mx_norm_rotate,
+    mx_norm_rotate_backward, mx_norm_rotate_backward_workspace_size, norm_rotate,
+    norm_rotate_backward, rotary_table)

@@ -19,8 +19,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmx.so")
-SOURCES = ["mx_kernels.hip", "mx_norm.hip", "mx_matmul.hip", "mx_kv.hip", "mx_api.cpp",
-           "mx_layer_api.cpp"]
+SOURCES = ["mx_kernels.hip", "mx_norm.hip", "mx_matmul.hip", "mx_kv.hip", "mx_rotary.hip",
+           "mx_api.cpp", "mx_layer_api.cpp", "mx_draft_api.cpp"]
 ARCH = "gfx950"
 
 

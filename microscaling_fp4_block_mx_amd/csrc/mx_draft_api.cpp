@@ -1,0 +1,193 @@
+// mx_draft_api.cpp - C ABI of positions and drafted tokens: synchronous
+// host-side argument validation, then asynchronous launches on the caller's
+// stream. Every check runs before any HIP call.
+#include <math.h>
+#include <stdint.h>
+
+#include <hip/hip_runtime.h>
+
+#include "mx_internal.h"
+#include "mx_layer.h"
+#include "mx_layer_checks.h"
+
+using namespace mxc;
+
+namespace {
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Rows of `width` bytes, `stride` bytes apart.
+struct Rows {
+  const void *p;
+  int64_t width, stride, rows;
+  int64_t bytes() const { return rows > 0 ? (rows - 1) * stride + width : 0; }
+};
+// Whether two sets of rows share bytes. Parts of the same rows (one stride) lie
+// between each other without sharing any.
+bool share(const Rows &a, const Rows &b) {
+  if (!overlap(Range{a.p, a.bytes()}, Range{b.p, b.bytes()})) return false;
+  if (a.stride != b.stride) return true;
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
+  const int64_t at = ((d % a.stride) + a.stride) % a.stride;  // of b's row inside a's
+  return at < a.width || at + b.width > a.stride;
+}
+bool share(const Rows &a, const void *p, int64_t bytes) {
+  return share(a, Rows{p, bytes, bytes, bytes > 0 && p ? 1 : 0});
+}
+
+mx_status_t check_rotary(const mx_rotary_t *r, int dim) {
+  if (!r || r->rot == 0) return MX_OK;
+  if (r->rot < 0 || r->rot % 16 || r->rot > dim || r->length < 1 ||
+      r->length > INT64_MAX / 4 / r->rot)
+    return MX_ERR_SHAPE;
+  return MX_OK;
+}
+mx_status_t check_rotary_pointers(const mx_rotary_t *r, bool positions) {
+  if (!r || r->rot == 0) return MX_OK;
+  if (!r->table || (positions && !r->positions)) return MX_ERR_NULL;
+  if (!aligned16(r->table) || !aligned4(r->positions)) return MX_ERR_ALIGN;
+  return MX_OK;
+}
+bool shares_rotary(const Rows &out, const mx_rotary_t *r, int64_t tokens) {
+  if (!r || r->rot == 0) return false;
+  return share(out, r->table, r->length * r->rot * 4) || share(out, r->positions, tokens * 4);
+}
+
+// Norm and rotation: what q's and k's shapes have to be.
+mx_status_t check_norm_rotate(int q_heads, int k_heads, int dtype, int64_t tokens, int dim, float eps,
+                              const mx_rotary_t *rotary) {
+  if (!dtype_ok(dtype)) return MX_ERR_DTYPE;
+  if (!(eps >= 0.0f) || isinf(eps)) return MX_ERR_SHAPE;
+  if (dim != 64 && dim != 128 && dim != 256) return MX_ERR_SHAPE;
+  if (tokens < 0 || tokens > INT32_MAX) return MX_ERR_SHAPE;
+  if (q_heads < 1 || q_heads > 65535 || k_heads < 0 || k_heads > 65535) return MX_ERR_SHAPE;
+  return check_rotary(rotary, dim);
+}
+mx_status_t check_stride(int64_t stride, int heads, int dim, int64_t tokens) {
+  if (stride < (int64_t)heads * dim || stride > INT32_MAX) return MX_ERR_SHAPE;
+  return tokens > 0 && stride > INT64_MAX / 8 / tokens ? MX_ERR_SHAPE : MX_OK;
+}
+bool stride_aligned(int64_t stride, int dtype) { return stride * elem_bytes(dtype) % 16 == 0; }
+
+const mx_rotary_t kNoRotation = {};
+
+}  // namespace
+
+extern "C" {
+
+mx_status_t mx_norm_rotate(const mx_heads_t *q, const mx_heads_t *k, mx_dtype_t dtype,
+                           int64_t tokens, int dim, float eps, const mx_rotary_t *rotary,
+                           void *stream) {
+  if (!q) return MX_ERR_NULL;
+  if (k && k->heads < 1) return MX_ERR_SHAPE;
+  if (mx_status_t s = check_norm_rotate(q->heads, k ? k->heads : 0, dtype, tokens, dim, eps, rotary))
+    return s;
+  const mx_heads_t *both[] = {q, k};
+  for (const mx_heads_t *h : both) {
+    if (!h) continue;
+    if (mx_status_t s = check_stride(h->x_stride, h->heads, dim, tokens)) return s;
+    if (mx_status_t s = check_stride(h->y_stride, h->heads, dim, tokens)) return s;
+  }
+  if (tokens == 0) return MX_OK;
+  const int64_t e = elem_bytes(dtype);
+  for (const mx_heads_t *h : both) {
+    if (!h) continue;
+    if (!h->x || !h->y) return MX_ERR_NULL;
+    if (!aligned16(h->x) || !aligned16(h->y) || !aligned16(h->weight) ||
+        !stride_aligned(h->x_stride, dtype) || !stride_aligned(h->y_stride, dtype))
+      return MX_ERR_ALIGN;
+  }
+  if (mx_status_t s = check_rotary_pointers(rotary, true)) return s;
+  for (const mx_heads_t *h : both) {
+    if (!h) continue;
+    const Rows y = {h->y, h->heads * dim * e, h->y_stride * e, tokens};
+    for (const mx_heads_t *o : both) {
+      if (!o) continue;
+      const Rows x = {o->x, o->heads * dim * e, o->x_stride * e, tokens};
+      const bool in_place = o == h && h->x == h->y && h->x_stride == h->y_stride;
+      if (!in_place && share(y, x)) return MX_ERR_ALIAS;
+      if (o->weight && share(y, o->weight, dim * e)) return MX_ERR_ALIAS;
+      if (o != h && share(y, Rows{o->y, o->heads * dim * e, o->y_stride * e, tokens}))
+        return MX_ERR_ALIAS;
+    }
+    if (shares_rotary(y, rotary, tokens)) return MX_ERR_ALIAS;
+  }
+  return finish(mxi_launch_norm_rotate(*q, k, dtype == MX_BF16, tokens, dim, eps,
+                                       rotary ? *rotary : kNoRotation, stream_of(stream)));
+}
+
+size_t mx_norm_rotate_backward_workspace_size(int64_t tokens, int dim) {
+  if (check_norm_rotate(1, 0, MX_BF16, tokens, dim, 0.0f, nullptr) != MX_OK) return 0;
+  return (size_t)mxi_norm_rotate_partials(tokens) * 2 * dim * sizeof(float);
+}
+
+mx_status_t mx_norm_rotate_backward(const mx_heads_grad_t *q, const mx_heads_grad_t *k,
+                                    mx_dtype_t dtype, int64_t tokens, int dim, float eps,
+                                    const mx_rotary_t *rotary, void *workspace,
+                                    size_t workspace_bytes, void *stream) {
+  if (!q) return MX_ERR_NULL;
+  if (k && k->heads < 1) return MX_ERR_SHAPE;
+  if (mx_status_t s = check_norm_rotate(q->heads, k ? k->heads : 0, dtype, tokens, dim, eps, rotary))
+    return s;
+  const mx_heads_grad_t *both[] = {q, k};
+  bool sums = false;
+  for (const mx_heads_grad_t *h : both) {
+    if (!h) continue;
+    if (mx_status_t s = check_stride(h->dy_stride, h->heads, dim, tokens)) return s;
+    if (mx_status_t s = check_stride(h->dx_stride, h->heads, dim, tokens)) return s;
+    if (!h->weight) continue;
+    sums = true;
+    if (mx_status_t s = check_stride(h->x_stride, h->heads, dim, tokens)) return s;
+    if (!h->dweight) return MX_ERR_NULL;
+    if (!aligned16(h->dweight)) return MX_ERR_ALIGN;
+  }
+  if (q->weight && k && k->weight &&
+      overlap(Range{q->dweight, 4 * (int64_t)dim}, Range{k->dweight, 4 * (int64_t)dim}))
+    return MX_ERR_ALIAS;
+  if (tokens > 0) {
+    const int64_t e = elem_bytes(dtype);
+    for (const mx_heads_grad_t *h : both) {
+      if (!h) continue;
+      if (!h->dy || !h->dx || (h->weight && !h->x)) return MX_ERR_NULL;
+      if (!aligned16(h->dy) || !aligned16(h->dx) || !stride_aligned(h->dy_stride, dtype) ||
+          !stride_aligned(h->dx_stride, dtype))
+        return MX_ERR_ALIGN;
+      if (h->weight &&
+          (!aligned16(h->x) || !aligned16(h->weight) || !stride_aligned(h->x_stride, dtype)))
+        return MX_ERR_ALIGN;
+    }
+    if (mx_status_t s = check_rotary_pointers(rotary, true)) return s;
+    const int64_t need = sums ? (int64_t)mx_norm_rotate_backward_workspace_size(tokens, dim) : 0;
+    if (need && (!workspace || !aligned16(workspace) || workspace_bytes < (size_t)need))
+      return MX_ERR_WORKSPACE;
+    const Rows ws = {workspace, need, need, need ? 1 : 0};
+    for (const mx_heads_grad_t *h : both) {
+      if (!h) continue;
+      const int64_t width = h->heads * dim * e;
+      const Rows dx = {h->dx, width, h->dx_stride * e, tokens};
+      const Rows dw = {h->dweight, 4 * (int64_t)dim, 4 * (int64_t)dim, h->weight ? 1 : 0};
+      for (const mx_heads_grad_t *o : both) {
+        if (!o) continue;
+        const int64_t ow = o->heads * dim * e;
+        const Rows dy = {o->dy, ow, o->dy_stride * e, tokens};
+        const Rows x = {o->x, ow, o->x_stride * e, o->weight ? tokens : 0};
+        const Rows w = {o->weight, dim * e, dim * e, o->weight ? 1 : 0};
+        const bool at_dy = o == h && h->dx == h->dy && h->dx_stride == h->dy_stride;
+        const bool at_x = o == h && h->dx == h->x && h->dx_stride == h->x_stride;
+        if ((!at_dy && share(dx, dy)) || (!at_x && share(dx, x)) || share(dx, w)) return MX_ERR_ALIAS;
+        if (share(dw, dy) || share(dw, x) || share(dw, w)) return MX_ERR_ALIAS;
+        if (share(ws, dy) || share(ws, x) || share(ws, w)) return MX_ERR_ALIAS;
+        if (o != h && share(dx, Rows{o->dx, ow, o->dx_stride * e, tokens})) return MX_ERR_ALIAS;
+        if (share(dx, o->dweight, o->weight ? 4 * (int64_t)dim : 0)) return MX_ERR_ALIAS;
+      }
+      if (share(ws, dx) || share(ws, dw) || shares_rotary(dx, rotary, tokens) ||
+          shares_rotary(dw, rotary, tokens) || shares_rotary(ws, rotary, tokens))
+        return MX_ERR_ALIAS;
+    }
+  }
+  return finish(mxi_launch_norm_rotate_backward(*q, k, dtype == MX_BF16, tokens, dim, eps,
+                                                rotary ? *rotary : kNoRotation,
+                                                static_cast<float *>(workspace), stream_of(stream)));
+}
+
+}  // extern "C"

@@ -43,4 +43,15 @@ hipError_t mxi_launch_kv_attention(const void *q, int64_t q_stride, int q_heads,
                                    const mx_kv_cache_t &cache, const mx_kv_batch_t &batch,
                                    int64_t max_length, float scale, void *out, void *workspace,
                                    hipStream_t st);
+
+// Heads' norms and rotation; `k` may be NULL, `rotary` with rot = 0 turns nothing.
+hipError_t mxi_launch_norm_rotate(const mx_heads_t &q, const mx_heads_t *k, int bf16,
+                                  int64_t tokens, int dim, float eps, const mx_rotary_t &rotary,
+                                  hipStream_t st);
+// Rows of partial weight gradients (2 dim floats each) of the gradient's launch.
+int64_t mxi_norm_rotate_partials(int64_t tokens);
+hipError_t mxi_launch_norm_rotate_backward(const mx_heads_grad_t &q, const mx_heads_grad_t *k,
+                                           int bf16, int64_t tokens, int dim, float eps,
+                                           const mx_rotary_t &rotary, float *partial,
+                                           hipStream_t st);
 #endif  // MX_LAYER_H

@@ -1,0 +1,206 @@
+"""Positions and drafted tokens beside the 8-bit cache: tensor-level helpers.
+
+The norms of queries and keys per head with the position rotation, and their
+gradient. Every step runs in the HIP kernels behind include/mx.h; this module
+allocates outputs and scratch with torch (on the current stream) and checks
+what the C entry points cannot see: devices, dtypes, shapes and contiguity. Bad
+arguments raise ``ValueError``, HIP errors ``RuntimeError``.
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+from typing import NamedTuple
+
+import torch
+
+from . import _DTYPES, load_library
+from .layer import _call, _heads_of, _ptr, _scratch, _want
+
+
+class MxRotary(ctypes.Structure):
+    """mx_rotary_t of include/mx.h (pointers as integers)."""
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("length", ctypes.c_int64), ("rot", ctypes.c_int), ("paired", ctypes.c_int)]
+
+
+class MxHeads(ctypes.Structure):
+    """mx_heads_t of include/mx.h (pointers as integers)."""
+    _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("y_stride", ctypes.c_int64), ("heads", ctypes.c_int)]
+
+
+class MxHeadsGrad(ctypes.Structure):
+    """mx_heads_grad_t of include/mx.h (pointers as integers)."""
+    _fields_ = [("dy", ctypes.c_void_p), ("dy_stride", ctypes.c_int64), ("x", ctypes.c_void_p),
+                ("x_stride", ctypes.c_int64), ("weight", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+                ("dx_stride", ctypes.c_int64), ("dweight", ctypes.c_void_p),
+                ("heads", ctypes.c_int)]
+
+
+class Rotary(NamedTuple):
+    """A rotation: ``table`` float32 [length, rot] (rotary_table), ``positions``
+    int32 [tokens], ``paired``: dims (2 i, 2 i + 1) turn instead of (i, i + rot / 2)."""
+    table: torch.Tensor
+    positions: torch.Tensor | None = None
+    paired: bool = False
+
+
+def rotary_table(length: int, rot: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """float32 [length, rot]: row p has the cosines, then the sines, of p / base^(2 i / rot),
+    i = 0 .. rot / 2 - 1 (angles in 64 bits)."""
+    if rot <= 0 or rot % 16:
+        raise ValueError(f"rot must be a positive multiple of 16, got {rot}")
+    f = base ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+    angles = torch.arange(length, dtype=torch.float64, device=device)[:, None] * f
+    return torch.cat([angles.cos(), angles.sin()], 1).float()
+
+
+# ---- C entry points, same names -------------------------------------------
+
+def mx_norm_rotate(q, k, dtype, tokens, dim, eps, rotary, stream) -> int:
+    return load_library().mx_norm_rotate(q, k, dtype, tokens, dim, eps, rotary, stream)
+
+
+def mx_norm_rotate_backward_workspace_size(tokens, dim) -> int:
+    return load_library().mx_norm_rotate_backward_workspace_size(tokens, dim)
+
+
+def mx_norm_rotate_backward(q, k, dtype, tokens, dim, eps, rotary, workspace, workspace_bytes,
+                            stream) -> int:
+    return load_library().mx_norm_rotate_backward(q, k, dtype, tokens, dim, eps, rotary, workspace,
+                                                  workspace_bytes, stream)
+
+
+def declare(lib) -> None:
+    """Argument and result types of the entry points."""
+    p, i64, i32, f32, size = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
+                              ctypes.c_size_t)
+    types = {
+        "mx_norm_rotate": [p, p, i32, i64, i32, f32, p, p],
+        "mx_norm_rotate_backward": [p, p, i32, i64, i32, f32, p, p, size, p],
+        "mx_norm_rotate_backward_workspace_size": [i64, i32],
+    }
+    for name, args in types.items():
+        f = getattr(lib, name)
+        f.argtypes = args
+        f.restype = size if name.endswith("_size") else i32
+
+
+# ---- tensor helpers --------------------------------------------------------
+
+_pack_rotary = struct.Struct("@PPqii").pack
+_pack_heads = struct.Struct("@PqPPqi4x").pack
+_pack_grad = struct.Struct("@PqPqPPqPi4x").pack
+
+
+def _rotary_of(rotary: Rotary | None, dev, dim: int, tokens: int, positions: bool):
+    """mx_rotary_t, or None without a rotation. `positions`: they must be given."""
+    if rotary is None:
+        return None
+    table, pos, paired = rotary
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("the rotation's table must be [length, rot]")
+    length, rot = table.shape
+    _want(table, "table", dev, torch.float32, length * rot)
+    if rot % 16 or not 0 < rot <= dim:
+        raise ValueError(f"rot must be a multiple of 16 up to {dim}, got {rot}")
+    if length < 1:
+        raise ValueError("the rotation's table has no positions")
+    if pos is not None or positions:
+        _want(pos, "positions", dev, torch.int32, tokens)
+    return _pack_rotary(table.data_ptr(), pos.data_ptr() if pos is not None else 0, length, rot,
+                        bool(paired))
+
+
+def _into(out, name: str, like, tokens: int, heads: int, dim: int):
+    """(out, its stride): a new tensor, or the one given (any stride between tokens)."""
+    if out is None:
+        return torch.empty(tokens, heads, dim, dtype=like.dtype, device=like.device), heads * dim
+    got = _heads_of(out, name, like.device, (like.dtype,))
+    if got[:3] != (tokens, heads, dim):
+        raise ValueError(f"{name} must be {(tokens, heads, dim)}, got {tuple(out.shape)}")
+    return out, got[3]
+
+
+def _address(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _on_gpu(t, name: str):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return t.device
+
+
+def norm_rotate(q: torch.Tensor, k: torch.Tensor | None = None,
+                q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                rotary: Rotary | None = None, eps: float = 1e-6,
+                out_q: torch.Tensor | None = None, out_k: torch.Tensor | None = None):
+    """Heads [tokens, heads, dim] of q (and k) through a norm over each head's
+    dims (weight [dim]; None: no norm) and the position rotation (None: none) ->
+    (q, k) new, contiguous, k None without one. Slices of one projection's rows
+    are fine. out_q may be q and out_k may be k, in place."""
+    dev = _on_gpu(q, "q")
+    tokens, heads, dim, stride = _heads_of(q, "q", dev, _DTYPES)
+    r = _rotary_of(rotary, dev, dim, tokens, True)
+
+    def pack(x, name, stride, heads, weight, out):
+        if weight is not None:
+            _want(weight, name + "_weight", dev, x.dtype, dim)
+        out, out_stride = _into(out, "out_" + name, x, tokens, heads, dim)
+        return out, _pack_heads(x.data_ptr(), stride, _address(weight), out.data_ptr(), out_stride,
+                                heads)
+
+    kb = None
+    if k is not None:
+        k_tokens, k_heads, k_dim, k_stride = _heads_of(k, "k", dev, (q.dtype,))
+        if k_tokens != tokens or k_dim != dim:
+            raise ValueError(f"k must be [{tokens}, heads, {dim}], got {tuple(k.shape)}")
+        out_k, kb = pack(k, "k", k_stride, k_heads, k_weight, out_k)
+    elif k_weight is not None or out_k is not None:
+        raise ValueError("k_weight and out_k need k")
+    out_q, qb = pack(q, "q", stride, heads, q_weight, out_q)
+    _call(dev, load_library().mx_norm_rotate, qb, kb, _DTYPES[q.dtype], tokens, dim, eps, r)
+    return out_q, out_k
+
+
+def norm_rotate_backward(dq: torch.Tensor, q: torch.Tensor, dk: torch.Tensor | None = None,
+                         k: torch.Tensor | None = None, q_weight: torch.Tensor | None = None,
+                         k_weight: torch.Tensor | None = None, rotary: Rotary | None = None,
+                         eps: float = 1e-6):
+    """Gradients of norm_rotate at its inputs q and k -> (dq, dk, dq_weight,
+    dk_weight); weights' in float32 [dim], None where there is no weight (or k)."""
+    dev = _on_gpu(q, "q")
+    tokens, heads, dim, stride = _heads_of(q, "q", dev, _DTYPES)
+    r = _rotary_of(rotary, dev, dim, tokens, True)
+    if (k is None) != (dk is None) or (k is None and k_weight is not None):
+        raise ValueError("k, dk and k_weight go together")
+
+    def pack(dy, x, name, stride, heads, weight):
+        got = _heads_of(dy, "d" + name, dev, (x.dtype,))
+        if got[:3] != (tokens, heads, dim):
+            raise ValueError(f"d{name} must be {(tokens, heads, dim)}, got {tuple(dy.shape)}")
+        dweight = None
+        if weight is not None:
+            _want(weight, name + "_weight", dev, x.dtype, dim)
+            dweight = torch.empty(dim, dtype=torch.float32, device=dev)
+        dx = torch.empty(tokens, heads, dim, dtype=x.dtype, device=dev)
+        return dx, dweight, _pack_grad(dy.data_ptr(), got[3], x.data_ptr(), stride, _address(weight),
+                                       dx.data_ptr(), heads * dim, _address(dweight), heads)
+
+    dxk = dwk = kb = None
+    if k is not None:
+        k_tokens, k_heads, k_dim, k_stride = _heads_of(k, "k", dev, (q.dtype,))
+        if k_tokens != tokens or k_dim != dim:
+            raise ValueError(f"k must be [{tokens}, heads, {dim}], got {tuple(k.shape)}")
+        dxk, dwk, kb = pack(dk, k, "k", k_stride, k_heads, k_weight)
+    dxq, dwq, qb = pack(dq, q, "q", stride, heads, q_weight)
+    lib = load_library()
+    size = 0
+    if q_weight is not None or k_weight is not None:
+        size = lib.mx_norm_rotate_backward_workspace_size(tokens, dim)
+    ws = _scratch(size, dev)
+    _call(dev, lib.mx_norm_rotate_backward, qb, kb, _DTYPES[q.dtype], tokens, dim, eps, r, _ptr(ws),
+          size)
+    return dxq, dxk, dwq, dwk
