@@ -535,6 +535,18 @@ mx_status_t mx_norm_rotate_backward(const mx_heads_grad_t *q, const mx_heads_gra
                                     const mx_rotary_t *rotary, void *workspace,
                                     size_t workspace_bytes, void *stream);
 
+/* mx_kv_append with the keys' norm and rotation on the way: a key enters the
+ * cache as R(k_weight k / sqrt(sum(k^2) / dim + eps)), formed in 64 bits and
+ * rounded to fp32, from which page bytes and codes follow as in mx_kv_append;
+ * values as there. k_weight [dim] in dtype, or NULL: no norm; rotary NULL: no
+ * rotation. rotary's positions may be NULL: a token's place in its sequence
+ * then (drafted tokens of a tree have others: their depth). A position outside
+ * the table makes its page NaN. rot is at most the cache's dim. */
+mx_status_t mx_kv_append_rotary(const void *k, const void *v, mx_dtype_t dtype, int64_t k_stride,
+                                int64_t v_stride, const void *k_weight, float eps,
+                                const mx_rotary_t *rotary, const mx_kv_cache_t *cache,
+                                const mx_kv_batch_t *batch, void *stream);
+
 /* Error reporting of this interface (no operation of the method, so no
  * passage defines it): the pages describe no error conventions; these two
  * calls only report the mx_status_t values above. */

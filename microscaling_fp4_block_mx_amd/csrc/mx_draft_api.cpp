@@ -113,7 +113,7 @@ mx_status_t mx_norm_rotate(const mx_heads_t *q, const mx_heads_t *k, mx_dtype_t 
     if (shares_rotary(y, rotary, tokens)) return MX_ERR_ALIAS;
   }
   return finish(mxi_launch_norm_rotate(*q, k, dtype == MX_BF16, tokens, dim, eps,
-                                       rotary ? *rotary : kNoRotation, stream_of(stream)));
+                                       rotary && rotary->rot ? *rotary : kNoRotation, stream_of(stream)));
 }
 
 size_t mx_norm_rotate_backward_workspace_size(int64_t tokens, int dim) {
@@ -186,8 +186,45 @@ mx_status_t mx_norm_rotate_backward(const mx_heads_grad_t *q, const mx_heads_gra
     }
   }
   return finish(mxi_launch_norm_rotate_backward(*q, k, dtype == MX_BF16, tokens, dim, eps,
-                                                rotary ? *rotary : kNoRotation,
+                                                rotary && rotary->rot ? *rotary : kNoRotation,
                                                 static_cast<float *>(workspace), stream_of(stream)));
+}
+
+mx_status_t mx_kv_append_rotary(const void *k, const void *v, mx_dtype_t dtype, int64_t k_stride,
+                                int64_t v_stride, const void *k_weight, float eps,
+                                const mx_rotary_t *rotary, const mx_kv_cache_t *cache,
+                                const mx_kv_batch_t *batch, void *stream) {
+  if (!dtype_ok(dtype)) return MX_ERR_DTYPE;
+  if (mx_status_t s = check_cache(cache, batch)) return s;
+  if (!(eps >= 0.0f) || isinf(eps)) return MX_ERR_SHAPE;
+  if (mx_status_t s = check_rotary(rotary, cache->dim)) return s;
+  if (batch->tokens == 0) return MX_OK;
+  const int64_t tokens = batch->tokens, e = elem_bytes(dtype);
+  if (mx_status_t s = check_stride(k_stride, cache->heads, cache->dim, tokens)) return s;
+  if (mx_status_t s = check_stride(v_stride, cache->heads, cache->dim, tokens)) return s;
+  if (!k || !v) return MX_ERR_NULL;
+  if (mx_status_t s = check_cache_pointers(cache, batch)) return s;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_weight) || !stride_aligned(k_stride, dtype) ||
+      !stride_aligned(v_stride, dtype))
+    return MX_ERR_ALIGN;
+  if (mx_status_t s = check_rotary_pointers(rotary, false)) return s;
+  const int64_t row = (int64_t)cache->heads * cache->dim;
+  const int64_t codes = cache->pages * row * cache->page, scales = cache->pages * cache->heads;
+  const bool turns = rotary && rotary->rot;
+  const Range out[] = {{cache->k_codes, codes}, {cache->k_scales, scales},
+                       {cache->v_codes, codes}, {cache->v_scales, scales}};
+  const Range in[] = {{k, ((tokens - 1) * k_stride + row) * e},
+                      {v, ((tokens - 1) * v_stride + row) * e},
+                      {k_weight, cache->dim * e},
+                      {turns ? rotary->table : nullptr, turns ? rotary->length * rotary->rot * 4 : 0},
+                      {turns ? rotary->positions : nullptr, tokens * 4},
+                      {batch->table, 4 * (int64_t)batch->batch * batch->width},
+                      {batch->cu, 4 * ((int64_t)batch->batch + 1)},
+                      {batch->lengths, 4 * (int64_t)batch->batch}};
+  if (clash(out, in)) return MX_ERR_ALIAS;
+  return finish(mxi_launch_kv_append_rotary(k, v, dtype == MX_BF16, k_stride, v_stride, k_weight,
+                                            eps, turns ? *rotary : kNoRotation, *cache, *batch,
+                                            stream_of(stream)));
 }
 
 }  // extern "C"

@@ -37,7 +37,7 @@
 #include <algorithm>
 
 #include "mx_layer.h"
-#include "mx_layer_device.h"
+#include "mx_rotary_device.h"
 
 namespace mxl {
 
@@ -56,6 +56,10 @@ struct AppendArgs {
   mx_kv_batch_t b;
   int shift;        // log2(page)
   uint32_t blocks;  // units times heads
+  // keys through a norm and a rotation on the way, where the kernel has them
+  const void *weight;  // or NULL: no norm
+  float eps;
+  mx_rotary_t r;
 };
 
 // Which sequence a unit of work belongs to: sequence i owns units from
@@ -102,8 +106,14 @@ __device__ __forceinline__ Raw<BF16> load_at(const void *base, int64_t elem) {
   return load_raw<BF16>(reinterpret_cast<const uint8_t *>(base) + elem * (BF16 ? 2 : 4), 0);
 }
 
-template <bool BF16, int T>
+// TURN: keys pass a norm (if there is a weight) and a rotation between their load
+// and all else, of pairs (i, i + rot / 2) (1) or neighbours (2), in 64 bits: a
+// page's byte changes where its largest number crosses a power of two, so the
+// last bit of a key can be one of the byte. Lanes 2 m and 2 m + 1 of a token then
+// hold the two items of dims whose pairs turn together.
+template <bool BF16, int T, int TURN>
 __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
+  constexpr bool KB = BF16 && TURN == 0;  // whether keys are held as bfloat16
   // new values' codes, [dim][token]; rows are one word longer than a page's,
   // so that the rows that an instruction writes to fall on different banks
   extern __shared__ __attribute__((aligned(16))) uint8_t vt[];
@@ -138,36 +148,126 @@ __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
   };
   auto slot_of = [&](int it) { return word_of(it) + ((it >> 4) & 3); };
   auto dim_of = [&](int it) { return (it & (wide ? 15 : 7)) * 8; };
+  auto key_dim_of = [&](int it) {
+    const int l = it & (wide ? 15 : 7);
+    return 8 * (TURN == 1 && 8 * l < a.r.rot ? (l >> 1) + (l & 1) * (a.r.rot >> 4) : l);
+  };
   // whether any lane of the wave has a slot in use: the wave's lanes go together
   auto any = [&](int it) { return first + (wide ? it >> 6 << 2 : it >> 6 << 3) < end; };
   auto mine = [&](int it) { return slot_of(it) >= kept && slot_of(it) < end; };
-  auto load = [&](const void *x, int64_t stride, int it) {
-    const int64_t tok = min(max(src0 + slot_of(it), (int64_t)0), most);
-    return load_at<BF16>(x, tok * stride + (int64_t)head * D + dim_of(it));
+  auto token_of = [&](int it) { return min(max(src0 + slot_of(it), (int64_t)0), most); };
+  auto load = [&](const void *x, int64_t stride, int it, int dim) {
+    return load_at<BF16>(x, token_of(it) * stride + (int64_t)head * D + dim);
+  };
+  auto load_key = [&](int it) { return load(a.k, a.k_stride, it, key_dim_of(it)); };
+  auto load_value = [&](int it) { return load(a.v, a.v_stride, it, dim_of(it)); };
+  float weight[8];
+  if (TURN && a.weight) {  // of this lane's dims: the same for all its items
+    const int d = key_dim_of(threadIdx.x);
+#pragma unroll
+    for (int j = 0; j < 8; j++) weight[j] = load_one<BF16>(a.weight, d + j);
+  }
+  // The key as it enters the cache. All lanes of a token go together; items
+  // that are not new tokens' become zeros.
+  auto key_of = [&](const Raw<BF16> &raw, int it) {
+    if constexpr (TURN == 0) {
+      return raw;
+    } else {
+      float f[8];
+      widen<BF16>(raw, f);
+      double x[8];
+#pragma unroll
+      for (int j = 0; j < 8; j++) x[j] = f[j];
+      if (a.weight) {
+        double ss = 0.0;
+#pragma unroll
+        for (int j = 0; j < 8; j++) ss = __builtin_fma(x[j], x[j], ss);
+        ss = sum_lanes<8>(ss);
+        if (wide) ss += dppd<0x140>(ss);
+        const double root = inverse_root(ss * (wide ? 1.0 / 128 : 1.0 / 64) + a.eps);
+#pragma unroll
+        for (int j = 0; j < 8; j++) x[j] = x[j] * root * weight[j];
+      }
+      const int d = key_dim_of(it);
+      double other[8];
+      if constexpr (TURN == 1) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) other[j] = dppd<0xB1>(x[j]);
+      }
+      if (d < a.r.rot) {
+        const int position = a.r.positions ? a.r.positions[token_of(it)] : (j << a.shift) + slot_of(it);
+        const Angles at = angles_of(a.r.table, a.r.length, a.r.rot, position);
+        const float *sines = at.row + (a.r.rot >> 1);
+        if constexpr (TURN == 1) {
+          const bool second = d >= a.r.rot >> 1;
+          const int from = second ? d - (a.r.rot >> 1) : d;
+          float c[8], s[8];
+          load8(at.row + from, c);
+          load8(sines + from, s);
+#pragma unroll
+          for (int j = 0; j < 8; j++) {
+            const double turned = other[j] * s[j];
+            x[j] = __builtin_fma(x[j], (double)c[j], second ? turned : -turned);
+          }
+        } else {
+          const f32x4 c = *reinterpret_cast<const f32x4 *>(at.row + (d >> 1));
+          const f32x4 s = *reinterpret_cast<const f32x4 *>(sines + (d >> 1));
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const double x0 = x[2 * j], cd = c[j], sd = s[j];
+            x[2 * j] = __builtin_fma(x0, cd, -(x[2 * j + 1] * sd));
+            x[2 * j + 1] = __builtin_fma(x[2 * j + 1], cd, x0 * sd);
+          }
+        }
+        if (at.none) {
+#pragma unroll
+          for (int j = 0; j < 8; j++) x[j] = __builtin_nan("");
+        }
+      }
+      const bool is = mine(it);
+      Raw<false> r;
+#pragma unroll
+      for (int j = 0; j < 8; j++) r.v[j >> 2][j & 3] = is ? __float_as_uint((float)x[j]) : 0u;
+      return r;
+    }
   };
 
   Raw<BF16> kr[kKeep], vr[kKeep];
+  Raw<KB> kept_keys[kKeep];
 #pragma unroll
   for (int u = 0; u < kKeep; u++) {
     const int it = threadIdx.x + T * u;
     kr[u] = vr[u] = Raw<BF16>{};
     if (mine(it)) {
-      kr[u] = load(a.k, a.k_stride, it);
-      vr[u] = load(a.v, a.v_stride, it);
+      kr[u] = load_key(it);
+      vr[u] = load_value(it);
     }
   }
   uint32_t mk = 0, mv = 0;
-  auto take = [&](const Raw<BF16> &k, const Raw<BF16> &v) {
+  auto take = [&](const Raw<KB> &k, const Raw<BF16> &v) {
     float f[8];
-    widen<BF16>(k, f);
+    widen<KB>(k, f);
     mk = max(mk, amax8(f));
     widen<BF16>(v, f);
     mv = max(mv, amax8(f));
   };
 #pragma unroll
-  for (int u = 0; u < kKeep; u++) take(kr[u], vr[u]);  // zeros where there is none
-  for (int it = threadIdx.x + T * kKeep; any(it); it += T)
-    if (mine(it)) take(load(a.k, a.k_stride, it), load(a.v, a.v_stride, it));
+  for (int u = 0; u < kKeep; u++) {  // zeros where there is none
+    kept_keys[u] = key_of(kr[u], threadIdx.x + T * u);
+    take(kept_keys[u], vr[u]);
+  }
+  for (int it = threadIdx.x + T * kKeep; any(it); it += T) {
+    if constexpr (TURN == 0) {
+      if (mine(it)) take(load_key(it), load_value(it));
+    } else {
+      Raw<BF16> k = {}, v = {};
+      if (mine(it)) {
+        k = load_key(it);
+        v = load_value(it);
+      }
+      take(key_of(k, it), v);
+    }
+  }
   mk = max16(mk);
   mv = max16(mv);
   mk = max(mk, (uint32_t)__shfl_xor((int)mk, 16));
@@ -220,11 +320,11 @@ __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
   auto limit = [](uint32_t b) { return b > 246u ? 0x1.fffffep127f : limit8(b); };
   const float most_k = limit(sk), most_v = limit(sv);
   const int row = P + 4;
-  auto put = [&](const Raw<BF16> &k, const Raw<BF16> &v, int it) {
+  auto put = [&](const Raw<KB> &k, const Raw<BF16> &v, int it) {
     float f[8];
     if (mine(it)) {
-      widen<BF16>(k, f);
-      *reinterpret_cast<u32x2 *>(kc + slot_of(it) * D + dim_of(it)) = encode8(f, sk, most_k);
+      widen<KB>(k, f);
+      *reinterpret_cast<u32x2 *>(kc + slot_of(it) * D + key_dim_of(it)) = encode8(f, sk, most_k);
     }
     widen<BF16>(v, f);
     const u32x2 w = encode8(f, sv, most_v);
@@ -240,9 +340,8 @@ __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
   };
 #pragma unroll
   for (int u = 0; u < kKeep; u++)
-    if (any(threadIdx.x + T * u)) put(kr[u], vr[u], threadIdx.x + T * u);
-  for (int it = threadIdx.x + T * kKeep; any(it); it += T)
-    put(load(a.k, a.k_stride, it), load(a.v, a.v_stride, it), it);
+    if (any(threadIdx.x + T * u)) put(kept_keys[u], vr[u], threadIdx.x + T * u);
+  for (int it = threadIdx.x + T * kKeep; any(it); it += T) put(key_of(load_key(it), it), load_value(it), it);
   __syncthreads();
   const int piece0 = kept >> 4, chunks = ((end + 15) >> 4) - piece0;  // of a row, with new tokens in them
   for (int it = threadIdx.x; it < D * chunks; it += T) {
@@ -1269,21 +1368,40 @@ static AttnPlan attn_plan(int64_t tokens, int batch, int q_heads, int heads, int
 
 using namespace mxl;
 
-hipError_t mxi_launch_kv_append(const void *k, const void *v, int bf16, int64_t k_stride,
-                                int64_t v_stride, const mx_kv_cache_t &cache,
-                                const mx_kv_batch_t &batch, hipStream_t st) {
-  const int64_t blocks = (batch.tokens / cache.page + 2 * (int64_t)batch.batch) * cache.heads;
-  const AppendArgs a = {k, v, k_stride, v_stride, cache, batch, log2_of(cache.page), (uint32_t)blocks};
-  const Spread xy = spread(blocks);
+template <int TURN>
+static hipError_t launch_append(const AppendArgs &a, int bf16, hipStream_t st) {
+  const Spread xy = spread(a.blocks);
   const dim3 grid(xy.first, xy.second);
-  const size_t lds = (size_t)cache.dim * (cache.page + 4);
+  const size_t lds = (size_t)a.c.dim * (a.c.page + 4);
   // a few new tokens per sequence: one wave a page, so that all pages are at
   // work at once (256 sequences of one token: 8.5 us; four
   // waves, and kept codes moved a word at a time: 19)
-  const bool few = batch.tokens <= 4 * (int64_t)batch.batch;
-  if (bf16) few ? k_kv_append<true, 64><<<grid, 64, lds, st>>>(a) : k_kv_append<true, 256><<<grid, 256, lds, st>>>(a);
-  else few ? k_kv_append<false, 64><<<grid, 64, lds, st>>>(a) : k_kv_append<false, 256><<<grid, 256, lds, st>>>(a);
+  const bool few = a.b.tokens <= 4 * (int64_t)a.b.batch;
+  if (bf16) few ? k_kv_append<true, 64, TURN><<<grid, 64, lds, st>>>(a) : k_kv_append<true, 256, TURN><<<grid, 256, lds, st>>>(a);
+  else few ? k_kv_append<false, 64, TURN><<<grid, 64, lds, st>>>(a) : k_kv_append<false, 256, TURN><<<grid, 256, lds, st>>>(a);
   return hipGetLastError();
+}
+static AppendArgs append_args(const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                              const mx_kv_cache_t &cache, const mx_kv_batch_t &batch) {
+  const int64_t blocks = (batch.tokens / cache.page + 2 * (int64_t)batch.batch) * cache.heads;
+  return AppendArgs{k, v, k_stride, v_stride, cache, batch, log2_of(cache.page), (uint32_t)blocks, nullptr, 0.0f, {}};
+}
+
+hipError_t mxi_launch_kv_append(const void *k, const void *v, int bf16, int64_t k_stride,
+                                int64_t v_stride, const mx_kv_cache_t &cache,
+                                const mx_kv_batch_t &batch, hipStream_t st) {
+  return launch_append<0>(append_args(k, v, k_stride, v_stride, cache, batch), bf16, st);
+}
+
+hipError_t mxi_launch_kv_append_rotary(const void *k, const void *v, int bf16, int64_t k_stride,
+                                       int64_t v_stride, const void *weight, float eps,
+                                       const mx_rotary_t &rotary, const mx_kv_cache_t &cache,
+                                       const mx_kv_batch_t &batch, hipStream_t st) {
+  AppendArgs a = append_args(k, v, k_stride, v_stride, cache, batch);
+  a.weight = weight;
+  a.eps = eps;
+  a.r = rotary;
+  return rotary.paired ? launch_append<2>(a, bf16, st) : launch_append<1>(a, bf16, st);
 }
 
 size_t mxi_kv_attention_workspace(int64_t tokens, int batch, int q_heads, int heads, int dim,

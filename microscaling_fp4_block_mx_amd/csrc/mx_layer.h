@@ -44,6 +44,11 @@ hipError_t mxi_launch_kv_attention(const void *q, int64_t q_stride, int q_heads,
                                    int64_t max_length, float scale, void *out, void *workspace,
                                    hipStream_t st);
 
+hipError_t mxi_launch_kv_append_rotary(const void *k, const void *v, int bf16, int64_t k_stride,
+                                       int64_t v_stride, const void *weight, float eps,
+                                       const mx_rotary_t &rotary, const mx_kv_cache_t &cache,
+                                       const mx_kv_batch_t &batch, hipStream_t st);
+
 // Heads' norms and rotation; `k` may be NULL, `rotary` with rot = 0 turns nothing.
 hipError_t mxi_launch_norm_rotate(const mx_heads_t &q, const mx_heads_t *k, int bf16,
                                   int64_t tokens, int dim, float eps, const mx_rotary_t &rotary,

@@ -1,7 +1,7 @@
 """Positions and drafted tokens beside the 8-bit cache: tensor-level helpers.
 
-The norms of queries and keys per head with the position rotation, and their
-gradient. Every step runs in the HIP kernels behind include/mx.h; this module
+The norms of queries and keys per head with the position rotation, their
+gradient, and the append that has both on the way. Every step runs in the HIP kernels behind include/mx.h; this module
 allocates outputs and scratch with torch (on the current stream) and checks
 what the C entry points cannot see: devices, dtypes, shapes and contiguity. Bad
 arguments raise ``ValueError``, HIP errors ``RuntimeError``.
@@ -15,7 +15,7 @@ from typing import NamedTuple
 import torch
 
 from . import _DTYPES, load_library
-from .layer import _call, _heads_of, _ptr, _scratch, _want
+from .layer import KVCache, _batch_of, _cache_of, _call, _heads_of, _ptr, _scratch, _want
 
 
 class MxRotary(ctypes.Structure):
@@ -72,6 +72,12 @@ def mx_norm_rotate_backward(q, k, dtype, tokens, dim, eps, rotary, workspace, wo
                                                   workspace_bytes, stream)
 
 
+def mx_kv_append_rotary(k, v, dtype, k_stride, v_stride, k_weight, eps, rotary, cache, batch,
+                        stream) -> int:
+    return load_library().mx_kv_append_rotary(k, v, dtype, k_stride, v_stride, k_weight, eps, rotary,
+                                              cache, batch, stream)
+
+
 def declare(lib) -> None:
     """Argument and result types of the entry points."""
     p, i64, i32, f32, size = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
@@ -79,6 +85,7 @@ def declare(lib) -> None:
     types = {
         "mx_norm_rotate": [p, p, i32, i64, i32, f32, p, p],
         "mx_norm_rotate_backward": [p, p, i32, i64, i32, f32, p, p, size, p],
+        "mx_kv_append_rotary": [p, p, i32, i64, i64, p, f32, p, p, p, p],
         "mx_norm_rotate_backward_workspace_size": [i64, i32],
     }
     for name, args in types.items():
@@ -204,3 +211,24 @@ def norm_rotate_backward(dq: torch.Tensor, q: torch.Tensor, dk: torch.Tensor | N
     _call(dev, lib.mx_norm_rotate_backward, qb, kb, _DTYPES[q.dtype], tokens, dim, eps, r, _ptr(ws),
           size)
     return dxq, dxk, dwq, dwk
+
+
+def kv_append_rotary(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor,
+                     cu: torch.Tensor, lengths: torch.Tensor, rotary: Rotary | None = None,
+                     weight: torch.Tensor | None = None, eps: float = 1e-6) -> None:
+    """kv_append with the keys' norm (weight [dim]; None: no norm) and rotation
+    (None: none) on the way. Without positions a token turns by its place in its
+    sequence."""
+    dev, held_heads, held_dim, _, c = _cache_of(cache)
+    tokens, heads, dim, stride = _heads_of(k, "k", dev, _DTYPES)
+    v_tokens, v_heads, v_dim, v_stride = _heads_of(v, "v", dev, (k.dtype,))
+    if v_tokens != tokens or v_heads != heads or v_dim != dim:
+        raise ValueError("k and v must have one shape")
+    if heads != held_heads or dim != held_dim:
+        raise ValueError(f"the cache holds {held_heads} heads of {held_dim}, got {heads} of {dim}")
+    if weight is not None:
+        _want(weight, "weight", dev, k.dtype, dim)
+    r = _rotary_of(rotary, dev, dim, tokens, False)
+    b = _batch_of(dev, table, cu, lengths, tokens)[2]
+    _call(dev, load_library().mx_kv_append_rotary, k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype],
+          stride, v_stride, _ptr(weight), eps, r, c, b)
