@@ -547,6 +547,26 @@ mx_status_t mx_kv_append_rotary(const void *k, const void *v, mx_dtype_t dtype, 
                                 const mx_rotary_t *rotary, const mx_kv_cache_t *cache,
                                 const mx_kv_batch_t *batch, void *stream);
 
+/* ---- Drafted tokens ---------------------------------------------------------
+ * A sequence's new tokens as the nodes of a tree: a small model has proposed
+ * several continuations, the large one reads all of them in one call, and those
+ * that it agrees with stay. */
+
+/* mx_kv_attention over a tree of new tokens, which the cache holds behind what
+ * the sequence held before (in the order of the rows): mask [tokens, words]
+ * (device, uint32), bit b of a row: whether this token sees new token b of its
+ * sequence (bit b % 32 of word b / 32), itself included where it does. All of a
+ * sequence's tokens see every key before the new ones. With the last n of
+ * lengths[i] keys being the new ones, key j is new token j - (lengths[i] - n).
+ * Bits past the sequence's new tokens do not count; new tokens past the row's
+ * bits are not seen. A token that sees nothing gives zeros. words is 1 to 65535.
+ * Everything else, the workspace (mx_kv_attention_workspace_size) included, is
+ * mx_kv_attention's, whose results a causal mask's are but for rounding. */
+mx_status_t mx_kv_attention_tree(const void *q, int64_t q_stride, int q_heads,
+                                 const mx_kv_cache_t *cache, const mx_kv_batch_t *batch,
+                                 const uint32_t *mask, int words, int64_t max_length, float scale,
+                                 void *out, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Error reporting of this interface (no operation of the method, so no
  * passage defines it): the pages describe no error conventions; these two
  * calls only report the mx_status_t values above. */

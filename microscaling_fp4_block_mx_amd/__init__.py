@@ -48,7 +48,8 @@ EXPORTS = ("mx_quantize", "mx_dequantize", "mx_fakequant", "mx_block_mse",
            "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace_size", "mx_matmul_mxfp8",
            "mx_matmul_mxfp8_workspace_size", "mx_kv_append", "mx_kv_attention",
            "mx_kv_attention_workspace_size", "mx_norm_rotate", "mx_norm_rotate_backward",
-           "mx_norm_rotate_backward_workspace_size", "mx_kv_append_rotary", "mx_status_string", "mx_last_error_detail")
+           "mx_norm_rotate_backward_workspace_size", "mx_kv_append_rotary", "mx_kv_attention_tree",
+           "mx_status_string", "mx_last_error_detail")
 
 _lib = None
 
@@ -601,5 +602,6 @@ from .layer import (  # noqa: E402
 
 from .draft import (  # noqa: E402
     MxHeads, MxHeadsGrad, MxRotary, Rotary, declare as declare_draft, kv_append_rotary,
-    mx_kv_append_rotary, mx_norm_rotate, mx_norm_rotate_backward,
-    mx_norm_rotate_backward_workspace_size, norm_rotate, norm_rotate_backward, rotary_table)
+    kv_attention_tree, mx_kv_append_rotary, mx_kv_attention_tree, mx_norm_rotate, mx_norm_rotate_backward,
+    mx_norm_rotate_backward_workspace_size, norm_rotate, norm_rotate_backward, rotary_table,
+    tree_mask)

@@ -227,4 +227,43 @@ mx_status_t mx_kv_append_rotary(const void *k, const void *v, mx_dtype_t dtype, 
                                             stream_of(stream)));
 }
 
+mx_status_t mx_kv_attention_tree(const void *q, int64_t q_stride, int q_heads,
+                                 const mx_kv_cache_t *cache, const mx_kv_batch_t *batch,
+                                 const uint32_t *mask, int words, int64_t max_length, float scale,
+                                 void *out, void *workspace, size_t workspace_bytes, void *stream) {
+  if (mx_status_t s = check_cache(cache, batch)) return s;
+  if (mx_status_t s = check_attention(batch->tokens, batch->batch, q_heads, cache->heads,
+                                      cache->dim, max_length))
+    return s;
+  if (words < 1 || words > 65535) return MX_ERR_SHAPE;
+  if (!(scale > 0.0f) || isinf(scale)) return MX_ERR_SHAPE;
+  if (batch->tokens == 0) return MX_OK;
+  const int64_t row = (int64_t)q_heads * cache->dim;
+  if (q_stride < row || q_stride > INT32_MAX) return MX_ERR_SHAPE;
+  if (!q || !out || !mask) return MX_ERR_NULL;
+  if (mx_status_t s = check_cache_pointers(cache, batch)) return s;
+  if (!aligned16(q) || !aligned16(out) || q_stride % 8 || !aligned4(mask)) return MX_ERR_ALIGN;
+  if (max_length == 0 || max_length > (int64_t)batch->width * cache->page)
+    max_length = (int64_t)batch->width * cache->page;
+  const size_t need = mxi_kv_attention_workspace(batch->tokens, batch->batch, q_heads,
+                                                 cache->heads, cache->dim, max_length);
+  if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need))
+    return MX_ERR_WORKSPACE;
+  const int64_t codes = cache->pages * (int64_t)cache->heads * cache->dim * cache->page;
+  const int64_t scales = cache->pages * cache->heads;
+  const Range in[] = {{q, ((batch->tokens - 1) * q_stride + row) * 2},
+                      {cache->k_codes, codes},
+                      {cache->k_scales, scales},
+                      {cache->v_codes, codes},
+                      {cache->v_scales, scales},
+                      {mask, 4 * batch->tokens * words},
+                      {batch->table, 4 * (int64_t)batch->batch * batch->width},
+                      {batch->cu, 4 * ((int64_t)batch->batch + 1)},
+                      {batch->lengths, 4 * (int64_t)batch->batch}};
+  const Range outs[] = {{out, batch->tokens * row * 2}, {workspace, (int64_t)need}};
+  if (clash(outs, in)) return MX_ERR_ALIAS;
+  return finish(mxi_launch_kv_attention_tree(q, q_stride, q_heads, *cache, *batch, mask, words,
+                                             max_length, scale, out, workspace, stream_of(stream)));
+}
+
 }  // extern "C"

@@ -376,6 +376,8 @@ struct AttnArgs {
   float scale2;      // softmax scale times log2(e)
   uint16_t *out;
   float *part;       // [token, q head, split][dim + 2]: sums, then maximum and total
+  const uint32_t *tree;  // [token][words]: which new tokens of its sequence a token sees, or NULL: causal
+  int words;
 };
 
 __device__ __forceinline__ i32x8 join8(u32x4 lo, u32x4 hi) {
@@ -485,10 +487,9 @@ struct Rows {
   }
 };
 
-// Masks RT x 16 rows of 128 scores past `limit` where `masked` (tile t's
-// accumulator i is token places(t) + i) and moves the running maxima; `less`
-// is what a weight's exponent, s c - less, takes off. Branches are taken for
-// all rows at once.
+// Masks RT x 16 rows of 128 scores where `masked` (tile t's accumulator i of row
+// x is hidden(x, t, i)) and moves the running maxima; `less` is what a weight's
+// exponent, s c - less, takes off. Branches are taken for all rows at once.
 //
 // FUSED: the exponent is one operation, which leaves the largest score's off 0
 // by what rounding took from the maximum: up to half a unit in its last place.
@@ -499,7 +500,7 @@ struct Rows {
 // dims, 37 -> 41 us).
 template <int D, int RT, bool FUSED, typename F>
 __device__ __forceinline__ void running_max(f32x4 (&s)[RT][8], Rows<D> (&r)[RT], float &c, bool masked,
-                                            const int (&limit)[RT], F places, float (&less)[RT]) {
+                                            F hidden, float (&less)[RT]) {
   if (masked) {
 #pragma unroll
     for (int x = 0; x < RT; x++)
@@ -507,7 +508,7 @@ __device__ __forceinline__ void running_max(f32x4 (&s)[RT][8], Rows<D> (&r)[RT],
       for (int t = 0; t < 8; t++) {
 #pragma unroll
         for (int i = 0; i < 4; i++)
-          if (places(t) + i > limit[x]) s[x][t][i] = -__builtin_inff();
+          if (hidden(x, t, i)) s[x][t][i] = -__builtin_inff();
         __builtin_amdgcn_sched_barrier(0);  // few conditions alive at a time
       }
   }
@@ -606,10 +607,12 @@ __device__ __forceinline__ u32x4 keep_tokens(u32x4 v, int valid) {
 struct Block {  // a block of query rows and the keys it sees
   int tok0, count;  // first token of the block, tokens in it
   int len;          // tokens in the sequence's cache
-  int seen0;        // keys the block's first token sees; the next one more
+  int seen0;        // keys the block's first token sees; the next one more (tree: keys that all see)
+  int fresh;        // new tokens of the sequence
   const int32_t *table;
   int last_page;
 };
+template <bool TREE>
 __device__ __forceinline__ bool find_block(const AttnArgs &a, int unit, Block &b) {
   // everything here is the same for the whole workgroup: kept in scalar registers
   auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
@@ -621,7 +624,8 @@ __device__ __forceinline__ bool find_block(const AttnArgs &a, int unit, Block &b
   b.len = (int)min((int64_t)max(uniform(a.b.lengths[i]), 0), room);
   b.tok0 = c0 + at;
   b.count = min(a.block_tokens, n - at);
-  b.seen0 = b.len - n + at + 1;
+  b.seen0 = TREE ? b.len - n : b.len - n + at + 1;
+  b.fresh = n;
   b.table = a.b.table + (int64_t)i * a.b.width;
   b.last_page = max(0, (b.len - 1) >> a.shift);
   return true;
@@ -636,6 +640,16 @@ __device__ __forceinline__ const int32_t *page_at(const AttnArgs &a, const Block
 __device__ __forceinline__ int page_of(const AttnArgs &a, const Block &b, int tile, int lane) {
   return *page_at(a, b, tile, lane);
 }
+// 32 bits of a row of a tree's masks from bit `from` on, of which `n` count:
+// keys before the new tokens (negative) are seen, bits past the row's are not.
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t *row, int words, int n, int from) {
+  const int w = from >> 5;
+  auto word = [&](int i) { return i < 0 ? 0xFFFFFFFFu : i < words ? row[i] : 0u; };
+  const uint32_t v = __builtin_amdgcn_alignbit(word(w + 1), word(w), (uint32_t)from & 31u);
+  const int keep = n - from;
+  return keep >= 32 ? v : keep <= 0 ? 0u : v & ((1u << keep) - 1u);
+}
+
 struct Runs {
   int a, b, c, d;
 };
@@ -749,7 +763,7 @@ __device__ __forceinline__ int swz_rows(int r) {
 // bfloat16 parts would take the error against 64 bits from 0.0019 of the
 // result's norm to its rounding's 0.0017, and the same call to 100 us, 4
 // sequences of 700 tokens from 9.0 to 9.6.)
-template <int D, int RT>
+template <int D, int RT, bool TREE>
 __global__ __launch_bounds__(256, D == 128 && RT == 2 ? 1 : 2) void k_attn_rows(const AttnArgs a) {
   constexpr int DT = D / 16, W = 4, S = 128 * D, L = S / 2048;  // bytes of a tile's keys, loads of a part
   __shared__ __attribute__((aligned(16))) uint8_t codes[W][S];
@@ -760,11 +774,11 @@ __global__ __launch_bounds__(256, D == 128 && RT == 2 ? 1 : 2) void k_attn_rows(
   // first one has no room for
   const int unit = a.splits > 1 ? blockIdx.x : blockIdx.z * gridDim.x + blockIdx.x;
   Block b;
-  if (unit >= a.units || !find_block(a, unit, b)) return;
+  if (unit >= a.units || !find_block<TREE>(a, unit, b)) return;
   const int head = blockIdx.y, split = a.splits > 1 ? blockIdx.z : 0;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
-  const int end = min(b.len, b.seen0 + b.count - 1);  // keys any row sees
+  const int end = TREE ? b.len : min(b.len, b.seen0 + b.count - 1);  // keys any row sees
   const int tiles = (max(end, 0) + 127) >> 7;
   // (the last split takes whatever the caller's bound on the lengths left out)
   const int t0 = split * a.chunk, t1 = split + 1 == a.splits ? tiles : min(tiles, t0 + a.chunk);
@@ -818,7 +832,7 @@ __global__ __launch_bounds__(256, D == 128 && RT == 2 ? 1 : 2) void k_attn_rows(
   for (int x = 0; x < RT; x++) {
     const int row = min(16 * x + l16, rows - 1);
     const int tok = row / a.group;
-    seen[x] = b.seen0 + tok;
+    seen[x] = TREE ? tok : b.seen0 + tok;
     q[x] = load_query<D>(a.q + (int64_t)(b.tok0 + tok) * a.q_stride +
                              ((int64_t)head * a.group + row % a.group) * D, lg);
     r[x].clear();
@@ -861,12 +875,23 @@ __global__ __launch_bounds__(256, D == 128 && RT == 2 ? 1 : 2) void k_attn_rows(
         else scores<D, 1>(kv, q[x], sc, s[x]);
       }
     }
-    int limit[RT];
+    const bool masked = tile * 128 + 128 > b.seen0;
+    int limit[RT];  // tree: bit 4 t + i is what the row sees of accumulator i of tile t
     float less[RT], c = a.scale2;
 #pragma unroll
-    for (int x = 0; x < RT; x++) limit[x] = seen[x] - 1 - tile * 128 - 16 * lg;
-    running_max<D, RT, false>(s, r, c, tile * 128 + 128 > b.seen0, limit,
-                       [](int t) { return 64 * (t >> 2) + 4 * (t & 3); }, less);
+    for (int x = 0; x < RT; x++) {
+      if constexpr (!TREE) {
+        limit[x] = seen[x] - 1 - tile * 128 - 16 * lg;
+      } else if (masked) {
+        const uint32_t *row = a.tree + (int64_t)(b.tok0 + seen[x]) * a.words;
+        const int from = tile * 128 + 16 * lg - b.seen0;
+        limit[x] = (int)((tree_bits(row, a.words, b.fresh, from) & 0xFFFFu) |
+                         tree_bits(row, a.words, b.fresh, from + 64) << 16);
+      }
+    }
+    running_max<D, RT, false>(s, r, c, masked, [&](int x, int t, int i) {
+      return TREE ? !(limit[x] >> (4 * t + i) & 1) : 64 * (t >> 2) + 4 * (t & 3) + i > limit[x];
+    }, less);
     u32x4 p[RT][4];
     weights<RT, false>(s, c, less, p);
     const uint32_t vb0 = sc >> 16 & 255u, vb1 = sc >> 24;
@@ -986,7 +1011,7 @@ __device__ __forceinline__ int splits_of(const AttnArgs &a, int tok) {
   const int64_t room = (int64_t)a.b.width << a.shift;
   const int len = (int)min((int64_t)max(a.b.lengths[i], 0), room);
   const int at = (tok - c0) / a.block_tokens * a.block_tokens;
-  const int end = min(len, len - n + at + min(a.block_tokens, n - at));
+  const int end = a.tree ? len : min(len, len - n + at + min(a.block_tokens, n - at));
   const int tiles = (max(end, 0) + 127) >> 7;
   return max(1, min(a.splits, (tiles + a.chunk - 1) / a.chunk));
 }
@@ -1100,7 +1125,7 @@ __device__ __forceinline__ int swz_k(int r) {
   return (r >> 3) & 3;
 }
 
-template <int D>
+template <int D, bool TREE>
 __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
   constexpr int DT = D / 16, RT = 2, S = 128 * D;
   constexpr int KL = S / 4096, VL = KL;  // direct loads per thread and tile
@@ -1111,10 +1136,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
   const uint32_t block = blockIdx.z * gridDim.x + blockIdx.x;
   const int head = block % a.c.heads, from_last = block / a.c.heads;
   Block b;
-  if (from_last >= a.units || !find_block(a, a.units - 1 - from_last, b)) return;
+  if (from_last >= a.units || !find_block<TREE>(a, a.units - 1 - from_last, b)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
-  const int end = min(b.len, b.seen0 + b.count - 1);
+  const int end = TREE ? b.len : min(b.len, b.seen0 + b.count - 1);
   const int tiles = (max(end, 0) + 127) >> 7;
   // this split's tiles, from an even one on (the buffers take turns); the last
   // split takes whatever the caller's bound on the lengths left out
@@ -1129,7 +1154,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
   for (int x = 0; x < RT; x++) {
     const int row = min(32 * wave + 16 * x + l16, rows - 1);
     const int tok = row / a.group;
-    seen[x] = b.seen0 + tok;
+    seen[x] = TREE ? tok : b.seen0 + tok;
     q[x] = load_query<D>(a.q + (int64_t)(b.tok0 + tok) * a.q_stride +
                              ((int64_t)head * a.group + row % a.group) * D, lg);
     r[x].clear();
@@ -1239,12 +1264,25 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
     for (int x = 0; x < RT; x++)
 #pragma unroll
       for (int t = 0; t < 8; t++) asm volatile("" : "+v"(s[x][t]));
-    int limit[RT];
+    const bool masked = tile * 128 + 128 > b.seen0;
+    int limit[RT];  // tree: bit 4 t + i is what the row sees of accumulator i of tile t
     float less[RT], c = a.scale2;
 #pragma unroll
-    for (int x = 0; x < RT; x++) limit[x] = seen[x] - 1 - tile * 128 - 8 * lg;
-    running_max<D, RT, true>(s, r, c, tile * 128 + 128 > b.seen0, limit,
-                       [](int t) { return 32 * (t >> 1) + 4 * (t & 1); }, less);
+    for (int x = 0; x < RT; x++) {
+      if constexpr (!TREE) {
+        limit[x] = seen[x] - 1 - tile * 128 - 8 * lg;
+      } else if (masked) {
+        const uint32_t *row = a.tree + (int64_t)(b.tok0 + seen[x]) * a.words;
+        uint32_t bits = 0;
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          bits |= (tree_bits(row, a.words, b.fresh, tile * 128 + 32 * j + 8 * lg - b.seen0) & 0xFFu) << (8 * j);
+        limit[x] = (int)bits;
+      }
+    }
+    running_max<D, RT, true>(s, r, c, masked, [&](int x, int t, int i) {
+      return TREE ? !(limit[x] >> (4 * t + i) & 1) : 32 * (t >> 1) + 4 * (t & 1) + i > limit[x];
+    }, less);
     u32x4 p[RT][4];  // of tokens 32 j + 8 lg ..
     weights<RT, true>(s, c, less, p);
     // the widened values of every wave are in LDS
@@ -1410,28 +1448,30 @@ size_t mxi_kv_attention_workspace(int64_t tokens, int batch, int q_heads, int he
   return p.most_splits > 1 ? (size_t)tokens * q_heads * p.most_splits * (dim + 4) * sizeof(float) : 0;
 }
 
-hipError_t mxi_launch_kv_attention(const void *q, int64_t q_stride, int q_heads,
+template <bool TREE>
+static hipError_t launch_attention(const void *q, int64_t q_stride, int q_heads,
                                    const mx_kv_cache_t &cache, const mx_kv_batch_t &batch,
-                                   int64_t max_length, float scale, void *out, void *workspace,
-                                   hipStream_t st) {
+                                   const uint32_t *tree, int words, int64_t max_length, float scale,
+                                   void *out, void *workspace, hipStream_t st) {
   const AttnPlan p = attn_plan(batch.tokens, batch.batch, q_heads, cache.heads, max_length);
   const AttnArgs a = {reinterpret_cast<const uint16_t *>(q), q_stride, q_heads,
                       q_heads / cache.heads, cache, batch, log2_of(cache.page), p.block_tokens,
                       p.chunk, p.splits, (int)p.units, scale * 1.44269504088896340736f,
-                      reinterpret_cast<uint16_t *>(out), reinterpret_cast<float *>(workspace)};
+                      reinterpret_cast<uint16_t *>(out), reinterpret_cast<float *>(workspace),
+                      tree, words};
   // (few rows are split for at most 1,024 sequences)
   const Spread xz = spread(p.few ? p.units : p.units * cache.heads);
   const dim3 grid(xz.first, (uint32_t)cache.heads, p.splits > 1 ? (uint32_t)p.splits : xz.second);
   if (!p.few) {
     const dim3 tgrid(xz.first, (uint32_t)p.splits, xz.second);
-    if (cache.dim == 64) k_attn_tiles<64><<<tgrid, 256, 0, st>>>(a);
-    else k_attn_tiles<128><<<tgrid, 256, 0, st>>>(a);
+    if (cache.dim == 64) k_attn_tiles<64, TREE><<<tgrid, 256, 0, st>>>(a);
+    else k_attn_tiles<128, TREE><<<tgrid, 256, 0, st>>>(a);
   } else if (cache.dim == 64) {
-    if (p.rt == 1) k_attn_rows<64, 1><<<grid, 256, 0, st>>>(a);
-    else k_attn_rows<64, 2><<<grid, 256, 0, st>>>(a);
+    if (p.rt == 1) k_attn_rows<64, 1, TREE><<<grid, 256, 0, st>>>(a);
+    else k_attn_rows<64, 2, TREE><<<grid, 256, 0, st>>>(a);
   } else {
-    if (p.rt == 1) k_attn_rows<128, 1><<<grid, 256, 0, st>>>(a);
-    else k_attn_rows<128, 2><<<grid, 256, 0, st>>>(a);
+    if (p.rt == 1) k_attn_rows<128, 1, TREE><<<grid, 256, 0, st>>>(a);
+    else k_attn_rows<128, 2, TREE><<<grid, 256, 0, st>>>(a);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
@@ -1448,4 +1488,18 @@ hipError_t mxi_launch_kv_attention(const void *q, int64_t q_stride, int q_heads,
   if (cache.dim == 64) k_attn_join<64><<<jgrid, 256, 0, st>>>(a);
   else k_attn_join<128><<<jgrid, 256, 0, st>>>(a);
   return hipGetLastError();
+}
+
+hipError_t mxi_launch_kv_attention(const void *q, int64_t q_stride, int q_heads,
+                                   const mx_kv_cache_t &cache, const mx_kv_batch_t &batch,
+                                   int64_t max_length, float scale, void *out, void *workspace,
+                                   hipStream_t st) {
+  return launch_attention<false>(q, q_stride, q_heads, cache, batch, nullptr, 0, max_length, scale, out, workspace, st);
+}
+
+hipError_t mxi_launch_kv_attention_tree(const void *q, int64_t q_stride, int q_heads,
+                                        const mx_kv_cache_t &cache, const mx_kv_batch_t &batch,
+                                        const uint32_t *mask, int words, int64_t max_length,
+                                        float scale, void *out, void *workspace, hipStream_t st) {
+  return launch_attention<true>(q, q_stride, q_heads, cache, batch, mask, words, max_length, scale, out, workspace, st);
 }

@@ -48,6 +48,11 @@ hipError_t mxi_launch_kv_append_rotary(const void *k, const void *v, int bf16, i
                                        int64_t v_stride, const void *weight, float eps,
                                        const mx_rotary_t &rotary, const mx_kv_cache_t &cache,
                                        const mx_kv_batch_t &batch, hipStream_t st);
+// The same scratch as mxi_launch_kv_attention's.
+hipError_t mxi_launch_kv_attention_tree(const void *q, int64_t q_stride, int q_heads,
+                                        const mx_kv_cache_t &cache, const mx_kv_batch_t &batch,
+                                        const uint32_t *mask, int words, int64_t max_length,
+                                        float scale, void *out, void *workspace, hipStream_t st);
 
 // Heads' norms and rotation; `k` may be NULL, `rotary` with rot = 0 turns nothing.
 hipError_t mxi_launch_norm_rotate(const mx_heads_t &q, const mx_heads_t *k, int bf16,

@@ -78,5 +78,16 @@ inline mx_status_t check_cache_pointers(const mx_kv_cache_t *c, const mx_kv_batc
   return MX_OK;
 }
 
+inline mx_status_t check_attention(int64_t tokens, int batch, int q_heads, int heads, int dim,
+                                   int64_t max_length) {
+  if (tokens < 0 || tokens > INT32_MAX / 2 || batch < 0 || batch > (1 << 24)) return MX_ERR_SHAPE;
+  if (heads < 1 || heads > 65535 || q_heads < heads || q_heads % heads || q_heads / heads > 128)
+    return MX_ERR_SHAPE;
+  if ((dim != 64 && dim != 128) || max_length < 0 || max_length > INT32_MAX) return MX_ERR_SHAPE;
+  // workgroups of one launch: a row of heads per token, and per sequence
+  if (tokens > 0 && (batch < 1 || (tokens + batch) > INT32_MAX / q_heads)) return MX_ERR_SHAPE;
+  return MX_OK;
+}
+
 }  // namespace mxc
 #endif  // MX_LAYER_CHECKS_H

@@ -1,7 +1,8 @@
 """Positions and drafted tokens beside the 8-bit cache: tensor-level helpers.
 
 The norms of queries and keys per head with the position rotation, their
-gradient, and the append that has both on the way. Every step runs in the HIP kernels behind include/mx.h; this module
+gradient, the append that has both on the way, and attention over a tree of
+drafted tokens. Every step runs in the HIP kernels behind include/mx.h; this module
 allocates outputs and scratch with torch (on the current stream) and checks
 what the C entry points cannot see: devices, dtypes, shapes and contiguity. Bad
 arguments raise ``ValueError``, HIP errors ``RuntimeError``.
@@ -9,6 +10,7 @@ arguments raise ``ValueError``, HIP errors ``RuntimeError``.
 from __future__ import annotations
 
 import ctypes
+import math
 import struct
 from typing import NamedTuple
 
@@ -56,6 +58,30 @@ def rotary_table(length: int, rot: int, base: float = 10000.0, device="cuda") ->
     return torch.cat([angles.cos(), angles.sin()], 1).float()
 
 
+def tree_mask(parents, device="cuda"):
+    """(mask int32 [tokens, words], depth int32 [tokens]) of drafted tokens: `parents`
+    lists, for each sequence, each node's parent (-1: none; parents come first). A
+    node sees its ancestors and itself; depth counts its ancestors. Formed on the
+    host, once for a tree's shape."""
+    parents = [list(p) for p in parents]
+    words = max(1, -(-max((len(p) for p in parents), default=0) // 32))
+    rows, depth = [], []
+    for tree in parents:
+        bits, deep = [], []
+        for j, up in enumerate(tree):
+            if not -1 <= up < j:
+                raise ValueError(f"node {j}'s parent must come before it, got {up}")
+            bits.append(1 << j | (bits[up] if up >= 0 else 0))
+            deep.append(deep[up] + 1 if up >= 0 else 0)
+        for b in bits:
+            for w in range(words):
+                word = b >> 32 * w & 0xFFFFFFFF
+                rows.append(word - (1 << 32) if word >> 31 else word)
+        depth += deep
+    return (torch.tensor(rows, dtype=torch.int32, device=device).view(-1, words),
+            torch.tensor(depth, dtype=torch.int32, device=device))
+
+
 # ---- C entry points, same names -------------------------------------------
 
 def mx_norm_rotate(q, k, dtype, tokens, dim, eps, rotary, stream) -> int:
@@ -78,6 +104,13 @@ def mx_kv_append_rotary(k, v, dtype, k_stride, v_stride, k_weight, eps, rotary, 
                                               cache, batch, stream)
 
 
+def mx_kv_attention_tree(q, q_stride, q_heads, cache, batch, mask, words, max_length, scale, out,
+                         workspace, workspace_bytes, stream) -> int:
+    return load_library().mx_kv_attention_tree(q, q_stride, q_heads, cache, batch, mask, words,
+                                               max_length, scale, out, workspace, workspace_bytes,
+                                               stream)
+
+
 def declare(lib) -> None:
     """Argument and result types of the entry points."""
     p, i64, i32, f32, size = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
@@ -86,6 +119,7 @@ def declare(lib) -> None:
         "mx_norm_rotate": [p, p, i32, i64, i32, f32, p, p],
         "mx_norm_rotate_backward": [p, p, i32, i64, i32, f32, p, p, size, p],
         "mx_kv_append_rotary": [p, p, i32, i64, i64, p, f32, p, p, p, p],
+        "mx_kv_attention_tree": [p, i64, i32, p, p, p, i32, i64, f32, p, p, size, p],
         "mx_norm_rotate_backward_workspace_size": [i64, i32],
     }
     for name, args in types.items():
@@ -232,3 +266,34 @@ def kv_append_rotary(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: to
     b = _batch_of(dev, table, cu, lengths, tokens)[2]
     _call(dev, load_library().mx_kv_append_rotary, k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype],
           stride, v_stride, _ptr(weight), eps, r, c, b)
+
+
+def kv_attention_tree(q: torch.Tensor, cache: KVCache, table: torch.Tensor, cu: torch.Tensor,
+                      lengths: torch.Tensor, mask: torch.Tensor, scale: float | None = None,
+                      max_length: int = 0, out: torch.Tensor | None = None) -> torch.Tensor:
+    """kv_attention where a sequence's new tokens see each other by `mask` int32
+    [tokens, words] (tree_mask): bit b, whether a token sees new token b of its
+    sequence. Every key before the new tokens is seen."""
+    dev, heads, held_dim, page, c = _cache_of(cache)
+    tokens, q_heads, dim, stride = _heads_of(q, "q", dev, (torch.bfloat16,))
+    if dim != held_dim:
+        raise ValueError(f"the cache holds heads of {held_dim}, got {dim}")
+    if q_heads < heads or q_heads % heads:
+        raise ValueError(f"q_heads must be a multiple of the cache's {heads}, got {q_heads}")
+    if not isinstance(mask, torch.Tensor) or mask.dim() != 2 or mask.shape[1] < 1:
+        raise ValueError("mask must be [tokens, words]")
+    words = mask.shape[1]
+    _want(mask, "mask", dev, torch.int32, tokens * words, words)
+    batch, width, b = _batch_of(dev, table, cu, lengths, tokens)
+    if out is None:
+        out = torch.empty(tokens, q_heads, dim, dtype=torch.bfloat16, device=dev)
+    else:
+        _want(out, "out", dev, torch.bfloat16, tokens * q_heads * dim, dim)
+    room = width * page
+    max_length = room if max_length <= 0 else min(max_length, room)
+    lib = load_library()
+    size = lib.mx_kv_attention_workspace_size(tokens, batch, q_heads, heads, dim, max_length)
+    ws = _scratch(size, dev)
+    _call(dev, lib.mx_kv_attention_tree, q.data_ptr(), stride, q_heads, c, b, mask.data_ptr(), words,
+          max_length, 1.0 / math.sqrt(dim) if scale is None else scale, out.data_ptr(), _ptr(ws), size)
+    return out

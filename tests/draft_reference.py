@@ -50,3 +50,64 @@ def heads_backward(dy, x, weight, eps, rotary):
     dx = s * (g - x * s * s * (g * x).sum(2, keepdim=True) / x.shape[2])
     terms = n * x * s
     return dx, terms.sum((0, 1)), terms.abs().sum((0, 1))
+
+
+F8 = torch.float8_e4m3fn
+
+
+def cache_value(codes, byte):
+    s = torch.ldexp(torch.ones(byte.shape, dtype=torch.float64), byte.to(torch.int32) - 127)
+    s = torch.where(byte == 255, torch.nan, s)
+    return codes.view(F8).double() * s[..., None, None]
+
+
+def ancestors(parents):
+    """bool [n, n]: which nodes a node sees (itself and its ancestors)."""
+    n = len(parents)
+    sees = torch.zeros(n, n, dtype=torch.bool)
+    for j, up in enumerate(parents):
+        if up >= 0:
+            sees[j] = sees[up]
+        sees[j, j] = True
+    return sees
+
+
+def words_of(sees, words):
+    """bool [n, m] -> int32 [n, words], bit b of a row being column b."""
+    out = torch.zeros(sees.shape[0], words, dtype=torch.int64)
+    for b in range(min(sees.shape[1], 32 * words)):
+        out[:, b // 32] |= sees[:, b].long() << (b % 32)
+    return torch.where(out >= 2 ** 31, out - 2 ** 32, out).int()
+
+
+def attention_tree(q, cache, table, cu, lengths, sees, scale):
+    """sees[i]: bool [n, n] of sequence i's new tokens -> (out, sum_j p_j |v_j|, the
+    largest sum |q_i k_i| * scale of a row)."""
+    kc, ks, vc, vs = cache
+    page, count = kc.shape[2], kc.shape[1]
+    tokens, q_heads, dim = q.shape
+    group = q_heads // count
+    out = torch.zeros((tokens, q_heads, dim), dtype=torch.float64)
+    mag, reach = torch.zeros_like(out), torch.zeros((tokens, q_heads), dtype=torch.float64)
+    for i in range(table.shape[0]):
+        a, n, length = int(cu[i]), int(cu[i + 1] - cu[i]), int(lengths[i])
+        if n == 0 or length == 0:
+            continue
+        ids = table[i, :-(-length // page)].long()
+        seen = torch.ones(n, length, dtype=torch.bool)
+        for key in range(max(0, length - n), length):
+            seen[:, key] = sees[i][:, key - (length - n)]
+        for h in range(count):
+            kd = cache_value(kc[ids, h], ks[ids, h]).reshape(-1, dim)[:length]
+            vd = cache_value(vc[ids, h], vs[ids, h]).transpose(1, 2).reshape(-1, dim)[:length]
+            for t in range(n):
+                at = seen[t]
+                if not bool(at.any()):
+                    continue
+                of = slice(h * group, (h + 1) * group)
+                x = q[a + t, of].double()
+                p = torch.softmax(x @ kd[at].t() * scale, 1)
+                out[a + t, of] = p @ vd[at]
+                mag[a + t, of] = p @ vd[at].abs()
+                reach[a + t, of] = (x.abs() @ kd[at].abs().t()).amax(1) * scale
+    return out, mag, reach
