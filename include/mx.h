@@ -567,6 +567,53 @@ mx_status_t mx_kv_attention_tree(const void *q, int64_t q_stride, int q_heads,
                                  const uint32_t *mask, int words, int64_t max_length, float scale,
                                  void *out, void *workspace, size_t workspace_bytes, void *stream);
 
+/* Verify drafted tokens against the target model's probabilities. Sequence i's
+ * nodes are rows cu[i] .. cu[i+1] - 1 (cu[0] = 0, cu[batch] = tokens): node 0 is
+ * its last token, each other one a drafted token ids[row] behind its parent, node
+ * parents[row] of the same sequence (parents come first; node 0's does not
+ * count; a node whose parents do not lead to node 0 is not reached). target
+ * [tokens, vocab]: row j, the target's probabilities of the token behind node j.
+ * draft [tokens, vocab], or NULL: row j, those that the draft's token of node
+ * j's first child was drawn from. numbers [tokens, 2]: uniform random numbers
+ * from 0 to below 1, u and v of each node.
+ * The walk starts at node 0. At a node with target row p and draft row q, whose
+ * children are those nodes that name it:
+ *   with a draft and a child: the first child, with token x, is followed if
+ *   u q(x) < p(x); else w = max(p - q, 0) (p, if nothing is left of it);
+ *   without: w = p.
+ *   Where no child was followed, t is the first token with w(0) + .. + w(t) > v
+ *   sum(w) and w(t) > 0 (if rounding leaves none, the last with w(t) > 0). The
+ *   first child with token t is followed (with a draft: but for the first one);
+ *   if there is none, t is the sequence's next token and the walk ends.
+ * path [batch, width] gets the nodes of the walk, 0 first, then -1; count [batch]
+ * how many; token [batch] the next token, -1 where w had nothing. Node number
+ * width of a path has no children. Tokens so found are distributed as the
+ * target's own, whichever other children there are. A sequence without nodes has
+ * count 0 and token -1; of one with more than 1,024 the first 1,024 count.
+ * Probabilities below 0, infinite or NaN count as 0; rows need not sum to 1.
+ * Products, differences and sums are in 64 bits. target and draft share a dtype
+ * and are 16-byte aligned. batch is at most 65535, width 1 to 1024. workspace:
+ * mx_verify_drafts_workspace_size(...) bytes, 16-byte aligned. */
+size_t mx_verify_drafts_workspace_size(int64_t tokens, int batch, int64_t vocab);
+mx_status_t mx_verify_drafts(const void *target, const void *draft, mx_dtype_t dtype,
+                             const int32_t *ids, const int32_t *parents, const int32_t *cu,
+                             const float *numbers, int64_t tokens, int batch, int64_t vocab,
+                             int width, int32_t *path, int32_t *count, int32_t *token,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/* Keep the accepted tokens of each sequence's tree in the cache, in place: of the
+ * new tokens behind lengths[i] held ones, path[i][j] moves to place lengths[i] +
+ * j, for j below count[i] (path [batch, path_width], count [batch]: as
+ * mx_verify_drafts gives them). The sequence then holds lengths[i] + count[i].
+ * A page that tokens move into gets the largest of its kept tokens' scale byte and
+ * those that the moved ones had; where a code's byte grows it is rounded once
+ * more. A path ends where its nodes are not in rising order or lie past the
+ * table's room. Tokens that move into pages outside the cache are dropped, those
+ * from there become zeros. Slots past the new end are left alone, and so is a
+ * sequence whose path is 0, 1, 2, ... batch's cu and tokens are not used. */
+mx_status_t mx_kv_keep(const mx_kv_cache_t *cache, const mx_kv_batch_t *batch, const int32_t *path,
+                       int path_width, const int32_t *count, void *stream);
+
 /* Error reporting of this interface (no operation of the method, so no
  * passage defines it): the pages describe no error conventions; these two
  * calls only report the mx_status_t values above. */

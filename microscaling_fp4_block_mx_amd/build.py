@@ -20,7 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmx.so")
 SOURCES = ["mx_kernels.hip", "mx_norm.hip", "mx_matmul.hip", "mx_kv.hip", "mx_rotary.hip",
-           "mx_api.cpp", "mx_layer_api.cpp", "mx_draft_api.cpp"]
+           "mx_verify.hip", "mx_api.cpp", "mx_layer_api.cpp", "mx_draft_api.cpp"]
 ARCH = "gfx950"
 
 

@@ -266,4 +266,69 @@ mx_status_t mx_kv_attention_tree(const void *q, int64_t q_stride, int q_heads,
                                              max_length, scale, out, workspace, stream_of(stream)));
 }
 
+static mx_status_t check_verify(int64_t tokens, int batch, int64_t vocab) {
+  if (tokens < 0 || tokens > INT32_MAX || batch < 0 || batch > 65535) return MX_ERR_SHAPE;
+  if (vocab < 1 || vocab > INT32_MAX || (tokens > 0 && batch < 1)) return MX_ERR_SHAPE;
+  // the rows' bytes, and workgroups of 8,192 elements of a row
+  if (tokens > 0 && vocab > INT64_MAX / 8 / tokens) return MX_ERR_SHAPE;
+  if ((vocab / 8192 + 2) * (int64_t)batch > INT32_MAX) return MX_ERR_SHAPE;
+  return MX_OK;
+}
+
+size_t mx_verify_drafts_workspace_size(int64_t tokens, int batch, int64_t vocab) {
+  if (check_verify(tokens, batch, vocab) != MX_OK || tokens == 0) return 0;
+  return mxi_verify_workspace(tokens, batch, vocab);
+}
+
+mx_status_t mx_verify_drafts(const void *target, const void *draft, mx_dtype_t dtype,
+                             const int32_t *ids, const int32_t *parents, const int32_t *cu,
+                             const float *numbers, int64_t tokens, int batch, int64_t vocab,
+                             int width, int32_t *path, int32_t *count, int32_t *token,
+                             void *workspace, size_t workspace_bytes, void *stream) {
+  if (!dtype_ok(dtype)) return MX_ERR_DTYPE;
+  if (mx_status_t s = check_verify(tokens, batch, vocab)) return s;
+  if (width < 1 || width > 1024) return MX_ERR_SHAPE;
+  if (batch == 0) return MX_OK;
+  if (!cu || !path || !count || !token) return MX_ERR_NULL;
+  if (!aligned4(cu) || !aligned4(path) || !aligned4(count) || !aligned4(token)) return MX_ERR_ALIGN;
+  const size_t need = mx_verify_drafts_workspace_size(tokens, batch, vocab);
+  if (tokens > 0) {
+    if (!target || !ids || !parents || !numbers) return MX_ERR_NULL;
+    if (!aligned16(target) || !aligned16(draft) || !aligned4(ids) || !aligned4(parents) ||
+        !aligned4(numbers))
+      return MX_ERR_ALIGN;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < need) return MX_ERR_WORKSPACE;
+  }
+  const int64_t rows = tokens * vocab * elem_bytes(dtype), b = 4 * (int64_t)batch;
+  const Range out[] = {{path, b * width}, {count, b}, {token, b}, {workspace, (int64_t)need}};
+  const Range in[] = {{target, rows}, {draft, rows}, {ids, 4 * tokens}, {parents, 4 * tokens},
+                      {cu, b + 4}, {numbers, 8 * tokens}};
+  if (clash(out, in)) return MX_ERR_ALIAS;
+  return finish(mxi_launch_verify(target, draft, dtype == MX_BF16, ids, parents, cu, numbers, tokens,
+                                  batch, vocab, width, path, count, token, workspace,
+                                  stream_of(stream)));
+}
+
+mx_status_t mx_kv_keep(const mx_kv_cache_t *cache, const mx_kv_batch_t *batch, const int32_t *path,
+                       int path_width, const int32_t *count, void *stream) {
+  if (!cache || !batch) return MX_ERR_NULL;
+  mx_kv_batch_t of = *batch;  // its cu and tokens do not count
+  of.cu = of.lengths;
+  of.tokens = 0;
+  if (mx_status_t s = check_cache(cache, &of)) return s;
+  if (path_width < 1 || (int64_t)path_width > kMaxLength) return MX_ERR_SHAPE;
+  if (of.batch == 0) return MX_OK;
+  if (of.width < 1 || cache->pages < 1) return MX_ERR_SHAPE;
+  if (mx_status_t s = check_cache_pointers(cache, &of)) return s;
+  if (!path || !count) return MX_ERR_NULL;
+  if (!aligned4(path) || !aligned4(count)) return MX_ERR_ALIGN;
+  const int64_t codes = cache->pages * (int64_t)cache->heads * cache->dim * cache->page;
+  const int64_t scales = cache->pages * cache->heads, b = 4 * (int64_t)of.batch;
+  const Range out[] = {{cache->k_codes, codes}, {cache->k_scales, scales},
+                       {cache->v_codes, codes}, {cache->v_scales, scales}};
+  const Range in[] = {{of.table, b * of.width}, {of.lengths, b}, {path, b * path_width}, {count, b}};
+  if (clash(out, in)) return MX_ERR_ALIAS;
+  return finish(mxi_launch_kv_keep(*cache, of, path, path_width, count, stream_of(stream)));
+}
+
 }  // extern "C"

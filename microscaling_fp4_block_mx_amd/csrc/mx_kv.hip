@@ -92,6 +92,18 @@ __device__ __forceinline__ uint32_t move4(uint32_t w, int d, bool nan) {
   return (uint32_t)r;
 }
 
+// The first `keep` of 16 codes moved, the others as they are.
+__device__ __forceinline__ u32x4 move16(u32x4 v, int keep, int d, bool nan) {
+  u32x4 w;
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    const int n = min(max(keep - 4 * e, 0), 4);
+    const uint32_t mask = n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1;
+    w[e] = (move4(v[e], d, nan) & mask) | (v[e] & ~mask);
+  }
+  return w;
+}
+
 // Items of eight elements that a thread keeps between the two passes (what a
 // page of 64 tokens of 128 dims takes); larger pages read the rest twice.
 constexpr int kKeep = 4;
@@ -296,15 +308,7 @@ __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
 #pragma unroll
       for (int u = 0; u < 4; u++) {
         if (c + u * T >= pieces) break;
-        const int keep = keeps(c + u * T);
-        u32x4 w;
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          const int n = min(max(keep - 4 * e, 0), 4);
-          const uint32_t mask = n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1;
-          w[e] = (move4(v[u][e], d, nan) & mask) | (v[u][e] & ~mask);
-        }
-        *reinterpret_cast<u32x4 *>(place(c + u * T)) = w;
+        *reinterpret_cast<u32x4 *>(place(c + u * T)) = move16(v[u], keeps(c + u * T), d, nan);
       }
     }
   };
@@ -358,6 +362,130 @@ __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
   if (threadIdx.x == 0) {
     if (!kept || sk != was_k) a.c.k_scales[at] = (uint8_t)sk;
     if (!kept || sv != was_v) a.c.v_scales[at] = (uint8_t)sv;
+  }
+}
+
+// ---- keep ---------------------------------------------------------------------------
+//
+// Accepted tokens of a tree, at held + path[j], move to held + j. A page that
+// tokens move into gets the largest of its kept tokens' byte (where it has any)
+// and those that the moved ones had; codes are rounded once more where their
+// byte grows. A path's nodes come in order, so no token lies before where it
+// goes: pages are done in order, and what a later one needs is still in place. A
+// workgroup takes a sequence and head. Latency is all there is: counts, tables,
+// bytes and codes, each a trip to memory that waits for the last.
+struct KeepArgs {
+  mx_kv_cache_t c;
+  const int32_t *table, *lengths, *path, *count;
+  int batch, width, path_width, shift;
+};
+constexpr int kMoved = 64;  // tokens on the move at a time
+
+__global__ __launch_bounds__(256) void k_kv_keep(const KeepArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t ks[kMoved * 128], vs[kMoved * 128];
+  __shared__ uint8_t kb[256], vb[256];  // bytes that a page's tokens come with
+  __shared__ int from_page[256], from_slot[256];
+  __shared__ int stays, ends;
+  __shared__ uint32_t most_k, most_v;
+  const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (block >= (int64_t)a.batch * a.c.heads) return;
+  const int i = (int)(block / a.c.heads), head = (int)(block % a.c.heads), tid = threadIdx.x;
+  const int P = a.c.page, D = a.c.dim, held = a.lengths[i];
+  const int many = min(a.count[i], a.path_width);
+  const int32_t *path = a.path + (int64_t)i * a.path_width;
+  const int32_t *table = a.table + (int64_t)i * a.width;
+  if (held < 0 || many <= 0) return;
+  if (tid == 0) {
+    stays = many;
+    ends = many;
+  }
+  __syncthreads();
+  for (int j = tid; j < many; j += 256) {
+    const int p = path[j], last = j ? path[j - 1] : -1;
+    if (p != j) atomicMin(&stays, j);
+    // not in order, or past the table's room: the path ends there
+    if (p <= last || (((int64_t)held + p) >> a.shift) >= a.width) atomicMin(&ends, j);
+  }
+  __syncthreads();
+  const int first = stays, end = ends;
+  if (first >= end) return;  // (end > 0: the last token to move lies inside the table)
+  for (int page = (held + first) >> a.shift; page <= (held + end - 1) >> a.shift; page++) {
+    const int begin = page << a.shift, lo = max(held + first, begin);
+    const int n = min(held + end, begin + P) - lo, kept = lo - begin;
+    const int64_t id = table[page];
+    if (id < 0 || id >= a.c.pages) continue;  // no page: its tokens are dropped
+    const int64_t at = id * a.c.heads + head;
+    const uint32_t was_k = kept ? a.c.k_scales[at] : 0u, was_v = kept ? a.c.v_scales[at] : 0u;
+    if (tid == 0) {
+      most_k = was_k;
+      most_v = was_v;
+    }
+    __syncthreads();
+    for (int s = tid; s < n; s += 256) {  // (n is at most a page: one token a thread)
+      const int src = held + path[lo - held + s];
+      const int from = table[src >> a.shift];
+      const bool none = from < 0 || from >= a.c.pages;  // its tokens become zeros
+      from_page[s] = none ? -1 : from;
+      from_slot[s] = src & (P - 1);
+      const int64_t b = (int64_t)from * a.c.heads + head;
+      kb[s] = none ? 0 : a.c.k_scales[b];
+      vb[s] = none ? 0 : a.c.v_scales[b];
+      atomicMax(&most_k, (uint32_t)kb[s]);
+      atomicMax(&most_v, (uint32_t)vb[s]);
+    }
+    __syncthreads();
+    const uint32_t sk = most_k, sv = most_v;
+    uint8_t *kc = a.c.k_codes + at * P * D, *vc = a.c.v_codes + at * P * D;
+    for (int s0 = 0; s0 < n; s0 += kMoved) {
+      const int m = min(n - s0, kMoved);
+      // what moves is read before anything is written
+      for (int it = tid; it < m * D / 16; it += 256) {
+        const int s = s0 + it / (D / 16), d = it % (D / 16) * 16;
+        u32x4 w = {0, 0, 0, 0};
+        if (from_page[s] >= 0)
+          w = *reinterpret_cast<const u32x4 *>(a.c.k_codes + (((int64_t)from_page[s] * a.c.heads + head) * P + from_slot[s]) * D + d);
+        *reinterpret_cast<u32x4 *>(ks + it * 16) = w;
+      }
+      for (int it = tid; it < m * D; it += 256) {
+        const int s = s0 + it / D, d = it % D;
+        vs[it] = from_page[s] < 0 ? 0
+                                  : a.c.v_codes[(((int64_t)from_page[s] * a.c.heads + head) * D + d) * P + from_slot[s]];
+      }
+      __syncthreads();
+      if (s0 == 0) {  // the kept tokens, to the new bytes
+        if (kept && sk > was_k)
+          for (int c = tid; c < kept * D / 16; c += 256) {
+            u32x4 *p = reinterpret_cast<u32x4 *>(kc + 16 * c);
+            *p = move16(*p, 16, (int)(sk - was_k), sk == 255u);
+          }
+        if (kept && sv > was_v) {
+          const int pieces = (kept + 15) >> 4;
+          for (int c = tid; c < D * pieces; c += 256) {
+            u32x4 *p = reinterpret_cast<u32x4 *>(vc + c / pieces * P + c % pieces * 16);
+            *p = move16(*p, kept - c % pieces * 16, (int)(sv - was_v), sv == 255u);
+          }
+        }
+        __syncthreads();  // before the moved tokens' bytes of the same words
+      }
+      for (int it = tid; it < m * D / 16; it += 256) {
+        const int s = it / (D / 16), d = it % (D / 16) * 16, by = (int)(sk - kb[s0 + s]);
+        u32x4 w = *reinterpret_cast<const u32x4 *>(ks + it * 16);
+        if (by) w = move16(w, 16, by, sk == 255u);
+        *reinterpret_cast<u32x4 *>(kc + (kept + s0 + s) * D + d) = w;
+      }
+      for (int it = tid; it < m * D; it += 256) {
+        const int s = it % m, d = it / m, by = (int)(sv - vb[s0 + s]);
+        uint32_t w = vs[s * D + d];
+        if (by) w = move4(w, by, sv == 255u);
+        vc[d * P + kept + s0 + s] = (uint8_t)w;
+      }
+      __syncthreads();
+    }
+    if (tid == 0) {
+      a.c.k_scales[at] = (uint8_t)sk;
+      a.c.v_scales[at] = (uint8_t)sv;
+    }
+    __syncthreads();
   }
 }
 
@@ -1440,6 +1568,16 @@ hipError_t mxi_launch_kv_append_rotary(const void *k, const void *v, int bf16, i
   a.eps = eps;
   a.r = rotary;
   return rotary.paired ? launch_append<2>(a, bf16, st) : launch_append<1>(a, bf16, st);
+}
+
+hipError_t mxi_launch_kv_keep(const mx_kv_cache_t &cache, const mx_kv_batch_t &batch,
+                              const int32_t *path, int path_width, const int32_t *count,
+                              hipStream_t st) {
+  const KeepArgs a = {cache, batch.table, batch.lengths, path, count, batch.batch, batch.width,
+                      path_width, log2_of(cache.page)};
+  const Spread xy = spread((int64_t)batch.batch * cache.heads);
+  k_kv_keep<<<dim3(xy.first, xy.second), 256, 0, st>>>(a);
+  return hipGetLastError();
 }
 
 size_t mxi_kv_attention_workspace(int64_t tokens, int batch, int q_heads, int heads, int dim,

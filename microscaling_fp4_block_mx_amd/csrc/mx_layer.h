@@ -64,4 +64,15 @@ hipError_t mxi_launch_norm_rotate_backward(const mx_heads_grad_t &q, const mx_he
                                            int bf16, int64_t tokens, int dim, float eps,
                                            const mx_rotary_t &rotary, float *partial,
                                            hipStream_t st);
+
+// Drafted tokens: scratch of a verification, the verification (`draft` may be
+// NULL), and the accepted tokens' move.
+size_t mxi_verify_workspace(int64_t tokens, int batch, int64_t vocab);
+hipError_t mxi_launch_verify(const void *target, const void *draft, int bf16, const int32_t *ids,
+                             const int32_t *parents, const int32_t *cu, const float *numbers,
+                             int64_t tokens, int batch, int64_t vocab, int width, int32_t *path,
+                             int32_t *count, int32_t *token, void *workspace, hipStream_t st);
+hipError_t mxi_launch_kv_keep(const mx_kv_cache_t &cache, const mx_kv_batch_t &batch,
+                              const int32_t *path, int path_width, const int32_t *count,
+                              hipStream_t st);
 #endif  // MX_LAYER_H

@@ -1,0 +1,392 @@
+// mx_verify.hip - verification of drafted tokens against the target model's
+// probabilities, from given random numbers.
+//
+// At a node of a sequence's tree, with the target's row p and (where the draft's
+// probabilities are given) the draft's row q: the first child's token x is taken
+// if u0 q(x) < p(x). If it is not, w = max(p - q, 0), or p without a draft, and
+// the first t with w_0 + .. + w_t > u1 sum(w) is drawn; a child with that token
+// is followed, else t is the sequence's next token. The result is distributed as
+// the target's own samples: a taken x and a t drawn from the residual together
+// are p, and t does not depend on the other children's tokens.
+//
+// Sums of a row run over up to hundreds of thousands of numbers and decide at
+// their borders: 64 bits. Three launches. The first finds each node's first child
+// and whether it is taken, and with that which nodes the walk can reach and has to
+// draw at (of a chain with a draft one): only their rows are read. The second sums
+// those rows in chunks. The third finds each one's chunk, reads it again and draws;
+// then it walks down.
+#include <algorithm>
+
+#include "mx_layer.h"
+#include "mx_layer_device.h"
+#include "mx_rotary_device.h"
+
+namespace mxl {
+
+constexpr int kNodes = 1024;   // nodes of a sequence that are looked at
+constexpr int kChunk = 2048;   // elements of a row that a wave sums at a time
+
+struct VerifyArgs {
+  const void *target, *draft;
+  const int32_t *ids, *parents, *cu;
+  const float *numbers;
+  int64_t tokens, vocab;
+  int batch, width, chunks;
+  int32_t *path, *count, *token;
+  // scratch: each node's first child (or -1), with kTaken where it is taken; each
+  // sequence's nodes to draw at, in order, and how many; their chunks' sums of w
+  // and of p
+  int32_t *kid, *draws, *many;
+  double *sums;
+};
+constexpr int32_t kTaken = 1 << 30;
+
+// A probability: what is negative, infinite or no number counts as 0.
+__device__ __forceinline__ float clean(float p) { return p > 0.0f && p < __builtin_inff() ? p : 0.0f; }
+
+struct Sequence {
+  int64_t first;
+  int nodes;
+};
+__device__ __forceinline__ Sequence sequence_of(const VerifyArgs &a, int i) {
+  const int64_t c0 = a.cu[i], n = a.cu[i + 1] - c0;
+  if (c0 < 0 || n <= 0 || c0 + n > a.tokens) return Sequence{0, 0};
+  return Sequence{c0, (int)(n < kNodes ? n : kNodes)};
+}
+
+// One wave a sequence.
+template <bool BF16>
+__global__ __launch_bounds__(64) void k_verify_plan(const VerifyArgs a) {
+  __shared__ int up[kNodes], kid[kNodes];
+  const int i = blockIdx.x, lane = threadIdx.x;
+  const Sequence s = sequence_of(a, i);
+  for (int j = lane; j < s.nodes; j += 64) {
+    up[j] = a.parents[s.first + j];
+    kid[j] = kNodes;
+  }
+  __syncthreads();
+  // nodes that the root reaches in fewer than `width` steps have a parent from
+  // here on, others none
+  int depth[kNodes / 64];
+#pragma unroll
+  for (int r = 0; r < kNodes / 64; r++) {
+    const int j = lane + 64 * r;
+    depth[r] = -1;
+    if (64 * r >= s.nodes) continue;
+    int x = j < s.nodes ? j : -1, d = 0;
+    while (x > 0 && d < a.width) {
+      const int p = up[x];
+      x = p >= 0 && p < x ? p : -1;
+      d++;
+    }
+    if (x == 0 && d < a.width) depth[r] = d;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kNodes / 64; r++) {
+    const int j = lane + 64 * r;
+    if (j >= s.nodes) continue;
+    if (depth[r] > 0) atomicMin(&kid[up[j]], j);
+    else up[j] = -1;
+  }
+  __syncthreads();
+  for (int j = lane; j < s.nodes; j += 64) {
+    const int k = kid[j];
+    int to = k == kNodes ? -1 : k;
+    if (a.draft && to >= 0) {
+      const int64_t row = s.first + j, x = a.ids[s.first + k];
+      if (x >= 0 && x < a.vocab) {
+        const double p = clean(load_one<BF16>(a.target, row * a.vocab + x));
+        const double q = clean(load_one<BF16>(a.draft, row * a.vocab + x));
+        if ((double)a.numbers[2 * row] * q < p) to |= kTaken;
+      }
+    }
+    kid[j] = to;
+    a.kid[s.first + j] = to;
+  }
+  __syncthreads();
+  int found = 0;
+#pragma unroll
+  for (int r = 0; r < kNodes / 64; r++) {
+    if (64 * r >= s.nodes) break;
+    const int j = lane + 64 * r;
+    // drawn at: reached, unless its first child is taken. With a draft a first
+    // child is reached where it is taken, another where the first one is not.
+    bool draws = depth[r] >= 0 && (kid[j] < 0 || !(kid[j] & kTaken));
+    for (int x = j; draws && x > 0; x = up[x]) {
+      const int k = kid[up[x]];
+      if (a.draft) draws = k == (x | kTaken) || (k != x && !(k & kTaken));
+    }
+    const uint64_t all = __ballot(draws);
+    if (draws) a.draws[s.first + found + __popcll(all & ((1ull << lane) - 1))] = j;
+    found += __popcll(all);
+  }
+  if (lane == 0) a.many[i] = found;
+}
+
+// A wave's part of a row: step u of lane l holds kChunk / steps / 64 neighbouring
+// elements. Rows begin anywhere: chunks are laid out from the 16-byte boundary
+// before a row on.
+template <bool BF16>
+struct Part {
+  static constexpr int A = BF16 ? 8 : 4, U = kChunk / 64 / A;
+  u32x4 v[U];
+};
+template <bool BF16>
+__device__ __forceinline__ Part<BF16> load_part(const void *base, const VerifyArgs &a, int64_t row, int chunk) {
+  constexpr int A = Part<BF16>::A, U = Part<BF16>::U, E = BF16 ? 2 : 4;
+  const int lane = threadIdx.x & 63;
+  const int64_t begin = row * a.vocab, end = begin + a.vocab, all = a.tokens * a.vocab;
+  const int64_t from = (begin & ~(int64_t)(A - 1)) + (int64_t)chunk * kChunk + lane * A;
+  Part<BF16> p;
+#pragma unroll
+  for (int u = 0; u < U; u++) {
+    const int64_t at = from + u * 64 * A;
+    const uint8_t *x = reinterpret_cast<const uint8_t *>(base) + at * E;
+    p.v[u] = u32x4{0, 0, 0, 0};
+    if (at < end) {
+      if (at + A <= all) {
+        p.v[u] = *reinterpret_cast<const u32x4 *>(x);
+      } else {  // the array's last elements
+        for (int e = 0; e < A; e++) {
+          if (at + e >= all) break;
+          if constexpr (BF16) p.v[u][e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t *>(x)[e] << (16 * (e & 1));
+          else p.v[u][e] = reinterpret_cast<const uint32_t *>(x)[e];
+        }
+      }
+    }
+  }
+  return p;
+}
+// Element e of step u as a probability, 0 outside the row; `index` is its place in the row.
+template <bool BF16>
+__device__ __forceinline__ float part_at(const Part<BF16> &p, int u, int e) {
+  const uint32_t w = BF16 ? p.v[u][e >> 1] : p.v[u][e];
+  return clean(__uint_as_float(!BF16 ? w : (e & 1) ? w & 0xFFFF0000u : w << 16));
+}
+template <bool BF16>
+__device__ __forceinline__ int64_t part_index(const VerifyArgs &a, int64_t row, int chunk, int u, int e) {
+  constexpr int A = Part<BF16>::A;
+  const int64_t before = (row * a.vocab) & (A - 1);
+  return (int64_t)chunk * kChunk + (u * 64 + (threadIdx.x & 63)) * A + e - before;
+}
+
+__device__ __forceinline__ double shfl(double v, int lane) { return __shfl(v, lane); }
+// Sum over the wave, the same bits on every lane.
+__device__ __forceinline__ double sum64d(double v) {
+  v = sum_lanes<16>(v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+// Sums of the lanes up to and including this one.
+__device__ __forceinline__ double scan64(double v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// Weight of an element of a row that is drawn from, and the target's share of it.
+template <bool BF16>
+__device__ __forceinline__ double weight_at(const VerifyArgs &a, const Part<BF16> &p, const Part<BF16> &q, bool residual,
+                                            int64_t row, int chunk, int u, int e, double &target) {
+  const int64_t i = part_index<BF16>(a, row, chunk, u, e);
+  target = i >= 0 && i < a.vocab ? (double)part_at<BF16>(p, u, e) : 0.0;
+  if (!residual) return target;
+  const double d = target - (i >= 0 && i < a.vocab ? (double)part_at<BF16>(q, u, e) : 0.0);
+  return d > 0.0 ? d : 0.0;
+}
+
+// A wave a chunk; a workgroup's z takes rows z, z + gridDim.z, ... of a sequence.
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_verify_sums(const VerifyArgs a) {
+  const int chunk = blockIdx.x * 4 + (threadIdx.x >> 6), i = blockIdx.y;
+  const Sequence s = sequence_of(a, i);
+  const int many = s.nodes ? a.many[i] : 0;
+  if (chunk >= a.chunks) return;
+  for (int r = blockIdx.z; r < many; r += gridDim.z) {
+    const int64_t row = s.first + a.draws[s.first + r];
+    const bool residual = a.draft && a.kid[row] >= 0;
+    const Part<BF16> p = load_part<BF16>(a.target, a, row, chunk);
+    Part<BF16> q = {};
+    if (residual) q = load_part<BF16>(a.draft, a, row, chunk);
+    double w = 0.0, t = 0.0;
+#pragma unroll
+    for (int u = 0; u < Part<BF16>::U; u++)
+#pragma unroll
+      for (int e = 0; e < Part<BF16>::A; e++) {
+        double one;
+        w += weight_at<BF16>(a, p, q, residual, row, chunk, u, e, one);
+        t += one;
+      }
+    w = sum64d(w);
+    t = sum64d(t);
+    if ((threadIdx.x & 63) == 0) {
+      double *to = a.sums + ((s.first + r) * a.chunks + chunk) * 2;
+      to[0] = w;
+      to[1] = t;
+    }
+  }
+}
+
+// Draws from a row, the whole wave together; -1 where nothing in it is positive.
+template <bool BF16>
+__device__ __forceinline__ int64_t draw_from(const VerifyArgs &a, int64_t slot, int64_t row, bool residual) {
+  const int lane = threadIdx.x & 63;
+  const double *sums = a.sums + slot * a.chunks * 2;
+  double total = 0.0;
+  int which = 0;  // w, or, where w has nothing, p
+  for (; which < 2; which++) {
+    double t = 0.0;
+    for (int c = lane; c < a.chunks; c += 64) t += sums[2 * c + which];
+    total = sum64d(t);
+    if (total > 0.0) break;
+  }
+  if (which == 2) return -1;
+  if (which == 1) residual = false;
+  const double bound = (double)a.numbers[2 * row + 1] * total;
+  // the chunk in which the sum passes the bound; if rounding leaves it below, the last with anything
+  double before = 0.0, base = 0.0;
+  int chunk = -1;
+  for (int c0 = 0; c0 < a.chunks; c0 += 64) {
+    const double v = c0 + lane < a.chunks ? sums[2 * (c0 + lane) + which] : 0.0;
+    const double incl = scan64(v);
+    const uint64_t any = __ballot(v > 0.0), past = __ballot(v > 0.0 && before + incl > bound);
+    const uint64_t take = past ? past & -past : any ? 1ull << (63 - __builtin_clzll(any)) : 0;
+    if (take) {
+      const int l = __builtin_ctzll(take);
+      chunk = c0 + l;
+      base = before + (shfl(incl, l) - shfl(v, l));
+      if (past) break;
+    }
+    before += shfl(incl, 63);
+  }
+  const Part<BF16> p = load_part<BF16>(a.target, a, row, chunk);
+  Part<BF16> q = {};
+  if (residual) q = load_part<BF16>(a.draft, a, row, chunk);
+  int64_t found = -1;
+#pragma unroll
+  for (int u = 0; u < Part<BF16>::U; u++) {
+    double v = 0.0, one;
+#pragma unroll
+    for (int e = 0; e < Part<BF16>::A; e++) v += weight_at<BF16>(a, p, q, residual, row, chunk, u, e, one);
+    const double incl = scan64(v);
+    const uint64_t any = __ballot(v > 0.0), past = __ballot(v > 0.0 && base + incl > bound);
+    const uint64_t take = past ? past & -past : any ? 1ull << (63 - __builtin_clzll(any)) : 0;
+    if (take) {
+      // the lane's own elements, one by one
+      const int l = __builtin_ctzll(take);
+      double sum = base + (incl - v);
+      int64_t mine = -1;
+      bool done = false;
+#pragma unroll
+      for (int e = 0; e < Part<BF16>::A; e++) {
+        const double w = weight_at<BF16>(a, p, q, residual, row, chunk, u, e, one);
+        sum += w;
+        if (w > 0.0 && !done) {
+          mine = part_index<BF16>(a, row, chunk, u, e);
+          done = sum > bound;
+        }
+      }
+      found = __shfl((long long)mine, l);
+      if (past) break;
+    }
+    base += shfl(incl, 63);
+  }
+  return found;
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_verify_walk(const VerifyArgs a) {
+  __shared__ int up[kNodes], kid[kNodes], id[kNodes], drawn[kNodes];
+  const int i = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const Sequence s = sequence_of(a, i);
+  int32_t *path = a.path + (int64_t)i * a.width;
+  for (int j = threadIdx.x; j < s.nodes; j += 256) {
+    up[j] = a.parents[s.first + j];
+    kid[j] = a.kid[s.first + j];
+    id[j] = a.ids[s.first + j];
+  }
+  const int many = s.nodes ? a.many[i] : 0;
+  for (int r = wave; r < many; r += 4) {
+    const int j = a.draws[s.first + r];
+    const int64_t row = s.first + j;
+    const int64_t t = draw_from<BF16>(a, s.first + r, row, a.draft && a.kid[row] >= 0);
+    if (lane == 0) drawn[j] = (int)t;
+  }
+  __syncthreads();
+  if (wave) return;
+  int node = 0, steps = 0, token = -1;
+  while (s.nodes) {
+    if (lane == 0) path[steps] = node;
+    steps++;
+    const int k = kid[node];
+    if (k >= 0 && (k & kTaken)) {
+      node = k & ~kTaken;
+      continue;
+    }
+    token = drawn[node];
+    int next = -1;
+    for (int j0 = node + 1; j0 < s.nodes && token >= 0 && steps < a.width && next < 0; j0 += 64) {
+      const int j = j0 + lane;
+      const bool hit = j < s.nodes && up[j] == node && id[j] == token && !(a.draft && j == k);
+      const uint64_t all = __ballot(hit);
+      if (all) next = j0 + __builtin_ctzll(all);
+    }
+    if (next < 0) break;
+    node = next;
+  }
+  for (int j = steps + lane; j < a.width; j += 64) path[j] = -1;
+  if (lane == 0) {
+    a.count[i] = steps;
+    a.token[i] = token;
+  }
+}
+
+static int verify_chunks(int64_t vocab) { return (int)((vocab + 7 + kChunk - 1) / kChunk); }
+static size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+}  // namespace mxl
+
+using namespace mxl;
+
+size_t mxi_verify_workspace(int64_t tokens, int batch, int64_t vocab) {
+  return (size_t)tokens * verify_chunks(vocab) * 16 + 2 * round16((size_t)tokens * 4) + round16((size_t)batch * 4);
+}
+
+hipError_t mxi_launch_verify(const void *target, const void *draft, int bf16, const int32_t *ids,
+                             const int32_t *parents, const int32_t *cu, const float *numbers,
+                             int64_t tokens, int batch, int64_t vocab, int width, int32_t *path,
+                             int32_t *count, int32_t *token, void *workspace, hipStream_t st) {
+  VerifyArgs a = {target, draft, ids, parents, cu, numbers, tokens, vocab, batch, width,
+                  verify_chunks(vocab), path, count, token, nullptr, nullptr, nullptr, nullptr};
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  a.sums = reinterpret_cast<double *>(ws);
+  ws += (size_t)tokens * a.chunks * 16;
+  a.kid = reinterpret_cast<int32_t *>(ws);
+  ws += round16((size_t)tokens * 4);
+  a.draws = reinterpret_cast<int32_t *>(ws);
+  ws += round16((size_t)tokens * 4);
+  a.many = reinterpret_cast<int32_t *>(ws);
+  if (tokens == 0) {  // outputs alone
+    k_verify_walk<false><<<batch, 256, 0, st>>>(a);
+    return hipGetLastError();
+  }
+  const int groups = (a.chunks + 3) / 4;
+  const int64_t mean = std::max<int64_t>(1, tokens / batch);
+  const int rows = (int)std::min<int64_t>(mean, std::max<int64_t>(1, 4096 / ((int64_t)groups * batch)));
+  const dim3 grid((uint32_t)groups, (uint32_t)batch, (uint32_t)rows);
+  if (bf16) {
+    k_verify_plan<true><<<batch, 64, 0, st>>>(a);
+    k_verify_sums<true><<<grid, 256, 0, st>>>(a);
+    k_verify_walk<true><<<batch, 256, 0, st>>>(a);
+  } else {
+    k_verify_plan<false><<<batch, 64, 0, st>>>(a);
+    k_verify_sums<false><<<grid, 256, 0, st>>>(a);
+    k_verify_walk<false><<<batch, 256, 0, st>>>(a);
+  }
+  return hipGetLastError();
+}

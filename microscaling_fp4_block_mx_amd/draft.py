@@ -1,8 +1,8 @@
 """Positions and drafted tokens beside the 8-bit cache: tensor-level helpers.
 
 The norms of queries and keys per head with the position rotation, their
-gradient, the append that has both on the way, and attention over a tree of
-drafted tokens. Every step runs in the HIP kernels behind include/mx.h; this module
+gradient, the append that has both on the way, attention over a tree of drafted
+tokens, their verification, and keeping the accepted ones. Every step runs in the HIP kernels behind include/mx.h; this module
 allocates outputs and scratch with torch (on the current stream) and checks
 what the C entry points cannot see: devices, dtypes, shapes and contiguity. Bad
 arguments raise ``ValueError``, HIP errors ``RuntimeError``.
@@ -17,7 +17,8 @@ from typing import NamedTuple
 import torch
 
 from . import _DTYPES, load_library
-from .layer import KVCache, _batch_of, _cache_of, _call, _heads_of, _ptr, _scratch, _want
+from .layer import (KVCache, _batch_of, _cache_of, _call, _heads_of, _pack_batch, _ptr, _scratch,
+                    _want)
 
 
 class MxRotary(ctypes.Structure):
@@ -111,6 +112,21 @@ def mx_kv_attention_tree(q, q_stride, q_heads, cache, batch, mask, words, max_le
                                                stream)
 
 
+def mx_verify_drafts_workspace_size(tokens, batch, vocab) -> int:
+    return load_library().mx_verify_drafts_workspace_size(tokens, batch, vocab)
+
+
+def mx_verify_drafts(target, draft, dtype, ids, parents, cu, numbers, tokens, batch, vocab, width,
+                     path, count, token, workspace, workspace_bytes, stream) -> int:
+    return load_library().mx_verify_drafts(target, draft, dtype, ids, parents, cu, numbers, tokens,
+                                           batch, vocab, width, path, count, token, workspace,
+                                           workspace_bytes, stream)
+
+
+def mx_kv_keep(cache, batch, path, path_width, count, stream) -> int:
+    return load_library().mx_kv_keep(cache, batch, path, path_width, count, stream)
+
+
 def declare(lib) -> None:
     """Argument and result types of the entry points."""
     p, i64, i32, f32, size = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
@@ -120,7 +136,10 @@ def declare(lib) -> None:
         "mx_norm_rotate_backward": [p, p, i32, i64, i32, f32, p, p, size, p],
         "mx_kv_append_rotary": [p, p, i32, i64, i64, p, f32, p, p, p, p],
         "mx_kv_attention_tree": [p, i64, i32, p, p, p, i32, i64, f32, p, p, size, p],
+        "mx_verify_drafts": [p, p, i32, p, p, p, p, i64, i32, i64, i32, p, p, p, p, size, p],
+        "mx_kv_keep": [p, p, p, i32, p, p],
         "mx_norm_rotate_backward_workspace_size": [i64, i32],
+        "mx_verify_drafts_workspace_size": [i64, i32, i64],
     }
     for name, args in types.items():
         f = getattr(lib, name)
@@ -297,3 +316,57 @@ def kv_attention_tree(q: torch.Tensor, cache: KVCache, table: torch.Tensor, cu: 
     _call(dev, lib.mx_kv_attention_tree, q.data_ptr(), stride, q_heads, c, b, mask.data_ptr(), words,
           max_length, 1.0 / math.sqrt(dim) if scale is None else scale, out.data_ptr(), _ptr(ws), size)
     return out
+
+
+def verify_drafts(target: torch.Tensor, ids: torch.Tensor, parents: torch.Tensor,
+                  cu: torch.Tensor, numbers: torch.Tensor, width: int,
+                  draft: torch.Tensor | None = None):
+    """Walk down each sequence's tree of drafted tokens as far as the target's
+    probabilities agree -> (path int32 [batch, width]: the nodes, 0 first, then -1;
+    count int32 [batch]; token int32 [batch]: the next token). target [tokens,
+    vocab] (and draft, if its probabilities are known); ids, parents int32
+    [tokens]; cu int32 [batch + 1]; numbers float32 [tokens, 2], uniform from 0 to
+    below 1. width: the longest path, node 0 included (the tree's depth + 1)."""
+    dev = _on_gpu(target, "target")
+    if target.dtype not in _DTYPES or target.dim() != 2 or not target.is_contiguous():
+        raise ValueError("target must be contiguous [tokens, vocab], float32 or bfloat16")
+    tokens, vocab = target.shape
+    if draft is not None:
+        _want(draft, "draft", dev, target.dtype, tokens * vocab, vocab)
+    _want(ids, "ids", dev, torch.int32, tokens)
+    _want(parents, "parents", dev, torch.int32, tokens)
+    if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or not len(cu):
+        raise ValueError("cu must be [batch + 1]")
+    batch = cu.shape[0] - 1
+    _want(cu, "cu", dev, torch.int32, batch + 1)
+    _want(numbers, "numbers", dev, torch.float32, 2 * tokens, 2)
+    if not 1 <= width <= 1024:
+        raise ValueError(f"width must be 1 to 1024, got {width}")
+    path = torch.empty(batch, width, dtype=torch.int32, device=dev)
+    count, token = torch.empty(2, batch, dtype=torch.int32, device=dev)
+    lib = load_library()
+    size = lib.mx_verify_drafts_workspace_size(tokens, batch, vocab)
+    ws = _scratch(size, dev)
+    _call(dev, lib.mx_verify_drafts, target.data_ptr(), _ptr(draft), _DTYPES[target.dtype],
+          ids.data_ptr(), parents.data_ptr(), cu.data_ptr(), numbers.data_ptr(), tokens, batch, vocab,
+          width, path.data_ptr(), count.data_ptr(), token.data_ptr(), _ptr(ws), size)
+    return path, count, token
+
+
+def kv_keep(cache: KVCache, table: torch.Tensor, lengths: torch.Tensor, path: torch.Tensor,
+            count: torch.Tensor) -> None:
+    """Keep the accepted tokens in the cache, in place: behind the lengths int32
+    [batch] that each sequence held, new token path[i][j] moves to place j, for j
+    below count[i] (verify_drafts gives both). It then holds lengths + count."""
+    dev, _, _, _, c = _cache_of(cache)
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be [batch, width]")
+    batch, width = table.shape
+    if not isinstance(path, torch.Tensor) or path.dim() != 2 or path.shape[0] != batch:
+        raise ValueError(f"path must be [{batch}, width]")
+    _want(table, "table", dev, torch.int32, batch * width)
+    _want(lengths, "lengths", dev, torch.int32, batch)
+    _want(path, "path", dev, torch.int32, path.numel())
+    _want(count, "count", dev, torch.int32, batch)
+    b = _pack_batch(table.data_ptr(), 0, lengths.data_ptr(), 0, batch, width)
+    _call(dev, load_library().mx_kv_keep, c, b, path.data_ptr(), path.shape[1], count.data_ptr())

@@ -111,3 +111,101 @@ def attention_tree(q, cache, table, cu, lengths, sees, scale):
                 mag[a + t, of] = p @ vd[at].abs()
                 reach[a + t, of] = (x.abs() @ kd[at].abs().t()).amax(1) * scale
     return out, mag, reach
+
+
+def verify(target, draft, ids, parents, cu, numbers, width):
+    """-> (path, count, token) as lists, one sequence and node at a time."""
+    def clean(p):
+        p = p.double()
+        return torch.where((p > 0) & torch.isfinite(p), p, 0.0)
+
+    paths, counts, tokens = [], [], []
+    vocab = target.shape[1]
+    for i in range(len(cu) - 1):
+        a, n = int(cu[i]), min(int(cu[i + 1] - cu[i]), 1024)
+        path, token, node = [], -1, 0
+        while n > 0:
+            path.append(node)
+            row = a + node
+            kids = [j for j in range(node + 1, n) if int(parents[a + j]) == node]
+            if len(path) >= width:
+                kids = []
+            p = clean(target[row])
+            w = p
+            if draft is not None and kids:
+                x, q = int(ids[a + kids[0]]), clean(draft[row])
+                if 0 <= x < vocab and float(numbers[row, 0]) * float(q[x]) < float(p[x]):
+                    node = kids[0]
+                    continue
+                kids = kids[1:]
+                w = (p - q).clamp(min=0)
+                if float(w.sum()) <= 0:
+                    w = p
+            token = -1
+            total = float(w.sum())
+            if total > 0:
+                past = (w.cumsum(0) > float(numbers[row, 1]) * total) & (w > 0)
+                at = torch.nonzero(past if bool(past.any()) else w > 0)
+                token = int(at[0]) if bool(past.any()) else int(at[-1])
+            follow = [j for j in kids if int(ids[a + j]) == token and token >= 0]
+            if not follow:
+                break
+            node = follow[0]
+        paths.append(path + [-1] * (width - len(path)))
+        counts.append(len(path))
+        tokens.append(token)
+    return paths, counts, tokens
+
+
+def keep(cache, table, lengths, path, count):
+    """kv_keep on CPU uint8 tensors, in place."""
+    kc, ks, vc, vs = cache
+    pool, page = kc.shape[0], kc.shape[2]
+
+    def moved(codes, by, to):
+        """[.., dim] codes at byte `by` as codes at byte `to`."""
+        if to == by:
+            return codes.clone()
+        if to == 255:
+            return codes & 0x80
+        u = codes.view(F8).double() * 2.0 ** (int(by) - int(to))
+        _, e = torch.frexp(u.abs())
+        step = torch.ldexp(torch.ones_like(u), (e - 1).clamp(min=-6) - 3)
+        return (torch.round(u / step) * step).float().to(F8).view(torch.uint8)
+
+    for i in range(table.shape[0]):
+        held, nodes = int(lengths[i]), []
+        for j in range(min(int(count[i]), path.shape[1])):
+            p = int(path[i, j])
+            if p <= (nodes[-1] if nodes else -1) or (held + p) // page >= table.shape[1]:
+                break
+            nodes.append(p)
+        first = 0
+        while first < len(nodes) and nodes[first] == first:
+            first += 1
+        if held < 0 or first == len(nodes):
+            continue
+        for codes, scales, turn in ((kc, ks, False), (vc, vs, True)):
+            for h in range(codes.shape[1]):
+                def rows(p):
+                    return codes[p, h].t() if turn else codes[p, h]
+                came = []
+                for p in nodes:
+                    at = int(table[i, (held + p) // page])
+                    if 0 <= at < pool:
+                        came.append((rows(at)[(held + p) % page].clone(), int(scales[at, h])))
+                    else:
+                        came.append((torch.zeros(rows(0).shape[1], dtype=torch.uint8), 0))
+                for pg in range((held + first) // page, (held + len(nodes) - 1) // page + 1):
+                    lo, hi = max(held + first, pg * page), min(held + len(nodes), (pg + 1) * page)
+                    at, kept = int(table[i, pg]), lo - pg * page
+                    if not 0 <= at < pool:
+                        continue
+                    was = int(scales[at, h]) if kept else 0
+                    byte = max([was] + [came[p - held][1] for p in range(lo, hi)])
+                    view = rows(at)
+                    if kept and byte > was:
+                        view[:kept] = moved(view[:kept].contiguous(), was, byte)
+                    for p in range(lo, hi):
+                        view[p - pg * page] = moved(came[p - held][0], came[p - held][1], byte)
+                    scales[at, h] = byte
