@@ -118,7 +118,7 @@ mx_status_t mx_norm_rotate(const mx_heads_t *q, const mx_heads_t *k, mx_dtype_t 
 
 size_t mx_norm_rotate_backward_workspace_size(int64_t tokens, int dim) {
   if (check_norm_rotate(1, 0, MX_BF16, tokens, dim, 0.0f, nullptr) != MX_OK) return 0;
-  return (size_t)mxi_norm_rotate_partials(tokens) * 2 * dim * sizeof(float);
+  return (size_t)mxi_norm_rotate_partials(tokens) * dim * sizeof(float);
 }
 
 mx_status_t mx_norm_rotate_backward(const mx_heads_grad_t *q, const mx_heads_grad_t *k,

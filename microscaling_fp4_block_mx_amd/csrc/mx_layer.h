@@ -58,7 +58,7 @@ hipError_t mxi_launch_kv_attention_tree(const void *q, int64_t q_stride, int q_h
 hipError_t mxi_launch_norm_rotate(const mx_heads_t &q, const mx_heads_t *k, int bf16,
                                   int64_t tokens, int dim, float eps, const mx_rotary_t &rotary,
                                   hipStream_t st);
-// Rows of partial weight gradients (2 dim floats each) of the gradient's launch.
+// Rows of partial weight gradients (dim floats each) of the gradient's launch.
 int64_t mxi_norm_rotate_partials(int64_t tokens);
 hipError_t mxi_launch_norm_rotate_backward(const mx_heads_grad_t &q, const mx_heads_grad_t *k,
                                            int bf16, int64_t tokens, int dim, float eps,

@@ -23,7 +23,7 @@ static hipError_t hit() {
 mx_status_t mxi_record_hip_error(hipError_t) { return MX_ERR_HIP; }
 hipError_t mxi_launch_norm_rotate(const mx_heads_t &, const mx_heads_t *, int, int64_t, int, float,
                                   const mx_rotary_t &, hipStream_t) { return hit(); }
-int64_t mxi_norm_rotate_partials(int64_t tokens) { return tokens < 64 ? tokens : 64; }
+int64_t mxi_norm_rotate_partials(int64_t tokens) { return 2 * (tokens < 64 ? tokens : 64); }
 hipError_t mxi_launch_norm_rotate_backward(const mx_heads_grad_t &, const mx_heads_grad_t *, int,
                                            int64_t, int, float, const mx_rotary_t &, float *,
                                            hipStream_t) { return hit(); }
