@@ -121,11 +121,10 @@ __device__ __forceinline__ Raw<BF16> load_at(const void *base, int64_t elem) {
 // TURN: keys pass a norm (if there is a weight) and a rotation between their load
 // and all else, of pairs (i, i + rot / 2) (1) or neighbours (2), in 64 bits: a
 // page's byte changes where its largest number crosses a power of two, so the
-// last bit of a key can be one of the byte. Lanes 2 m and 2 m + 1 of a token then
-// hold the two items of dims whose pairs turn together.
+// last bit of a key can be one of the byte. dim / 16 lanes then hold a token's key,
+// two items each, both members of a pair in one lane.
 template <bool BF16, int T, int TURN>
 __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
-  constexpr bool KB = BF16 && TURN == 0;  // whether keys are held as bfloat16
   // new values' codes, [dim][token]; rows are one word longer than a page's,
   // so that the rows that an instruction writes to fall on different banks
   extern __shared__ __attribute__((aligned(16))) uint8_t vt[];
@@ -160,126 +159,128 @@ __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
   };
   auto slot_of = [&](int it) { return word_of(it) + ((it >> 4) & 3); };
   auto dim_of = [&](int it) { return (it & (wide ? 15 : 7)) * 8; };
-  auto key_dim_of = [&](int it) {
-    const int l = it & (wide ? 15 : 7);
-    return 8 * (TURN == 1 && 8 * l < a.r.rot ? (l >> 1) + (l & 1) * (a.r.rot >> 4) : l);
-  };
   // whether any lane of the wave has a slot in use: the wave's lanes go together
   auto any = [&](int it) { return first + (wide ? it >> 6 << 2 : it >> 6 << 3) < end; };
   auto mine = [&](int it) { return slot_of(it) >= kept && slot_of(it) < end; };
-  auto token_of = [&](int it) { return min(max(src0 + slot_of(it), (int64_t)0), most); };
-  auto load = [&](const void *x, int64_t stride, int it, int dim) {
-    return load_at<BF16>(x, token_of(it) * stride + (int64_t)head * D + dim);
+  auto token_at = [&](int slot) { return min(max(src0 + slot, (int64_t)0), most); };
+  auto load = [&](const void *x, int64_t stride, int it) {
+    return load_at<BF16>(x, token_at(slot_of(it)) * stride + (int64_t)head * D + dim_of(it));
   };
-  auto load_key = [&](int it) { return load(a.k, a.k_stride, it, key_dim_of(it)); };
-  auto load_value = [&](int it) { return load(a.v, a.v_stride, it, dim_of(it)); };
-  float weight[8];
-  if (TURN && a.weight) {  // of this lane's dims: the same for all its items
-    const int d = key_dim_of(threadIdx.x);
-#pragma unroll
-    for (int j = 0; j < 8; j++) weight[j] = load_one<BF16>(a.weight, d + j);
-  }
-  // The key as it enters the cache. All lanes of a token go together; items
-  // that are not new tokens' become zeros.
-  auto key_of = [&](const Raw<BF16> &raw, int it) {
-    if constexpr (TURN == 0) {
-      return raw;
-    } else {
-      float f[8];
-      widen<BF16>(raw, f);
-      double x[8];
-#pragma unroll
-      for (int j = 0; j < 8; j++) x[j] = f[j];
-      if (a.weight) {
-        double ss = 0.0;
-#pragma unroll
-        for (int j = 0; j < 8; j++) ss = __builtin_fma(x[j], x[j], ss);
-        ss = sum_lanes<8>(ss);
-        if (wide) ss += dppd<0x140>(ss);
-        const double root = inverse_root(ss * (wide ? 1.0 / 128 : 1.0 / 64) + a.eps);
-#pragma unroll
-        for (int j = 0; j < 8; j++) x[j] = x[j] * root * weight[j];
-      }
-      const int d = key_dim_of(it);
-      double other[8];
-      if constexpr (TURN == 1) {
-#pragma unroll
-        for (int j = 0; j < 8; j++) other[j] = dppd<0xB1>(x[j]);
-      }
-      if (d < a.r.rot) {
-        const int position = a.r.positions ? a.r.positions[token_of(it)] : (j << a.shift) + slot_of(it);
-        const Angles at = angles_of(a.r.table, a.r.length, a.r.rot, position);
-        const float *sines = at.row + (a.r.rot >> 1);
-        if constexpr (TURN == 1) {
-          const bool second = d >= a.r.rot >> 1;
-          const int from = second ? d - (a.r.rot >> 1) : d;
-          float c[8], s[8];
-          load8(at.row + from, c);
-          load8(sines + from, s);
-#pragma unroll
-          for (int j = 0; j < 8; j++) {
-            const double turned = other[j] * s[j];
-            x[j] = __builtin_fma(x[j], (double)c[j], second ? turned : -turned);
-          }
-        } else {
-          const f32x4 c = *reinterpret_cast<const f32x4 *>(at.row + (d >> 1));
-          const f32x4 s = *reinterpret_cast<const f32x4 *>(sines + (d >> 1));
-#pragma unroll
-          for (int j = 0; j < 4; j++) {
-            const double x0 = x[2 * j], cd = c[j], sd = s[j];
-            x[2 * j] = __builtin_fma(x0, cd, -(x[2 * j + 1] * sd));
-            x[2 * j + 1] = __builtin_fma(x[2 * j + 1], cd, x0 * sd);
-          }
-        }
-        if (at.none) {
-#pragma unroll
-          for (int j = 0; j < 8; j++) x[j] = __builtin_nan("");
-        }
-      }
-      const bool is = mine(it);
-      Raw<false> r;
-#pragma unroll
-      for (int j = 0; j < 8; j++) r.v[j >> 2][j & 3] = is ? __float_as_uint((float)x[j]) : 0u;
-      return r;
+  // Keys on their way through norm and rotation: item `it` is lane t of slot
+  // key_slot_of(it), dims 8 ka .. and 8 kb ... (T is a multiple of the lanes of a
+  // token: t, ka and kb are the same for all of a thread's items.)
+  const int lanes = D >> 4, t = threadIdx.x & (lanes - 1);
+  auto key_slot_of = [&](int it) { return kept + it / lanes; };
+  int ka = 0, kb = 0;
+  bool turns = false;
+  Raw<BF16> wa = {}, wb = {};
+  if constexpr (TURN != 0) {
+    items_of<TURN == 2>(t, a.r.rot, ka, kb, turns);
+    if (a.weight) {
+      wa = load_weight<BF16>(a.weight, ka);
+      wb = load_weight<BF16>(a.weight, kb);
     }
+  }
+  struct Key {
+    Raw<BF16> a, b;
+    int position;
+  };
+  auto load_key = [&](int it) {
+    Key k;
+    const int slot = min(key_slot_of(it), P - 1);
+    const int64_t tok = token_at(slot);
+    const uint8_t *x = reinterpret_cast<const uint8_t *>(a.k) + (tok * a.k_stride + (int64_t)head * D) * (BF16 ? 2 : 4);
+    k.a = load_raw<BF16>(x, ka);
+    k.b = load_raw<BF16>(x, kb);
+    k.position = a.r.positions && turns ? a.r.positions[tok] : (j << a.shift) + slot;
+    return k;
+  };
+  struct Turned {  // as it enters the cache
+    float a[8], b[8];
+  };
+  auto turned = [&](const Key &k) {
+    double x[8], y[8];
+    widen64<BF16>(k.a, x);
+    widen64<BF16>(k.b, y);
+    if (a.weight) {
+      double ss = 0.0;
+#pragma unroll
+      for (int e = 0; e < 8; e++) ss = __builtin_fma(x[e], x[e], __builtin_fma(y[e], y[e], ss));
+      ss = sum_lanes<4>(ss);
+      if (wide) ss += dppd<0x141>(ss);
+      const double root = inverse_root(ss * (wide ? 1.0 / 128 : 1.0 / 64) + a.eps);
+      float u[8], v[8];
+      widen<BF16>(wa, u);
+      widen<BF16>(wb, v);
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        x[e] = x[e] * root * u[e];
+        y[e] = y[e] * root * v[e];
+      }
+    }
+    if (turns) {
+      Turns angles;
+      angles.load(a.r, k.position, t);
+      turn<TURN == 2, false>(x, y, angles.c, angles.s);
+    }
+    Turned r;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      r.a[e] = (float)x[e];
+      r.b[e] = (float)y[e];
+    }
+    return r;
   };
 
+  constexpr int kTurn = kKeep / 2;
   Raw<BF16> kr[kKeep], vr[kKeep];
-  Raw<KB> kept_keys[kKeep];
+  Turned tr[kTurn];
+  uint32_t mk = 0, mv = 0;
+  if constexpr (TURN == 0) {
 #pragma unroll
-  for (int u = 0; u < kKeep; u++) {
-    const int it = threadIdx.x + T * u;
-    kr[u] = vr[u] = Raw<BF16>{};
-    if (mine(it)) {
-      kr[u] = load_key(it);
-      vr[u] = load_value(it);
+    for (int u = 0; u < kKeep; u++) {
+      const int it = threadIdx.x + T * u;
+      kr[u] = vr[u] = Raw<BF16>{};
+      if (mine(it)) {
+        kr[u] = load(a.k, a.k_stride, it);
+        vr[u] = load(a.v, a.v_stride, it);
+      }
+    }
+  } else {
+    Key k[kTurn];
+#pragma unroll
+    for (int u = 0; u < kTurn; u++)
+      if (key_slot_of(threadIdx.x + T * u) < end) k[u] = load_key(threadIdx.x + T * u);
+#pragma unroll
+    for (int u = 0; u < kKeep; u++) {
+      const int it = threadIdx.x + T * u;
+      vr[u] = Raw<BF16>{};
+      if (mine(it)) vr[u] = load(a.v, a.v_stride, it);
+    }
+#pragma unroll
+    for (int u = 0; u < kTurn; u++)
+      if (key_slot_of(threadIdx.x + T * u) < end) {  // (the lanes of a token go together)
+        tr[u] = turned(k[u]);
+        mk = max(mk, max(amax8(tr[u].a), amax8(tr[u].b)));
+      }
+    for (int it = threadIdx.x + T * kTurn; key_slot_of(it) < end; it += T) {
+      const Turned r = turned(load_key(it));
+      mk = max(mk, max(amax8(r.a), amax8(r.b)));
     }
   }
-  uint32_t mk = 0, mv = 0;
-  auto take = [&](const Raw<KB> &k, const Raw<BF16> &v) {
+  auto take = [&](const Raw<BF16> &k, const Raw<BF16> &v) {
     float f[8];
-    widen<KB>(k, f);
-    mk = max(mk, amax8(f));
+    if constexpr (TURN == 0) {
+      widen<BF16>(k, f);
+      mk = max(mk, amax8(f));
+    }
     widen<BF16>(v, f);
     mv = max(mv, amax8(f));
   };
 #pragma unroll
-  for (int u = 0; u < kKeep; u++) {  // zeros where there is none
-    kept_keys[u] = key_of(kr[u], threadIdx.x + T * u);
-    take(kept_keys[u], vr[u]);
-  }
-  for (int it = threadIdx.x + T * kKeep; any(it); it += T) {
-    if constexpr (TURN == 0) {
-      if (mine(it)) take(load_key(it), load_value(it));
-    } else {
-      Raw<BF16> k = {}, v = {};
-      if (mine(it)) {
-        k = load_key(it);
-        v = load_value(it);
-      }
-      take(key_of(k, it), v);
-    }
-  }
+  for (int u = 0; u < kKeep; u++) take(kr[u], vr[u]);  // zeros where there is none
+  for (int it = threadIdx.x + T * kKeep; any(it); it += T)
+    if (mine(it)) take(TURN == 0 ? load(a.k, a.k_stride, it) : Raw<BF16>{}, load(a.v, a.v_stride, it));
   mk = max16(mk);
   mv = max16(mv);
   mk = max(mk, (uint32_t)__shfl_xor((int)mk, 16));
@@ -324,11 +325,11 @@ __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
   auto limit = [](uint32_t b) { return b > 246u ? 0x1.fffffep127f : limit8(b); };
   const float most_k = limit(sk), most_v = limit(sv);
   const int row = P + 4;
-  auto put = [&](const Raw<KB> &k, const Raw<BF16> &v, int it) {
+  auto put = [&](const Raw<BF16> &k, const Raw<BF16> &v, int it) {
     float f[8];
-    if (mine(it)) {
-      widen<KB>(k, f);
-      *reinterpret_cast<u32x2 *>(kc + slot_of(it) * D + key_dim_of(it)) = encode8(f, sk, most_k);
+    if (TURN == 0 && mine(it)) {
+      widen<BF16>(k, f);
+      *reinterpret_cast<u32x2 *>(kc + slot_of(it) * D + dim_of(it)) = encode8(f, sk, most_k);
     }
     widen<BF16>(v, f);
     const u32x2 w = encode8(f, sv, most_v);
@@ -344,8 +345,20 @@ __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
   };
 #pragma unroll
   for (int u = 0; u < kKeep; u++)
-    if (any(threadIdx.x + T * u)) put(kept_keys[u], vr[u], threadIdx.x + T * u);
-  for (int it = threadIdx.x + T * kKeep; any(it); it += T) put(key_of(load_key(it), it), load_value(it), it);
+    if (any(threadIdx.x + T * u)) put(kr[u], vr[u], threadIdx.x + T * u);
+  for (int it = threadIdx.x + T * kKeep; any(it); it += T)
+    put(TURN == 0 ? load(a.k, a.k_stride, it) : Raw<BF16>{}, load(a.v, a.v_stride, it), it);
+  if constexpr (TURN != 0) {
+    auto put_key = [&](const Turned &r, int it) {
+      uint8_t *to = kc + key_slot_of(it) * D;
+      *reinterpret_cast<u32x2 *>(to + 8 * ka) = encode8(r.a, sk, most_k);
+      *reinterpret_cast<u32x2 *>(to + 8 * kb) = encode8(r.b, sk, most_k);
+    };
+#pragma unroll
+    for (int u = 0; u < kTurn; u++)
+      if (key_slot_of(threadIdx.x + T * u) < end) put_key(tr[u], threadIdx.x + T * u);
+    for (int it = threadIdx.x + T * kTurn; key_slot_of(it) < end; it += T) put_key(turned(load_key(it)), it);
+  }
   __syncthreads();
   const int piece0 = kept >> 4, chunks = ((end + 15) >> 4) - piece0;  // of a row, with new tokens in them
   for (int it = threadIdx.x; it < D * chunks; it += T) {

@@ -2,6 +2,7 @@
 // sums over the lanes of a head in 64 bits, the root, cosines and sines.
 #ifndef MX_ROTARY_DEVICE_H
 #define MX_ROTARY_DEVICE_H
+#include "mx.h"
 #include "mx_layer_device.h"
 
 namespace mxl {
@@ -53,6 +54,65 @@ __device__ __forceinline__ Angles angles_of(const float *table, int64_t length, 
   const bool none = position < 0 || position >= length;
   return Angles{table + (none ? 0 : (int64_t)position * rot), none};
 }
+
+// Items A and B (of eight dims) of lane t of a head, and whether they turn.
+// PAIRED: neighbours; else A and the item half of the rotated dims further on,
+// and neighbours behind the rotated dims. Either way the lane's eight pairs
+// are pairs 8 t .. 8 t + 7.
+template <bool PAIRED>
+__device__ __forceinline__ void items_of(int t, int rot, int &a, int &b, bool &turns) {
+  turns = 16 * t < rot;
+  const int half = rot >> 4;
+  a = !PAIRED && turns ? t : 2 * t;
+  b = !PAIRED && turns ? t + half : 2 * t + 1;
+}
+
+// Turns a lane's pairs, or back.
+template <bool PAIRED, bool BACK>
+__device__ __forceinline__ void turn(double (&a)[8], double (&b)[8], const float (&c)[8], const float (&s)[8]) {
+  auto pair = [&](double &x, double &y, int e) {
+    const double cd = c[e], sd = BACK ? -s[e] : s[e], x0 = x;
+    x = __builtin_fma(x0, cd, -(y * sd));
+    y = __builtin_fma(y, cd, x0 * sd);
+  };
+#pragma unroll
+  for (int e = 0; e < 8; e++) {
+    if constexpr (!PAIRED) pair(a[e], b[e], e);
+    else if (e < 4) pair(a[2 * e], a[2 * e + 1], e);
+    else pair(b[2 * e - 8], b[2 * e - 7], e);
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void widen64(const Raw<BF16> &r, double (&d)[8]) {
+  float f[8];
+  widen<BF16>(r, f);
+#pragma unroll
+  for (int j = 0; j < 8; j++) d[j] = f[j];
+}
+// Weights stay in the caches: default policy.
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> load_weight(const void *w, int item) {
+  const u32x4 *p = reinterpret_cast<const u32x4 *>(w) + (BF16 ? 1 : 2) * item;
+  Raw<BF16> r;
+  r.v[0] = p[0];
+  if constexpr (!BF16) r.v[1] = p[1];
+  return r;
+}
+
+// Cosines and sines of a lane's pairs; NaN cosines where a position has none.
+struct Turns {
+  float c[8], s[8];
+  __device__ __forceinline__ void load(const mx_rotary_t &r, int position, int t) {
+    const Angles at = angles_of(r.table, r.length, r.rot, position);
+    load8(at.row + 8 * t, c);
+    load8(at.row + (r.rot >> 1) + 8 * t, s);
+    if (at.none) {
+#pragma unroll
+      for (int j = 0; j < 8; j++) c[j] = __builtin_nanf("");
+    }
+  }
+};
 
 }  // namespace mxl
 #endif  // MX_ROTARY_DEVICE_H
