@@ -108,78 +108,256 @@ __device__ __forceinline__ u32x4 move16(u32x4 v, int keep, int d, bool nan) {
 // page of 64 tokens of 128 dims takes); larger pages read the rest twice.
 constexpr int kKeep = 4;
 
-// One workgroup per page and head. Prompts are bound by HBM: 6 sequences of up
-// to 8,000 tokens, 8 heads of 128, 201 MB in 41 us (4.9 TB/s); with the values'
-// bytes written to LDS one at a time 44.6, with the tokens read twice 72. A
-// token per sequence is a chain of loads that wait for each other (cu, table
-// and lengths, scale, codes): 64 sequences 5 us, 256 8.5.
 template <bool BF16>
 __device__ __forceinline__ Raw<BF16> load_at(const void *base, int64_t elem) {
   return load_raw<BF16>(reinterpret_cast<const uint8_t *>(base) + elem * (BF16 ? 2 : 4), 0);
 }
 
-// TURN: keys pass a norm (if there is a weight) and a rotation between their load
-// and all else, of pairs (i, i + rot / 2) (1) or neighbours (2), in 64 bits: a
-// page's byte changes where its largest number crosses a power of two, so the
-// last bit of a key can be one of the byte. dim / 16 lanes then hold a token's key,
-// two items each, both members of a pair in one lane.
-template <bool BF16, int T, int TURN>
-__global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
-  // new values' codes, [dim][token]; rows are one word longer than a page's,
-  // so that the rows that an instruction writes to fall on different banks
-  extern __shared__ __attribute__((aligned(16))) uint8_t vt[];
-  __shared__ uint32_t am[2][T / 64];
+// A workgroup's page of a sequence, and its head.
+struct AppendPage {
+  int head, page;       // the page's number in its sequence
+  int kept, end;        // slots that stay, slots in use after
+  int64_t src0, most;   // token of slot 0; the last token there is
+  int64_t at;           // of the page and head in the scales
+  __device__ __forceinline__ int64_t token(int slot) const { return min(max(src0 + slot, (int64_t)0), most); }
+};
+__device__ __forceinline__ bool find_page(const AppendArgs &a, AppendPage &p) {
   const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x;
-  if (block >= a.blocks) return;
-  const int unit = block / a.c.heads, head = block % a.c.heads;
-  const int P = a.c.page, D = a.c.dim;
+  if (block >= a.blocks) return false;
+  const int unit = block / a.c.heads, P = a.c.page;
+  p.head = block % a.c.heads;
   const int i = find_sequence(a.b.cu, a.b.batch, P, 2, unit);
   const int c0 = a.b.cu[i], n = a.b.cu[i + 1] - c0, held = a.b.lengths[i];
   const int j = (held >> a.shift) + (unit - (c0 / P + 2 * i));  // page of the sequence
   // (a unit before the first sequence's has pages before the sequence's first)
   if (n <= 0 || held < 0 || j < held >> a.shift || j >= a.b.width || ((int64_t)j << a.shift) >= (int64_t)held + n)
-    return;
-  const int kept = max(0, held - (j << a.shift));            // slots that stay
-  const int end = min((int64_t)P, (int64_t)held + n - ((int64_t)j << a.shift));  // slots in use after
+    return false;
+  p.page = j;
+  p.kept = max(0, held - (j << a.shift));
+  p.end = min((int64_t)P, (int64_t)held + n - ((int64_t)j << a.shift));
   const int64_t id = a.b.table[(int64_t)i * a.b.width + j];
-  if (id < 0 || id >= a.c.pages) return;  // no page: its tokens are dropped
-  const int64_t src0 = (int64_t)c0 + ((int64_t)j << a.shift) - held;  // token of slot 0
-  const int64_t most = a.b.tokens - 1;
-  const int64_t at = id * a.c.heads + head;
-  // An item is eight dims of a token. Lanes l, l + 16, l + 32, l + 48 of a wave
-  // hold four tokens that share a word of a values' row.
-  const int wide = D == 128, first = kept & ~3;
-  uint32_t was_k = 0, was_v = 0;
-  if (kept) {
-    was_k = a.c.k_scales[at];
-    was_v = a.c.v_scales[at];
-  }
-  auto word_of = [&](int it) {  // first of the four slots
+  if (id < 0 || id >= a.c.pages) return false;  // no page: its tokens are dropped
+  p.src0 = (int64_t)c0 + ((int64_t)j << a.shift) - held;
+  p.most = a.b.tokens - 1;
+  p.at = id * a.c.heads + p.head;
+  return true;
+}
+
+// Items of eight dims of a token. Lanes l, l + 16, l + 32, l + 48 of a wave hold
+// four tokens that share a word of a values' row.
+struct AppendItems {
+  int first, kept, end, wide;
+  __device__ __forceinline__ AppendItems(const AppendPage &p, int dim)
+      : first(p.kept & ~3), kept(p.kept), end(p.end), wide(dim == 128) {}
+  __device__ __forceinline__ int word(int it) const {  // first of the four slots
     return first + (wide ? it >> 6 << 2 : (it >> 6 << 3) + ((it & 8) >> 1));
-  };
-  auto slot_of = [&](int it) { return word_of(it) + ((it >> 4) & 3); };
-  auto dim_of = [&](int it) { return (it & (wide ? 15 : 7)) * 8; };
+  }
+  __device__ __forceinline__ int slot(int it) const { return word(it) + ((it >> 4) & 3); }
+  __device__ __forceinline__ int dim(int it) const { return (it & (wide ? 15 : 7)) * 8; }
   // whether any lane of the wave has a slot in use: the wave's lanes go together
-  auto any = [&](int it) { return first + (wide ? it >> 6 << 2 : it >> 6 << 3) < end; };
-  auto mine = [&](int it) { return slot_of(it) >= kept && slot_of(it) < end; };
-  auto token_at = [&](int slot) { return min(max(src0 + slot, (int64_t)0), most); };
-  auto load = [&](const void *x, int64_t stride, int it) {
-    return load_at<BF16>(x, token_at(slot_of(it)) * stride + (int64_t)head * D + dim_of(it));
-  };
-  // Keys on their way through norm and rotation: item `it` is lane t of slot
-  // key_slot_of(it), dims 8 ka .. and 8 kb ... (T is a multiple of the lanes of a
-  // token: t, ka and kb are the same for all of a thread's items.)
-  const int lanes = D >> 4, t = threadIdx.x & (lanes - 1);
-  auto key_slot_of = [&](int it) { return kept + it / lanes; };
-  int ka = 0, kb = 0;
-  bool turns = false;
-  Raw<BF16> wa = {}, wb = {};
-  if constexpr (TURN != 0) {
-    items_of<TURN == 2>(t, a.r.rot, ka, kb, turns);
-    if (a.weight) {
-      wa = load_weight<BF16>(a.weight, ka);
-      wb = load_weight<BF16>(a.weight, kb);
+  __device__ __forceinline__ bool any(int it) const { return first + (wide ? it >> 6 << 2 : it >> 6 << 3) < end; }
+  __device__ __forceinline__ bool mine(int it) const { return slot(it) >= kept && slot(it) < end; }
+};
+
+// Largest over the workgroup of two numbers that its threads have; `am` is this
+// call's own.
+template <int T>
+__device__ __forceinline__ void largest2(uint32_t &x, uint32_t &y, uint32_t (&am)[2][T / 64]) {
+  x = max16(x);
+  y = max16(y);
+  x = max(x, (uint32_t)__shfl_xor((int)x, 16));
+  y = max(y, (uint32_t)__shfl_xor((int)y, 16));
+  x = max(x, (uint32_t)__shfl_xor((int)x, 32));
+  y = max(y, (uint32_t)__shfl_xor((int)y, 32));
+  if ((threadIdx.x & 63) == 0) {
+    am[0][threadIdx.x >> 6] = x;
+    am[1][threadIdx.x >> 6] = y;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < T / 64; w++) {
+    x = max(x, am[0][w]);
+    y = max(y, am[1][w]);
+  }
+}
+
+// Kept codes move to a new byte 16 at a time, four such pieces asked for
+// together; what a piece holds past the kept tokens stays.
+template <int T, typename F, typename G>
+__device__ __forceinline__ void move_codes(int pieces, F place, G keeps, int d, bool nan) {
+  for (int c = threadIdx.x; c < pieces; c += 4 * T) {
+    u32x4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; u++) v[u] = *reinterpret_cast<const u32x4 *>(place(min(c + u * T, pieces - 1)));
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      if (c + u * T >= pieces) break;
+      *reinterpret_cast<u32x4 *>(place(c + u * T)) = move16(v[u], keeps(c + u * T), d, nan);
     }
+  }
+}
+template <int T>
+__device__ __forceinline__ void move_keys(uint8_t *kc, int kept, int D, uint32_t from, uint32_t to) {
+  if (kept && to > from)
+    move_codes<T>(kept * D / 16, [&](int c) { return kc + 16 * c; }, [](int) { return 16; }, (int)(to - from), to == 255u);
+}
+template <int T>
+__device__ __forceinline__ void move_values(uint8_t *vc, int kept, int D, int P, uint32_t from, uint32_t to) {
+  if (!kept || to <= from) return;
+  const int n = (kept + 15) >> 4;
+  move_codes<T>(D * n, [&](int c) { return vc + c / n * P + c % n * 16; }, [&](int c) { return kept - c % n * 16; },
+                (int)(to - from), to == 255u);
+  __syncthreads();  // before the new tokens' bytes of the same words
+}
+
+// a kept byte may be any: above 246 every finite number is below 448 scales
+__device__ __forceinline__ float append_limit(uint32_t b) { return b > 246u ? 0x1.fffffep127f : limit8(b); }
+
+// A value item's codes into vt, [dim][token], whose rows are `row` bytes.
+template <bool BF16>
+__device__ __forceinline__ void put_value(uint8_t *vt, int row, const AppendItems &items, const Raw<BF16> &v, int it,
+                                          uint32_t byte, float most) {
+  float f[8];
+  widen<BF16>(v, f);
+  const u32x2 w = encode8(f, byte, most);
+  // four lanes' tokens t = 2 b + a, eight dims each, become two dims of four
+  // tokens: halves of the dims change places over b, then quarters over a
+  const auto x = __builtin_amdgcn_permlane32_swap(w[0], w[1], false, false);
+  const uint32_t lo = __builtin_amdgcn_perm(x[1], x[0], 0x05040100u);  // dims 0, 1 of tokens a, a + 2
+  const uint32_t hi = __builtin_amdgcn_perm(x[1], x[0], 0x07060302u);  // dims 2, 3
+  const auto y = __builtin_amdgcn_permlane16_swap(lo, hi, false, false);
+  uint32_t *to = reinterpret_cast<uint32_t *>(vt + (items.dim(it) + 2 * ((it >> 4) & 3)) * row + items.word(it));
+  to[0] = __builtin_amdgcn_perm(y[1], y[0], 0x06020400u);
+  to[row >> 2] = __builtin_amdgcn_perm(y[1], y[0], 0x07030501u);
+}
+// The new tokens' bytes from vt to the page.
+template <int T>
+__device__ __forceinline__ void write_values(uint8_t *vc, const uint8_t *vt, int row, int kept, int end, int D, int P) {
+  const int piece0 = kept >> 4, chunks = ((end + 15) >> 4) - piece0;  // of a row, with new tokens in them
+  for (int it = threadIdx.x; it < D * chunks; it += T) {
+    const int d = it / chunks, s = (piece0 + it % chunks) * 16;
+    const int lo = max(kept, s), hi = min(end, s + 16);
+    uint8_t *dst = vc + (int64_t)d * P;
+    if (lo == s && hi == s + 16) {
+      const uint32_t *from = reinterpret_cast<const uint32_t *>(vt + d * row + s);
+      *reinterpret_cast<u32x4 *>(dst + s) = u32x4{from[0], from[1], from[2], from[3]};
+    } else {
+      for (int q = lo; q < hi; q++) dst[q] = vt[d * row + q];
+    }
+  }
+}
+
+// One workgroup per page and head. Prompts are bound by HBM: 6 sequences of up
+// to 8,000 tokens, 8 heads of 128, 201 MB in 41 us (4.9 TB/s); with the values'
+// bytes written to LDS one at a time 44.6, with the tokens read twice 72. A
+// token per sequence is a chain of loads that wait for each other (cu, table
+// and lengths, scale, codes): 64 sequences 5 us, 256 8.5.
+template <bool BF16, int T>
+__global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
+  // new values' codes, [dim][token]; rows are one word longer than a page's,
+  // so that the rows that an instruction writes to fall on different banks
+  extern __shared__ __attribute__((aligned(16))) uint8_t vt[];
+  __shared__ uint32_t am[2][T / 64];
+  AppendPage p;
+  if (!find_page(a, p)) return;
+  const int P = a.c.page, D = a.c.dim;
+  const AppendItems items(p, D);
+  uint32_t was_k = 0, was_v = 0;
+  if (p.kept) {
+    was_k = a.c.k_scales[p.at];
+    was_v = a.c.v_scales[p.at];
+  }
+  auto load = [&](const void *x, int64_t stride, int it) {
+    return load_at<BF16>(x, p.token(items.slot(it)) * stride + (int64_t)p.head * D + items.dim(it));
+  };
+  Raw<BF16> kr[kKeep], vr[kKeep];
+#pragma unroll
+  for (int u = 0; u < kKeep; u++) {
+    const int it = threadIdx.x + T * u;
+    kr[u] = vr[u] = Raw<BF16>{};
+    if (items.mine(it)) {
+      kr[u] = load(a.k, a.k_stride, it);
+      vr[u] = load(a.v, a.v_stride, it);
+    }
+  }
+  uint32_t mk = 0, mv = 0;
+  auto take = [&](const Raw<BF16> &k, const Raw<BF16> &v) {
+    float f[8];
+    widen<BF16>(k, f);
+    mk = max(mk, amax8(f));
+    widen<BF16>(v, f);
+    mv = max(mv, amax8(f));
+  };
+#pragma unroll
+  for (int u = 0; u < kKeep; u++) take(kr[u], vr[u]);  // zeros where there is none
+  for (int it = threadIdx.x + T * kKeep; items.any(it); it += T)
+    if (items.mine(it)) take(load(a.k, a.k_stride, it), load(a.v, a.v_stride, it));
+  largest2<T>(mk, mv, am);
+  const uint32_t sk = max(scale_byte8(mk), was_k), sv = max(scale_byte8(mv), was_v);
+  uint8_t *kc = a.c.k_codes + p.at * P * D, *vc = a.c.v_codes + p.at * P * D;
+  move_keys<T>(kc, p.kept, D, was_k, sk);
+  move_values<T>(vc, p.kept, D, P, was_v, sv);
+  const float most_k = append_limit(sk), most_v = append_limit(sv);
+  const int row = P + 4;
+  auto put = [&](const Raw<BF16> &k, const Raw<BF16> &v, int it) {
+    if (items.mine(it)) {
+      float f[8];
+      widen<BF16>(k, f);
+      *reinterpret_cast<u32x2 *>(kc + items.slot(it) * D + items.dim(it)) = encode8(f, sk, most_k);
+    }
+    put_value<BF16>(vt, row, items, v, it, sv, most_v);
+  };
+#pragma unroll
+  for (int u = 0; u < kKeep; u++)
+    if (items.any(threadIdx.x + T * u)) put(kr[u], vr[u], threadIdx.x + T * u);
+  for (int it = threadIdx.x + T * kKeep; items.any(it); it += T)
+    put(load(a.k, a.k_stride, it), load(a.v, a.v_stride, it), it);
+  __syncthreads();
+  write_values<T>(vc, vt, row, p.kept, p.end, D, P);
+  if (threadIdx.x == 0) {
+    if (!p.kept || sk != was_k) a.c.k_scales[p.at] = (uint8_t)sk;
+    if (!p.kept || sv != was_v) a.c.v_scales[p.at] = (uint8_t)sv;
+  }
+}
+
+// The same with the keys' norm (if there is a weight) and rotation on the way, in
+// 64 bits: a page's byte changes where its largest number crosses a power of two,
+// so the last bit of a key can be one of the byte. dim / 16 lanes hold a token's
+// key, two items each, both members of a pair in one lane. The values go first,
+// while the keys are on their way: what is held of the two at once decides how
+// many waves a unit has.
+template <bool BF16, int T, int D, bool PAIRED>
+__global__ __launch_bounds__(T, BF16 ? 4 : 1) void k_kv_append_rotary(const AppendArgs a) {
+  constexpr int kTurn = kKeep / 2;
+  extern __shared__ __attribute__((aligned(16))) uint8_t vt[];
+  __shared__ uint32_t am[2][2][T / 64];
+  AppendPage p;
+  if (!find_page(a, p)) return;
+  const int P = a.c.page;
+  const AppendItems items(p, D);
+  // the same for all threads, and in scalar registers: the branches that they
+  // decide are the workgroup's
+  auto uniform = [](uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); };
+  uint32_t was_k = 0, was_v = 0;
+  if (p.kept) {
+    was_k = uniform(a.c.k_scales[p.at]);
+    was_v = uniform(a.c.v_scales[p.at]);
+  }
+  auto load_value = [&](int it) {
+    return load_at<BF16>(a.v, p.token(items.slot(it)) * a.v_stride + (int64_t)p.head * D + items.dim(it));
+  };
+  // Key item `it` is lane t of a token, dims 8 ka .. and 8 kb ... (T is a multiple
+  // of the lanes of a token: t, ka and kb are the same for all of a thread's items.)
+  constexpr int lanes = D / 16;
+  const int t = threadIdx.x % lanes;
+  auto slot_of = [&](int it) { return p.kept + it / lanes; };
+  int ka, kb;
+  bool turns;
+  items_of<PAIRED>(t, a.r.rot, ka, kb, turns);
+  Raw<BF16> wa = {}, wb = {};
+  if (a.weight) {
+    wa = load_weight<BF16>(a.weight, ka);
+    wb = load_weight<BF16>(a.weight, kb);
   }
   struct Key {
     Raw<BF16> a, b;
@@ -187,12 +365,12 @@ __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
   };
   auto load_key = [&](int it) {
     Key k;
-    const int slot = min(key_slot_of(it), P - 1);
-    const int64_t tok = token_at(slot);
-    const uint8_t *x = reinterpret_cast<const uint8_t *>(a.k) + (tok * a.k_stride + (int64_t)head * D) * (BF16 ? 2 : 4);
+    const int slot = slot_of(it);
+    const int64_t tok = p.token(slot);
+    const uint8_t *x = reinterpret_cast<const uint8_t *>(a.k) + (tok * a.k_stride + (int64_t)p.head * D) * (BF16 ? 2 : 4);
     k.a = load_raw<BF16>(x, ka);
     k.b = load_raw<BF16>(x, kb);
-    k.position = a.r.positions && turns ? a.r.positions[tok] : (j << a.shift) + slot;
+    k.position = a.r.positions && turns ? a.r.positions[tok] : (p.page << a.shift) + slot;
     return k;
   };
   struct Turned {  // as it enters the cache
@@ -206,9 +384,10 @@ __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
       double ss = 0.0;
 #pragma unroll
       for (int e = 0; e < 8; e++) ss = __builtin_fma(x[e], x[e], __builtin_fma(y[e], y[e], ss));
-      ss = sum_lanes<4>(ss);
-      if (wide) ss += dppd<0x141>(ss);
-      const double root = inverse_root(ss * (wide ? 1.0 / 128 : 1.0 / 64) + a.eps);
+      const double root = inverse_root(sum_lanes<lanes>(ss) * (1.0 / D) + a.eps);
+      // widened each time: held in 64 bits they would cost a wave of four
+      renew<BF16>(wa);
+      renew<BF16>(wb);
       float u[8], v[8];
       widen<BF16>(wa, u);
       widen<BF16>(wb, v);
@@ -221,7 +400,7 @@ __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
     if (turns) {
       Turns angles;
       angles.load(a.r, k.position, t);
-      turn<TURN == 2, false>(x, y, angles.c, angles.s);
+      turn<PAIRED, false>(x, y, angles.c, angles.s);
     }
     Turned r;
 #pragma unroll
@@ -232,149 +411,67 @@ __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
     return r;
   };
 
-  constexpr int kTurn = kKeep / 2;
-  Raw<BF16> kr[kKeep], vr[kKeep];
-  Turned tr[kTurn];
-  uint32_t mk = 0, mv = 0;
-  if constexpr (TURN == 0) {
+  Raw<BF16> vr[kKeep];
+  Key kr[kTurn];
 #pragma unroll
-    for (int u = 0; u < kKeep; u++) {
-      const int it = threadIdx.x + T * u;
-      kr[u] = vr[u] = Raw<BF16>{};
-      if (mine(it)) {
-        kr[u] = load(a.k, a.k_stride, it);
-        vr[u] = load(a.v, a.v_stride, it);
-      }
-    }
-  } else {
-    Key k[kTurn];
-#pragma unroll
-    for (int u = 0; u < kTurn; u++)
-      if (key_slot_of(threadIdx.x + T * u) < end) k[u] = load_key(threadIdx.x + T * u);
-#pragma unroll
-    for (int u = 0; u < kKeep; u++) {
-      const int it = threadIdx.x + T * u;
-      vr[u] = Raw<BF16>{};
-      if (mine(it)) vr[u] = load(a.v, a.v_stride, it);
-    }
-#pragma unroll
-    for (int u = 0; u < kTurn; u++)
-      if (key_slot_of(threadIdx.x + T * u) < end) {  // (the lanes of a token go together)
-        tr[u] = turned(k[u]);
-        mk = max(mk, max(amax8(tr[u].a), amax8(tr[u].b)));
-      }
-    for (int it = threadIdx.x + T * kTurn; key_slot_of(it) < end; it += T) {
-      const Turned r = turned(load_key(it));
-      mk = max(mk, max(amax8(r.a), amax8(r.b)));
-    }
+  for (int u = 0; u < kKeep; u++) {
+    const int it = threadIdx.x + T * u;
+    vr[u] = Raw<BF16>{};
+    if (items.mine(it)) vr[u] = load_value(it);
   }
-  auto take = [&](const Raw<BF16> &k, const Raw<BF16> &v) {
+#pragma unroll
+  for (int u = 0; u < kTurn; u++)
+    if (slot_of(threadIdx.x + T * u) < p.end) kr[u] = load_key(threadIdx.x + T * u);
+  uint8_t *kc = a.c.k_codes + p.at * P * D, *vc = a.c.v_codes + p.at * P * D;
+  const int row = P + 4;
+
+  uint32_t mk = 0, mv = 0, none = 0;
+  auto take = [&](const Raw<BF16> &v) {
     float f[8];
-    if constexpr (TURN == 0) {
-      widen<BF16>(k, f);
-      mk = max(mk, amax8(f));
-    }
     widen<BF16>(v, f);
     mv = max(mv, amax8(f));
   };
 #pragma unroll
-  for (int u = 0; u < kKeep; u++) take(kr[u], vr[u]);  // zeros where there is none
-  for (int it = threadIdx.x + T * kKeep; any(it); it += T)
-    if (mine(it)) take(TURN == 0 ? load(a.k, a.k_stride, it) : Raw<BF16>{}, load(a.v, a.v_stride, it));
-  mk = max16(mk);
-  mv = max16(mv);
-  mk = max(mk, (uint32_t)__shfl_xor((int)mk, 16));
-  mv = max(mv, (uint32_t)__shfl_xor((int)mv, 16));
-  mk = max(mk, (uint32_t)__shfl_xor((int)mk, 32));
-  mv = max(mv, (uint32_t)__shfl_xor((int)mv, 32));
-  if ((threadIdx.x & 63) == 0) {
-    am[0][threadIdx.x >> 6] = mk;
-    am[1][threadIdx.x >> 6] = mv;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < T / 64; w++) {
-    mk = max(mk, am[0][w]);
-    mv = max(mv, am[1][w]);
-  }
-  const uint32_t sk = max(scale_byte8(mk), was_k), sv = max(scale_byte8(mv), was_v);
-  uint8_t *kc = a.c.k_codes + at * P * D, *vc = a.c.v_codes + at * P * D;
-  // kept codes move to the new bytes 16 at a time, four such pieces asked for
-  // together; what a piece holds past the kept tokens stays
-  auto move = [&](int pieces, auto place, auto keeps, int d, bool nan) {
-    for (int c = threadIdx.x; c < pieces; c += 4 * T) {
-      u32x4 v[4];
-#pragma unroll
-      for (int u = 0; u < 4; u++) v[u] = *reinterpret_cast<const u32x4 *>(place(min(c + u * T, pieces - 1)));
-#pragma unroll
-      for (int u = 0; u < 4; u++) {
-        if (c + u * T >= pieces) break;
-        *reinterpret_cast<u32x4 *>(place(c + u * T)) = move16(v[u], keeps(c + u * T), d, nan);
-      }
-    }
-  };
-  if (kept && sk > was_k)
-    move(kept * D / 16, [&](int c) { return kc + 16 * c; }, [](int) { return 16; }, (int)(sk - was_k), sk == 255u);
-  if (kept && sv > was_v) {
-    const int n = (kept + 15) >> 4;
-    move(D * n, [&](int c) { return vc + c / n * P + c % n * 16; },
-         [&](int c) { return kept - c % n * 16; }, (int)(sv - was_v), sv == 255u);
-    __syncthreads();  // before the new tokens' bytes of the same words
-  }
-  // a kept byte may be any: above 246 every finite number is below 448 scales
-  auto limit = [](uint32_t b) { return b > 246u ? 0x1.fffffep127f : limit8(b); };
-  const float most_k = limit(sk), most_v = limit(sv);
-  const int row = P + 4;
-  auto put = [&](const Raw<BF16> &k, const Raw<BF16> &v, int it) {
-    float f[8];
-    if (TURN == 0 && mine(it)) {
-      widen<BF16>(k, f);
-      *reinterpret_cast<u32x2 *>(kc + slot_of(it) * D + dim_of(it)) = encode8(f, sk, most_k);
-    }
-    widen<BF16>(v, f);
-    const u32x2 w = encode8(f, sv, most_v);
-    // four lanes' tokens t = 2 b + a, eight dims each, become two dims of four
-    // tokens: halves of the dims change places over b, then quarters over a
-    const auto x = __builtin_amdgcn_permlane32_swap(w[0], w[1], false, false);
-    const uint32_t lo = __builtin_amdgcn_perm(x[1], x[0], 0x05040100u);  // dims 0, 1 of tokens a, a + 2
-    const uint32_t hi = __builtin_amdgcn_perm(x[1], x[0], 0x07060302u);  // dims 2, 3
-    const auto y = __builtin_amdgcn_permlane16_swap(lo, hi, false, false);
-    uint32_t *to = reinterpret_cast<uint32_t *>(vt + (dim_of(it) + 2 * ((it >> 4) & 3)) * row + word_of(it));
-    to[0] = __builtin_amdgcn_perm(y[1], y[0], 0x06020400u);
-    to[row >> 2] = __builtin_amdgcn_perm(y[1], y[0], 0x07030501u);
-  };
+  for (int u = 0; u < kKeep; u++) take(vr[u]);  // zeros where there is none
+  for (int it = threadIdx.x + T * kKeep; items.any(it); it += T)
+    if (items.mine(it)) take(load_value(it));
+  largest2<T>(mv, none, am[0]);
+  const uint32_t sv = max(scale_byte8(uniform(mv)), was_v);
+  move_values<T>(vc, p.kept, D, P, was_v, sv);
+  const float most_v = append_limit(sv);
 #pragma unroll
   for (int u = 0; u < kKeep; u++)
-    if (any(threadIdx.x + T * u)) put(kr[u], vr[u], threadIdx.x + T * u);
-  for (int it = threadIdx.x + T * kKeep; any(it); it += T)
-    put(TURN == 0 ? load(a.k, a.k_stride, it) : Raw<BF16>{}, load(a.v, a.v_stride, it), it);
-  if constexpr (TURN != 0) {
-    auto put_key = [&](const Turned &r, int it) {
-      uint8_t *to = kc + key_slot_of(it) * D;
-      *reinterpret_cast<u32x2 *>(to + 8 * ka) = encode8(r.a, sk, most_k);
-      *reinterpret_cast<u32x2 *>(to + 8 * kb) = encode8(r.b, sk, most_k);
-    };
+    if (items.any(threadIdx.x + T * u)) put_value<BF16>(vt, row, items, vr[u], threadIdx.x + T * u, sv, most_v);
+  for (int it = threadIdx.x + T * kKeep; items.any(it); it += T)
+    put_value<BF16>(vt, row, items, load_value(it), it, sv, most_v);
+
+  Turned tr[kTurn];
+  auto take_key = [&](const Turned &r) { mk = max(mk, max(amax8(r.a), amax8(r.b))); };
 #pragma unroll
-    for (int u = 0; u < kTurn; u++)
-      if (key_slot_of(threadIdx.x + T * u) < end) put_key(tr[u], threadIdx.x + T * u);
-    for (int it = threadIdx.x + T * kTurn; key_slot_of(it) < end; it += T) put_key(turned(load_key(it)), it);
-  }
-  __syncthreads();
-  const int piece0 = kept >> 4, chunks = ((end + 15) >> 4) - piece0;  // of a row, with new tokens in them
-  for (int it = threadIdx.x; it < D * chunks; it += T) {
-    const int d = it / chunks, s = (piece0 + it % chunks) * 16;
-    const int lo = max(kept, s), hi = min(end, s + 16);
-    uint8_t *dst = vc + (int64_t)d * P;
-    if (lo == s && hi == s + 16) {
-      const uint32_t *from = reinterpret_cast<const uint32_t *>(vt + d * row + s);
-      *reinterpret_cast<u32x4 *>(dst + s) = u32x4{from[0], from[1], from[2], from[3]};
-    } else {
-      for (int q = lo; q < hi; q++) dst[q] = vt[d * row + q];
+  for (int u = 0; u < kTurn; u++)
+    if (slot_of(threadIdx.x + T * u) < p.end) {  // (the lanes of a token go together)
+      tr[u] = turned(kr[u]);
+      take_key(tr[u]);
+      __builtin_amdgcn_sched_barrier(0);  // one key's numbers at a time
     }
-  }
+  for (int it = threadIdx.x + T * kTurn; slot_of(it) < p.end; it += T) take_key(turned(load_key(it)));
+  largest2<T>(mk, none, am[1]);  // (and vt is whole)
+  const uint32_t sk = max(scale_byte8(uniform(mk)), was_k);
+  move_keys<T>(kc, p.kept, D, was_k, sk);
+  const float most_k = append_limit(sk);
+  auto put_key = [&](const Turned &r, int it) {
+    uint8_t *to = kc + slot_of(it) * D;
+    *reinterpret_cast<u32x2 *>(to + 8 * ka) = encode8(r.a, sk, most_k);
+    *reinterpret_cast<u32x2 *>(to + 8 * kb) = encode8(r.b, sk, most_k);
+  };
+#pragma unroll
+  for (int u = 0; u < kTurn; u++)
+    if (slot_of(threadIdx.x + T * u) < p.end) put_key(tr[u], threadIdx.x + T * u);
+  for (int it = threadIdx.x + T * kTurn; slot_of(it) < p.end; it += T) put_key(turned(load_key(it)), it);
+  write_values<T>(vc, vt, row, p.kept, p.end, D, P);
   if (threadIdx.x == 0) {
-    if (!kept || sk != was_k) a.c.k_scales[at] = (uint8_t)sk;
-    if (!kept || sv != was_v) a.c.v_scales[at] = (uint8_t)sv;
+    if (!p.kept || sk != was_k) a.c.k_scales[p.at] = (uint8_t)sk;
+    if (!p.kept || sv != was_v) a.c.v_scales[p.at] = (uint8_t)sv;
   }
 }
 
@@ -1547,19 +1644,10 @@ static AttnPlan attn_plan(int64_t tokens, int batch, int q_heads, int heads, int
 
 using namespace mxl;
 
-template <int TURN>
-static hipError_t launch_append(const AppendArgs &a, int bf16, hipStream_t st) {
-  const Spread xy = spread(a.blocks);
-  const dim3 grid(xy.first, xy.second);
-  const size_t lds = (size_t)a.c.dim * (a.c.page + 4);
-  // a few new tokens per sequence: one wave a page, so that all pages are at
-  // work at once (256 sequences of one token: 8.5 us; four
-  // waves, and kept codes moved a word at a time: 19)
-  const bool few = a.b.tokens <= 4 * (int64_t)a.b.batch;
-  if (bf16) few ? k_kv_append<true, 64, TURN><<<grid, 64, lds, st>>>(a) : k_kv_append<true, 256, TURN><<<grid, 256, lds, st>>>(a);
-  else few ? k_kv_append<false, 64, TURN><<<grid, 64, lds, st>>>(a) : k_kv_append<false, 256, TURN><<<grid, 256, lds, st>>>(a);
-  return hipGetLastError();
-}
+// A few new tokens per sequence: one wave a page, so that all pages are at
+// work at once (256 sequences of one token: 8.5 us; four
+// waves, and kept codes moved a word at a time: 19)
+static bool few_tokens(const AppendArgs &a) { return a.b.tokens <= 4 * (int64_t)a.b.batch; }
 static AppendArgs append_args(const void *k, const void *v, int64_t k_stride, int64_t v_stride,
                               const mx_kv_cache_t &cache, const mx_kv_batch_t &batch) {
   const int64_t blocks = (batch.tokens / cache.page + 2 * (int64_t)batch.batch) * cache.heads;
@@ -1569,9 +1657,26 @@ static AppendArgs append_args(const void *k, const void *v, int64_t k_stride, in
 hipError_t mxi_launch_kv_append(const void *k, const void *v, int bf16, int64_t k_stride,
                                 int64_t v_stride, const mx_kv_cache_t &cache,
                                 const mx_kv_batch_t &batch, hipStream_t st) {
-  return launch_append<0>(append_args(k, v, k_stride, v_stride, cache, batch), bf16, st);
+  const AppendArgs a = append_args(k, v, k_stride, v_stride, cache, batch);
+  const Spread xy = spread(a.blocks);
+  const dim3 grid(xy.first, xy.second);
+  const size_t lds = (size_t)cache.dim * (cache.page + 4);
+  const bool few = few_tokens(a);
+  if (bf16) few ? k_kv_append<true, 64><<<grid, 64, lds, st>>>(a) : k_kv_append<true, 256><<<grid, 256, lds, st>>>(a);
+  else few ? k_kv_append<false, 64><<<grid, 64, lds, st>>>(a) : k_kv_append<false, 256><<<grid, 256, lds, st>>>(a);
+  return hipGetLastError();
 }
 
+template <bool BF16, bool PAIRED>
+static hipError_t launch_append_rotary(const AppendArgs &a, hipStream_t st) {
+  const Spread xy = spread(a.blocks);
+  const dim3 grid(xy.first, xy.second);
+  const size_t lds = (size_t)a.c.dim * (a.c.page + 4);
+  const bool few = few_tokens(a);
+  if (a.c.dim == 64) few ? k_kv_append_rotary<BF16, 64, 64, PAIRED><<<grid, 64, lds, st>>>(a) : k_kv_append_rotary<BF16, 256, 64, PAIRED><<<grid, 256, lds, st>>>(a);
+  else few ? k_kv_append_rotary<BF16, 64, 128, PAIRED><<<grid, 64, lds, st>>>(a) : k_kv_append_rotary<BF16, 256, 128, PAIRED><<<grid, 256, lds, st>>>(a);
+  return hipGetLastError();
+}
 hipError_t mxi_launch_kv_append_rotary(const void *k, const void *v, int bf16, int64_t k_stride,
                                        int64_t v_stride, const void *weight, float eps,
                                        const mx_rotary_t &rotary, const mx_kv_cache_t &cache,
@@ -1580,7 +1685,8 @@ hipError_t mxi_launch_kv_append_rotary(const void *k, const void *v, int bf16, i
   a.weight = weight;
   a.eps = eps;
   a.r = rotary;
-  return rotary.paired ? launch_append<2>(a, bf16, st) : launch_append<1>(a, bf16, st);
+  if (bf16) return rotary.paired ? launch_append_rotary<true, true>(a, st) : launch_append_rotary<true, false>(a, st);
+  return rotary.paired ? launch_append_rotary<false, true>(a, st) : launch_append_rotary<false, false>(a, st);
 }
 
 hipError_t mxi_launch_kv_keep(const mx_kv_cache_t &cache, const mx_kv_batch_t &batch,
