@@ -34,15 +34,15 @@ struct VerifyArgs {
   int batch, width, chunks;
   int32_t *path, *count, *token;
   // scratch: each node's first child (or -1), with kTaken where it is taken; each
-  // sequence's nodes to draw at, in order, and how many; their chunks' sums of w
-  // and of p
+  // sequence's nodes to draw at, in order, with kResidual where from p - q, and how
+  // many; their chunks' sums of w and of p
   int32_t *kid, *draws, *many;
   double *sums;
 };
-constexpr int32_t kTaken = 1 << 30;
+constexpr int32_t kTaken = 1 << 30, kResidual = 1 << 30;
 
 // A probability: what is negative, infinite or no number counts as 0.
-__device__ __forceinline__ float clean(float p) { return p > 0.0f && p < __builtin_inff() ? p : 0.0f; }
+__device__ __forceinline__ float clean(float p) { return __float_as_uint(p) - 1u < 0x7F7FFFFFu ? p : 0.0f; }
 
 struct Sequence {
   int64_t first;
@@ -57,11 +57,12 @@ __device__ __forceinline__ Sequence sequence_of(const VerifyArgs &a, int i) {
 // One wave a sequence.
 template <bool BF16>
 __global__ __launch_bounds__(64) void k_verify_plan(const VerifyArgs a) {
-  __shared__ int up[kNodes], kid[kNodes];
+  __shared__ int up[kNodes], kid[kNodes], id[kNodes];
   const int i = blockIdx.x, lane = threadIdx.x;
   const Sequence s = sequence_of(a, i);
   for (int j = lane; j < s.nodes; j += 64) {
     up[j] = a.parents[s.first + j];
+    id[j] = a.ids[s.first + j];
     kid[j] = kNodes;
   }
   __syncthreads();
@@ -94,7 +95,7 @@ __global__ __launch_bounds__(64) void k_verify_plan(const VerifyArgs a) {
     const int k = kid[j];
     int to = k == kNodes ? -1 : k;
     if (a.draft && to >= 0) {
-      const int64_t row = s.first + j, x = a.ids[s.first + k];
+      const int64_t row = s.first + j, x = id[k];
       if (x >= 0 && x < a.vocab) {
         const double p = clean(load_one<BF16>(a.target, row * a.vocab + x));
         const double q = clean(load_one<BF16>(a.draft, row * a.vocab + x));
@@ -118,15 +119,16 @@ __global__ __launch_bounds__(64) void k_verify_plan(const VerifyArgs a) {
       if (a.draft) draws = k == (x | kTaken) || (k != x && !(k & kTaken));
     }
     const uint64_t all = __ballot(draws);
-    if (draws) a.draws[s.first + found + __popcll(all & ((1ull << lane) - 1))] = j;
+    if (draws)
+      a.draws[s.first + found + __popcll(all & ((1ull << lane) - 1))] = j | (a.draft && kid[j] >= 0 ? kResidual : 0);
     found += __popcll(all);
   }
   if (lane == 0) a.many[i] = found;
 }
 
-// A wave's part of a row: step u of lane l holds kChunk / steps / 64 neighbouring
-// elements. Rows begin anywhere: chunks are laid out from the 16-byte boundary
-// before a row on.
+// A wave's part of a row: step u of lane l holds 16 bytes of neighbouring elements,
+// zeros outside the row. Rows begin anywhere: chunks are laid out from the 16-byte
+// boundary before a row on.
 template <bool BF16>
 struct Part {
   static constexpr int A = BF16 ? 8 : 4, U = kChunk / 64 / A;
@@ -135,35 +137,40 @@ struct Part {
 template <bool BF16>
 __device__ __forceinline__ Part<BF16> load_part(const void *base, const VerifyArgs &a, int64_t row, int chunk) {
   constexpr int A = Part<BF16>::A, U = Part<BF16>::U, E = BF16 ? 2 : 4;
-  const int lane = threadIdx.x & 63;
-  const int64_t begin = row * a.vocab, end = begin + a.vocab, all = a.tokens * a.vocab;
-  const int64_t from = (begin & ~(int64_t)(A - 1)) + (int64_t)chunk * kChunk + lane * A;
+  const int64_t begin = row * a.vocab, end = begin + a.vocab;
+  const int64_t from = (begin & ~(int64_t)(A - 1)) + (int64_t)chunk * kChunk + (threadIdx.x & 63) * A;
+  const uint8_t *x = reinterpret_cast<const uint8_t *>(base) + from * E;
   Part<BF16> p;
 #pragma unroll
   for (int u = 0; u < U; u++) {
     const int64_t at = from + u * 64 * A;
-    const uint8_t *x = reinterpret_cast<const uint8_t *>(base) + at * E;
     p.v[u] = u32x4{0, 0, 0, 0};
-    if (at < end) {
-      if (at + A <= all) {
-        p.v[u] = *reinterpret_cast<const u32x4 *>(x);
-      } else {  // the array's last elements
-        for (int e = 0; e < A; e++) {
-          if (at + e >= all) break;
-          if constexpr (BF16) p.v[u][e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t *>(x)[e] << (16 * (e & 1));
-          else p.v[u][e] = reinterpret_cast<const uint32_t *>(x)[e];
-        }
+    if (at >= begin && at + A <= end) p.v[u] = *reinterpret_cast<const u32x4 *>(x + u * 64 * A * E);
+  }
+  // the row's first and last elements, where they share their 16 bytes with others'
+  if ((begin | end) & (A - 1)) {
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int64_t at = from + u * 64 * A;
+      if (at >= end || at + A <= begin || (at >= begin && at + A <= end)) continue;
+#pragma unroll
+      for (int e = 0; e < A; e++) {
+        if (at + e < begin || at + e >= end) continue;
+        const uint8_t *one = x + (u * 64 * A + e) * E;
+        if constexpr (BF16) p.v[u][e >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t *>(one) << (16 * (e & 1));
+        else p.v[u][e] = *reinterpret_cast<const uint32_t *>(one);
       }
     }
   }
   return p;
 }
-// Element e of step u as a probability, 0 outside the row; `index` is its place in the row.
+// Element e of 16 bytes as a probability.
 template <bool BF16>
-__device__ __forceinline__ float part_at(const Part<BF16> &p, int u, int e) {
-  const uint32_t w = BF16 ? p.v[u][e >> 1] : p.v[u][e];
+__device__ __forceinline__ float probability(u32x4 v, int e) {
+  const uint32_t w = BF16 ? v[e >> 1] : v[e];
   return clean(__uint_as_float(!BF16 ? w : (e & 1) ? w & 0xFFFF0000u : w << 16));
 }
+// Place in the row of element e of step u.
 template <bool BF16>
 __device__ __forceinline__ int64_t part_index(const VerifyArgs &a, int64_t row, int chunk, int u, int e) {
   constexpr int A = Part<BF16>::A;
@@ -178,50 +185,65 @@ __device__ __forceinline__ double sum64d(double v) {
   v += __shfl_xor(v, 16);
   return v + __shfl_xor(v, 32);
 }
-// Sums of the lanes up to and including this one.
+// Sums of the lanes up to and including this one: within 16 lanes by shifts of 1,
+// 2, 4 and 8 (row_shr), then the last lane of a row to the next one, and that of
+// the first two rows to the others (row_bcast 15 and 31).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double shifted(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 __device__ __forceinline__ double scan64(double v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
-  return v;
+  v += shifted<0x111, 0xF>(v);
+  v += shifted<0x112, 0xF>(v);
+  v += shifted<0x114, 0xF>(v);
+  v += shifted<0x118, 0xF>(v);
+  v += shifted<0x142, 0xA>(v);
+  return v + shifted<0x143, 0xC>(v);
 }
 
-// Weight of an element of a row that is drawn from, and the target's share of it.
+// Weight of an element of a row that is drawn from.
 template <bool BF16>
-__device__ __forceinline__ double weight_at(const VerifyArgs &a, const Part<BF16> &p, const Part<BF16> &q, bool residual,
-                                            int64_t row, int chunk, int u, int e, double &target) {
-  const int64_t i = part_index<BF16>(a, row, chunk, u, e);
-  target = i >= 0 && i < a.vocab ? (double)part_at<BF16>(p, u, e) : 0.0;
-  if (!residual) return target;
-  const double d = target - (i >= 0 && i < a.vocab ? (double)part_at<BF16>(q, u, e) : 0.0);
-  return d > 0.0 ? d : 0.0;
+__device__ __forceinline__ double weight_of(u32x4 p, u32x4 q, bool residual, int e) {
+  const double t = probability<BF16>(p, e);
+  if (!residual) return t;
+  return __builtin_fmax(t - (double)probability<BF16>(q, e), 0.0);
 }
 
 // A wave a chunk; a workgroup's z takes rows z, z + gridDim.z, ... of a sequence.
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_verify_sums(const VerifyArgs a) {
-  const int chunk = blockIdx.x * 4 + (threadIdx.x >> 6), i = blockIdx.y;
+  auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+  const int chunk = uniform(blockIdx.x * 4 + (threadIdx.x >> 6)), i = blockIdx.y;
   const Sequence s = sequence_of(a, i);
-  const int many = s.nodes ? a.many[i] : 0;
-  if (chunk >= a.chunks) return;
+  if (chunk >= a.chunks || (int)blockIdx.z >= s.nodes) return;
+  int draws = uniform(a.draws[s.first + blockIdx.z]);  // asked for beside how many there are
+  const int many = uniform(a.many[i]);
   for (int r = blockIdx.z; r < many; r += gridDim.z) {
-    const int64_t row = s.first + a.draws[s.first + r];
-    const bool residual = a.draft && a.kid[row] >= 0;
+    if (r >= (int)gridDim.z) draws = uniform(a.draws[s.first + r]);
+    const int64_t row = s.first + (draws & ~kResidual);
+    const bool residual = draws & kResidual;
     const Part<BF16> p = load_part<BF16>(a.target, a, row, chunk);
     Part<BF16> q = {};
     if (residual) q = load_part<BF16>(a.draft, a, row, chunk);
     double w = 0.0, t = 0.0;
+    if (residual) {
 #pragma unroll
-    for (int u = 0; u < Part<BF16>::U; u++)
+      for (int u = 0; u < Part<BF16>::U; u++)
 #pragma unroll
-      for (int e = 0; e < Part<BF16>::A; e++) {
-        double one;
-        w += weight_at<BF16>(a, p, q, residual, row, chunk, u, e, one);
-        t += one;
-      }
+        for (int e = 0; e < Part<BF16>::A; e++) {
+          w += weight_of<BF16>(p.v[u], q.v[u], true, e);
+          t += weight_of<BF16>(p.v[u], q.v[u], false, e);
+        }
+    } else {
+#pragma unroll
+      for (int u = 0; u < Part<BF16>::U; u++)
+#pragma unroll
+        for (int e = 0; e < Part<BF16>::A; e++) t += weight_of<BF16>(p.v[u], q.v[u], false, e);
+      w = t;
+    }
     w = sum64d(w);
     t = sum64d(t);
     if ((threadIdx.x & 63) == 0) {
@@ -237,22 +259,24 @@ template <bool BF16>
 __device__ __forceinline__ int64_t draw_from(const VerifyArgs &a, int64_t slot, int64_t row, bool residual) {
   const int lane = threadIdx.x & 63;
   const double *sums = a.sums + slot * a.chunks * 2;
-  double total = 0.0;
-  int which = 0;  // w, or, where w has nothing, p
+  const double number = a.numbers[2 * row + 1];
+  double total = 0.0, head = 0.0;  // head: of the first 64 chunks
+  int which = 0;                   // w, or, where w has nothing, p
   for (; which < 2; which++) {
-    double t = 0.0;
-    for (int c = lane; c < a.chunks; c += 64) t += sums[2 * c + which];
+    head = lane < a.chunks ? sums[2 * lane + which] : 0.0;
+    double t = head;
+    for (int c = lane + 64; c < a.chunks; c += 64) t += sums[2 * c + which];
     total = sum64d(t);
     if (total > 0.0) break;
   }
   if (which == 2) return -1;
   if (which == 1) residual = false;
-  const double bound = (double)a.numbers[2 * row + 1] * total;
+  const double bound = number * total;
   // the chunk in which the sum passes the bound; if rounding leaves it below, the last with anything
   double before = 0.0, base = 0.0;
   int chunk = -1;
   for (int c0 = 0; c0 < a.chunks; c0 += 64) {
-    const double v = c0 + lane < a.chunks ? sums[2 * (c0 + lane) + which] : 0.0;
+    const double v = c0 == 0 ? head : c0 + lane < a.chunks ? sums[2 * (c0 + lane) + which] : 0.0;
     const double incl = scan64(v);
     const uint64_t any = __ballot(v > 0.0), past = __ballot(v > 0.0 && before + incl > bound);
     const uint64_t take = past ? past & -past : any ? 1ull << (63 - __builtin_clzll(any)) : 0;
@@ -264,58 +288,74 @@ __device__ __forceinline__ int64_t draw_from(const VerifyArgs &a, int64_t slot, 
     }
     before += shfl(incl, 63);
   }
+  chunk = __builtin_amdgcn_readfirstlane(chunk);
   const Part<BF16> p = load_part<BF16>(a.target, a, row, chunk);
   Part<BF16> q = {};
   if (residual) q = load_part<BF16>(a.draft, a, row, chunk);
-  int64_t found = -1;
+  // the step in which it does, from the steps' sums, then the lane, then its element
+  int step = 0;
+  u32x4 mine_p = {0, 0, 0, 0}, mine_q = {0, 0, 0, 0};
+  double mine = 0.0, at = base;
+  bool over = false;
 #pragma unroll
   for (int u = 0; u < Part<BF16>::U; u++) {
-    double v = 0.0, one;
+    double v = 0.0;
 #pragma unroll
-    for (int e = 0; e < Part<BF16>::A; e++) v += weight_at<BF16>(a, p, q, residual, row, chunk, u, e, one);
-    const double incl = scan64(v);
-    const uint64_t any = __ballot(v > 0.0), past = __ballot(v > 0.0 && base + incl > bound);
-    const uint64_t take = past ? past & -past : any ? 1ull << (63 - __builtin_clzll(any)) : 0;
-    if (take) {
-      // the lane's own elements, one by one
-      const int l = __builtin_ctzll(take);
-      double sum = base + (incl - v);
-      int64_t mine = -1;
-      bool done = false;
-#pragma unroll
-      for (int e = 0; e < Part<BF16>::A; e++) {
-        const double w = weight_at<BF16>(a, p, q, residual, row, chunk, u, e, one);
-        sum += w;
-        if (w > 0.0 && !done) {
-          mine = part_index<BF16>(a, row, chunk, u, e);
-          done = sum > bound;
-        }
-      }
-      found = __shfl((long long)mine, l);
-      if (past) break;
+    for (int e = 0; e < Part<BF16>::A; e++) v += weight_of<BF16>(p.v[u], q.v[u], residual, e);
+    const double all = sum64d(v);
+    if (all > 0.0 && !over) {
+      step = u;
+      mine = v;
+      mine_p = p.v[u];
+      mine_q = q.v[u];
+      base = at;
+      over = at + all > bound;
     }
-    base += shfl(incl, 63);
+    at += all;
+    __builtin_amdgcn_sched_barrier(0);  // few numbers in 64 bits at a time
   }
-  return found;
+  const double incl = scan64(mine);
+  const uint64_t any = __ballot(mine > 0.0), past = __ballot(mine > 0.0 && base + incl > bound);
+  if (!any) return -1;
+  const int l = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(any);
+  double sum = base + (incl - mine);
+  int64_t found = -1;
+  bool done = false;
+#pragma unroll
+  for (int e = 0; e < Part<BF16>::A; e++) {
+    const double w = weight_of<BF16>(mine_p, mine_q, residual, e);
+    sum += w;
+    if (w > 0.0 && !done) {
+      found = part_index<BF16>(a, row, chunk, step, e);
+      done = sum > bound;
+    }
+  }
+  return __shfl((long long)found, l);
 }
 
+// A wave a row to draw at, all of a sequence's at once where they are 16 or fewer.
 template <bool BF16>
-__global__ __launch_bounds__(256) void k_verify_walk(const VerifyArgs a) {
+__global__ __launch_bounds__(1024) void k_verify_walk(const VerifyArgs a) {
   __shared__ int up[kNodes], kid[kNodes], id[kNodes], drawn[kNodes];
-  const int i = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // (the wave's number and what follows from it is in scalar registers)
+  auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+  const int i = blockIdx.x, lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const Sequence s = sequence_of(a, i);
   int32_t *path = a.path + (int64_t)i * a.width;
-  for (int j = threadIdx.x; j < s.nodes; j += 256) {
+  for (int j = threadIdx.x; j < s.nodes; j += blockDim.x) {
     up[j] = a.parents[s.first + j];
     kid[j] = a.kid[s.first + j];
     id[j] = a.ids[s.first + j];
   }
-  const int many = s.nodes ? a.many[i] : 0;
-  for (int r = wave; r < many; r += 4) {
-    const int j = a.draws[s.first + r];
-    const int64_t row = s.first + j;
-    const int64_t t = draw_from<BF16>(a, s.first + r, row, a.draft && a.kid[row] >= 0);
-    if (lane == 0) drawn[j] = (int)t;
+  if (wave < s.nodes) {
+    int draws = uniform(a.draws[s.first + wave]);  // asked for beside how many there are
+    const int many = uniform(a.many[i]);
+    for (int r = wave; r < many; r += blockDim.x >> 6) {
+      if (r != wave) draws = uniform(a.draws[s.first + r]);
+      const int j = draws & ~kResidual;
+      const int64_t t = draw_from<BF16>(a, s.first + r, s.first + j, draws & kResidual);
+      if (lane == 0) drawn[j] = (int)t;
+    }
   }
   __syncthreads();
   if (wave) return;
@@ -372,21 +412,22 @@ hipError_t mxi_launch_verify(const void *target, const void *draft, int bf16, co
   ws += round16((size_t)tokens * 4);
   a.many = reinterpret_cast<int32_t *>(ws);
   if (tokens == 0) {  // outputs alone
-    k_verify_walk<false><<<batch, 256, 0, st>>>(a);
+    k_verify_walk<false><<<batch, 64, 0, st>>>(a);
     return hipGetLastError();
   }
   const int groups = (a.chunks + 3) / 4;
   const int64_t mean = std::max<int64_t>(1, tokens / batch);
   const int rows = (int)std::min<int64_t>(mean, std::max<int64_t>(1, 4096 / ((int64_t)groups * batch)));
   const dim3 grid((uint32_t)groups, (uint32_t)batch, (uint32_t)rows);
+  const int threads = 64 * (int)std::min<int64_t>(16, mean);
   if (bf16) {
     k_verify_plan<true><<<batch, 64, 0, st>>>(a);
     k_verify_sums<true><<<grid, 256, 0, st>>>(a);
-    k_verify_walk<true><<<batch, 256, 0, st>>>(a);
+    k_verify_walk<true><<<batch, threads, 0, st>>>(a);
   } else {
     k_verify_plan<false><<<batch, 64, 0, st>>>(a);
     k_verify_sums<false><<<grid, 256, 0, st>>>(a);
-    k_verify_walk<false><<<batch, 256, 0, st>>>(a);
+    k_verify_walk<false><<<batch, threads, 0, st>>>(a);
   }
   return hipGetLastError();
 }
