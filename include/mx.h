@@ -560,8 +560,12 @@ mx_status_t mx_kv_append_rotary(const void *k, const void *v, mx_dtype_t dtype, 
  * lengths[i] keys being the new ones, key j is new token j - (lengths[i] - n).
  * Bits past the sequence's new tokens do not count; new tokens past the row's
  * bits are not seen. A token that sees nothing gives zeros. words is 1 to 65535.
- * Everything else, the workspace (mx_kv_attention_workspace_size) included, is
- * mx_kv_attention's, whose results a causal mask's are but for rounding. */
+ * workspace: mx_kv_attention_tree_workspace_size(...) bytes, 16-byte aligned, at
+ * most 69 MiB where more than 32 rows of query heads read a kv head in the mean.
+ * Everything else is mx_kv_attention's, whose results a causal mask's are but for
+ * rounding. */
+size_t mx_kv_attention_tree_workspace_size(int64_t tokens, int batch, int q_heads, int heads,
+                                           int dim, int64_t max_length);
 mx_status_t mx_kv_attention_tree(const void *q, int64_t q_stride, int q_heads,
                                  const mx_kv_cache_t *cache, const mx_kv_batch_t *batch,
                                  const uint32_t *mask, int words, int64_t max_length, float scale,

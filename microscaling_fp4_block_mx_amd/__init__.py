@@ -48,7 +48,7 @@ EXPORTS = ("mx_quantize", "mx_dequantize", "mx_fakequant", "mx_block_mse",
            "mx_rmsnorm_backward", "mx_rmsnorm_backward_workspace_size", "mx_matmul_mxfp8",
            "mx_matmul_mxfp8_workspace_size", "mx_kv_append", "mx_kv_attention",
            "mx_kv_attention_workspace_size", "mx_norm_rotate", "mx_norm_rotate_backward",
-           "mx_norm_rotate_backward_workspace_size", "mx_kv_append_rotary", "mx_kv_attention_tree",
+           "mx_norm_rotate_backward_workspace_size", "mx_kv_append_rotary", "mx_kv_attention_tree", "mx_kv_attention_tree_workspace_size",
            "mx_verify_drafts", "mx_verify_drafts_workspace_size", "mx_kv_keep", "mx_status_string", "mx_last_error_detail")
 
 _lib = None
@@ -602,7 +602,8 @@ from .layer import (  # noqa: E402
 
 from .draft import (  # noqa: E402
     MxHeads, MxHeadsGrad, MxRotary, Rotary, declare as declare_draft, kv_append_rotary,
-    kv_attention_tree, kv_keep, mx_kv_append_rotary, mx_kv_attention_tree, mx_kv_keep,
+    kv_attention_tree, kv_keep, mx_kv_append_rotary, mx_kv_attention_tree,
+    mx_kv_attention_tree_workspace_size, mx_kv_keep,
     mx_norm_rotate, mx_norm_rotate_backward, mx_norm_rotate_backward_workspace_size,
     mx_verify_drafts, mx_verify_drafts_workspace_size, norm_rotate, norm_rotate_backward,
     rotary_table, tree_mask, verify_drafts)

@@ -227,6 +227,14 @@ mx_status_t mx_kv_append_rotary(const void *k, const void *v, mx_dtype_t dtype, 
                                             stream_of(stream)));
 }
 
+size_t mx_kv_attention_tree_workspace_size(int64_t tokens, int batch, int q_heads, int heads,
+                                           int dim, int64_t max_length) {
+  if (check_attention(tokens, batch, q_heads, heads, dim, max_length) != MX_OK || tokens == 0)
+    return 0;
+  return mxi_kv_attention_tree_workspace(tokens, batch, q_heads, heads, dim,
+                                         max_length == 0 ? INT32_MAX : max_length);
+}
+
 mx_status_t mx_kv_attention_tree(const void *q, int64_t q_stride, int q_heads,
                                  const mx_kv_cache_t *cache, const mx_kv_batch_t *batch,
                                  const uint32_t *mask, int words, int64_t max_length, float scale,
@@ -245,7 +253,7 @@ mx_status_t mx_kv_attention_tree(const void *q, int64_t q_stride, int q_heads,
   if (!aligned16(q) || !aligned16(out) || q_stride % 8 || !aligned4(mask)) return MX_ERR_ALIGN;
   if (max_length == 0 || max_length > (int64_t)batch->width * cache->page)
     max_length = (int64_t)batch->width * cache->page;
-  const size_t need = mxi_kv_attention_workspace(batch->tokens, batch->batch, q_heads,
+  const size_t need = mxi_kv_attention_tree_workspace(batch->tokens, batch->batch, q_heads,
                                                  cache->heads, cache->dim, max_length);
   if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need))
     return MX_ERR_WORKSPACE;

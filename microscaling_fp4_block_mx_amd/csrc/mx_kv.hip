@@ -1363,27 +1363,15 @@ __device__ __forceinline__ int swz_k(int r) {
   return (r >> 3) & 3;
 }
 
-template <int D, bool TREE>
-__global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
+// One block of rows and its tiles t0 .. t1 - 1; `write(x, row, state)` takes what
+// comes of the wave's 16 rows x, for each row that is one.
+template <int D, bool TREE, typename F>
+__device__ __forceinline__ void attend_tiles(const AttnArgs &a, const Block &b, int head, int t0, int t1,
+                                             uint8_t (&ks)[256 * D], uint8_t (&vs)[256 * D], F write) {
   constexpr int DT = D / 16, RT = 2, S = 128 * D;
   constexpr int KL = S / 4096, VL = KL;  // direct loads per thread and tile
-  __shared__ __attribute__((aligned(16))) uint8_t ks[2 * S], vs[2 * S];
-  // kv heads fastest: the eight XCDs, which are dealt workgroups in turn,
-  // keep to few heads each. The last blocks of a sequence see the most keys:
-  // they start first.
-  const uint32_t block = blockIdx.z * gridDim.x + blockIdx.x;
-  const int head = block % a.c.heads, from_last = block / a.c.heads;
-  Block b;
-  if (from_last >= a.units || !find_block<TREE>(a, a.units - 1 - from_last, b)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
-  const int end = TREE ? b.len : min(b.len, b.seen0 + b.count - 1);
-  const int tiles = (max(end, 0) + 127) >> 7;
-  // this split's tiles, from an even one on (the buffers take turns); the last
-  // split takes whatever the caller's bound on the lengths left out
-  const int split = blockIdx.y, t0 = split * a.chunk;
-  const int t1 = split + 1 == a.splits ? tiles : min(tiles, t0 + a.chunk);
-  if (split > 0 && t0 >= tiles) return;  // the sum takes only splits that exist
   const int rows = b.count * a.group;
   Query<D> q[RT];
   Rows<D> r[RT];
@@ -1467,7 +1455,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
     if (tile + 1 < t1) {
       bytes = *byte_at(a, mine, head, lane);
       mine = page_of(a, b, tile + 2, lane);
-      load(tile + 1, (tile + 1) & 1, id);
+      load(tile + 1, (tile + 1 - t0) & 1, id);
     }
     auto keys = [&](int t) {
       const int at = (32 * (t >> 1) + 4 * (t & 1)) * D;
@@ -1548,29 +1536,194 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
 #pragma unroll
   for (int x = 0; x < RT; x++) {
     const int row = 32 * wave + 16 * x + l16;
-    if (row < rows) {
-      const float l = r[x].l[0], inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const int64_t tok = b.tok0 + row / a.group;
-      const int64_t qh = (int64_t)head * a.group + row % a.group;
-      if (a.splits > 1) {
-        float *p = a.part + ((tok * a.q_heads + qh) * a.splits + split) * (D + 4);
-#pragma unroll
-        for (int d = 0; d < DT; d++) *reinterpret_cast<f32x4 *>(p + 16 * d + 4 * lg) = r[x].o[d];
-        if (lg == 0) {
-          p[D] = r[x].m;
-          p[D + 1] = l;
-        }
-      } else {
-        uint16_t *p = a.out + (tok * a.q_heads + qh) * D + 4 * lg;
-#pragma unroll
-        for (int d = 0; d < DT; d++) {
-          const f32x4 o = r[x].o[d];
-          *reinterpret_cast<u32x2 *>(p + 16 * d) =
-              u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
-        }
-      }
-    }
+    if (row < rows) write(row, r[x]);
   }
+}
+
+// Where a row's result goes: to the output, or what is left to be joined.
+template <int D>
+__device__ __forceinline__ void write_row(const AttnArgs &a, const Block &b, int head, int row, const Rows<D> &r) {
+  const int lg = (threadIdx.x & 63) >> 4;
+  const float l = r.l[0], inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int64_t tok = b.tok0 + row / a.group, qh = (int64_t)head * a.group + row % a.group;
+  uint16_t *p = a.out + (tok * a.q_heads + qh) * D + 4 * lg;
+#pragma unroll
+  for (int d = 0; d < D / 16; d++) {
+    const f32x4 o = r.o[d];
+    *reinterpret_cast<u32x2 *>(p + 16 * d) = u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+  }
+}
+template <int D>
+__device__ __forceinline__ void write_part(float *p, const Rows<D> &r) {
+  const int lg = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int d = 0; d < D / 16; d++) *reinterpret_cast<f32x4 *>(p + 16 * d + 4 * lg) = r.o[d];
+  if (lg == 0) {
+    p[D] = r.m;
+    p[D + 1] = r.l[0];
+  }
+}
+
+template <int D, bool TREE>
+__global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t ks[256 * D], vs[256 * D];
+  // kv heads fastest: the eight XCDs, which are dealt workgroups in turn,
+  // keep to few heads each. The last blocks of a sequence see the most keys:
+  // they start first.
+  const uint32_t block = blockIdx.z * gridDim.x + blockIdx.x;
+  const int head = block % a.c.heads, from_last = block / a.c.heads;
+  Block b;
+  if (from_last >= a.units || !find_block<TREE>(a, a.units - 1 - from_last, b)) return;
+  const int end = TREE ? b.len : min(b.len, b.seen0 + b.count - 1);
+  const int tiles = (max(end, 0) + 127) >> 7;
+  // this split's tiles; the last split takes whatever the caller's bound on the
+  // lengths left out
+  const int split = blockIdx.y, t0 = split * a.chunk;
+  const int t1 = split + 1 == a.splits ? tiles : min(tiles, t0 + a.chunk);
+  if (split > 0 && t0 >= tiles) return;  // the sum takes only splits that exist
+  attend_tiles<D, TREE>(a, b, head, t0, t1, ks, vs, [&](int row, const Rows<D> &r) {
+    if (a.splits > 1) {
+      const int64_t tok = b.tok0 + row / a.group, qh = (int64_t)head * a.group + row % a.group;
+      write_part<D>(a.part + ((tok * a.q_heads + qh) * a.splits + split) * (D + 4), r);
+    } else {
+      write_row<D>(a, b, head, row, r);
+    }
+  });
+}
+
+// Trees whose rows fill no card in blocks: every workgroup gets an even share of
+// all the tiles there are. Blocks of rows lie end to end, each as long as it has
+// tiles (at least one), sequence after sequence; workgroup g of a head takes
+// places g per .. (g + 1) per - 1, which may be the end of one block, some whole
+// ones and the beginning of another. What a block got from several workgroups
+// is left in their room (the first and the last block of each: two rooms) and
+// joined. (Splits of one length for all sequences left the units that ended first
+// idle: 16 sequences of up to 24 tokens in 8,000 to 32,000, 41 % of the time.)
+constexpr int kLeastTiles = 8;    // of a workgroup's share
+constexpr int kSharers = 64;      // sequences: one a lane
+struct Stretch {
+  int c0, n, len;     // the lane's sequence: first token, tokens, length
+  int blocks, tiles;  // its blocks of rows, places of each
+  int64_t end;        // of its places
+  int64_t total, per; // places there are, places of a workgroup
+  __device__ __forceinline__ explicit Stretch(const AttnArgs &a) {
+    const int lane = threadIdx.x & 63;
+    c0 = n = len = blocks = 0;
+    if (lane < a.b.batch) {
+      c0 = a.b.cu[lane];
+      n = a.b.cu[lane + 1] - c0;
+      const int64_t room = (int64_t)a.b.width << a.shift;
+      len = (int)min((int64_t)max(a.b.lengths[lane], 0), room);
+      if (n > 0 && c0 >= 0 && (int64_t)c0 + n <= a.b.tokens) blocks = (n + a.block_tokens - 1) / a.block_tokens;
+    }
+    tiles = max(1, (len + 127) >> 7);
+    end = (int64_t)blocks * tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t o = __shfl_up((long long)end, d);
+      end += lane >= d ? o : 0;
+    }
+    total = __shfl((long long)end, 63);
+    per = max((int64_t)kLeastTiles, (total + a.splits - 1) / a.splits);
+  }
+  __device__ __forceinline__ static int of(int v, int i) { return __builtin_amdgcn_readlane(v, i); }
+  __device__ __forceinline__ int64_t begin_of(int i) const {
+    return __shfl((long long)(end - (int64_t)blocks * tiles), i);
+  }
+};
+
+template <int D>
+__global__ __launch_bounds__(256, 2) void k_attn_share(const AttnArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t ks[256 * D], vs[256 * D];
+  auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+  const int head = blockIdx.x % a.c.heads, g = blockIdx.x / a.c.heads;
+  const Stretch s(a);
+  const int64_t first = g * s.per;
+  // (a block's tiles are counted in 32 bits, and so is what a share takes at a time)
+  if (first >= s.total) return;
+  int64_t left = min(s.total - first, s.per);
+  int i = uniform(__builtin_ctzll(__ballot(s.end > first)));
+  const int64_t into = first - s.begin_of(i);
+  int block = uniform((int)(into / Stretch::of(s.tiles, i))), t0 = uniform((int)(into % Stretch::of(s.tiles, i)));
+  bool later = false;
+  while (left > 0) {
+    if (block >= Stretch::of(s.blocks, i)) {  // on to the next sequence
+      if (++i >= kSharers) break;
+      block = 0;
+      continue;
+    }
+    const int tiles = Stretch::of(s.tiles, i), n = Stretch::of(s.n, i);
+    const int t1 = uniform((int)min((int64_t)tiles, t0 + left));
+    Block b;
+    b.len = Stretch::of(s.len, i);
+    b.tok0 = Stretch::of(s.c0, i) + block * a.block_tokens;
+    b.count = min(a.block_tokens, n - block * a.block_tokens);
+    b.seen0 = b.len - n;
+    b.fresh = n;
+    b.table = a.b.table + (int64_t)i * a.b.width;
+    b.last_page = max(0, (b.len - 1) >> a.shift);
+    const bool whole = t0 == 0 && t1 == tiles;
+    float *room_of = a.part + ((int64_t)blockIdx.x * 2 + later) * 128 * (D + 4);
+    attend_tiles<D, true>(a, b, head, t0, min(t1, (b.len + 127) >> 7), ks, vs, [&](int row, const Rows<D> &r) {
+      if (whole) write_row<D>(a, b, head, row, r);
+      else write_part<D>(room_of + row * (D + 4), r);
+    });
+    left -= t1 - t0;
+    t0 = 0;
+    block++;
+    later = true;
+    __syncthreads();  // every wave is done with the tiles in LDS
+  }
+}
+
+// Joins what workgroups left of the rows of a token: D / 4 threads a row.
+template <int D>
+__global__ __launch_bounds__(256) void k_attn_share_join(const AttnArgs a) {
+  constexpr int C = D / 4, R = 256 / C, P = D + 4;
+  const int tok = blockIdx.x, c = threadIdx.x % C, qh = blockIdx.y * R + threadIdx.x / C;
+  const Stretch s(a);
+  const uint64_t owner = __ballot(s.blocks > 0 && tok >= s.c0 && tok < s.c0 + s.n);
+  if (!owner || qh >= a.q_heads) return;
+  const int i = __builtin_ctzll(owner);
+  const int c0 = Stretch::of(s.c0, i), tiles = Stretch::of(s.tiles, i), block = (tok - c0) / a.block_tokens;
+  const int64_t begin = s.begin_of(i) + (int64_t)block * tiles;
+  const int g0 = (int)(begin / s.per), g1 = (int)((begin + tiles - 1) / s.per);
+  if (g0 == g1) return;  // one workgroup had it all
+  const int head = qh / a.group;
+  const int row = (tok - c0 - block * a.block_tokens) * a.group + qh % a.group;
+  auto part = [&](int g) {  // of a workgroup that began before this block the later room
+    return a.part + ((((int64_t)g * a.c.heads + head) * 2 + (g * s.per < begin)) * 128 + row) * P;
+  };
+  // four workgroups' at a time, whose loads go together
+  float m = -__builtin_inff(), l = 0.0f;
+  f32x4 o = {0, 0, 0, 0};
+  for (int g = g0; g <= g1; g += 4) {
+    float pm[4], pl[4];
+    f32x4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      const float *p = part(min(g + u, g1));
+      pm[u] = g + u <= g1 ? p[D] : -__builtin_inff();
+      pl[u] = p[D + 1];
+      v[u] = *reinterpret_cast<const f32x4 *>(p + 4 * c);
+    }
+    const float top = __builtin_fmaxf(__builtin_fmaxf(m, __builtin_fmaxf(pm[0], pm[1])), __builtin_fmaxf(pm[2], pm[3]));
+    const float ms = top == -__builtin_inff() ? 0.0f : top, old = __builtin_amdgcn_exp2f(m - ms);
+    l *= old;
+    o *= old;
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      const float f = __builtin_amdgcn_exp2f(pm[u] - ms);
+      if (g + u > g1) break;
+      l = __builtin_fmaf(f, pl[u], l);
+#pragma unroll
+      for (int e = 0; e < 4; e++) o[e] = __builtin_fmaf(f, v[u][e], o[e]);
+    }
+    m = top;
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  *reinterpret_cast<u32x2 *>(a.out + ((int64_t)tok * a.q_heads + qh) * D + 4 * c) =
+      u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
 }
 
 static int log2_of(int x) {
@@ -1640,6 +1793,15 @@ static AttnPlan attn_plan(int64_t tokens, int batch, int q_heads, int heads, int
   return p;
 }
 
+// Workgroups of a head that share a tree's tiles, 0 where they do not: few rows,
+// whose kernel splits the keys itself, more sequences than a wave has lanes, and
+// blocks enough to fill the card over and over. Two workgroups a compute unit.
+static int tree_share(const AttnPlan &p, int batch, int heads, int64_t max_length) {
+  if (p.few || batch > kSharers || p.units * heads > 4096) return 0;
+  const int64_t tiles = p.units * std::max<int64_t>(1, (max_length + 127) / 128);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(512 / heads, (tiles + kLeastTiles - 1) / kLeastTiles));
+}
+
 }  // namespace mxl
 
 using namespace mxl;
@@ -1699,6 +1861,14 @@ hipError_t mxi_launch_kv_keep(const mx_kv_cache_t &cache, const mx_kv_batch_t &b
   return hipGetLastError();
 }
 
+size_t mxi_kv_attention_tree_workspace(int64_t tokens, int batch, int q_heads, int heads, int dim,
+                                       int64_t max_length) {
+  const AttnPlan p = attn_plan(tokens, batch, q_heads, heads, max_length);
+  if (const int64_t share = tree_share(p, batch, heads, max_length))
+    return (size_t)(share * heads * 2 * 128) * (dim + 4) * sizeof(float);
+  return mxi_kv_attention_workspace(tokens, batch, q_heads, heads, dim, max_length);
+}
+
 size_t mxi_kv_attention_workspace(int64_t tokens, int batch, int q_heads, int heads, int dim,
                                   int64_t max_length) {
   const AttnPlan p = attn_plan(tokens, batch, q_heads, heads, max_length);
@@ -1716,6 +1886,22 @@ static hipError_t launch_attention(const void *q, int64_t q_stride, int q_heads,
                       p.chunk, p.splits, (int)p.units, scale * 1.44269504088896340736f,
                       reinterpret_cast<uint16_t *>(out), reinterpret_cast<float *>(workspace),
                       tree, words};
+  if constexpr (TREE) {
+    if (const int share = tree_share(p, batch.batch, cache.heads, max_length)) {
+      AttnArgs t = a;
+      t.splits = share;
+      const int rows = 1024 / cache.dim;  // of a workgroup that joins
+      const dim3 jgrid((uint32_t)batch.tokens, (uint32_t)((q_heads + rows - 1) / rows));
+      if (cache.dim == 64) {
+        k_attn_share<64><<<share * cache.heads, 256, 0, st>>>(t);
+        k_attn_share_join<64><<<jgrid, 256, 0, st>>>(t);
+      } else {
+        k_attn_share<128><<<share * cache.heads, 256, 0, st>>>(t);
+        k_attn_share_join<128><<<jgrid, 256, 0, st>>>(t);
+      }
+      return hipGetLastError();
+    }
+  }
   // (few rows are split for at most 1,024 sequences)
   const Spread xz = spread(p.few ? p.units : p.units * cache.heads);
   const dim3 grid(xz.first, (uint32_t)cache.heads, p.splits > 1 ? (uint32_t)p.splits : xz.second);

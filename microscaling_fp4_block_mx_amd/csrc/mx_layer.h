@@ -48,7 +48,8 @@ hipError_t mxi_launch_kv_append_rotary(const void *k, const void *v, int bf16, i
                                        int64_t v_stride, const void *weight, float eps,
                                        const mx_rotary_t &rotary, const mx_kv_cache_t &cache,
                                        const mx_kv_batch_t &batch, hipStream_t st);
-// The same scratch as mxi_launch_kv_attention's.
+size_t mxi_kv_attention_tree_workspace(int64_t tokens, int batch, int q_heads, int heads, int dim,
+                                       int64_t max_length);
 hipError_t mxi_launch_kv_attention_tree(const void *q, int64_t q_stride, int q_heads,
                                         const mx_kv_cache_t &cache, const mx_kv_batch_t &batch,
                                         const uint32_t *mask, int words, int64_t max_length,

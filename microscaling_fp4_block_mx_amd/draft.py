@@ -105,6 +105,11 @@ def mx_kv_append_rotary(k, v, dtype, k_stride, v_stride, k_weight, eps, rotary, 
                                               cache, batch, stream)
 
 
+def mx_kv_attention_tree_workspace_size(tokens, batch, q_heads, heads, dim, max_length) -> int:
+    return load_library().mx_kv_attention_tree_workspace_size(tokens, batch, q_heads, heads, dim,
+                                                              max_length)
+
+
 def mx_kv_attention_tree(q, q_stride, q_heads, cache, batch, mask, words, max_length, scale, out,
                          workspace, workspace_bytes, stream) -> int:
     return load_library().mx_kv_attention_tree(q, q_stride, q_heads, cache, batch, mask, words,
@@ -138,6 +143,7 @@ def declare(lib) -> None:
         "mx_kv_attention_tree": [p, i64, i32, p, p, p, i32, i64, f32, p, p, size, p],
         "mx_verify_drafts": [p, p, i32, p, p, p, p, i64, i32, i64, i32, p, p, p, p, size, p],
         "mx_kv_keep": [p, p, p, i32, p, p],
+        "mx_kv_attention_tree_workspace_size": [i64, i32, i32, i32, i32, i64],
         "mx_norm_rotate_backward_workspace_size": [i64, i32],
         "mx_verify_drafts_workspace_size": [i64, i32, i64],
     }
@@ -311,7 +317,7 @@ def kv_attention_tree(q: torch.Tensor, cache: KVCache, table: torch.Tensor, cu: 
     room = width * page
     max_length = room if max_length <= 0 else min(max_length, room)
     lib = load_library()
-    size = lib.mx_kv_attention_workspace_size(tokens, batch, q_heads, heads, dim, max_length)
+    size = lib.mx_kv_attention_tree_workspace_size(tokens, batch, q_heads, heads, dim, max_length)
     ws = _scratch(size, dev)
     _call(dev, lib.mx_kv_attention_tree, q.data_ptr(), stride, q_heads, c, b, mask.data_ptr(), words,
           max_length, 1.0 / math.sqrt(dim) if scale is None else scale, out.data_ptr(), _ptr(ws), size)

@@ -30,7 +30,7 @@ hipError_t mxi_launch_norm_rotate_backward(const mx_heads_grad_t &, const mx_hea
 hipError_t mxi_launch_kv_append_rotary(const void *, const void *, int, int64_t, int64_t, const void *,
                                        float, const mx_rotary_t &, const mx_kv_cache_t &,
                                        const mx_kv_batch_t &, hipStream_t) { return hit(); }
-size_t mxi_kv_attention_workspace(int64_t tokens, int, int, int, int, int64_t max_length) {
+size_t mxi_kv_attention_tree_workspace(int64_t tokens, int, int, int, int, int64_t max_length) {
   return max_length > 512 ? (size_t)tokens * 64 : 0;
 }
 hipError_t mxi_launch_kv_attention_tree(const void *, int64_t, int, const mx_kv_cache_t &,

@@ -132,7 +132,16 @@ def test_a_causal_mask_is_causal_attention(new):
     cu = i32([0, new, 2 * new, 3 * new]).cuda()
     mask = torch.cat([ref.words_of(m, 3) for m in masks([new] * 3, "chain", 0)]).cuda()
     args = (q, w.gpu, w.table.cuda(), cu, i32(lengths).cuda())
-    assert torch.equal(mx.kv_attention_tree(*args, mask), mx.kv_attention(*args))
+    a, b = mx.kv_attention_tree(*args, mask).cpu().double(), mx.kv_attention(*args).cpu().double()
+    if new == 3:
+        assert torch.equal(a, b)  # one kernel, one split of the keys
+        return
+    # the keys are divided otherwise: scores are the same bits, a weight is rounded to bf16 against another
+    # maximum (2^-9 of itself, in the sums above and below the line, on both sides: 4 x 2^-9 of sum p |v|), the
+    # result once on each side (half a step, 2^-8 of it, each); sums in 32 bits lie below 2^-14 of sum p |v|
+    _, mag, _ = ref.attention_tree(q.cpu(), w.cpu, w.table, cu.cpu(), i32(lengths),
+                                   masks([new] * 3, "chain", 0), 1 / math.sqrt(128))
+    assert bool(((a - b).abs() <= 2.0 ** -7 * b.abs() + (2.0 ** -7 + 2.0 ** -13) * mag).all())
 
 
 @pytest.mark.parametrize("new", [5, 8, 70])
