@@ -1365,10 +1365,10 @@ __device__ __forceinline__ int swz_k(int r) {
 
 // One block of rows and its tiles t0 .. t1 - 1; `write(x, row, state)` takes what
 // comes of the wave's 16 rows x, for each row that is one.
-template <int D, bool TREE, typename F>
+template <int D, bool TREE, int RT, typename F>
 __device__ __forceinline__ void attend_tiles(const AttnArgs &a, const Block &b, int head, int t0, int t1,
                                              uint8_t (&ks)[256 * D], uint8_t (&vs)[256 * D], F write) {
-  constexpr int DT = D / 16, RT = 2, S = 128 * D;
+  constexpr int DT = D / 16, S = 128 * D;
   constexpr int KL = S / 4096, VL = KL;  // direct loads per thread and tile
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
@@ -1378,7 +1378,7 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs &a, const Block &b, 
   int seen[RT];
 #pragma unroll
   for (int x = 0; x < RT; x++) {
-    const int row = min(32 * wave + 16 * x + l16, rows - 1);
+    const int row = min(16 * RT * wave + 16 * x + l16, rows - 1);
     const int tok = row / a.group;
     seen[x] = TREE ? tok : b.seen0 + tok;
     q[x] = load_query<D>(a.q + (int64_t)(b.tok0 + tok) * a.q_stride +
@@ -1535,7 +1535,7 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs &a, const Block &b, 
   }
 #pragma unroll
   for (int x = 0; x < RT; x++) {
-    const int row = 32 * wave + 16 * x + l16;
+    const int row = 16 * RT * wave + 16 * x + l16;
     if (row < rows) write(row, r[x]);
   }
 }
@@ -1581,7 +1581,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
   const int split = blockIdx.y, t0 = split * a.chunk;
   const int t1 = split + 1 == a.splits ? tiles : min(tiles, t0 + a.chunk);
   if (split > 0 && t0 >= tiles) return;  // the sum takes only splits that exist
-  attend_tiles<D, TREE>(a, b, head, t0, t1, ks, vs, [&](int row, const Rows<D> &r) {
+  attend_tiles<D, TREE, 2>(a, b, head, t0, t1, ks, vs, [&](int row, const Rows<D> &r) {
     if (a.splits > 1) {
       const int64_t tok = b.tok0 + row / a.group, qh = (int64_t)head * a.group + row % a.group;
       write_part<D>(a.part + ((tok * a.q_heads + qh) * a.splits + split) * (D + 4), r);
@@ -1597,9 +1597,12 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
 // places g per .. (g + 1) per - 1, which may be the end of one block, some whole
 // ones and the beginning of another. What a block got from several workgroups
 // is left in their room (the first and the last block of each: two rooms) and
-// joined. (Splits of one length for all sequences left the units that ended first
-// idle: 16 sequences of up to 24 tokens in 8,000 to 32,000, 41 % of the time.)
-constexpr int kLeastTiles = 8;    // of a workgroup's share
+// joined. 16 sequences of up to 24 tokens in 8,000 to 32,000, 32 query heads on 8 of
+// 128 dims: 182 us and 8 for the join (splits of one length for all sequences, which
+// left units idle for 41 % of the time, 241 and 8). Bound by issue, as above: matrix
+// cores 47 % and vector arithmetic 52 % of a unit's cycles, for 128 rows a block of
+// which 72 are in use.
+constexpr int kLeastTiles = 4;    // of a workgroup's share
 constexpr int kSharers = 64;      // sequences: one a lane
 struct Stretch {
   int c0, n, len;     // the lane's sequence: first token, tokens, length
@@ -1632,31 +1635,47 @@ struct Stretch {
   }
 };
 
-template <int D>
+// RT: 16-row parts of a wave, a block being 64 RT rows.
+template <int D, int RT>
 __global__ __launch_bounds__(256, 2) void k_attn_share(const AttnArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t ks[256 * D], vs[256 * D];
+  __shared__ int of[5][kSharers];  // what a sequence's lane knows: not held in registers meanwhile
   auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
   const int head = blockIdx.x % a.c.heads, g = blockIdx.x / a.c.heads;
-  const Stretch s(a);
-  const int64_t first = g * s.per;
-  // (a block's tiles are counted in 32 bits, and so is what a share takes at a time)
-  if (first >= s.total) return;
-  int64_t left = min(s.total - first, s.per);
-  int i = uniform(__builtin_ctzll(__ballot(s.end > first)));
-  const int64_t into = first - s.begin_of(i);
-  int block = uniform((int)(into / Stretch::of(s.tiles, i))), t0 = uniform((int)(into % Stretch::of(s.tiles, i)));
+  int64_t left;
+  int i, block, t0;
+  {
+    const Stretch s(a);
+    if (threadIdx.x < kSharers) {
+      of[0][threadIdx.x] = s.c0;
+      of[1][threadIdx.x] = s.n;
+      of[2][threadIdx.x] = s.len;
+      of[3][threadIdx.x] = s.blocks;
+      of[4][threadIdx.x] = s.tiles;
+    }
+    const int64_t first = g * s.per;
+    left = min(s.total - first, s.per);
+    i = __builtin_ctzll(__ballot(s.end > first) | 1ull << 63);
+    const int64_t into = first - s.begin_of(i);
+    block = (int)(into / Stretch::of(s.tiles, i));
+    t0 = (int)(into % Stretch::of(s.tiles, i));
+  }
+  __syncthreads();
+  i = uniform(i);
+  block = uniform(block);
+  t0 = uniform(t0);
   bool later = false;
-  while (left > 0) {
-    if (block >= Stretch::of(s.blocks, i)) {  // on to the next sequence
-      if (++i >= kSharers) break;
+  while (left > 0 && i < kSharers) {
+    if (block >= uniform(of[3][i])) {  // on to the next sequence
+      i++;
       block = 0;
       continue;
     }
-    const int tiles = Stretch::of(s.tiles, i), n = Stretch::of(s.n, i);
+    const int n = uniform(of[1][i]), tiles = uniform(of[4][i]);
     const int t1 = uniform((int)min((int64_t)tiles, t0 + left));
     Block b;
-    b.len = Stretch::of(s.len, i);
-    b.tok0 = Stretch::of(s.c0, i) + block * a.block_tokens;
+    b.len = uniform(of[2][i]);
+    b.tok0 = uniform(of[0][i]) + block * a.block_tokens;
     b.count = min(a.block_tokens, n - block * a.block_tokens);
     b.seen0 = b.len - n;
     b.fresh = n;
@@ -1664,7 +1683,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_share(const AttnArgs a) {
     b.last_page = max(0, (b.len - 1) >> a.shift);
     const bool whole = t0 == 0 && t1 == tiles;
     float *room_of = a.part + ((int64_t)blockIdx.x * 2 + later) * 128 * (D + 4);
-    attend_tiles<D, true>(a, b, head, t0, min(t1, (b.len + 127) >> 7), ks, vs, [&](int row, const Rows<D> &r) {
+    attend_tiles<D, true, RT>(a, b, head, t0, min(t1, (b.len + 127) >> 7), ks, vs, [&](int row, const Rows<D> &r) {
       if (whole) write_row<D>(a, b, head, row, r);
       else write_part<D>(room_of + row * (D + 4), r);
     });
@@ -1793,13 +1812,35 @@ static AttnPlan attn_plan(int64_t tokens, int batch, int q_heads, int heads, int
   return p;
 }
 
-// Workgroups of a head that share a tree's tiles, 0 where they do not: few rows,
-// whose kernel splits the keys itself, more sequences than a wave has lanes, and
-// blocks enough to fill the card over and over. Two workgroups a compute unit.
-static int tree_share(const AttnPlan &p, int batch, int heads, int64_t max_length) {
-  if (p.few || batch > kSharers || p.units * heads > 4096) return 0;
-  const int64_t tiles = p.units * std::max<int64_t>(1, (max_length + 127) / 128);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(512 / heads, (tiles + kLeastTiles - 1) / kLeastTiles));
+// Workgroups of a head that share a tree's tiles, and 16-row parts of their waves;
+// none where the kernels of causal attention take it: up to 16 rows, more sequences
+// than a wave has lanes, and blocks enough to fill the card over and over. 17 to 32
+// rows of 128 dims share where sequences may be longer than 1,024 (16 sequences of up
+// to 12 tokens in 32,000: 132 us, 204 with a wave to 32 rows; 48 of 8 in 3,000 56 and
+// 79; 16 of 8 in 700 22 and 15), of 64 dims they do not (48 of 8 in 6,000: 65 and
+// 58). Up to 64 rows go in blocks of 64 (16 sequences of up to 16 tokens in 32,000, 4
+// query heads to a kv head: 133 us). Two workgroups a compute unit, of four tiles at
+// least (eight: 16 of 48 tokens in 2,000 46 us, four 38).
+struct TreePlan {
+  int share, rt, block_tokens;
+};
+static TreePlan tree_plan(const AttnPlan &p, int64_t tokens, int batch, int q_heads, int heads, int dim,
+                          int64_t max_length) {
+  if (p.few && (p.rt == 1 || dim == 64 || max_length <= 1024)) return TreePlan{};
+  if (batch > kSharers || p.units * heads > 4096) return TreePlan{};
+  const int group = q_heads / heads;
+  const int rt = (tokens + batch - 1) / batch * group <= 64 && group <= 64 ? 1 : 2;
+  const int block_tokens = 64 * rt / group;
+  const int64_t tiles = (tokens / block_tokens + batch) * std::max<int64_t>(1, (max_length + 127) / 128);
+  const int64_t share = std::min<int64_t>(512 / heads, (tiles + kLeastTiles - 1) / kLeastTiles);
+  return TreePlan{(int)std::max<int64_t>(1, share), rt, block_tokens};
+}
+template <int D>
+static void launch_share(const AttnArgs &a, int rt, hipStream_t st) {
+  if (rt == 1) k_attn_share<D, 1><<<a.splits * a.c.heads, 256, 0, st>>>(a);
+  else k_attn_share<D, 2><<<a.splits * a.c.heads, 256, 0, st>>>(a);
+  const int rows = 1024 / D;  // of a workgroup that joins
+  k_attn_share_join<D><<<dim3((uint32_t)a.b.tokens, (uint32_t)((a.q_heads + rows - 1) / rows)), 256, 0, st>>>(a);
 }
 
 }  // namespace mxl
@@ -1864,7 +1905,7 @@ hipError_t mxi_launch_kv_keep(const mx_kv_cache_t &cache, const mx_kv_batch_t &b
 size_t mxi_kv_attention_tree_workspace(int64_t tokens, int batch, int q_heads, int heads, int dim,
                                        int64_t max_length) {
   const AttnPlan p = attn_plan(tokens, batch, q_heads, heads, max_length);
-  if (const int64_t share = tree_share(p, batch, heads, max_length))
+  if (const int64_t share = tree_plan(p, tokens, batch, q_heads, heads, dim, max_length).share)
     return (size_t)(share * heads * 2 * 128) * (dim + 4) * sizeof(float);
   return mxi_kv_attention_workspace(tokens, batch, q_heads, heads, dim, max_length);
 }
@@ -1887,18 +1928,13 @@ static hipError_t launch_attention(const void *q, int64_t q_stride, int q_heads,
                       reinterpret_cast<uint16_t *>(out), reinterpret_cast<float *>(workspace),
                       tree, words};
   if constexpr (TREE) {
-    if (const int share = tree_share(p, batch.batch, cache.heads, max_length)) {
+    const TreePlan plan = tree_plan(p, batch.tokens, batch.batch, q_heads, cache.heads, cache.dim, max_length);
+    if (plan.share) {
       AttnArgs t = a;
-      t.splits = share;
-      const int rows = 1024 / cache.dim;  // of a workgroup that joins
-      const dim3 jgrid((uint32_t)batch.tokens, (uint32_t)((q_heads + rows - 1) / rows));
-      if (cache.dim == 64) {
-        k_attn_share<64><<<share * cache.heads, 256, 0, st>>>(t);
-        k_attn_share_join<64><<<jgrid, 256, 0, st>>>(t);
-      } else {
-        k_attn_share<128><<<share * cache.heads, 256, 0, st>>>(t);
-        k_attn_share_join<128><<<jgrid, 256, 0, st>>>(t);
-      }
+      t.splits = plan.share;
+      t.block_tokens = plan.block_tokens;
+      if (cache.dim == 64) launch_share<64>(t, plan.rt, st);
+      else launch_share<128>(t, plan.rt, st);
       return hipGetLastError();
     }
   }
