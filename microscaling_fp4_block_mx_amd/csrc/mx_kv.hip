@@ -1593,20 +1593,22 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
 
 // Trees whose rows fill no card in blocks: every workgroup gets an even share of
 // all the tiles there are. Blocks of rows lie end to end, each as long as it has
-// tiles (at least one), sequence after sequence; workgroup g of a head takes
+// tiles and some for its beginning, sequence after sequence; workgroup g of a head takes
 // places g per .. (g + 1) per - 1, which may be the end of one block, some whole
 // ones and the beginning of another. What a block got from several workgroups
 // is left in their room (the first and the last block of each: two rooms) and
 // joined. 16 sequences of up to 24 tokens in 8,000 to 32,000, 32 query heads on 8 of
-// 128 dims: 182 us and 8 for the join (splits of one length for all sequences, which
-// left units idle for 41 % of the time, 241 and 8). Bound by issue, as above: matrix
-// cores 47 % and vector arithmetic 52 % of a unit's cycles, for 128 rows a block of
-// which 72 are in use.
+// 128 dims: 161 to 195 us and 8 for the join in blocks of 64 rows, 169 to 182 in
+// blocks of 128 (splits of one length for all sequences, which left units idle for 41 %
+// of the time, 241 and 8). Bound by issue, as above: matrix cores 47 % and vector
+// arithmetic 52 % of a unit's cycles.
 constexpr int kLeastTiles = 4;    // of a workgroup's share
 constexpr int kSharers = 64;      // sequences: one a lane
+constexpr int kBegin = 2;         // what beginning a block counts for, in tiles (4 trees of up to
+                                  // 63 in 8,000: 36 us with nothing, 33 with one, 32 with two)
 struct Stretch {
   int c0, n, len;     // the lane's sequence: first token, tokens, length
-  int blocks, tiles;  // its blocks of rows, places of each
+  int blocks, tiles;  // its blocks of rows, places of each: kBegin, then its tiles
   int64_t end;        // of its places
   int64_t total, per; // places there are, places of a workgroup
   __device__ __forceinline__ explicit Stretch(const AttnArgs &a) {
@@ -1619,7 +1621,7 @@ struct Stretch {
       len = (int)min((int64_t)max(a.b.lengths[lane], 0), room);
       if (n > 0 && c0 >= 0 && (int64_t)c0 + n <= a.b.tokens) blocks = (n + a.block_tokens - 1) / a.block_tokens;
     }
-    tiles = max(1, (len + 127) >> 7);
+    tiles = ((len + 127) >> 7) + kBegin;
     end = (int64_t)blocks * tiles;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -1683,7 +1685,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_share(const AttnArgs a) {
     b.last_page = max(0, (b.len - 1) >> a.shift);
     const bool whole = t0 == 0 && t1 == tiles;
     float *room_of = a.part + ((int64_t)blockIdx.x * 2 + later) * 128 * (D + 4);
-    attend_tiles<D, true, RT>(a, b, head, t0, min(t1, (b.len + 127) >> 7), ks, vs, [&](int row, const Rows<D> &r) {
+    attend_tiles<D, true, RT>(a, b, head, max(0, t0 - kBegin), max(0, t1 - kBegin), ks, vs, [&](int row, const Rows<D> &r) {
       if (whole) write_row<D>(a, b, head, row, r);
       else write_part<D>(room_of + row * (D + 4), r);
     });

@@ -10,11 +10,10 @@
 // are p, and t does not depend on the other children's tokens.
 //
 // Sums of a row run over up to hundreds of thousands of numbers and decide at
-// their borders: 64 bits. Three launches. The first finds each node's first child
-// and whether it is taken, and with that which nodes the walk can reach and has to
-// draw at (of a chain with a draft one): only their rows are read. The second sums
-// those rows in chunks. The third finds each one's chunk, reads it again and draws;
-// then it walks down.
+// their borders: 64 bits. Two launches. The first finds each node's first child and
+// whether it is taken, and with that which nodes the walk can reach and has to draw at
+// (of a chain with a draft one): only their rows are read, and summed in chunks. The
+// second finds each one's chunk, reads it again and draws; then it walks down.
 #include <algorithm>
 
 #include "mx_layer.h"
@@ -54,76 +53,66 @@ __device__ __forceinline__ Sequence sequence_of(const VerifyArgs &a, int i) {
   return Sequence{c0, (int)(n < kNodes ? n : kNodes)};
 }
 
-// One wave a sequence.
+// What a sequence's walk can meet, found by the whole workgroup.
+struct Plan {
+  int up[kNodes], kid[kNodes], id[kNodes], depth[kNodes], draws[kNodes];
+  int many;
+};
 template <bool BF16>
-__global__ __launch_bounds__(64) void k_verify_plan(const VerifyArgs a) {
-  __shared__ int up[kNodes], kid[kNodes], id[kNodes];
-  const int i = blockIdx.x, lane = threadIdx.x;
-  const Sequence s = sequence_of(a, i);
-  for (int j = lane; j < s.nodes; j += 64) {
-    up[j] = a.parents[s.first + j];
-    id[j] = a.ids[s.first + j];
-    kid[j] = kNodes;
+__device__ __forceinline__ void make_plan(const VerifyArgs &a, const Sequence &s, Plan &p) {
+  const int lane = threadIdx.x & 63;
+  for (int j = threadIdx.x; j < s.nodes; j += blockDim.x) {
+    p.up[j] = a.parents[s.first + j];
+    p.id[j] = a.ids[s.first + j];
+    p.kid[j] = kNodes;
   }
   __syncthreads();
-  // nodes that the root reaches in fewer than `width` steps have a parent from
-  // here on, others none
-  int depth[kNodes / 64];
-#pragma unroll
-  for (int r = 0; r < kNodes / 64; r++) {
-    const int j = lane + 64 * r;
-    depth[r] = -1;
-    if (64 * r >= s.nodes) continue;
-    int x = j < s.nodes ? j : -1, d = 0;
+  // nodes that the root reaches in fewer than `width` steps have a depth
+  for (int j = threadIdx.x; j < s.nodes; j += blockDim.x) {
+    int x = j, d = 0;
     while (x > 0 && d < a.width) {
-      const int p = up[x];
-      x = p >= 0 && p < x ? p : -1;
+      const int up = p.up[x];
+      x = up >= 0 && up < x ? up : -1;
       d++;
     }
-    if (x == 0 && d < a.width) depth[r] = d;
+    p.depth[j] = x == 0 && d < a.width ? d : -1;
   }
   __syncthreads();
-#pragma unroll
-  for (int r = 0; r < kNodes / 64; r++) {
-    const int j = lane + 64 * r;
-    if (j >= s.nodes) continue;
-    if (depth[r] > 0) atomicMin(&kid[up[j]], j);
-    else up[j] = -1;
-  }
+  for (int j = threadIdx.x; j < s.nodes; j += blockDim.x)
+    if (p.depth[j] > 0) atomicMin(&p.kid[p.up[j]], j);
   __syncthreads();
-  for (int j = lane; j < s.nodes; j += 64) {
-    const int k = kid[j];
+  for (int j = threadIdx.x; j < s.nodes; j += blockDim.x) {
+    const int k = p.kid[j];
     int to = k == kNodes ? -1 : k;
     if (a.draft && to >= 0) {
-      const int64_t row = s.first + j, x = id[k];
+      const int64_t row = s.first + j, x = p.id[k];
       if (x >= 0 && x < a.vocab) {
-        const double p = clean(load_one<BF16>(a.target, row * a.vocab + x));
+        const double t = clean(load_one<BF16>(a.target, row * a.vocab + x));
         const double q = clean(load_one<BF16>(a.draft, row * a.vocab + x));
-        if ((double)a.numbers[2 * row] * q < p) to |= kTaken;
+        if ((double)a.numbers[2 * row] * q < t) to |= kTaken;
       }
     }
-    kid[j] = to;
-    a.kid[s.first + j] = to;
+    p.kid[j] = to;
   }
   __syncthreads();
-  int found = 0;
-#pragma unroll
-  for (int r = 0; r < kNodes / 64; r++) {
-    if (64 * r >= s.nodes) break;
-    const int j = lane + 64 * r;
-    // drawn at: reached, unless its first child is taken. With a draft a first
-    // child is reached where it is taken, another where the first one is not.
-    bool draws = depth[r] >= 0 && (kid[j] < 0 || !(kid[j] & kTaken));
-    for (int x = j; draws && x > 0; x = up[x]) {
-      const int k = kid[up[x]];
-      if (a.draft) draws = k == (x | kTaken) || (k != x && !(k & kTaken));
+  if (threadIdx.x < 64) {
+    int found = 0;
+    for (int j0 = 0; j0 < s.nodes; j0 += 64) {
+      const int j = j0 + lane;
+      // drawn at: reached, unless its first child is taken. With a draft a first
+      // child is reached where it is taken, another where the first one is not.
+      bool draws = j < s.nodes && p.depth[j] >= 0 && (p.kid[j] < 0 || !(p.kid[j] & kTaken));
+      for (int x = j; draws && x > 0; x = p.up[x]) {
+        const int k = p.kid[p.up[x]];
+        if (a.draft) draws = k == (x | kTaken) || (k != x && !(k & kTaken));
+      }
+      const uint64_t all = __ballot(draws);
+      if (draws) p.draws[found + __popcll(all & ((1ull << lane) - 1))] = j | (a.draft && p.kid[j] >= 0 ? kResidual : 0);
+      found += __popcll(all);
     }
-    const uint64_t all = __ballot(draws);
-    if (draws)
-      a.draws[s.first + found + __popcll(all & ((1ull << lane) - 1))] = j | (a.draft && kid[j] >= 0 ? kResidual : 0);
-    found += __popcll(all);
+    if (lane == 0) p.many = found;
   }
-  if (lane == 0) a.many[i] = found;
+  __syncthreads();
 }
 
 // A wave's part of a row: step u of lane l holds 16 bytes of neighbouring elements,
@@ -212,17 +201,29 @@ __device__ __forceinline__ double weight_of(u32x4 p, u32x4 q, bool residual, int
   return __builtin_fmax(t - (double)probability<BF16>(q, e), 0.0);
 }
 
-// A wave a chunk; a workgroup's z takes rows z, z + gridDim.z, ... of a sequence.
+// A wave a chunk; a workgroup's z takes rows z, z + gridDim.z, ... of a sequence. Each
+// finds out by itself which those are (a launch of its own for that took 3 to 5.5 us);
+// one of a sequence leaves it for the walk. 64 chains of 8 over 128,000 tokens, fp32:
+// 65 MB.
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_verify_sums(const VerifyArgs a) {
+  __shared__ Plan plan;
   auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
   const int chunk = uniform(blockIdx.x * 4 + (threadIdx.x >> 6)), i = blockIdx.y;
   const Sequence s = sequence_of(a, i);
-  if (chunk >= a.chunks || (int)blockIdx.z >= s.nodes) return;
-  int draws = uniform(a.draws[s.first + blockIdx.z]);  // asked for beside how many there are
-  const int many = uniform(a.many[i]);
+  if ((int)blockIdx.z >= max(s.nodes, 1)) return;
+  make_plan<BF16>(a, s, plan);
+  const int many = uniform(plan.many);
+  if (blockIdx.x == 0 && blockIdx.z == 0) {
+    for (int j = threadIdx.x; j < s.nodes; j += 256) {
+      a.kid[s.first + j] = plan.kid[j];
+      if (j < many) a.draws[s.first + j] = plan.draws[j];
+    }
+    if (threadIdx.x == 0) a.many[i] = many;
+  }
+  if (chunk >= a.chunks) return;
   for (int r = blockIdx.z; r < many; r += gridDim.z) {
-    if (r >= (int)gridDim.z) draws = uniform(a.draws[s.first + r]);
+    const int draws = uniform(plan.draws[r]);
     const int64_t row = s.first + (draws & ~kResidual);
     const bool residual = draws & kResidual;
     const Part<BF16> p = load_part<BF16>(a.target, a, row, chunk);
@@ -417,15 +418,15 @@ hipError_t mxi_launch_verify(const void *target, const void *draft, int bf16, co
   }
   const int groups = (a.chunks + 3) / 4;
   const int64_t mean = std::max<int64_t>(1, tokens / batch);
-  const int rows = (int)std::min<int64_t>(mean, std::max<int64_t>(1, 4096 / ((int64_t)groups * batch)));
+  // workgroups for four a compute unit: each makes the plan (64 chains of 8 over 128,000
+  // tokens 21.8 us, with four times as many 27.6)
+  const int rows = (int)std::min<int64_t>(mean, std::max<int64_t>(1, 1024 / ((int64_t)groups * batch)));
   const dim3 grid((uint32_t)groups, (uint32_t)batch, (uint32_t)rows);
   const int threads = 64 * (int)std::min<int64_t>(16, mean);
   if (bf16) {
-    k_verify_plan<true><<<batch, 64, 0, st>>>(a);
     k_verify_sums<true><<<grid, 256, 0, st>>>(a);
     k_verify_walk<true><<<batch, threads, 0, st>>>(a);
   } else {
-    k_verify_plan<false><<<batch, 64, 0, st>>>(a);
     k_verify_sums<false><<<grid, 256, 0, st>>>(a);
     k_verify_walk<false><<<batch, threads, 0, st>>>(a);
   }

@@ -171,6 +171,21 @@ def test_pages_outside_the_cache_and_offsets():
     assert all(torch.equal(a, b) for a, b in zip(before, w.gpu))
 
 
+@pytest.mark.parametrize("paired", [False, True])
+@pytest.mark.parametrize("dim,page", [(64, 256), (128, 128), (128, 256)])
+def test_scales_that_grow(dim, page, paired):
+    """Kept codes of both kinds move to new bytes, a step and many, under new tokens of every slot."""
+    totals = [page + 40, 3 * page, 37]
+    w = Turned(totals, 2, dim, page, page)
+    w.turn(dim, paired, False, max(totals), torch.bfloat16)
+    held = [0, 0, 0]
+    for t, step in enumerate((3, 16, 17, 1, 40, 33)):
+        new = [min(step, n - h) for n, h in zip(totals, held)]
+        w.append(new, held, by=2.0 ** (3 * t))
+        w.same()
+        held = [h + n for h, n in zip(held, new)]
+
+
 def test_streams_and_graphs():
     """A captured append, replayed for other tokens, over a cache set back in between."""
     w = Turned([40, 90], 2, 128, 32, 10)

@@ -162,6 +162,39 @@ def test_what_is_not_seen_does_not_reach(new):
     check_attention(got, want, mag, reach)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("batch,new,group,longest", [
+    (5, 7, 4, 2500),     # up to 32 rows, long contexts
+    (9, 16, 4, 700),     # blocks of 64 rows, some sequences with two
+    (3, 40, 8, 1100),    # several blocks of 128 rows a sequence
+    (2, 3, 65, 400),     # more than 64 query heads to a kv head
+    (64, 12, 4, 140),    # as many sequences as share their tiles
+    (70, 11, 4, 140),    # more
+    (33, 9, 128, 90),    # a token a block
+])
+def test_divisions_of_the_work(batch, new, group, longest, dim):
+    """Ragged batches with idle slots and empty sequences, through every way of dividing rows and keys."""
+    g = torch.Generator().manual_seed(batch)
+    counts = [int(torch.randint(1, new + 1, (1,), generator=g)) for _ in range(batch)]
+    counts[0], counts[batch // 2] = new, 0
+    lengths = [n + int(torch.randint(0, longest - n, (1,), generator=g)) for n in counts]
+    lengths[0] = longest
+    held = list(lengths)
+    lengths[-1] = 0 if batch > 2 else lengths[-1]  # rows that see nothing
+    w = World(held, 1, dim, 64, batch)
+    w.append(held, [0] * batch)
+    check_attention(*run(w, counts, lengths, group, masks(counts, "tree", 3)))
+
+
+@pytest.mark.parametrize("heads", [1, 5, 16])
+def test_heads(heads):
+    """Workgroups by kv heads, shares of one and of many tiles."""
+    lengths, new = [3000, 40, 900, 33], [20, 20, 1, 33]
+    w = World(lengths, heads, 128, 32, heads)
+    w.append(lengths, [0] * 4)
+    check_attention(*run(w, new, lengths, 4, masks(new, "tree", 5)))
+
+
 def test_tree_mask():
     parents = [[-1, 0, 0, 1, 1, 2, 5], [-1], [], [-1] + list(range(39))]
     mask, depth = mx.tree_mask(parents, device="cpu")

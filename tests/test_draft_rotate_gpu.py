@@ -218,6 +218,42 @@ def test_many_tokens():
     near(k, ref.heads(qkv[:, 2:3], w[1], EPS, (table, pos, False)), torch.float32, 4.0)
 
 
+def test_rows_past_32_bits():
+    """More than 2^31 elements, forward in place and backward, the last tokens against 64 bits."""
+    tokens, heads, dim = 131100, 128, 128
+    assert tokens * heads * dim > 2 ** 31
+    x = torch.empty(tokens, heads, dim, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for at in range(0, tokens, 8192):
+        x[at:at + 8192].normal_(generator=g)
+    w = (torch.rand(dim, generator=torch.Generator().manual_seed(2)) + 0.5).bfloat16()
+    pos = (torch.arange(tokens, dtype=torch.int32) % 50)
+    table = ref.table_of(50, 128)
+    rotary = mx.Rotary(table.cuda(), pos.cuda())
+    some = [0, 65535, tokens - 9, tokens - 1]
+    kept = x[some].cpu()
+    dx, _, dw, _ = mx.norm_rotate_backward(x, x, None, None, w.cuda(), None, rotary)
+    want = ref.heads_backward(kept, kept, w, EPS, (table, pos[some], False))[0]
+    near(dx[some], want, torch.bfloat16, want.abs().amax())
+    assert bool(torch.isfinite(dw).all())
+    del dx
+    mx.norm_rotate(x, None, w.cuda(), None, rotary, EPS, out_q=x)
+    near(x[some], ref.heads(kept, w, EPS, (table, pos[some], False)), torch.bfloat16, 8.0)
+
+
+def test_tables_past_32_bits():
+    """A table of more than 2^31 bytes, positions at its end."""
+    length = (1 << 23) + 5
+    table = torch.zeros(length, 128, device="cuda")
+    table[:, :64] = 1.0
+    last = ref.table_of(4, 128)
+    table[-4:] = last.cuda()
+    x = torch.randn(4, 2, 128, generator=torch.Generator().manual_seed(3))
+    pos = torch.arange(length - 4, length, dtype=torch.int32)
+    y, _ = mx.norm_rotate(x.cuda(), rotary=mx.Rotary(table, pos.cuda()))
+    near(y, ref.heads(x, None, 0.0, (last, torch.arange(4), False)), torch.float32, 4.0)
+
+
 def test_streams_and_graphs():
     """Replays of a captured pass, forward and backward, with eager work between them."""
     qkv, w, pos = inputs(70, 4, 2, 128, torch.bfloat16, 12)
