@@ -63,16 +63,17 @@ struct AppendArgs {
 };
 
 // Which sequence a unit of work belongs to: sequence i owns units from
-// cu[i] / per + extra i on, which leaves it at least n / per + extra. The
+// units(cu[i]) + extra i on, units being a quotient by some number `per`, which
+// leaves it at least n / per + extra. The
 // wave's lanes look at up to 64 sequences at once (one trip to memory for up
 // to 64 sequences, two up to 4096).
-__device__ __forceinline__ int find_sequence(const int32_t *cu, int batch, int per, int extra,
-                                             int unit) {
+template <typename F>
+__device__ __forceinline__ int find_sequence(const int32_t *cu, int batch, F units, int extra, int unit) {
   const int lane = threadIdx.x & 63;
   int lo = 0, n = batch;
   while (n > 1) {
     const int step = (n + 63) >> 6, at = lo + lane * step;
-    const bool below = lane * step < n && cu[at] / per + extra * at <= unit;
+    const bool below = lane * step < n && units(cu[at]) + extra * at <= unit;
     // the lanes that hold are the first ones; sequence lo always does
     const int skip = max((int)__popcll(__ballot(below)) - 1, 0) * step;
     lo += skip;
@@ -126,9 +127,10 @@ __device__ __forceinline__ bool find_page(const AppendArgs &a, AppendPage &p) {
   if (block >= a.blocks) return false;
   const int unit = block / a.c.heads, P = a.c.page;
   p.head = block % a.c.heads;
-  const int i = find_sequence(a.b.cu, a.b.batch, P, 2, unit);
+  auto pages = [&](int tokens) { return (tokens + (tokens >> 31 & (P - 1))) >> a.shift; };  // tokens / P
+  const int i = find_sequence(a.b.cu, a.b.batch, pages, 2, unit);
   const int c0 = a.b.cu[i], n = a.b.cu[i + 1] - c0, held = a.b.lengths[i];
-  const int j = (held >> a.shift) + (unit - (c0 / P + 2 * i));  // page of the sequence
+  const int j = (held >> a.shift) + (unit - (pages(c0) + 2 * i));  // page of the sequence
   // (a unit before the first sequence's has pages before the sequence's first)
   if (n <= 0 || held < 0 || j < held >> a.shift || j >= a.b.width || ((int64_t)j << a.shift) >= (int64_t)held + n)
     return false;
@@ -234,8 +236,10 @@ __device__ __forceinline__ void put_value(uint8_t *vt, int row, const AppendItem
 template <int T>
 __device__ __forceinline__ void write_values(uint8_t *vc, const uint8_t *vt, int row, int kept, int end, int D, int P) {
   const int piece0 = kept >> 4, chunks = ((end + 15) >> 4) - piece0;  // of a row, with new tokens in them
+  const bool all = chunks == P >> 4;  // a power of two
+  const int shift = 31 - __builtin_clz(P >> 4);
   for (int it = threadIdx.x; it < D * chunks; it += T) {
-    const int d = it / chunks, s = (piece0 + it % chunks) * 16;
+    const int d = all ? it >> shift : it / chunks, s = (piece0 + it - d * chunks) * 16;
     const int lo = max(kept, s), hi = min(end, s + 16);
     uint8_t *dst = vc + (int64_t)d * P;
     if (lo == s && hi == s + 16) {
@@ -854,7 +858,7 @@ template <bool TREE>
 __device__ __forceinline__ bool find_block(const AttnArgs &a, int unit, Block &b) {
   // everything here is the same for the whole workgroup: kept in scalar registers
   auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
-  const int i = uniform(find_sequence(a.b.cu, a.b.batch, a.block_tokens, 1, unit));
+  const int i = uniform(find_sequence(a.b.cu, a.b.batch, [&](int x) { return x / a.block_tokens; }, 1, unit));
   const int c0 = uniform(a.b.cu[i]), n = uniform(a.b.cu[i + 1]) - c0;
   const int at = (unit - (c0 / a.block_tokens + i)) * a.block_tokens;
   if (at >= n || at < 0 || c0 < 0 || (int64_t)c0 + n > a.b.tokens) return false;
@@ -1244,7 +1248,7 @@ __global__ __launch_bounds__(256, D == 128 && RT == 2 ? 1 : 2) void k_attn_rows(
 
 // How many splits of a token's block the first kernel wrote, as it had it.
 __device__ __forceinline__ int splits_of(const AttnArgs &a, int tok) {
-  const int i = find_sequence(a.b.cu, a.b.batch, 1, 0, tok);
+  const int i = find_sequence(a.b.cu, a.b.batch, [](int x) { return x; }, 0, tok);
   const int c0 = a.b.cu[i], n = a.b.cu[i + 1] - c0;
   const int64_t room = (int64_t)a.b.width << a.shift;
   const int len = (int)min((int64_t)max(a.b.lengths[i], 0), room);
