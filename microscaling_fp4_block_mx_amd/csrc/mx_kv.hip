@@ -122,11 +122,21 @@ struct AppendPage {
   int64_t at;           // of the page and head in the scales
   __device__ __forceinline__ int64_t token(int slot) const { return min(max(src0 + slot, (int64_t)0), most); }
 };
+// TOGETHER: the heads of a page run on one of the eight XCDs, which are dealt
+// workgroups in turn (its cache then has what they share).
+template <bool TOGETHER>
 __device__ __forceinline__ bool find_page(const AppendArgs &a, AppendPage &p) {
   const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x;
   if (block >= a.blocks) return false;
-  const int unit = block / a.c.heads, P = a.c.page;
-  p.head = block % a.c.heads;
+  const int P = a.c.page;
+  int unit;
+  if constexpr (TOGETHER) {
+    unit = (block >> 3) / a.c.heads * 8 + (block & 7);
+    p.head = (block >> 3) % a.c.heads;
+  } else {
+    unit = block / a.c.heads;
+    p.head = block % a.c.heads;
+  }
   auto pages = [&](int tokens) { return (tokens + (tokens >> 31 & (P - 1))) >> a.shift; };  // tokens / P
   const int i = find_sequence(a.b.cu, a.b.batch, pages, 2, unit);
   const int c0 = a.b.cu[i], n = a.b.cu[i + 1] - c0, held = a.b.lengths[i];
@@ -263,7 +273,7 @@ __global__ __launch_bounds__(T) void k_kv_append(const AppendArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t vt[];
   __shared__ uint32_t am[2][T / 64];
   AppendPage p;
-  if (!find_page(a, p)) return;
+  if (!find_page<false>(a, p)) return;
   const int P = a.c.page, D = a.c.dim;
   const AppendItems items(p, D);
   uint32_t was_k = 0, was_v = 0;
@@ -336,7 +346,7 @@ __global__ __launch_bounds__(T, BF16 ? 4 : 1) void k_kv_append_rotary(const Appe
   extern __shared__ __attribute__((aligned(16))) uint8_t vt[];
   __shared__ uint32_t am[2][2][T / 64];
   AppendPage p;
-  if (!find_page(a, p)) return;
+  if (!find_page<(T > 64)>(a, p)) return;
   const int P = a.c.page;
   const AppendItems items(p, D);
   // the same for all threads, and in scalar registers: the branches that they
@@ -1877,7 +1887,8 @@ hipError_t mxi_launch_kv_append(const void *k, const void *v, int bf16, int64_t 
 }
 
 template <bool BF16, bool PAIRED>
-static hipError_t launch_append_rotary(const AppendArgs &a, hipStream_t st) {
+static hipError_t launch_append_rotary(AppendArgs a, hipStream_t st) {
+  if (!few_tokens(a)) a.blocks = (a.blocks / a.c.heads + 7) / 8 * 8 * a.c.heads;  // whole rounds of the XCDs
   const Spread xy = spread(a.blocks);
   const dim3 grid(xy.first, xy.second);
   const size_t lds = (size_t)a.c.dim * (a.c.page + 4);
