@@ -671,16 +671,30 @@ __device__ __forceinline__ void split4(const float (&x)[4], float to, float back
 }
 
 template <int D>
-__device__ __forceinline__ Query<D> load_query(const uint16_t *row, int lg) {
+struct RawQuery {
+  u32x4 w[D / 64][2];
+};
+template <int D>
+__device__ __forceinline__ RawQuery<D> load_raw_query(const uint16_t *row, int lg) {
+  RawQuery<D> q;
+#pragma unroll
+  for (int h = 0; h < D / 64; h++) {
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(row + 64 * h + 16 * lg);
+    q.w[h][0] = p[0];
+    q.w[h][1] = p[1];
+  }
+  return q;
+}
+template <int D>
+__device__ __forceinline__ Query<D> split_query(const RawQuery<D> &raw) {
+  const int lg = (threadIdx.x & 63) >> 4;
   float f[D / 64][16];
   uint32_t m = 0;
 #pragma unroll
   for (int h = 0; h < D / 64; h++) {
-    const u32x4 *p = reinterpret_cast<const u32x4 *>(row + 64 * h + 16 * lg);
-    const u32x4 w[2] = {p[0], p[1]};
 #pragma unroll
     for (int j = 0; j < 16; j++) {
-      const uint32_t x = w[j >> 3][(j >> 1) & 3];
+      const uint32_t x = raw.w[h][j >> 3][(j >> 1) & 3];
       f[h][j] = __uint_as_float((j & 1) ? (x & 0xFFFF0000u) : (x << 16));
       m = max(m, __float_as_uint(f[h][j]) & 0x7FFFFFFFu);
     }
@@ -714,6 +728,10 @@ __device__ __forceinline__ Query<D> load_query(const uint16_t *row, int lg) {
     q.bytes = bad ? 0xFFFFu : byte | (byte - 4u) << 8;
   }
   return q;
+}
+template <int D>
+__device__ __forceinline__ Query<D> load_query(const uint16_t *row, int lg) {
+  return split_query<D>(load_raw_query<D>(row, lg));
 }
 
 // Largest of the four lanes l % 16 + 16 g (a row of scores is spread over them).
@@ -1387,6 +1405,9 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs &a, const Block &b, 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
   const int rows = b.count * a.group;
+  // pages are asked for first, then q, which is split while the first tile is on its way
+  const int first_page = page_of(a, b, t0, lane);
+  RawQuery<D> raw_q[RT];
   Query<D> q[RT];
   Rows<D> r[RT];
   int seen[RT];
@@ -1395,8 +1416,8 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs &a, const Block &b, 
     const int row = min(16 * RT * wave + 16 * x + l16, rows - 1);
     const int tok = row / a.group;
     seen[x] = TREE ? tok : b.seen0 + tok;
-    q[x] = load_query<D>(a.q + (int64_t)(b.tok0 + tok) * a.q_stride +
-                             ((int64_t)head * a.group + row % a.group) * D, lg);
+    raw_q[x] = load_raw_query<D>(a.q + (int64_t)(b.tok0 + tok) * a.q_stride +
+                                 ((int64_t)head * a.group + row % a.group) * D, lg);
     r[x].clear();
   }
   const int64_t PD = (int64_t)a.c.page * D;
@@ -1436,11 +1457,12 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs &a, const Block &b, 
   int mine = 0;        // pages of the next tile
   uint32_t bytes = 0;  // scale bytes of this one
   if (t0 < t1) {
-    const int now = page_of(a, b, t0, lane);
-    bytes = *byte_at(a, now, head, lane);
+    bytes = *byte_at(a, first_page, head, lane);
     mine = page_of(a, b, t0 + 1, lane);
-    load(t0, 0, runs_of(a, now));
+    load(t0, 0, runs_of(a, first_page));
   }
+#pragma unroll
+  for (int x = 0; x < RT; x++) q[x] = split_query<D>(raw_q[x]);
   int flip = S;
   for (int tile = t0; tile < t1; tile++) {
     // this tile's codes, its scale bytes and the next one's pages have
