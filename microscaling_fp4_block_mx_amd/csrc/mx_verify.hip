@@ -354,22 +354,26 @@ __global__ __launch_bounds__(1024) void k_verify_walk(const VerifyArgs a) {
     for (int r = wave; r < many; r += blockDim.x >> 6) {
       if (r != wave) draws = uniform(a.draws[s.first + r]);
       const int j = draws & ~kResidual;
+      if (j >= s.nodes) continue;  // (another sequence's, where cu falls)
       const int64_t t = draw_from<BF16>(a, s.first + r, s.first + j, draws & kResidual);
       if (lane == 0) drawn[j] = (int)t;
     }
   }
   __syncthreads();
   if (wave) return;
+  // (nodes rise and stay inside, also where cu falls and sequences share rows of
+  // the scratch)
   int node = 0, steps = 0, token = -1;
   while (s.nodes) {
     if (lane == 0) path[steps] = node;
     steps++;
-    const int k = kid[node];
-    if (k >= 0 && (k & kTaken)) {
-      node = k & ~kTaken;
+    const int k = kid[node], taken = k & ~kTaken;
+    if (k >= 0 && (k & kTaken) && taken > node && taken < s.nodes && steps < a.width) {
+      node = taken;
       continue;
     }
     token = drawn[node];
+    token = token >= 0 && token < a.vocab ? token : -1;
     int next = -1;
     for (int j0 = node + 1; j0 < s.nodes && token >= 0 && steps < a.width && next < 0; j0 += 64) {
       const int j = j0 + lane;

@@ -136,6 +136,20 @@ def test_tokens_and_parents_out_of_range():
         assert not {4, 7, 9} & set(got[0][0]) and 1 not in got[0][1]
 
 
+@pytest.mark.parametrize("with_draft", [False, True])
+def test_sequences_that_share_rows(with_draft):
+    """Where cu falls, against its description, the sequences that share rows have
+    any result that is one: rising nodes of theirs, a token of the vocabulary."""
+    w = world([700, 24, 3], 50, 21, chain=True, near=0.01)
+    cu = [0, 700, 24, 724, 3, 727]
+    path, count, token = call(w[0], w[1] if with_draft else None, w[2], w[3], i32(cu), w[5], 600)
+    for i, (p, c, t) in enumerate(zip(path, count, token)):
+        n = max(cu[i + 1] - cu[i], 0)
+        assert (c == 0 and t == -1) if n == 0 else (1 <= c <= min(n, 600) and -1 <= t < 50)
+        assert p[c:] == [-1] * (600 - c) and sorted(set(p[:c])) == p[:c]
+        assert n == 0 or (p[0] == 0 and p[c - 1] < n)
+
+
 def test_siblings_with_one_token():
     """Of several children with the drawn token the first is followed."""
     parents, ids = i32([-1, 0, 0, 0, 2, 2]), i32([0, 7, 9, 9, 3, 3])
