@@ -503,7 +503,7 @@ typedef struct {
 /* y = R(weight x / sqrt(sum(x^2) / dim + eps)) for every head of q and, unless
  * it is NULL, of k, R being the rotation (rotary NULL: none). x, weight and y
  * share one dtype; the norm and the rotation are formed in 64 bits and rounded
- * once, so that a finite head may be of any size. dim is 64, 128 or 256. y may
+ * to fp32, then to dtype, so that a finite head may be of any size. dim is 64, 128 or 256. y may
  * equal x, with its stride (in place); other overlaps of an output are
  * MX_ERR_ALIAS. A head of zeros alone with eps = 0 gives NaN. */
 mx_status_t mx_norm_rotate(const mx_heads_t *q, const mx_heads_t *k, mx_dtype_t dtype,
@@ -561,7 +561,7 @@ mx_status_t mx_kv_append_rotary(const void *k, const void *v, mx_dtype_t dtype, 
  * Bits past the sequence's new tokens do not count; new tokens past the row's
  * bits are not seen. A token that sees nothing gives zeros. words is 1 to 65535.
  * workspace: mx_kv_attention_tree_workspace_size(...) bytes, 16-byte aligned, at
- * most 69 MiB where more than 32 rows of query heads read a kv head in the mean.
+ * most 66 MiB where more than 32 rows of query heads read a kv head in the mean.
  * Everything else is mx_kv_attention's, whose results a causal mask's are but for
  * rounding. */
 size_t mx_kv_attention_tree_workspace_size(int64_t tokens, int batch, int q_heads, int heads,

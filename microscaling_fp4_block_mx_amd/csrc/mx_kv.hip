@@ -1852,7 +1852,8 @@ static AttnPlan attn_plan(int64_t tokens, int batch, int q_heads, int heads, int
 
 // Workgroups of a head that share a tree's tiles, and 16-row parts of their waves;
 // none where the kernels of causal attention take it: up to 16 rows, more sequences
-// than a wave has lanes, and blocks enough to fill the card over and over. 17 to 32
+// than a wave has lanes, blocks enough to fill the card over and over, and heads for
+// which one workgroup each would be more than two a compute unit. 17 to 32
 // rows of 128 dims share where sequences may be longer than 1,024 (16 sequences of up
 // to 12 tokens in 32,000: 132 us, 204 with a wave to 32 rows; 48 of 8 in 3,000 56 and
 // 79; 16 of 8 in 700 22 and 15), of 64 dims they do not (48 of 8 in 6,000: 65 and
@@ -1865,7 +1866,7 @@ struct TreePlan {
 static TreePlan tree_plan(const AttnPlan &p, int64_t tokens, int batch, int q_heads, int heads, int dim,
                           int64_t max_length) {
   if (p.few && (p.rt == 1 || dim == 64 || max_length <= 1024)) return TreePlan{};
-  if (batch > kSharers || p.units * heads > 4096) return TreePlan{};
+  if (batch > kSharers || heads > 512 || p.units * heads > 4096) return TreePlan{};
   const int group = q_heads / heads;
   const int rt = (tokens + batch - 1) / batch * group <= 64 && group <= 64 ? 1 : 2;
   const int block_tokens = 64 * rt / group;

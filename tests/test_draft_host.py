@@ -76,6 +76,17 @@ def test_workspace_sizes():
     assert mx.mx_verify_drafts_workspace_size(8, 1, 1 << 20) > mx.mx_verify_drafts_workspace_size(8, 1, 1 << 10)
 
 
+def test_attention_scratch_is_bounded_and_grows_with_the_length():
+    for tokens, batch, q_heads, heads, dim in (
+            (1, 1, 128, 1, 64), (63, 1, 600, 600, 64), (40, 1, 2000, 2000, 128), (33, 1, 4096, 4096, 128),
+            (384, 16, 32, 8, 128), (4096, 64, 64, 8, 128), (4160, 65, 64, 8, 128), (8192, 1, 64, 8, 64)):
+        before = 0
+        for length in (1, 100, 1024, 1025, 5000, 33000, 1 << 20, 1 << 30, 0):  # 0: any
+            size = mx.mx_kv_attention_tree_workspace_size(tokens, batch, q_heads, heads, dim, length)
+            assert before <= size <= 66 << 20
+            before = size
+
+
 def test_helpers_refuse_cpu_tensors():
     x = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
     cache = mx.kv_cache(2, 1, 64, 32, device="cpu")
