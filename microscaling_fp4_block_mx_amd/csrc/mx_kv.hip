@@ -1395,25 +1395,25 @@ __device__ __forceinline__ int swz_k(int r) {
   return (r >> 3) & 3;
 }
 
-// One block of rows and its tiles t0 .. t1 - 1; `write(x, row, state)` takes what
-// comes of the wave's 16 rows x, for each row that is one.
-template <int D, bool TREE, int RT, typename F>
-__device__ __forceinline__ void attend_tiles(const AttnArgs &a, const Block &b, int head, int t0, int t1,
-                                             uint8_t (&ks)[256 * D], uint8_t (&vs)[256 * D], F write) {
+// A wave's R parts of 16 rows, part x from row part_of(x) of the block on.
+template <int D, bool TREE, int R, typename G, typename F>
+__device__ __forceinline__ void attend_parts(const AttnArgs &a, const Block &b, int head, int t0, int t1,
+                                             uint8_t (&ks)[256 * D], uint8_t (&vs)[256 * D], G part_of, F write) {
   constexpr int DT = D / 16, S = 128 * D;
   constexpr int KL = S / 4096, VL = KL;  // direct loads per thread and tile
+  constexpr int N = R ? R : 1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
   const int rows = b.count * a.group;
   // pages are asked for first, then q, which is split while the first tile is on its way
   const int first_page = page_of(a, b, t0, lane);
-  RawQuery<D> raw_q[RT];
-  Query<D> q[RT];
-  Rows<D> r[RT];
-  int seen[RT];
+  RawQuery<D> raw_q[N];
+  Query<D> q[N];
+  Rows<D> r[N];
+  int seen[N];
 #pragma unroll
-  for (int x = 0; x < RT; x++) {
-    const int row = min(16 * RT * wave + 16 * x + l16, rows - 1);
+  for (int x = 0; x < R; x++) {
+    const int row = min(part_of(x) + l16, rows - 1);
     const int tok = row / a.group;
     seen[x] = TREE ? tok : b.seen0 + tok;
     raw_q[x] = load_raw_query<D>(a.q + (int64_t)(b.tok0 + tok) * a.q_stride +
@@ -1462,7 +1462,7 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs &a, const Block &b, 
     load(t0, 0, runs_of(a, first_page));
   }
 #pragma unroll
-  for (int x = 0; x < RT; x++) q[x] = split_query<D>(raw_q[x]);
+  for (int x = 0; x < R; x++) q[x] = split_query<D>(raw_q[x]);
   int flip = S;
   for (int tile = t0; tile < t1; tile++) {
     // this tile's codes, its scale bytes and the next one's pages have
@@ -1493,86 +1493,110 @@ __device__ __forceinline__ void attend_tiles(const AttnArgs &a, const Block &b, 
       mine = page_of(a, b, tile + 2, lane);
       load(tile + 1, (tile + 1 - t0) & 1, id);
     }
-    auto keys = [&](int t) {
-      const int at = (32 * (t >> 1) + 4 * (t & 1)) * D;
-      const u32x4 lo = *reinterpret_cast<const u32x4 *>(kp0 + at);
-      if constexpr (D == 64) return join8(lo, lo);
-      else return join8(lo, *reinterpret_cast<const u32x4 *>(kp1 + at));
-    };
-    // operands are read two tiles ahead
-    f32x4 s[RT][8];
-    i32x8 f[3] = {keys(0), keys(1)};
-    auto score = [&](auto run) {  // the two tiles of a run of 32 tokens
-      constexpr int J = decltype(run)::value;
+    if constexpr (R == 0) {  // the second barrier of the others
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      continue;
+    } else {
+      auto keys = [&](int t) {
+        const int at = (32 * (t >> 1) + 4 * (t & 1)) * D;
+        const u32x4 lo = *reinterpret_cast<const u32x4 *>(kp0 + at);
+        if constexpr (D == 64) return join8(lo, lo);
+        else return join8(lo, *reinterpret_cast<const u32x4 *>(kp1 + at));
+      };
+      // operands are read two tiles ahead
+      f32x4 s[R][8];
+      i32x8 f[3] = {keys(0), keys(1)};
+      auto score = [&](auto run) {  // the two tiles of a run of 32 tokens
+        constexpr int J = decltype(run)::value;
 #pragma unroll
-      for (int t = 2 * J; t < 2 * J + 2; t++) {
-        if (t + 2 < 8) f[(t + 2) % 3] = keys(t + 2);
+        for (int t = 2 * J; t < 2 * J + 2; t++) {
+          if (t + 2 < 8) f[(t + 2) % 3] = keys(t + 2);
 #pragma unroll
-        for (int x = 0; x < RT; x++) s[x][t] = mma<J, 0>(f[t % 3], q[x].v[0], f32x4{0, 0, 0, 0}, sc, q[x].bytes);
-        if constexpr (D == 128) {
+          for (int x = 0; x < R; x++) s[x][t] = mma<J, 0>(f[t % 3], q[x].v[0], f32x4{0, 0, 0, 0}, sc, q[x].bytes);
+          if constexpr (D == 128) {
 #pragma unroll
-          for (int x = 0; x < RT; x++) s[x][t] = mma<J, 1>(f[t % 3], q[x].v[1], s[x][t], sc, q[x].bytes);
+            for (int x = 0; x < R; x++) s[x][t] = mma<J, 1>(f[t % 3], q[x].v[1], s[x][t], sc, q[x].bytes);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
+      };
+      score(std::integral_constant<int, 0>());
+      score(std::integral_constant<int, 1>());
+      score(std::integral_constant<int, 2>());
+      score(std::integral_constant<int, 3>());
+      // all scores are taken here, while a key operand is at hand (the compiler
+      // would move some past the branches below, and keep the operands)
+#pragma unroll
+      for (int x = 0; x < R; x++)
+#pragma unroll
+        for (int t = 0; t < 8; t++) asm volatile("" : "+v"(s[x][t]));
+      const bool masked = tile * 128 + 128 > b.seen0;
+      int limit[R];  // tree: bit 4 t + i is what the row sees of accumulator i of tile t
+      float less[R], c = a.scale2;
+#pragma unroll
+      for (int x = 0; x < R; x++) {
+        if constexpr (!TREE) {
+          limit[x] = seen[x] - 1 - tile * 128 - 8 * lg;
+        } else if (masked) {
+          const uint32_t *row = a.tree + (int64_t)(b.tok0 + seen[x]) * a.words;
+          uint32_t bits = 0;
+#pragma unroll
+          for (int j = 0; j < 4; j++)
+            bits |= (tree_bits(row, a.words, b.fresh, tile * 128 + 32 * j + 8 * lg - b.seen0) & 0xFFu) << (8 * j);
+          limit[x] = (int)bits;
+        }
       }
-    };
-    score(std::integral_constant<int, 0>());
-    score(std::integral_constant<int, 1>());
-    score(std::integral_constant<int, 2>());
-    score(std::integral_constant<int, 3>());
-    // all scores are taken here, while a key operand is at hand (the compiler
-    // would move some past the branches below, and keep the operands)
+      running_max<D, R, true>(s, r, c, masked, [&](int x, int t, int i) {
+        return TREE ? !(limit[x] >> (4 * t + i) & 1) : 32 * (t >> 1) + 4 * (t & 1) + i > limit[x];
+      }, less);
+      u32x4 p[R][4];  // of tokens 32 j + 8 lg ..
+      weights<R, true>(s, c, less, p);
+      // the widened values of every wave are in LDS
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      u32x4 g[2][4];
+      auto values = [&](int d) {
 #pragma unroll
-    for (int x = 0; x < RT; x++)
+        for (int j = 0; j < 4; j++) g[d & 1][j] = *reinterpret_cast<const u32x4 *>(vp[j] + 4096 * d);
+      };
+      values(0);
 #pragma unroll
-      for (int t = 0; t < 8; t++) asm volatile("" : "+v"(s[x][t]));
-    const bool masked = tile * 128 + 128 > b.seen0;
-    int limit[RT];  // tree: bit 4 t + i is what the row sees of accumulator i of tile t
-    float less[RT], c = a.scale2;
-#pragma unroll
-    for (int x = 0; x < RT; x++) {
-      if constexpr (!TREE) {
-        limit[x] = seen[x] - 1 - tile * 128 - 8 * lg;
-      } else if (masked) {
-        const uint32_t *row = a.tree + (int64_t)(b.tok0 + seen[x]) * a.words;
-        uint32_t bits = 0;
+      for (int d = 0; d < DT; d++) {
+        if (d + 1 < DT) values(d + 1);
 #pragma unroll
         for (int j = 0; j < 4; j++)
-          bits |= (tree_bits(row, a.words, b.fresh, tile * 128 + 32 * j + 8 * lg - b.seen0) & 0xFFu) << (8 * j);
-        limit[x] = (int)bits;
+#pragma unroll
+          for (int x = 0; x < R; x++) r[x].o[d] = mma16(g[d & 1][j], p[x][j], r[x].o[d]);
       }
+#pragma unroll
+      for (int x = 0; x < R; x++) r[x].l = add_weights(p[x], r[x].l);
+      kp0 += flip;  // to the other buffer
+      kp1 += flip;
+      flip = -flip;
     }
-    running_max<D, RT, true>(s, r, c, masked, [&](int x, int t, int i) {
-      return TREE ? !(limit[x] >> (4 * t + i) & 1) : 32 * (t >> 1) + 4 * (t & 1) + i > limit[x];
-    }, less);
-    u32x4 p[RT][4];  // of tokens 32 j + 8 lg ..
-    weights<RT, true>(s, c, less, p);
-    // the widened values of every wave are in LDS
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    u32x4 g[2][4];
-    auto values = [&](int d) {
-#pragma unroll
-      for (int j = 0; j < 4; j++) g[d & 1][j] = *reinterpret_cast<const u32x4 *>(vp[j] + 4096 * d);
-    };
-    values(0);
-#pragma unroll
-    for (int d = 0; d < DT; d++) {
-      if (d + 1 < DT) values(d + 1);
-#pragma unroll
-      for (int j = 0; j < 4; j++)
-#pragma unroll
-        for (int x = 0; x < RT; x++) r[x].o[d] = mma16(g[d & 1][j], p[x][j], r[x].o[d]);
-    }
-#pragma unroll
-    for (int x = 0; x < RT; x++) r[x].l = add_weights(p[x], r[x].l);
-    kp0 += flip;  // to the other buffer
-    kp1 += flip;
-    flip = -flip;
   }
 #pragma unroll
-  for (int x = 0; x < RT; x++) {
-    const int row = 16 * RT * wave + 16 * x + l16;
+  for (int x = 0; x < R; x++) {
+    const int row = part_of(x) + l16;
     if (row < rows) write(row, r[x]);
+  }
+}
+
+// One block of rows and its tiles t0 .. t1 - 1, 16 RT rows a wave; `write(row, state)`
+// takes what comes of each row. A prompt's block is full but for its last. A tree's
+// rows are often fewer: they are dealt out a part of 16 at a time, and a wave does
+// those that it has (the way through the tiles is its own, the barriers are as many).
+template <int D, bool TREE, int RT, typename F>
+__device__ __forceinline__ void attend_tiles(const AttnArgs &a, const Block &b, int head, int t0, int t1,
+                                             uint8_t (&ks)[256 * D], uint8_t (&vs)[256 * D], F write) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if constexpr (!TREE) {
+    attend_parts<D, TREE, RT>(a, b, head, t0, t1, ks, vs, [&](int x) { return 16 * (RT * wave + x); }, write);
+  } else {
+    auto part_of = [&](int x) { return 16 * (4 * x + wave); };
+    const int rows = __builtin_amdgcn_readfirstlane(b.count * a.group);
+    if (part_of(RT - 1) < rows) attend_parts<D, TREE, RT>(a, b, head, t0, t1, ks, vs, part_of, write);
+    else if (RT == 2 && part_of(0) < rows) attend_parts<D, TREE, 1>(a, b, head, t0, t1, ks, vs, part_of, write);
+    else attend_parts<D, TREE, 0>(a, b, head, t0, t1, ks, vs, part_of, write);
   }
 }
 
