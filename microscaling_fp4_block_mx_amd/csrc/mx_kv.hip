@@ -1881,8 +1881,10 @@ static AttnPlan attn_plan(int64_t tokens, int batch, int q_heads, int heads, int
 // rows of 128 dims share where sequences may be longer than 1,024 (16 sequences of up
 // to 12 tokens in 32,000: 132 us, 204 with a wave to 32 rows; 48 of 8 in 3,000 56 and
 // 79; 16 of 8 in 700 22 and 15), of 64 dims they do not (48 of 8 in 6,000: 65 and
-// 58). Up to 64 rows go in blocks of 64 (16 sequences of up to 16 tokens in 32,000, 4
-// query heads to a kv head: 133 us). Two workgroups a compute unit, of four tiles at
+// 58). Blocks of 64 rows up to 48 in the mean, since a sequence of more than 64 is then
+// two blocks, which both read its keys (16 sequences of up to 16 tokens in 32,000, 4
+// query heads to a kv head: 127 us, in blocks of 128 rows 133; of up to 24, 64 rows in
+// the mean: 199 and 180). Two workgroups a compute unit, of four tiles at
 // least (eight: 16 of 48 tokens in 2,000 46 us, four 38).
 struct TreePlan {
   int share, rt, block_tokens;
@@ -1892,7 +1894,7 @@ static TreePlan tree_plan(const AttnPlan &p, int64_t tokens, int batch, int q_he
   if (p.few && (p.rt == 1 || dim == 64 || max_length <= 1024)) return TreePlan{};
   if (batch > kSharers || heads > 512 || p.units * heads > 4096) return TreePlan{};
   const int group = q_heads / heads;
-  const int rt = (tokens + batch - 1) / batch * group <= 64 && group <= 64 ? 1 : 2;
+  const int rt = (tokens + batch - 1) / batch * group <= 48 && group <= 64 ? 1 : 2;
   const int block_tokens = 64 * rt / group;
   const int64_t tiles = (tokens / block_tokens + batch) * std::max<int64_t>(1, (max_length + 127) / 128);
   const int64_t share = std::min<int64_t>(512 / heads, (tiles + kLeastTiles - 1) / kLeastTiles);
