@@ -1658,10 +1658,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
 // ones and the beginning of another. What a block got from several workgroups
 // is left in their room (the first and the last block of each: two rooms) and
 // joined. 16 sequences of up to 24 tokens in 8,000 to 32,000, 32 query heads on 8 of
-// 128 dims: 161 to 195 us and 8 for the join in blocks of 64 rows, 169 to 182 in
-// blocks of 128 (splits of one length for all sequences, which left units idle for 41 %
-// of the time, 241 and 8). Bound by issue, as above: matrix cores 47 % and vector
-// arithmetic 52 % of a unit's cycles.
+// 128 dims: 148 us and 8 for the join (splits of one length for all sequences, which
+// left units idle for 41 % of the time, 241 and 8). Bound by what a wave does in a row
+// (scores, weights, sums): 3.9 TB/s, matrix cores 33 % and vector arithmetic 41 % of a
+// unit's cycles.
 constexpr int kLeastTiles = 4;    // of a workgroup's share
 constexpr int kSharers = 64;      // sequences: one a lane
 constexpr int kBegin = 2;         // what beginning a block counts for, in tiles (4 trees of up to
@@ -1879,7 +1879,7 @@ static AttnPlan attn_plan(int64_t tokens, int batch, int q_heads, int heads, int
 // than a wave has lanes, blocks enough to fill the card over and over, and heads for
 // which one workgroup each would be more than two a compute unit. 17 to 32
 // rows of 128 dims share where sequences may be longer than 1,024 (16 sequences of up
-// to 12 tokens in 32,000: 132 us, 204 with a wave to 32 rows; 48 of 8 in 3,000 56 and
+// to 12 tokens in 32,000: 124 us, 204 with a wave to 32 rows; 48 of 8 in 3,000 56 and
 // 79; 16 of 8 in 700 22 and 15), of 64 dims they do not (48 of 8 in 6,000: 65 and
 // 58). Blocks of 64 rows up to 48 in the mean, since a sequence of more than 64 is then
 // two blocks, which both read its keys (16 sequences of up to 16 tokens in 32,000, 4
