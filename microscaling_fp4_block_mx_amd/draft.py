@@ -2,10 +2,11 @@
 
 The norms of queries and keys per head with the position rotation, their
 gradient, the append that has both on the way, attention over a tree of drafted
-tokens, their verification, and keeping the accepted ones. Every step runs in the HIP kernels behind include/mx.h; this module
-allocates outputs and scratch with torch (on the current stream) and checks
-what the C entry points cannot see: devices, dtypes, shapes and contiguity. Bad
-arguments raise ``ValueError``, HIP errors ``RuntimeError``.
+tokens, their verification, and keeping the accepted ones. Every step runs in the
+HIP kernels behind include/mx.h; this module allocates outputs and scratch with
+torch (on the current stream) and checks what the C entry points cannot see:
+devices, dtypes, shapes and contiguity. Bad arguments raise ``ValueError``, HIP
+errors ``RuntimeError``.
 """
 from __future__ import annotations
 
@@ -16,9 +17,11 @@ from typing import NamedTuple
 
 import torch
 
-from . import _DTYPES, load_library
-from .layer import (KVCache, _batch_of, _cache_of, _call, _heads_of, _pack_batch, _ptr, _scratch,
-                    _want)
+from . import _DTYPES, _need, load_library
+from .layer import (_I32, KVCache, _batch_of, _cache_of, _call, _heads_of, _pack_batch, _ptr,
+                    _scratch, _Tensor, _want)
+
+_F32 = torch.float32
 
 
 class MxRotary(ctypes.Structure):
@@ -165,16 +168,17 @@ def _rotary_of(rotary: Rotary | None, dev, dim: int, tokens: int, positions: boo
     if rotary is None:
         return None
     table, pos, paired = rotary
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+    if not isinstance(table, _Tensor) or len(table.shape) != 2:
         raise ValueError("the rotation's table must be [length, rot]")
     length, rot = table.shape
-    _want(table, "table", dev, torch.float32, length * rot)
+    if not (table.dtype is _F32 and table.device == dev and table.is_contiguous()):
+        _need(table, "table", dev, _F32)
     if rot % 16 or not 0 < rot <= dim:
         raise ValueError(f"rot must be a multiple of 16 up to {dim}, got {rot}")
     if length < 1:
         raise ValueError("the rotation's table has no positions")
     if pos is not None or positions:
-        _want(pos, "positions", dev, torch.int32, tokens)
+        _want(pos, "positions", dev, _I32, tokens)
     return _pack_rotary(table.data_ptr(), pos.data_ptr() if pos is not None else 0, length, rot,
                         bool(paired))
 
@@ -194,7 +198,7 @@ def _address(t) -> int:
 
 
 def _on_gpu(t, name: str):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     return t.device
 
@@ -305,10 +309,10 @@ def kv_attention_tree(q: torch.Tensor, cache: KVCache, table: torch.Tensor, cu: 
         raise ValueError(f"the cache holds heads of {held_dim}, got {dim}")
     if q_heads < heads or q_heads % heads:
         raise ValueError(f"q_heads must be a multiple of the cache's {heads}, got {q_heads}")
-    if not isinstance(mask, torch.Tensor) or mask.dim() != 2 or mask.shape[1] < 1:
+    if not isinstance(mask, _Tensor) or len(mask.shape) != 2 or mask.shape[1] < 1:
         raise ValueError("mask must be [tokens, words]")
     words = mask.shape[1]
-    _want(mask, "mask", dev, torch.int32, tokens * words, words)
+    _want(mask, "mask", dev, _I32, tokens * words)
     batch, width, b = _batch_of(dev, table, cu, lengths, tokens)
     if out is None:
         out = torch.empty(tokens, q_heads, dim, dtype=torch.bfloat16, device=dev)
@@ -334,22 +338,23 @@ def verify_drafts(target: torch.Tensor, ids: torch.Tensor, parents: torch.Tensor
     [tokens]; cu int32 [batch + 1]; numbers float32 [tokens, 2], uniform from 0 to
     below 1. width: the longest path, node 0 included (the tree's depth + 1)."""
     dev = _on_gpu(target, "target")
-    if target.dtype not in _DTYPES or target.dim() != 2 or not target.is_contiguous():
+    if target.dtype not in _DTYPES or len(target.shape) != 2 or not target.is_contiguous():
         raise ValueError("target must be contiguous [tokens, vocab], float32 or bfloat16")
     tokens, vocab = target.shape
     if draft is not None:
         _want(draft, "draft", dev, target.dtype, tokens * vocab, vocab)
-    _want(ids, "ids", dev, torch.int32, tokens)
-    _want(parents, "parents", dev, torch.int32, tokens)
-    if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or not len(cu):
+    _want(ids, "ids", dev, _I32, tokens)
+    _want(parents, "parents", dev, _I32, tokens)
+    if not isinstance(cu, _Tensor) or len(cu.shape) != 1 or not cu.shape[0]:
         raise ValueError("cu must be [batch + 1]")
     batch = cu.shape[0] - 1
-    _want(cu, "cu", dev, torch.int32, batch + 1)
-    _want(numbers, "numbers", dev, torch.float32, 2 * tokens, 2)
+    _want(cu, "cu", dev, _I32, batch + 1)
+    _want(numbers, "numbers", dev, _F32, 2 * tokens, 2)
     if not 1 <= width <= 1024:
         raise ValueError(f"width must be 1 to 1024, got {width}")
-    path = torch.empty(batch, width, dtype=torch.int32, device=dev)
-    count, token = torch.empty(2, batch, dtype=torch.int32, device=dev)
+    path = torch.empty(batch, width, dtype=_I32, device=dev)
+    count = torch.empty(batch, dtype=_I32, device=dev)
+    token = torch.empty(batch, dtype=_I32, device=dev)
     lib = load_library()
     size = lib.mx_verify_drafts_workspace_size(tokens, batch, vocab)
     ws = _scratch(size, dev)
@@ -365,14 +370,14 @@ def kv_keep(cache: KVCache, table: torch.Tensor, lengths: torch.Tensor, path: to
     [batch] that each sequence held, new token path[i][j] moves to place j, for j
     below count[i] (verify_drafts gives both). It then holds lengths + count."""
     dev, _, _, _, c = _cache_of(cache)
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+    if not isinstance(table, _Tensor) or len(table.shape) != 2:
         raise ValueError("table must be [batch, width]")
     batch, width = table.shape
-    if not isinstance(path, torch.Tensor) or path.dim() != 2 or path.shape[0] != batch:
+    if not isinstance(path, _Tensor) or len(path.shape) != 2 or path.shape[0] != batch:
         raise ValueError(f"path must be [{batch}, width]")
-    _want(table, "table", dev, torch.int32, batch * width)
-    _want(lengths, "lengths", dev, torch.int32, batch)
-    _want(path, "path", dev, torch.int32, path.numel())
-    _want(count, "count", dev, torch.int32, batch)
+    _want(table, "table", dev, _I32, batch * width)
+    _want(lengths, "lengths", dev, _I32, batch)
+    _want(path, "path", dev, _I32, path.numel())
+    _want(count, "count", dev, _I32, batch)
     b = _pack_batch(table.data_ptr(), 0, lengths.data_ptr(), 0, batch, width)
     _call(dev, load_library().mx_kv_keep, c, b, path.data_ptr(), path.shape[1], count.data_ptr())

@@ -20,6 +20,7 @@ import torch
 from . import _DTYPES, _need, _raise, _stream, load_library
 
 BLOCKS = (32, 128)
+_Tensor, _U8, _I32 = torch.Tensor, torch.uint8, torch.int32
 
 
 class MxKVCache(ctypes.Structure):
@@ -158,7 +159,7 @@ def _matrix(x, name: str, dtypes=_DTYPES):
 def _want(t, name: str, dev, dtype, numel: int, last: int = 0):
     """_need() with its outcome found in fewer steps where all is well. `last`:
     what the last dimension must be (0: any) of more than one."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == numel
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.numel() == numel
             and t.device == dev and t.is_contiguous()):
         _need(t, name, dev, dtype, numel)
     if last and t.dim() > 1 and t.size(-1) != last:
@@ -307,14 +308,15 @@ def matmul_mxfp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sca
 
 
 def _heads_of(t, name: str, dev, dtypes):
-    """[tokens, heads, dim] with adjacent heads; any stride between tokens."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != dev:
+    """[tokens, heads, dim] with adjacent heads; any stride between tokens (dev: a GPU)."""
+    if not isinstance(t, _Tensor) or t.device != dev:
         raise ValueError(f"{name} must be a tensor on {dev}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be one of {list(dtypes)}, got {t.dtype}")
-    if t.dim() != 3:
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{name} must be [tokens, heads, dim]")
-    tokens, heads, dim = t.shape
+    tokens, heads, dim = shape
     step, head, one = t.stride()
     if (dim > 1 and one != 1) or (heads > 1 and head != dim):
         raise ValueError(f"{name}'s heads must lie next to each other")
@@ -325,27 +327,41 @@ def _cache_of(cache: KVCache):
     """(device, heads, dim, page, mx_kv_cache_t)"""
     k, ks, v, vs = cache
     dev = getattr(k, "device", None)
-    _need(k, "k_codes", dev, torch.uint8)
-    if k.dim() != 4:
+    if not (isinstance(k, _Tensor) and k.is_cuda and k.dtype is _U8 and k.is_contiguous()):
+        _need(k, "k_codes", dev, _U8)
+    shape = k.shape
+    if len(shape) != 4:
         raise ValueError("k_codes must be [pages, heads, page, dim]")
-    pages, heads, page, dim = k.shape
-    _want(v, "v_codes", dev, torch.uint8, k.numel())
-    if v.shape != (pages, heads, dim, page):
+    pages, heads, page, dim = shape
+    # as in _want, one shape that fits for all that it checks
+    if not (isinstance(v, _Tensor) and v.dtype is _U8 and v.device == dev and v.is_contiguous()
+            and v.shape == (pages, heads, dim, page)):
+        _want(v, "v_codes", dev, _U8, k.numel())
         raise ValueError(f"v_codes must be {(pages, heads, dim, page)}, got {tuple(v.shape)}")
-    _want(ks, "k_scales", dev, torch.uint8, pages * heads, heads)
-    _want(vs, "v_scales", dev, torch.uint8, pages * heads, heads)
+    one = (pages, heads)
+    if not (isinstance(ks, _Tensor) and ks.dtype is _U8 and ks.device == dev
+            and ks.is_contiguous() and ks.shape == one):
+        _want(ks, "k_scales", dev, _U8, pages * heads, heads)
+    if not (isinstance(vs, _Tensor) and vs.dtype is _U8 and vs.device == dev
+            and vs.is_contiguous() and vs.shape == one):
+        _want(vs, "v_scales", dev, _U8, pages * heads, heads)
     return dev, heads, dim, page, _pack_cache(k.data_ptr(), ks.data_ptr(), v.data_ptr(),
                                               vs.data_ptr(), pages, heads, dim, page)
 
 
 def _batch_of(dev, table, cu, lengths, tokens):
     """(batch, width, mx_kv_batch_t)"""
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+    if not isinstance(table, _Tensor) or len(table.shape) != 2:
         raise ValueError("table must be [batch, width]")
     batch, width = table.shape
-    _want(table, "table", dev, torch.int32, batch * width)
-    _want(cu, "cu", dev, torch.int32, batch + 1)
-    _want(lengths, "lengths", dev, torch.int32, batch)
+    if not (table.dtype is _I32 and table.device == dev and table.is_contiguous()):
+        _need(table, "table", dev, _I32)
+    if not (isinstance(cu, _Tensor) and cu.dtype is _I32 and cu.device == dev
+            and cu.is_contiguous() and cu.shape == (batch + 1,)):
+        _want(cu, "cu", dev, _I32, batch + 1)
+    if not (isinstance(lengths, _Tensor) and lengths.dtype is _I32 and lengths.device == dev
+            and lengths.is_contiguous() and lengths.shape == (batch,)):
+        _want(lengths, "lengths", dev, _I32, batch)
     return batch, width, _pack_batch(table.data_ptr(), cu.data_ptr(), lengths.data_ptr(), tokens,
                                      batch, width)
 
