@@ -117,35 +117,36 @@ __device__ __forceinline__ void make_plan(const VerifyArgs &a, const Sequence &s
 
 // A wave's part of a row: step u of lane l holds 16 bytes of neighbouring elements,
 // zeros outside the row. Rows begin anywhere: chunks are laid out from the 16-byte
-// boundary before a row on.
+// boundary before a row on. A step is a run of the row, or, LANES, a lane has one.
 template <bool BF16>
 struct Part {
   static constexpr int A = BF16 ? 8 : 4, U = kChunk / 64 / A;
   u32x4 v[U];
 };
-template <bool BF16>
+template <bool BF16, bool LANES>
 __device__ __forceinline__ Part<BF16> load_part(const void *base, const VerifyArgs &a, int64_t row, int chunk) {
   constexpr int A = Part<BF16>::A, U = Part<BF16>::U, E = BF16 ? 2 : 4;
+  constexpr int STEP = LANES ? A : 64 * A;  // elements from step to step
   const int64_t begin = row * a.vocab, end = begin + a.vocab;
-  const int64_t from = (begin & ~(int64_t)(A - 1)) + (int64_t)chunk * kChunk + (threadIdx.x & 63) * A;
+  const int64_t from = (begin & ~(int64_t)(A - 1)) + (int64_t)chunk * kChunk + (threadIdx.x & 63) * (LANES ? A * U : A);
   const uint8_t *x = reinterpret_cast<const uint8_t *>(base) + from * E;
   Part<BF16> p;
 #pragma unroll
   for (int u = 0; u < U; u++) {
-    const int64_t at = from + u * 64 * A;
+    const int64_t at = from + u * STEP;
     p.v[u] = u32x4{0, 0, 0, 0};
-    if (at >= begin && at + A <= end) p.v[u] = *reinterpret_cast<const u32x4 *>(x + u * 64 * A * E);
+    if (at >= begin && at + A <= end) p.v[u] = *reinterpret_cast<const u32x4 *>(x + u * STEP * E);
   }
   // the row's first and last elements, where they share their 16 bytes with others'
   if ((begin | end) & (A - 1)) {
 #pragma unroll
     for (int u = 0; u < U; u++) {
-      const int64_t at = from + u * 64 * A;
+      const int64_t at = from + u * STEP;
       if (at >= end || at + A <= begin || (at >= begin && at + A <= end)) continue;
 #pragma unroll
       for (int e = 0; e < A; e++) {
         if (at + e < begin || at + e >= end) continue;
-        const uint8_t *one = x + (u * 64 * A + e) * E;
+        const uint8_t *one = x + (u * STEP + e) * E;
         if constexpr (BF16) p.v[u][e >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t *>(one) << (16 * (e & 1));
         else p.v[u][e] = *reinterpret_cast<const uint32_t *>(one);
       }
@@ -159,14 +160,6 @@ __device__ __forceinline__ float probability(u32x4 v, int e) {
   const uint32_t w = BF16 ? v[e >> 1] : v[e];
   return clean(__uint_as_float(!BF16 ? w : (e & 1) ? w & 0xFFFF0000u : w << 16));
 }
-// Place in the row of element e of step u.
-template <bool BF16>
-__device__ __forceinline__ int64_t part_index(const VerifyArgs &a, int64_t row, int chunk, int u, int e) {
-  constexpr int A = Part<BF16>::A;
-  const int64_t before = (row * a.vocab) & (A - 1);
-  return (int64_t)chunk * kChunk + (u * 64 + (threadIdx.x & 63)) * A + e - before;
-}
-
 __device__ __forceinline__ double shfl(double v, int lane) { return __shfl(v, lane); }
 // Sum over the wave, the same bits on every lane.
 __device__ __forceinline__ double sum64d(double v) {
@@ -226,9 +219,9 @@ __global__ __launch_bounds__(256) void k_verify_sums(const VerifyArgs a) {
     const int draws = uniform(plan.draws[r]);
     const int64_t row = s.first + (draws & ~kResidual);
     const bool residual = draws & kResidual;
-    const Part<BF16> p = load_part<BF16>(a.target, a, row, chunk);
+    const Part<BF16> p = load_part<BF16, false>(a.target, a, row, chunk);
     Part<BF16> q = {};
-    if (residual) q = load_part<BF16>(a.draft, a, row, chunk);
+    if (residual) q = load_part<BF16, false>(a.draft, a, row, chunk);
     double w = 0.0, t = 0.0;
     if (residual) {
 #pragma unroll
@@ -290,48 +283,54 @@ __device__ __forceinline__ int64_t draw_from(const VerifyArgs &a, int64_t slot, 
     before += shfl(incl, 63);
   }
   chunk = __builtin_amdgcn_readfirstlane(chunk);
-  const Part<BF16> p = load_part<BF16>(a.target, a, row, chunk);
+  constexpr int A = Part<BF16>::A, U = Part<BF16>::U;
+  const Part<BF16> p = load_part<BF16, true>(a.target, a, row, chunk);
   Part<BF16> q = {};
-  if (residual) q = load_part<BF16>(a.draft, a, row, chunk);
-  // the step in which it does, from the steps' sums, then the lane, then its element
-  int step = 0;
-  u32x4 mine_p = {0, 0, 0, 0}, mine_q = {0, 0, 0, 0};
-  double mine = 0.0, at = base;
-  bool over = false;
+  if (residual) q = load_part<BF16, true>(a.draft, a, row, chunk);
+  // the lane in which it does, from the lanes' sums, then its step, then its element
+  double part[U], mine = 0.0;
 #pragma unroll
-  for (int u = 0; u < Part<BF16>::U; u++) {
-    double v = 0.0;
+  for (int u = 0; u < U; u++) {
+    part[u] = 0.0;
 #pragma unroll
-    for (int e = 0; e < Part<BF16>::A; e++) v += weight_of<BF16>(p.v[u], q.v[u], residual, e);
-    const double all = sum64d(v);
-    if (all > 0.0 && !over) {
-      step = u;
-      mine = v;
-      mine_p = p.v[u];
-      mine_q = q.v[u];
-      base = at;
-      over = at + all > bound;
-    }
-    at += all;
+    for (int e = 0; e < A; e++) part[u] += weight_of<BF16>(p.v[u], q.v[u], residual, e);
+    asm volatile("" : "+v"(part[u]));  // formed here and held, not formed again below
+    mine += part[u];
     __builtin_amdgcn_sched_barrier(0);  // few numbers in 64 bits at a time
   }
   const double incl = scan64(mine);
   const uint64_t any = __ballot(mine > 0.0), past = __ballot(mine > 0.0 && base + incl > bound);
   if (!any) return -1;
   const int l = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(any);
-  double sum = base + (incl - mine);
-  int64_t found = -1;
+  double at = base + (incl - mine), sum = at;
+  int step = 0;
+  u32x4 mine_p = {0, 0, 0, 0}, mine_q = {0, 0, 0, 0};
+  bool over = false;
+#pragma unroll
+  for (int u = 0; u < U; u++) {
+    if (part[u] > 0.0 && !over) {
+      step = u;
+      mine_p = p.v[u];
+      mine_q = q.v[u];
+      sum = at;
+      over = at + part[u] > bound;
+    }
+    at += part[u];
+  }
+  int last = -1;
   bool done = false;
 #pragma unroll
-  for (int e = 0; e < Part<BF16>::A; e++) {
+  for (int e = 0; e < A; e++) {
     const double w = weight_of<BF16>(mine_p, mine_q, residual, e);
     sum += w;
     if (w > 0.0 && !done) {
-      found = part_index<BF16>(a, row, chunk, step, e);
+      last = e;
       done = sum > bound;
     }
   }
-  return __shfl((long long)found, l);
+  // (places count from the boundary before the row)
+  const int64_t found = (int64_t)chunk * kChunk + (lane * U + step) * A + last - ((row * a.vocab) & (A - 1));
+  return __shfl((long long)(last < 0 ? -1 : found), l);
 }
 
 // A wave a row to draw at, all of a sequence's at once where they are 16 or fewer.
@@ -341,16 +340,19 @@ __global__ __launch_bounds__(1024) void k_verify_walk(const VerifyArgs a) {
   // (the wave's number and what follows from it is in scalar registers)
   auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
   const int i = blockIdx.x, lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int found = a.tokens ? a.many[i] : 0;
   const Sequence s = sequence_of(a, i);
   int32_t *path = a.path + (int64_t)i * a.width;
+  // the wave's row is asked for beside how many there are, before what the walk needs
+  const int first = wave < s.nodes ? a.draws[s.first + wave] : 0;
   for (int j = threadIdx.x; j < s.nodes; j += blockDim.x) {
     up[j] = a.parents[s.first + j];
     kid[j] = a.kid[s.first + j];
     id[j] = a.ids[s.first + j];
   }
   if (wave < s.nodes) {
-    int draws = uniform(a.draws[s.first + wave]);  // asked for beside how many there are
-    const int many = uniform(a.many[i]);
+    int draws = uniform(first);
+    const int many = uniform(found);
     for (int r = wave; r < many; r += blockDim.x >> 6) {
       if (r != wave) draws = uniform(a.draws[s.first + r]);
       const int j = draws & ~kResidual;
