@@ -35,7 +35,7 @@ class Turned(World):
         self.angles = dref.table_of(length, rot, rot) if rot else None
         self.weight = (torch.randn(self.dim, generator=self.g) * 0.3 + 1).to(dtype) if norm else None
 
-    def append(self, new, held, by=1.0, positions=None, edit=None, strided=False):
+    def append(self, new, held, by=1.0, positions=None, edit=None, strided=False, behind=0):
         cu, place = [0], []
         for n, h in zip(new, held):
             cu.append(cu[-1] + n)
@@ -51,7 +51,8 @@ class Turned(World):
         rotary = None
         if self.angles is not None:
             rotary = mx.Rotary(self.angles.cuda(), None if positions is None else at.cuda(), self.paired)
-        gk, gv = k.cuda(), v.cuda()
+        more = torch.full((behind, self.heads, self.dim), math.nan, dtype=self.dtype)  # of no sequence
+        gk, gv = torch.cat([k, more]).cuda(), torch.cat([v, more]).cuda()
         if strided:  # parts of one projection's rows
             rows = torch.cat([gk, gk, gv], 1)
             gk, gv = rows[:, self.heads:2 * self.heads], rows[:, 2 * self.heads:]
@@ -155,6 +156,16 @@ def test_nothing_on_the_way_is_the_plain_append():
     w = Turned([77, 3], 2, 64, 32, 8)
     w.turn(0, False, False, 1, torch.bfloat16)
     w.append([77, 3], [0, 0])
+    w.same()
+
+
+def test_tokens_behind_the_last_sequence():
+    """A padded batch: tokens behind cu's last are dropped."""
+    w = Turned([200, 90], 2, 64, 32, 10)
+    w.turn(64, False, True, 400, torch.bfloat16)
+    w.append([150, 77], [0, 0], behind=300)
+    w.append([1, 1], [150, 77], behind=1)
+    w.append([1, 1], [151, 78], behind=90)
     w.same()
 
 

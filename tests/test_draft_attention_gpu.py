@@ -186,6 +186,37 @@ def test_divisions_of_the_work(batch, new, group, longest, dim):
     check_attention(*run(w, counts, lengths, group, masks(counts, "tree", 3)))
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("most", [16, 32])
+def test_parts_of_blocks(most, dim):
+    """Blocks of 64 and of 128 rows with every number of rows that a wave or two have none of."""
+    new = [n for n in range(1, most + 1) if most == 16 or n % 4 < 2]
+    lengths = [n + 130 * (i % 7) + 3 * n for i, n in enumerate(new)]
+    w = World(lengths, 2, dim, 32, most)
+    w.append(lengths, [0] * len(new))
+    check_attention(*run(w, new, lengths, 4, masks(new, "tree", 11), max_length=2000))
+
+
+@pytest.mark.parametrize("new", [[3, 2], [40, 30], [4] * 70])
+def test_rows_behind_the_last_sequence(new):
+    """A padded batch: rows of q and of the mask behind cu's last are not read, those of out stay."""
+    n, more = sum(new), 37
+    lengths = [x + 500 for x in new]
+    w = World(lengths, 2, 128, 64, 9)
+    w.append(lengths, [0] * len(new))
+    sees = masks(new, "tree", 12)
+    words = -(-max(new) // 32)
+    q = w.numbers(n, 8)
+    cu = i32([sum(new[:i]) for i in range(len(new) + 1)])
+    out = torch.full((n + more, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    bits = torch.cat([ref.words_of(m, words) for m in sees] + [torch.full((more, words), -1, dtype=torch.int32)])
+    nan = torch.full((more, 8, 128), math.nan, dtype=torch.bfloat16)
+    got = mx.kv_attention_tree(torch.cat([q, nan]).cuda(), w.gpu, w.table.cuda(), cu.cuda(), i32(lengths).cuda(),
+                               bits.cuda(), out=out).cpu()
+    assert bool((got[n:] == 7.0).all())
+    check_attention(got[:n], *ref.attention_tree(q, w.cpu, w.table, cu, i32(lengths), sees, 1 / math.sqrt(128)))
+
+
 @pytest.mark.parametrize("heads", [1, 5, 16])
 def test_heads(heads):
     """Workgroups by kv heads, shares of one and of many tiles."""

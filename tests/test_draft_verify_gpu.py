@@ -137,6 +137,19 @@ def test_tokens_and_parents_out_of_range():
 
 
 @pytest.mark.parametrize("with_draft", [False, True])
+def test_rows_behind_the_last_sequence(with_draft):
+    """A padded batch: the rows behind cu's last do not count."""
+    w = world([5, 9, 30], 700, 22)
+    cu = i32([0, 5, 14])
+    draft = w[1] if with_draft else None
+    want = ref.verify(w[0][:14], None if draft is None else draft[:14], w[2][:14], w[3][:14], cu, w[5][:14], 9)
+    w[0][14:] = math.nan
+    w[1][14:] = math.nan
+    w[2][14:], w[3][14:] = -1, 1 << 30
+    assert call(w[0], draft, w[2], w[3], cu, w[5], 9) == [want[0], want[1], want[2]]
+
+
+@pytest.mark.parametrize("with_draft", [False, True])
 def test_sequences_that_share_rows(with_draft):
     """Where cu falls, against its description, the sequences that share rows have
     any result that is one: rising nodes of theirs, a token of the vocabulary."""
