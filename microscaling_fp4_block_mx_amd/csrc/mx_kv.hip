@@ -1691,6 +1691,7 @@ struct Stretch {
     total = __shfl((long long)end, 63);
     per = max((int64_t)kLeastTiles, (total + a.splits - 1) / a.splits);
   }
+  // what lane i knows, for all lanes of the wave together: none may have left
   __device__ __forceinline__ static int of(int v, int i) { return __builtin_amdgcn_readlane(v, i); }
   __device__ __forceinline__ int64_t begin_of(int i) const {
     return __shfl((long long)(end - (int64_t)blocks * tiles), i);
@@ -1764,12 +1765,14 @@ __global__ __launch_bounds__(256) void k_attn_share_join(const AttnArgs a) {
   const int tok = blockIdx.x, c = threadIdx.x % C, qh = blockIdx.y * R + threadIdx.x / C;
   const Stretch s(a);
   const uint64_t owner = __ballot(s.blocks > 0 && tok >= s.c0 && tok < s.c0 + s.n);
-  if (!owner || qh >= a.q_heads) return;
+  if (!owner) return;
   const int i = __builtin_ctzll(owner);
   const int c0 = Stretch::of(s.c0, i), tiles = Stretch::of(s.tiles, i), block = (tok - c0) / a.block_tokens;
   const int64_t begin = s.begin_of(i) + (int64_t)block * tiles;
   const int g0 = (int)(begin / s.per), g1 = (int)((begin + tiles - 1) / s.per);
   if (g0 == g1) return;  // one workgroup had it all
+  // (not before: lane i is asked for its sequence above, and may have no query head)
+  if (qh >= a.q_heads) return;
   const int head = qh / a.group;
   const int row = (tok - c0 - block * a.block_tokens) * a.group + qh % a.group;
   auto part = [&](int g) {  // of a workgroup that began before this block the later room

@@ -1,0 +1,66 @@
+"""Attention over trees whose blocks of rows are cut between workgroups, against
+64 bits: large ragged batches, and query heads that do not fill the last wave of
+the join. Tolerances are those of test_draft_attention_gpu.py; `out` holds a number
+that no result is near, so that a row which nothing writes shows."""
+import math
+
+import pytest
+import torch
+
+import draft_reference as ref
+import microscaling_fp4_block_mx_amd as mx
+from test_draft_attention_gpu import masks
+from test_layer_kv_gpu import World, check_attention, i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    mx.load_library()
+    yield
+    torch.cuda.synchronize()
+
+
+def batch_of(batch, group, rows, longest, seed):
+    """(new tokens, lengths): ragged, one sequence idle, one `longest`, more than `rows` rows in the mean."""
+    g = torch.Generator().manual_seed(seed)
+    most = 2 * rows // group + 2
+    new = [int(torch.randint(1, most + 1, (1,), generator=g)) for _ in range(batch)]
+    new[batch // 2] = 0
+    while -(-sum(new) // batch) * group <= rows:
+        new[int(torch.randint(0, batch // 2, (1,), generator=g))] += 1
+    lengths = [n + int(torch.randint(0, 900, (1,), generator=g)) for n in new]
+    lengths[batch // 3] = longest
+    return new, lengths
+
+
+def check(w, new, lengths, group, seed=1):
+    cu = i32([sum(new[:i]) for i in range(len(new) + 1)])
+    sees = masks(new, "tree", seed)
+    words = max(1, -(-max(new) // 32))
+    q = w.numbers(int(cu[-1]), w.heads * group)
+    mask = torch.cat([ref.words_of(m, words) for m in sees])
+    out = torch.full(q.shape, 1e30, dtype=torch.bfloat16, device="cuda")
+    mx.kv_attention_tree(q.cuda(), w.gpu, w.table.cuda(), cu.cuda(), i32(lengths).cuda(), mask.cuda(), out=out)
+    check_attention(out.cpu(), *ref.attention_tree(q, w.cpu, w.table, cu, i32(lengths), sees, 1 / math.sqrt(w.dim)))
+
+
+def shares(tokens, batch, q_heads, heads, dim, room):
+    """Whether workgroups share such a call's tiles: its scratch is the causal call's where they do not."""
+    args = tokens, batch, q_heads, heads, dim, room
+    return mx.mx_kv_attention_tree_workspace_size(*args) != mx.mx_kv_attention_workspace_size(*args)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("batch", [24, 33, 40, 64])
+@pytest.mark.parametrize("heads,group", [(1, 1), (1, 2), (1, 3), (1, 5), (2, 3), (1, 7), (2, 7), (1, 17)])
+def test_query_heads_that_leave_part_of_a_wave(heads, group, batch, dim):
+    """The last wave that joins has 4 (dims of 64) or 2 rows (of 128), some of them past the query heads."""
+    new, lengths = batch_of(batch, group, 32, 2500, 100 * batch + group)
+    w = World(lengths, heads, dim, 64, batch + group)
+    assert shares(sum(new), batch, heads * group, heads, dim, w.table.shape[1] * 64)
+    w.append(lengths, [0] * batch)
+    check(w, new, lengths, group)
