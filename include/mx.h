@@ -415,9 +415,9 @@ typedef struct {
  * lists the pages of sequence i in order; its new tokens are rows cu[i] ..
  * cu[i+1] - 1 of the token arrays (cu[0] = 0, cu[batch] = tokens); lengths[i]
  * is its length. A sequence may have no new tokens. width * page is at most
- * 2^31 - 2048. (Tokens before cu[0], were it not 0, belong to no sequence:
- * nothing is appended for them, and their rows of attention's output are
- * undefined.) Page numbers outside the cache are not followed: tokens appended
+ * 2^31 - 2048. (Tokens before cu[0], were it not 0, and from cu[batch] on, as a
+ * padded batch has them, belong to no sequence: nothing is appended for them, and
+ * their rows of attention's output stay as they were.) Page numbers outside the cache are not followed: tokens appended
  * there are dropped, attention reads the cache's last page instead. Pages that
  * are written must belong to one sequence. */
 typedef struct {

@@ -1274,10 +1274,12 @@ __global__ __launch_bounds__(256, D == 128 && RT == 2 ? 1 : 2) void k_attn_rows(
   }
 }
 
-// How many splits of a token's block the first kernel wrote, as it had it.
+// How many splits of a token's block the first kernel wrote, as it had it; none
+// of a token of no sequence, whose row of the output stays.
 __device__ __forceinline__ int splits_of(const AttnArgs &a, int tok) {
   const int i = find_sequence(a.b.cu, a.b.batch, [](int x) { return x; }, 0, tok);
-  const int c0 = a.b.cu[i], n = a.b.cu[i + 1] - c0;
+  const int c0 = a.b.cu[i], c1 = a.b.cu[i + 1], n = c1 - c0;
+  if (c0 < 0 || tok < c0 || tok >= c1 || c1 > a.b.tokens) return 0;
   const int64_t room = (int64_t)a.b.width << a.shift;
   const int len = (int)min((int64_t)max(a.b.lengths[i], 0), room);
   const int at = (tok - c0) / a.block_tokens * a.block_tokens;
@@ -1293,7 +1295,7 @@ __global__ __launch_bounds__(256) void k_attn_join_few(const AttnArgs a) {
   constexpr int C = D / 4, R = 256 / C, P = D + 4;
   const int tok = blockIdx.x, c = threadIdx.x % C, qh = blockIdx.y * R + threadIdx.x / C;
   const int live = splits_of(a, tok);
-  if (qh >= a.q_heads) return;
+  if (!live || qh >= a.q_heads) return;
   const int64_t row = (int64_t)tok * a.q_heads + qh;
   const float *p = a.part + row * a.splits * P;
   float m = -__builtin_inff();
@@ -1325,6 +1327,7 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a) {
   const int64_t row = blockIdx.x;
   const int tok = (int)(row / a.q_heads);
   const int live = splits_of(a, tok);
+  if (!live) return;
   const float *p = a.part + row * a.splits * P;
   const int wave = threadIdx.x >> 6;
 
