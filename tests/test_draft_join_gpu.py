@@ -64,3 +64,35 @@ def test_query_heads_that_leave_part_of_a_wave(heads, group, batch, dim):
     assert shares(sum(new), batch, heads * group, heads, dim, w.table.shape[1] * 64)
     w.append(lengths, [0] * batch)
     check(w, new, lengths, group)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("batch,heads,group,longest", [
+    (65, 1, 1, 900),     # more sequences than share, in one piece
+    (65, 1, 3, 5000),    # split, a workgroup joins a row
+    (70, 2, 5, 5000),    # split, rows joined together, the last ones of a workgroup past the query heads
+    (2, 520, 1, 100),    # more kv heads than share
+    (64, 64, 40, 300),   # more blocks of rows than share
+])
+def test_batches_that_do_not_share(batch, heads, group, longest, dim):
+    """More than 32 rows in the mean, divided as causal attention divides prompts."""
+    new, lengths = batch_of(batch, group, 32, longest, 10 * batch + group)
+    if heads > 2:  # short sequences: the reference takes them a head and token at a time
+        lengths = [n + x % 40 if x < longest else x for n, x in zip(new, lengths)]
+    w = World(lengths, heads, dim, 64, batch + group)
+    assert not shares(sum(new), batch, heads * group, heads, dim, w.table.shape[1] * 64)
+    w.append(lengths, [0] * batch)
+    check(w, new, lengths, group)
+
+
+@pytest.mark.parametrize("new,group", [(8, 4), (3, 7)])
+def test_as_many_sequences_as_share(new, group):
+    """Up to 32 rows of 128 dims share in long contexts: 64 sequences do, 65 do not."""
+    for batch in (64, 65):
+        lengths = [new + 13 * i % 700 for i in range(batch)]
+        lengths[5], lengths[63] = 2500, 1300
+        w = World(lengths, 1, 128, 64, 3)
+        room = w.table.shape[1] * 64
+        assert shares(batch * new, batch, group, 1, 128, room) == (batch == 64)
+        w.append(lengths, [0] * batch)
+        check(w, [new] * batch, lengths, group)
