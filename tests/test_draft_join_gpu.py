@@ -96,3 +96,41 @@ def test_as_many_sequences_as_share(new, group):
         assert shares(batch * new, batch, group, 1, 128, room) == (batch == 64)
         w.append(lengths, [0] * batch)
         check(w, [new] * batch, lengths, group)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_cut_blocks_on_streams_and_in_graphs(dim):
+    """A captured call, replayed for other inputs, and one on another stream, beside eager ones."""
+    new, lengths = batch_of(40, 5, 32, 2500, dim)
+    w = World(lengths, 1, dim, 64, 2)
+    assert shares(sum(new), 40, 5, 1, dim, w.table.shape[1] * 64)
+    w.append(lengths, [0] * 40)
+    words = max(1, -(-max(new) // 32))
+    table, at = w.table.cuda(), i32(lengths).cuda()
+    cu = i32([sum(new[:i]) for i in range(41)]).cuda()
+    q = w.numbers(sum(new), 5).cuda()
+    mask = torch.cat([ref.words_of(m, words) for m in masks(new, "tree", 1)]).cuda()
+    out = torch.empty_like(q)
+
+    def call(out=None):
+        return mx.kv_attention_tree(q, w.gpu, table, cu, at, mask, out=out)
+
+    want = call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(out)
+    side.synchronize()
+    assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out)
+    for seed in range(4):
+        q.copy_(w.numbers(sum(new), 5))
+        mask.copy_(torch.cat([ref.words_of(m, words) for m in masks(new, "any", seed)]))
+        want = call()
+        out.fill_(1e30)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
