@@ -453,9 +453,10 @@ mx_status_t mx_kv_append(const void *k, const void *v, mx_dtype_t dtype, int64_t
  * 8-bit products as those of a bf16 mx_matmul_mxfp8 (the bits that they drop
  * come to less than 2^-10 of sum |q k|); q enters them exactly where an element
  * is above 2^-13 of its row's largest, else off by at most 2^-21 of the
- * largest. The softmax's weights have a relative error of at most 2^-8, and
- * their sum is that of the weights as used. Cached values past bfloat16's range (a byte
- * above 246, which no quantizer here makes) may count as its largest. scale > 0.
+ * largest. The softmax's weights have a relative error of at most 2^-8 (those
+ * below 2^-126 of the row's largest may count as 0), and their sum is that of
+ * the weights as used. Cached values past bfloat16's range (a byte above 246,
+ * which no quantizer here makes) may count as its largest. scale > 0.
  * max_length: an upper bound on lengths that the launch is planned for (0:
  * width * page); a larger length is still right, only slower. workspace:
  * mx_kv_attention_workspace_size(...) bytes, 16-byte aligned (partial results

@@ -20,11 +20,11 @@
 //
 // The second product is a bfloat16 one: values are widened to it (exact, their
 // bytes applied), weights rounded to it, which moves each by at most 2^-9 of
-// itself however far below the largest it lies. (Two E4M3 parts, as q has,
-// end 2^-22 below the largest weight: a tail of many such keys is lost.) The
+// itself however far below the largest it lies, down to 2^-126. (Two E4M3 parts,
+// as q has, end 2^-22 below the largest weight: a tail of many such keys is lost.) The
 // weights' sum is a product with a row of ones, of the weights as rounded.
 //
-// Two kernels. Few rows (single tokens) are bound by reading the cache: one
+// Three kernels. Few rows (single tokens) are bound by reading the cache: one
 // wave per 128 tokens at a time, the sequence split over workgroups. With
 // g = lane / 16, tile t (of 16 rows) and accumulator i hold token 64 (t / 4) +
 // 16 g + 4 (t % 4) + i of 128, and the second product's lane holds tokens
@@ -34,6 +34,9 @@
 // instruction issue: per 32 rows and 128 tokens, 2,200 cycles of products
 // beside 2,400 of vector arithmetic, half of it the exponentials. There the
 // workgroup widens the values once. Token 32 (t / 2) + 8 g + 4 (t % 2) + i.
+//
+// Trees of drafted tokens lie between: the second kernel's way through a tile, with
+// the tiles of a whole batch shared out evenly, and a join of its own.
 #include <algorithm>
 
 #include "mx_layer.h"
@@ -1661,10 +1664,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_tiles(const AttnArgs a) {
 // ones and the beginning of another. What a block got from several workgroups
 // is left in their room (the first and the last block of each: two rooms) and
 // joined. 16 sequences of up to 24 tokens in 8,000 to 32,000, 32 query heads on 8 of
-// 128 dims: 148 us and 8 for the join (splits of one length for all sequences, which
-// left units idle for 41 % of the time, 241 and 8). Bound by what a wave does in a row
-// (scores, weights, sums): 3.9 TB/s, matrix cores 33 % and vector arithmetic 41 % of a
-// unit's cycles.
+// 128 dims: 150 to 154 us a call in a long run, traced 151 and 8 for the join (splits of
+// one length for all sequences, which left units idle for 41 % of the time, 241 and 8).
+// Bound by what a wave does in a row (scores, weights, sums): 3.9 TB/s, matrix cores
+// 33 % and vector arithmetic 41 % of a unit's cycles.
 constexpr int kLeastTiles = 4;    // of a workgroup's share
 constexpr int kSharers = 64;      // sequences: one a lane
 constexpr int kBegin = 2;         // what beginning a block counts for, in tiles (4 trees of up to
@@ -1883,15 +1886,16 @@ static AttnPlan attn_plan(int64_t tokens, int batch, int q_heads, int heads, int
 // Workgroups of a head that share a tree's tiles, and 16-row parts of their waves;
 // none where the kernels of causal attention take it: up to 16 rows, more sequences
 // than a wave has lanes, blocks enough to fill the card over and over, and heads for
-// which one workgroup each would be more than two a compute unit. 17 to 32
-// rows of 128 dims share where sequences may be longer than 1,024 (16 sequences of up
-// to 12 tokens in 32,000: 124 us, 204 with a wave to 32 rows; 48 of 8 in 3,000 56 and
-// 79; 16 of 8 in 700 22 and 15), of 64 dims they do not (48 of 8 in 6,000: 65 and
-// 58). Blocks of 64 rows up to 48 in the mean, since a sequence of more than 64 is then
-// two blocks, which both read its keys (16 sequences of up to 16 tokens in 32,000, 4
-// query heads to a kv head: 127 us, in blocks of 128 rows 133; of up to 24, 64 rows in
-// the mean: 199 and 180). Two workgroups a compute unit, of four tiles at
-// least (eight: 16 of 48 tokens in 2,000 46 us, four 38).
+// which one workgroup each would be more than two a compute unit. Figures: us a call
+// of sequences of up to so many new tokens, 32 query heads on 8. 17 to 32 rows of 128
+// dims share where sequences may be longer than 1,024 (16 x 12 in 32,000: 121, with
+// a wave to 32 rows 204; 48 x 8 in 3,000 51 and 78; 16 x 8 in 700 18 and 15), of 64 dims
+// they do not (48 x 8 in 6,000: 56 and 55). Blocks of 64 rows up to 48 in the mean,
+// since a sequence of more than 64 is then two blocks, which both read its keys (16 x
+// 16 in 32,000, 48 rows in the mean: 121, in blocks of 128 rows 124; 16 x 24, 64 rows:
+// 164 and 152). Two workgroups a compute unit, of four tiles at least (16 x 48 in 2,000:
+// 36, of eight 40). 64 sequences that share beside the same that do not, as 65
+// would: 64 x 12 in 8,000 141 and 165, 64 x 24 178 and 257, in 700 43 and 40.
 struct TreePlan {
   int share, rt, block_tokens;
 };

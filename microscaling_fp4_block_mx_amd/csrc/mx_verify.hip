@@ -12,8 +12,9 @@
 // Sums of a row run over up to hundreds of thousands of numbers and decide at
 // their borders: 64 bits. Two launches. The first finds each node's first child and
 // whether it is taken, and with that which nodes the walk can reach and has to draw at
-// (of a chain with a draft one): only their rows are read, and summed in chunks. The
-// second finds each one's chunk, reads it again and draws; then it walks down.
+// (of a chain with a draft one; without a draft all that it can reach): only their rows
+// are read, and summed in chunks. The second finds each one's chunk, reads it again and
+// draws; then it walks down.
 #include <algorithm>
 
 #include "mx_layer.h"
